@@ -229,8 +229,11 @@ def prepare(case, seed):
     else:
         H, I = case["H"], case["I"]
         s["x"], s["residual"] = _normal((M, H), g, torch.bfloat16), _normal((M, H), g, torch.bfloat16)
-        s["codes"], s["scales"] = _weights(E, 2 * I, H, g)
-        s["codes_down"], s["scales_down"] = _weights(E, H, I, g)
+        layer = s["layer"] = {"H": H, "I": I, "E": E}
+        layer["gate_up_codes"], layer["gate_up_scales"] = _weights(E, 2 * I, H, g)
+        layer["down_codes"], layer["down_scales"] = _weights(E, H, I, g)
+        # the call's workspace: sorted rows, quantised rows of both products, expert outputs
+        s["work"] = torch.zeros((1 << 20) + R * (4 * H + 2 * I), dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -259,13 +262,14 @@ def _run_plain(s):
     q, e = _plain_quantise(s["x"].float())
     x = (q.unflatten(-1, (-1, BLOCK)) * _power(e).unsqueeze(-1)).flatten(-2)
     rows = torch.where(live, x[(row_route.clamp(min=0) // k).long()], 0.0)
-    y = _plain_product(rows, offsets, s["codes"], s["scales"])
     if s["op"] == "product":
-        return {"y": y.to(dt)}
+        return {"y": _plain_product(rows, offsets, s["codes"], s["scales"]).to(dt)}
+    layer = s["layer"]
+    y = _plain_product(rows, offsets, layer["gate_up_codes"], layer["gate_up_scales"])
     g, u = y.chunk(2, 1)
     q, e = _plain_quantise(g / (1 + torch.exp(-g)) * u)
     p = (q.unflatten(-1, (-1, BLOCK)) * _power(e).unsqueeze(-1)).flatten(-2)
-    y = _plain_product(p, offsets, s["codes_down"], s["scales_down"]).to(dt)
+    y = _plain_product(p, offsets, layer["down_codes"], layer["down_scales"]).to(dt)
     return {"out": _plain_unsort(y, route_row, s["w"], s["residual"]).to(dt)}
 
 
@@ -278,17 +282,15 @@ def _run_own(s):
     if s["op"] == "grad":
         grad_rows, grad_w = moe.moe_token_unsort_grad(s["grad_out"], s["rows"], s["route_row"], s["w"])
         return {"grad_rows": grad_rows, "grad_weights": grad_w, "grad_x": moe.moe_token_sort_grad(s["grad_in"], s["route_row"])}
+    if s["op"] == "experts":
+        return {"out": moe.moe_microscale_ffn(s["x"], s["layer"], s["ids"], s["w"], residual=s["residual"], workspace=s["work"])}
     offsets, row_route, route_row = moe.moe_token_plan(s["ids"], s["E"])
     if s["op"] == "route":
         rows = moe.moe_token_sort(s["x"], route_row)
         out = moe.moe_token_unsort(s["rows"], route_row, s["w"], residual=s["residual"])
         return {"offsets": offsets, "row_route": row_route, "route_row": route_row, "rows": rows, "out": out}
     codes, scales = moe.moe_microscale_quantize(s["x"], route_row=route_row)
-    if s["op"] == "product":
-        return {"y": moe.moe_microscale_product(codes, scales, s["codes"], s["scales"], offsets=offsets, dtype=dt, workspace=s["work"])}
-    codes, scales = moe.moe_microscale_gated_product(codes, scales, s["codes"], s["scales"], offsets=offsets, workspace=s["work"])
-    y = moe.moe_microscale_product(codes, scales, s["codes_down"], s["scales_down"], offsets=offsets, dtype=dt, workspace=s["work"])
-    return {"out": moe.moe_token_unsort(y, route_row, s["w"], residual=s["residual"])}
+    return {"y": moe.moe_microscale_product(codes, scales, s["codes"], s["scales"], offsets=offsets, dtype=dt, workspace=s["work"])}
 
 
 def run(state):
@@ -384,21 +386,23 @@ def exact(case, seed):
         out = s["residual"].double().index_add_(0, token, s["rows"][:n].double() * w.reshape(-1)[order].unsqueeze(1))
         return {"offsets": None, "row_route": None, "route_row": None, "rows": rows, "out": out}
     x = _exact_quantise(s["x"].double())
-    N = s["codes"].shape[1]
+    experts = s["op"] == "experts"
+    codes, scales = (s["layer"]["gate_up_codes"], s["layer"]["gate_up_scales"]) if experts else (s["codes"], s["scales"])
+    N = codes.shape[1]
     y = torch.zeros((R, N), dtype=torch.float64, device="cuda")
-    out = s["residual"].double() if s["op"] == "experts" else None
+    out = s["residual"].double() if experts else None
     at = 0
     for e, rs in enumerate(by):
         if not rs:
             continue
         t = token[at:at + len(rs)]
-        z = x[t] @ _exact_weights(s["codes"], s["scales"], e).T
-        if s["op"] == "product":
+        z = x[t] @ _exact_weights(codes, scales, e).T
+        if not experts:
             y[at:at + len(rs)] = z
         else:
             g, u = z[:, : N // 2], z[:, N // 2:]
             p = _exact_quantise(g / (1 + torch.exp(-g)) * u)
-            z = p @ _exact_weights(s["codes_down"], s["scales_down"], e).T
+            z = p @ _exact_weights(s["layer"]["down_codes"], s["layer"]["down_scales"], e).T
             out.index_add_(0, t, z * w.reshape(-1)[order[at:at + len(rs)]].unsqueeze(1))
         at += len(rs)
-    return {"y": y} if s["op"] == "product" else {"out": out}
+    return {"out": out} if experts else {"y": y}
