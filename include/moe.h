@@ -390,6 +390,140 @@ int moe_reader_ffn(const void *h, const moe_reader_t *rd, int M, int k, const in
                    const float *topk_weights, int K, int nscan, const void *residual, void *out,
                    int32_t *selected, float *xr, void *workspace, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Tokens sorted by expert and back, for prompts and for training.
+ *
+ * The M x k routes r = m*k + j are put in (expert, r) order without padding.  A route whose
+ * id lies outside [0, E) is dropped: it adds nothing to any result and gets a zero gradient,
+ * but owns one row past the last expert's, so that rows and routes stay one to one.
+ *
+ * Element types of the rows: MOE_DT_*.  Matrices have contiguous columns and a row pitch (ld,
+ * in elements, >= H); any H >= 1, any pitch and any element-aligned pointer is taken, and rows
+ * whose pointers, pitches and length are multiples of 16 bytes move fastest.  k <= 32,
+ * M * k < 2^24.  Sums are fp32 in fixed orders; each value is rounded once, when stored.
+ * Outputs must not overlap inputs.
+ */
+#define MOE_DT_BF16 0
+#define MOE_DT_F16  1
+#define MOE_DT_F32  2
+
+/*
+ * The sorted order of topk_ids [M,k]: offsets [E+1] (expert e owns rows offsets[e] ..
+ * offsets[e+1] - 1; offsets[E] = valid routes), route_row [M,k] (the row of each route; for a
+ * dropped route the bitwise complement of its row, which lies past offsets[E]) and row_route
+ * [M*k] (the route of each row, -1 for the rows of dropped routes).  E <= 1024.  One launch,
+ * no workspace, stable: bitwise identical on every run.  M == 0 writes offsets only.
+ */
+int moe_token_plan(const int32_t *topk_ids, int M, int k, int E, int32_t *offsets,
+                   int32_t *row_route, int32_t *route_row, void *stream);
+
+/* rows[row(m,j)] = x[m] for every route; the rows of dropped routes are zero. */
+int moe_token_sort(const void *x, int64_t ldx, int dtype, int M, int k, int H,
+                   const int32_t *route_row, void *rows, int64_t ldr, void *stream);
+
+/* Gradient of moe_token_sort: grad_x[m] = sum_j grad_rows[row(m,j)] over valid routes. */
+int moe_token_sort_grad(const void *grad_rows, int64_t ldr, int dtype, int M, int k, int H,
+                        const int32_t *route_row, void *grad_x, int64_t ldx, void *stream);
+
+/*
+ * out[m] = residual[m] + sum_j topk_weights[m,j] * rows[row(m,j)] over valid routes, slots in
+ * ascending order.  topk_weights [M,k] fp32, NULL for weights of one; residual NULL for none.
+ */
+int moe_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
+                     const int32_t *route_row, const float *topk_weights, const void *residual,
+                     int64_t ldres, void *out, int64_t ldo, void *stream);
+
+/*
+ * Gradients of moe_token_unsort (the residual's is grad_out itself):
+ *   grad_rows[row(m,j)] = topk_weights[m,j] * grad_out[m]  (zero for dropped routes)
+ *   grad_weights[m,j]   = <grad_out[m], rows[row(m,j)]>    (fp32; zero for dropped routes)
+ */
+int moe_token_unsort_grad(const void *grad_out, int64_t ldo, const void *rows, int64_t ldr,
+                          int dtype, int M, int k, int H, const int32_t *route_row,
+                          const float *topk_weights, void *grad_rows, int64_t ldg,
+                          float *grad_weights, void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * 4-bit block floating point (the OCP Microscaling Formats Specification's MXFP4) and
+ * grouped products of it on the block-scaled tensor-core MMAs.
+ *
+ * A matrix [rows][cols], cols a multiple of 32 up to 2^20, is held as
+ *   codes  [rows][cols/2] uint8: two E2M1 codes a byte, the even column in the low half;
+ *   scales [rows][pitch] uint8: byte X + 127 of each block of 32 columns, pitch =
+ *          moe_microscale_pitch(cols), cols/32 rounded up to a multiple of 16.
+ * both 16-byte aligned and contiguous.  X = clamp(floor(log2 max|x|) - 2, -127, 127); a code
+ * is x / 2^X rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the even code),
+ * saturating at 6.  A block with an infinity or a NaN gets scale byte 255, whose values are
+ * NaN.
+ */
+int moe_microscale_pitch(int cols);  /* scale bytes of a row; 0 for unsupported cols */
+
+/*
+ * x [rows][cols] of MOE_DT_* (row pitch ldx) to codes and scales; padding bytes are written
+ * as 0.  route_row NULL: row by row.  Else route_row [rows][k] of a token plan: x holds tokens,
+ * codes and scales hold rows * k sorted rows, each token quantised once and written to the
+ * rows of its routes (zeros in the rows of dropped ones).
+ */
+int moe_microscale_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int cols,
+                            const int32_t *route_row, int k, uint8_t *codes, uint8_t *scales,
+                            void *stream);
+
+/* Codes and scales back to values (exact in bf16 and fp32; fp16 rounds and overflows). */
+int moe_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                              int cols, void *x, int64_t ldx, int dtype, void *stream);
+
+/* The first bytes of the workspace of the products below: a status word that must be zero
+ * before the first call, read back with moe_read_device_status. */
+#define MOE_MICROSCALE_STATUS_BYTES 256
+
+/*
+ * y[r][n] = <x[r], w[e][n]> for the rows r of expert e: x [rows][K], w [E][N][K], y [rows][N]
+ * of MOE_DT_* with row pitch ldy.  offsets [E+1] (device) as moe_token_plan gives them; rows
+ * past offsets[E] are set to zero; NULL means one group (E == 1).  Any N >= 1, K a multiple
+ * of 32, E <= 1024, E * N < 2^30, rows < 2^24.  Accumulation is fp32 in K order: a row's bits do not depend
+ * on the other rows.  workspace: ws_bytes >= MOE_MICROSCALE_STATUS_BYTES, 16-byte aligned.
+ */
+int moe_microscale_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
+                           const int32_t *offsets, const uint8_t *w_codes,
+                           const uint8_t *w_scales, int E, int N, int K, int dtype, void *y,
+                           int64_t ldy, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The same with w holding N/2 gate rows, then N/2 up rows per expert (N a multiple of 64):
+ * p = SiLU(g) * u in fp32, quantised to codes [rows][N/4] and scales
+ * [rows][moe_microscale_pitch(N/2)]; rows past offsets[E] are zero.
+ */
+int moe_microscale_gated_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
+                                 const int32_t *offsets, const uint8_t *w_codes,
+                                 const uint8_t *w_scales, int E, int N, int K, uint8_t *codes,
+                                 uint8_t *scales, void *workspace, size_t ws_bytes,
+                                 void *stream);
+
+/* A layer's 4-bit expert weights: gate_up [E][2I][H] (I gate rows, then I up rows per expert)
+ * and down [E][H][I], each as codes and scales. */
+typedef struct moe_microscale_weights {
+    int32_t H, I, E;
+    int32_t reserved;
+    const uint8_t *gate_up_codes;
+    const uint8_t *gate_up_scales;
+    const uint8_t *down_codes;
+    const uint8_t *down_scales;
+} moe_microscale_weights_t;
+
+/* Workspace bytes of moe_microscale_ffn; 0 on unsupported arguments. */
+size_t moe_microscale_workspace_bytes(const moe_microscale_weights_t *w, int M, int k);
+
+/*
+ * The expert step with 4-bit weights and activations, for given routes: h is quantised per
+ * token, p per route.  Arguments as moe_expert_ffn's; out [M,H] bf16 = bf16(residual +
+ * sum_j a_j y_j) with y rounded to bf16.  H and I multiples of 32, E <= 1024, E * max(2I, H) <
+ * 2^30.  workspace: 256-byte aligned, ws_bytes >= moe_microscale_workspace_bytes, its first
+ * MOE_MICROSCALE_STATUS_BYTES zero before the first call.
+ */
+int moe_microscale_ffn(const void *h, const moe_microscale_weights_t *w, int M, int k,
+                       const int32_t *topk_ids, const float *topk_weights, const void *residual,
+                       void *out, void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

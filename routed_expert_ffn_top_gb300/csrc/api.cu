@@ -157,9 +157,9 @@ static bool make_tmap_3d_bf16(CUtensorMap *tm, const void *base, uint64_t d0, ui
 }
 
 // 2-D row-major tensor [outer][inner] of `elem` bytes, box [box_outer][box_inner].
-static bool make_tmap_2d(CUtensorMap *tm, const void *base, CUtensorMapDataType dt, int elem,
-                         uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
-                         CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
+bool make_tmap_2d(CUtensorMap *tm, const void *base, CUtensorMapDataType dt, int elem,
+                  uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
+                  CUtensorMapSwizzle swizzle) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {inner, outer};

@@ -1,0 +1,276 @@
+// api_tokens.cu -- C entry points (include/moe.h) of the token sort and of 4-bit block
+// floating point: argument validation, tensor maps, and the 4-bit expert step.
+#include "moe_internal.cuh"
+
+using namespace moe;
+
+static bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+static int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+static int dtype_bytes(int dtype) {
+    return dtype == MOE_DT_F32 ? 4 : (dtype == MOE_DT_BF16 || dtype == MOE_DT_F16 ? 2 : 0);
+}
+
+static int check_routes(int M, int k) {
+    if (M < 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (k > 32 || (int64_t)M * k >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// A matrix of `rows` rows of H elements, row pitch ld: its sizes, and its pointer's alignment
+// to the element.
+static int check_matrix(const void *p, int64_t ld, int H, int elem) {
+    if (!p || ld < H || !aligned(p, elem)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------------------ token sort
+extern "C" int moe_token_plan(const int32_t *topk_ids, int M, int k, int E, int32_t *offsets,
+                              int32_t *row_route, int32_t *route_row, void *stream) {
+    const int rc = check_routes(M, k);
+    if (rc != MOE_OK) return rc;
+    if (E <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > kPlanMaxExperts) return MOE_ERR_UNSUPPORTED;
+    if (!offsets || !aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
+    if (M > 0 && (!topk_ids || !row_route || !route_row || !aligned(topk_ids, 4) ||
+                  !aligned(row_route, 4) || !aligned(route_row, 4)))
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_token_plan(topk_ids, M, k, E, offsets, row_route, route_row,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+static int check_token_args(int dtype, int M, int k, int H, const int32_t *route_row) {
+    const int rc = check_routes(M, k);
+    if (rc != MOE_OK) return rc;
+    if (dtype_bytes(dtype) == 0 || H <= 0) return MOE_ERR_INVALID_ARG;
+    if (M > 0 && (!route_row || !aligned(route_row, 4))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+extern "C" int moe_token_sort(const void *x, int64_t ldx, int dtype, int M, int k, int H,
+                              const int32_t *route_row, void *rows, int64_t ldr, void *stream) {
+    int rc = check_token_args(dtype, M, k, H, route_row);
+    if (rc != MOE_OK) return rc;
+    if (M == 0) return MOE_OK;
+    const int elem = dtype_bytes(dtype);
+    if ((rc = check_matrix(x, ldx, H, elem)) != MOE_OK) return rc;
+    if ((rc = check_matrix(rows, ldr, H, elem)) != MOE_OK) return rc;
+    return cuda_status(launch_token_sort(x, ldx, elem, M, k, H, route_row, rows, ldr,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int moe_token_sort_grad(const void *grad_rows, int64_t ldr, int dtype, int M, int k, int H,
+                                   const int32_t *route_row, void *grad_x, int64_t ldx, void *stream) {
+    return moe_token_unsort(grad_rows, ldr, dtype, M, k, H, route_row, nullptr, nullptr, 0, grad_x, ldx, stream);
+}
+
+extern "C" int moe_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
+                                const int32_t *route_row, const float *topk_weights,
+                                const void *residual, int64_t ldres, void *out, int64_t ldo,
+                                void *stream) {
+    int rc = check_token_args(dtype, M, k, H, route_row);
+    if (rc != MOE_OK) return rc;
+    if (M == 0) return MOE_OK;
+    const int elem = dtype_bytes(dtype);
+    if ((rc = check_matrix(rows, ldr, H, elem)) != MOE_OK) return rc;
+    if ((rc = check_matrix(out, ldo, H, elem)) != MOE_OK) return rc;
+    if (residual && (rc = check_matrix(residual, ldres, H, elem)) != MOE_OK) return rc;
+    if (topk_weights && !aligned(topk_weights, 4)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_token_unsort(rows, ldr, dtype, M, k, H, route_row, topk_weights, residual,
+                                           residual ? ldres : 0, out, ldo, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int moe_token_unsort_grad(const void *grad_out, int64_t ldo, const void *rows, int64_t ldr,
+                                     int dtype, int M, int k, int H, const int32_t *route_row,
+                                     const float *topk_weights, void *grad_rows, int64_t ldg,
+                                     float *grad_weights, void *stream) {
+    int rc = check_token_args(dtype, M, k, H, route_row);
+    if (rc != MOE_OK) return rc;
+    if (M == 0) return MOE_OK;
+    const int elem = dtype_bytes(dtype);
+    if ((rc = check_matrix(grad_out, ldo, H, elem)) != MOE_OK) return rc;
+    if ((rc = check_matrix(rows, ldr, H, elem)) != MOE_OK) return rc;
+    if ((rc = check_matrix(grad_rows, ldg, H, elem)) != MOE_OK) return rc;
+    if (!grad_weights || !aligned(grad_weights, 4) || (topk_weights && !aligned(topk_weights, 4)))
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_token_unsort_grad(grad_out, ldo, rows, ldr, dtype, M, k, H, route_row,
+                                                topk_weights, grad_rows, ldg, grad_weights,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------- 4-bit block floating point
+// Columns of a quantised matrix: whole blocks, and rows short enough for 32-bit offsets.
+static int check_cols(int cols) {
+    if (cols <= 0) return MOE_ERR_INVALID_ARG;
+    return cols % 32 != 0 || cols > (1 << 20) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+extern "C" int moe_microscale_pitch(int cols) { return check_cols(cols) == MOE_OK ? microscale_pitch(cols) : 0; }
+
+extern "C" int moe_microscale_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int cols,
+                                       const int32_t *route_row, int k, uint8_t *codes, uint8_t *scales,
+                                       void *stream) {
+    if (rows < 0 || dtype_bytes(dtype) == 0) return MOE_ERR_INVALID_ARG;
+    int rc = check_cols(cols);
+    if (rc != MOE_OK) return rc;
+    if (rows >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+    if (route_row) {
+        if (rows >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+        if ((rc = check_routes((int)rows, k)) != MOE_OK) return rc;
+        if (!aligned(route_row, 4)) return MOE_ERR_INVALID_ARG;
+    }
+    if (rows == 0) return MOE_OK;
+    if ((rc = check_matrix(x, ldx, cols, dtype_bytes(dtype))) != MOE_OK) return rc;
+    if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_microscale_quantize(x, ldx, dtype, rows, cols, route_row, route_row ? k : 1,
+                                                  codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int moe_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int cols,
+                                         void *x, int64_t ldx, int dtype, void *stream) {
+    if (rows < 0 || dtype_bytes(dtype) == 0) return MOE_ERR_INVALID_ARG;
+    int rc = check_cols(cols);
+    if (rc != MOE_OK) return rc;
+    if (rows >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if ((rc = check_matrix(x, ldx, cols, dtype_bytes(dtype))) != MOE_OK) return rc;
+    if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_microscale_dequantize(codes, scales, rows, cols, x, ldx, dtype,
+                                                    static_cast<cudaStream_t>(stream)));
+}
+
+// Sizes and pointers of a grouped product of rows [rows][K] and weights [E][N][K].
+static int check_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows, const int32_t *offsets,
+                         const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K,
+                         const void *workspace, size_t ws_bytes) {
+    if (rows < 0 || E <= 0 || N <= 0) return MOE_ERR_INVALID_ARG;
+    const int rc = check_cols(K);
+    if (rc != MOE_OK) return rc;
+    if (E > kMicroscaleMaxExperts || (int64_t)E * N >= ((int64_t)1 << 30) || rows >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (!offsets && E != 1) return MOE_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) || (offsets && !aligned(offsets, 4))) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < MOE_MICROSCALE_STATUS_BYTES) return MOE_ERR_WORKSPACE;
+    if (rows == 0) return MOE_OK;
+    if (!x_codes || !x_scales || !w_codes || !w_scales) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x_codes, 16) || !aligned(x_scales, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
+                         const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K) {
+    const int pitch = microscale_pitch(K);
+    const uint32_t half = (uint32_t)microscale_tile_n(rows, E) / 2;
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    return make_tmap_2d(&tm->a, x_codes, u8, 1, K / 2, rows, 128, 128, sw) &&
+           make_tmap_2d(&tm->a_small, x_codes, u8, 1, K / 2, rows, 128, 32, sw) &&
+           make_tmap_2d(&tm->sa, x_scales, u8, 1, pitch, rows, 16, 128) &&
+           make_tmap_2d(&tm->sa_small, x_scales, u8, 1, pitch, rows, 16, 32) &&
+           make_tmap_2d(&tm->b, w_codes, u8, 1, K / 2, (uint64_t)E * N, 128, half, sw) &&
+           make_tmap_2d(&tm->sb, w_scales, u8, 1, pitch, (uint64_t)E * N, 16, half);
+}
+
+extern "C" int moe_microscale_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
+                                      const int32_t *offsets, const uint8_t *w_codes,
+                                      const uint8_t *w_scales, int E, int N, int K, int dtype, void *y,
+                                      int64_t ldy, void *workspace, size_t ws_bytes, void *stream) {
+    int rc = check_product(x_codes, x_scales, rows, offsets, w_codes, w_scales, E, N, K, workspace, ws_bytes);
+    if (rc != MOE_OK) return rc;
+    if (dtype_bytes(dtype) == 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if ((rc = check_matrix(y, ldy, N, dtype_bytes(dtype))) != MOE_OK) return rc;
+    MicroscaleMaps tm;
+    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K)) return MOE_ERR_CUDA;
+    return cuda_status(launch_microscale_gemm(tm, rows, offsets, E, N, K, dtype, y, ldy, nullptr, nullptr,
+                                              static_cast<int32_t *>(workspace),
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int moe_microscale_gated_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
+                                            const int32_t *offsets, const uint8_t *w_codes,
+                                            const uint8_t *w_scales, int E, int N, int K, uint8_t *codes,
+                                            uint8_t *scales, void *workspace, size_t ws_bytes, void *stream) {
+    int rc = check_product(x_codes, x_scales, rows, offsets, w_codes, w_scales, E, N, K, workspace, ws_bytes);
+    if (rc != MOE_OK) return rc;
+    if (N % 64 != 0) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_INVALID_ARG;
+    MicroscaleMaps tm;
+    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K)) return MOE_ERR_CUDA;
+    return cuda_status(launch_microscale_gemm(tm, rows, offsets, E, N, K, MOE_DT_BF16, nullptr, 0, codes, scales,
+                                              static_cast<int32_t *>(workspace),
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+// ----------------------------------------------------------------------- the expert step
+struct MicroscaleWs {
+    size_t offsets, row_route, route_row, x_codes, x_scales, p_codes, p_scales, y, total;
+};
+
+static MicroscaleWs microscale_ws(int E, int H, int I, int64_t R) {
+    MicroscaleWs L;
+    size_t off = MOE_MICROSCALE_STATUS_BYTES;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = (off + bytes + 255) / 256 * 256;
+        return at;
+    };
+    L.offsets = take((size_t)(E + 1) * 4);
+    L.row_route = take((size_t)R * 4);
+    L.route_row = take((size_t)R * 4);
+    L.x_codes = take((size_t)R * (H / 2));
+    L.x_scales = take((size_t)R * microscale_pitch(H));
+    L.p_codes = take((size_t)R * (I / 2));
+    L.p_scales = take((size_t)R * microscale_pitch(I));
+    L.y = take((size_t)R * H * 2);
+    L.total = off;
+    return L;
+}
+
+static int check_microscale_weights(const moe_microscale_weights_t *w) {
+    if (!w || w->H <= 0 || w->I <= 0 || w->E <= 0) return MOE_ERR_INVALID_ARG;
+    if (check_cols(w->H) != MOE_OK || check_cols(w->I) != MOE_OK) return MOE_ERR_UNSUPPORTED;
+    if (w->E > kMicroscaleMaxExperts || (int64_t)w->E * w->I * 2 >= ((int64_t)1 << 30) ||
+        (int64_t)w->E * w->H >= ((int64_t)1 << 30))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+extern "C" size_t moe_microscale_workspace_bytes(const moe_microscale_weights_t *w, int M, int k) {
+    if (check_microscale_weights(w) != MOE_OK || check_routes(M, k) != MOE_OK) return 0;
+    return microscale_ws(w->E, w->H, w->I, (int64_t)M * k).total;
+}
+
+extern "C" int moe_microscale_ffn(const void *h, const moe_microscale_weights_t *w, int M, int k,
+                                  const int32_t *topk_ids, const float *topk_weights, const void *residual,
+                                  void *out, void *workspace, size_t ws_bytes, void *stream) {
+    int rc = check_microscale_weights(w);
+    if (rc != MOE_OK) return rc;
+    if ((rc = check_routes(M, k)) != MOE_OK) return rc;
+    if (M == 0) return MOE_OK;
+    if (!h || !topk_ids || !topk_weights || !out || !workspace || !aligned(workspace, 256) ||
+        !aligned(h, 16) || !aligned(out, 16) || (residual && !aligned(residual, 16)))
+        return MOE_ERR_INVALID_ARG;
+    const int64_t R = (int64_t)M * k;
+    const MicroscaleWs L = microscale_ws(w->E, w->H, w->I, R);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    int32_t *offsets = reinterpret_cast<int32_t *>(ws + L.offsets);
+    int32_t *route_row = reinterpret_cast<int32_t *>(ws + L.route_row);
+    rc = moe_token_plan(topk_ids, M, k, w->E, offsets, reinterpret_cast<int32_t *>(ws + L.row_route), route_row, stream);
+    if (rc != MOE_OK) return rc;
+    rc = moe_microscale_quantize(h, w->H, MOE_DT_BF16, M, w->H, route_row, k, ws + L.x_codes, ws + L.x_scales, stream);
+    if (rc != MOE_OK) return rc;
+    rc = moe_microscale_gated_product(ws + L.x_codes, ws + L.x_scales, R, offsets, w->gate_up_codes,
+                                      w->gate_up_scales, w->E, 2 * w->I, w->H, ws + L.p_codes, ws + L.p_scales,
+                                      workspace, ws_bytes, stream);
+    if (rc != MOE_OK) return rc;
+    // y is rounded to bf16: it is written and read once per route, and fp32 would double the
+    // largest transfer of the step at long prompts for 2^-9 relative error on each of k terms
+    rc = moe_microscale_product(ws + L.p_codes, ws + L.p_scales, R, offsets, w->down_codes, w->down_scales, w->E,
+                                w->H, w->I, MOE_DT_BF16, ws + L.y, w->H, workspace, ws_bytes, stream);
+    if (rc != MOE_OK) return rc;
+    return moe_token_unsort(ws + L.y, w->H, MOE_DT_BF16, M, k, w->H, route_row, topk_weights, residual, w->H, out,
+                            w->H, stream);
+}

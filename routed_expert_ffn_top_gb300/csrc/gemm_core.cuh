@@ -91,7 +91,8 @@ struct GCtl {
     int route[2][kGemmBlock];  // down epilogue: route of each tile row, per accumulator
 };
 
-__device__ __forceinline__ bool gwait(uint64_t *bar, uint32_t parity, GCtl &ctl) {
+template <typename Ctl>
+__device__ __forceinline__ bool gwait(uint64_t *bar, uint32_t parity, Ctl &ctl) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     while (true) {

@@ -1,0 +1,227 @@
+// microscale.cu -- 4-bit block floating point (the OCP Microscaling Formats Specification's
+// MXFP4): quantisation of rows and the way back.
+//
+// A block is 32 consecutive values of a row.  Its scale is a power of two 2^X held as the
+// byte X + 127, with X = clamp(floor(log2 max|x|) - 2, -127, 127) (2 is the exponent of the
+// largest code, 6 = 1.5 * 2^2); a value's code is x / 2^X rounded to the nearest of
+// 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign, ties to the even code, saturating at 6.  Division
+// by 2^X is exact, so each value is rounded once.  A block without a nonzero value has scale
+// byte 0; a block with an infinity or a NaN has scale byte 255, which makes all its values
+// NaN, and codes 0.
+//
+// Codes are packed two to a byte, the even column in the low half: [rows][cols / 2].  Scale
+// rows are padded to a multiple of 16 bytes, [rows][pitch] (the tensor-map rule on row
+// pitches), and the padding is written as 0.
+#include "microscale.cuh"
+
+namespace moe {
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+
+// Eight consecutive elements; kVec: 16-byte accesses.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
+    if constexpr (kVec) {
+        constexpr int n = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 8; i += n) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p + i);
+            const T *t = reinterpret_cast<const T *>(&u);
+#pragma unroll
+            for (int q = 0; q < n; ++q) v[i + q] = to_f32(t[q]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+    }
+}
+
+struct QuantArgs {
+    const void *x;
+    int64_t ldx;
+    int64_t rows;
+    int cols, pitch, k;
+    const int32_t *route_row;  // NULL: row m goes to row m; else to the rows of its k routes
+    uint8_t *codes, *scales;
+};
+
+// A unit is 512 columns of one row, one warp: lane l takes columns 8 l and 256 + 8 l, four
+// lanes share a block.  512 columns are 16 scale bytes, one store.  With route_row a token is
+// quantised once and stored k times (tail rows of dropped routes as zeros).
+// Memory bound: elem + 1/2 + 1/32 bytes a value.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256) microscale_quantize_kernel(const QuantArgs a, int nchunk) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t units = a.rows * nchunk;
+    const int64_t stride = (int64_t)gridDim.x * 8;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += stride) {
+        const int64_t m = u / nchunk;
+        const int c0 = (int)(u - m * nchunk) * 512;
+        const T *x = static_cast<const T *>(a.x) + m * a.ldx + c0 + lane * 8;
+        const bool in[2] = {c0 + lane * 8 < a.cols, c0 + 256 + lane * 8 < a.cols};
+        float v[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[h][i] = 0.0f;
+            if (in[h]) load8<T, kVec>(x + 256 * h, v[h]);
+        }
+        const int row_l = a.route_row && lane < a.k ? a.route_row[m * a.k + lane] : 0;
+        uint32_t code[2];
+        uint4 sc;
+        uint32_t sb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = __float_as_uint(v[h][i]) & 0x7fffffffu;
+                top = b > top ? b : top;
+            }
+            uint32_t o = __shfl_xor_sync(0xffffffffu, top, 1);
+            top = o > top ? o : top;
+            o = __shfl_xor_sync(0xffffffffu, top, 2);
+            top = o > top ? o : top;
+            const uint32_t byte = microscale_byte(top);
+            const float inv = microscale_inverse(byte);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[h][i] *= inv;
+            code[h] = byte == 255u ? 0u : fp4x8(v[h]);
+            sb[h] = byte;
+        }
+        // the warp's 16 scale bytes: block b of half h in lane 4 b
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                lo |= __shfl_sync(0xffffffffu, sb[h], 4 * b) << (8 * b);
+                hi |= __shfl_sync(0xffffffffu, sb[h], 16 + 4 * b) << (8 * b);
+            }
+            if (h == 0) sc.x = lo, sc.y = hi;
+            else sc.z = lo, sc.w = hi;
+        }
+        const int n = a.route_row ? a.k : 1;
+        for (int j = 0; j < n; ++j) {
+            int64_t at = m;
+            bool live = true;
+            if (a.route_row) {
+                const int row = __shfl_sync(0xffffffffu, row_l, j);
+                live = row >= 0;
+                at = live ? row : ~row;
+                if (at >= a.rows * a.k) continue;
+            }
+            uint8_t *dst = a.codes + at * (a.cols / 2) + (c0 + lane * 8) / 2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (in[h]) *reinterpret_cast<uint32_t *>(dst + 128 * h) = live ? code[h] : 0u;
+            if (lane == 0)
+                *reinterpret_cast<uint4 *>(a.scales + at * a.pitch + c0 / 32) = live ? sc : uint4{0, 0, 0, 0};
+        }
+    }
+}
+
+struct DequantArgs {
+    const uint8_t *codes, *scales;
+    int64_t rows;
+    int cols, pitch;
+    void *x;
+    int64_t ldx;
+};
+
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+
+// A unit is 512 columns of one row, as above.  A code's value times 2^X is exact in fp32 and
+// in bf16; fp16 rounds it (to infinity past its range).
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(256) microscale_dequantize_kernel(const DequantArgs a, int nchunk) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t units = a.rows * nchunk;
+    const int64_t stride = (int64_t)gridDim.x * 8;
+    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += stride) {
+        const int64_t m = u / nchunk;
+        const int c0 = (int)(u - m * nchunk) * 512 + lane * 8;
+        uint32_t code[2], byte[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 256 * h;
+            code[h] = c < a.cols ? *reinterpret_cast<const uint32_t *>(a.codes + m * (a.cols / 2) + c / 2) : 0u;
+            byte[h] = c < a.cols ? a.scales[m * a.pitch + c / 32] : 0u;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 256 * h;
+            if (c >= a.cols) continue;
+            const float s = microscale_value(byte[h]);
+            alignas(16) T o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // magnitude bits eem: 0.5 m for ee = 0, else (2 + m) 2^(ee - 2)
+                const uint32_t q = code[h] >> (4 * i);
+                const uint32_t ee = (q >> 1) & 3u, mm = q & 1u;
+                const float mag = ee == 0 ? 0.5f * (float)mm : __uint_as_float(((ee + 126u) << 23) | (mm << 22));
+                put(&o[i], ((q & 8u) ? -mag : mag) * s);
+            }
+            T *dst = static_cast<T *>(a.x) + m * a.ldx + c;
+            if constexpr (kVec) {
+                constexpr int n = 16 / sizeof(T);
+#pragma unroll
+                for (int i = 0; i < 8; i += n)
+                    *reinterpret_cast<uint4 *>(dst + i) = *reinterpret_cast<const uint4 *>(&o[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = o[i];
+            }
+        }
+    }
+}
+
+static unsigned ctas_for(int64_t units) {
+    const int64_t n = (units + 7) / 8, most = (int64_t)num_sms() * 64;
+    return (unsigned)(n < 1 ? 1 : n < most ? n : most);
+}
+
+template <typename T>
+static cudaError_t quantize_as(const QuantArgs &a, cudaStream_t stream) {
+    const int nchunk = (a.cols + 511) / 512;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.ldx * sizeof(T))) % 16 == 0;
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = launch_config(dim3(ctas_for(a.rows * nchunk)), dim3(256), 0, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, vec ? microscale_quantize_kernel<T, true> : microscale_quantize_kernel<T, false>, a, nchunk);
+}
+
+template <typename T>
+static cudaError_t dequantize_as(const DequantArgs &a, cudaStream_t stream) {
+    const int nchunk = (a.cols + 511) / 512;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.ldx * sizeof(T))) % 16 == 0;
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = launch_config(dim3(ctas_for(a.rows * nchunk)), dim3(256), 0, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, vec ? microscale_dequantize_kernel<T, true> : microscale_dequantize_kernel<T, false>, a, nchunk);
+}
+
+cudaError_t launch_microscale_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int cols,
+                                       const int32_t *route_row, int k, uint8_t *codes, uint8_t *scales,
+                                       cudaStream_t stream) {
+    const QuantArgs a{x, ldx, rows, cols, microscale_pitch(cols), k, route_row, codes, scales};
+    if (dtype == MOE_DT_F32) return quantize_as<float>(a, stream);
+    if (dtype == MOE_DT_F16) return quantize_as<__half>(a, stream);
+    return quantize_as<__nv_bfloat16>(a, stream);
+}
+
+cudaError_t launch_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                         int cols, void *x, int64_t ldx, int dtype, cudaStream_t stream) {
+    const DequantArgs a{codes, scales, rows, cols, microscale_pitch(cols), x, ldx};
+    if (dtype == MOE_DT_F32) return dequantize_as<float>(a, stream);
+    if (dtype == MOE_DT_F16) return dequantize_as<__half>(a, stream);
+    return dequantize_as<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace moe

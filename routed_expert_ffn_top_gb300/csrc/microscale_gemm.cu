@@ -1,0 +1,534 @@
+// microscale_gemm.cu -- the grouped product of 4-bit block-scaled rows and expert weights on
+// the block-scaled tensor-core MMAs (tcgen05.mma kind::mxf4, E2M1 codes, one E8M0 scale per
+// 32 along K).
+//
+// Rows [rows][K] are grouped by expert (offsets, as the token plan gives them); expert e's
+// weights are [N][K], so
+//   y[r][n] = sum_b 2^(X_r,b + X_n,b) sum_{i in block b} c_r,i c_n,i,      r in e's rows.
+// Products and scales are exact; the sums over K run in the tensor core's fp32 accumulators in
+// K order, so a row's result does not depend on its group, its tile or the grid.
+//
+// A unit is a tile of up to 128 rows of one expert (the MMA's M side) times kN of its output
+// channels (the N side).  Groups need no padding: a tile's row box may run into the next
+// expert's rows, whose results are dropped by the epilogue (a row of A only reaches its own
+// row of D).  The gated form takes kN/2 gate channels and the kN/2 up channels beside them,
+// computes p = SiLU(g) u in fp32 and quantises it in the epilogue, so g and u never leave the
+// chip.
+//
+// Per CTA, 10 warps: 0-3 drain the accumulators, 4-7 bring the scales from shared memory into
+// tensor memory, 8 issues the copies, 9 the MMAs.  A stage is 256 of K: 128-byte rows of
+// codes, 128-byte swizzled, and 16-byte rows of scales (a copy's inner extent is 16 bytes at
+// least, so two stages share their scale bytes and each uses its half).  The MMA reads the
+// scale of row r at lane r % 32, column r / 32, four K blocks a 32-bit column, repeated in the
+// four lane quadrants.  Accumulators are double-buffered, so a tile's epilogue overlaps the
+// next one's MMAs.
+#include <type_traits>
+
+#include "gemm_core.cuh"
+#include "microscale.cuh"
+
+namespace moe {
+
+constexpr int kMxThreads = 320;
+constexpr int kMxStageK = 256;
+constexpr int kMxRows = 128;
+constexpr int kMxMaxStages = 8;
+constexpr int kMxSmallBox = 32;  // rows per copy for tiles that are not full
+
+template <int kN>
+struct MxTile {
+    static constexpr int kABytes = kMxRows * 128;
+    static constexpr int kBBytes = kN * 128;
+    static constexpr int kSABytes = kMxRows * 16;
+    static constexpr int kSBBytes = kN * 16;
+    static constexpr int kStageBytes = kABytes + kBBytes + kSABytes + kSBBytes;
+    static constexpr int kStages = kN == 192 ? 4 : 8;
+    static constexpr int kACols = kMxRows / 32;  // scale columns per 128 of K
+    static constexpr int kBCols = kN / 32;
+    static constexpr int kBPad = (kBCols + 3) / 4 * 4;     // every set starts at a multiple of 4
+    static constexpr int kSfCols = 2 * (kACols + kBPad);   // per stage
+    static constexpr int kSfCol0 = 2 * kN;                 // after the two accumulators
+    static constexpr uint32_t kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
+    static_assert(kStageBytes % 1024 == 0, "stage alignment");
+    static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
+    static_assert(kStages <= kMxMaxStages, "barriers");
+};
+
+struct MxCtl {
+    uint64_t full[kMxMaxStages];
+    uint64_t empty[kMxMaxStages];
+    uint64_t sfull[kMxMaxStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t done;
+    uint32_t tmem;
+    volatile int abort;
+    int32_t wsum[kMxThreads / 32];
+    int32_t valid_rows;
+    int32_t first[kMicroscaleMaxExperts + 1];  // row tiles before expert e
+    int32_t begin[kMicroscaleMaxExperts + 1];  // first row of expert e
+};
+
+struct MxArgs {
+    const int32_t *offsets;  // NULL: one group of all rows
+    int64_t rows;
+    int E, N, K;
+    int nct;                 // column tiles
+    int vec;                 // y rows allow 32-byte stores
+    void *y;
+    int64_t ldy;
+    uint8_t *codes, *scales;  // gated output
+    int pitch;                // its scale row bytes
+    int32_t *status;
+};
+
+// Instruction descriptor of kind::mxf4 with M = 128: E2M1 A and B (K-major), E8M0 scales; the
+// scale ids pick the 16-bit half of the scale columns (0: bytes 0-1, 2: bytes 2-3).
+__device__ __forceinline__ constexpr uint32_t mx_idesc(int N, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(kMxRows >> 4) << 24) | (sf_id << 29);
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+// 32 consecutive fp32 columns of this warp's lanes; complete after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// The registers are operands so that no use of them moves above the wait.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                   "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                   "+r"(r[28])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+__device__ __forceinline__ void put_f32(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put_f32(__half *p, float v) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void put_f32(float *p, float v) { *p = v; }
+
+// 32 columns of one row from column n: whole 32-byte sectors where the row allows.
+template <typename T>
+__device__ __forceinline__ void store_row32(const MxArgs &a, int64_t row, int n, const uint32_t (&v)[32]) {
+    T *dst = static_cast<T *>(a.y) + row * a.ldy + n;
+    if (a.vec && n + 32 <= a.N) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) st_global_32(dst + i, &v[i]);
+        } else {
+            uint32_t o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = pack2<T>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            st_global_32(dst, &o[0]);
+            st_global_32(dst + 16, &o[8]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (n + i < a.N) put_f32(dst + i, __uint_as_float(v[i]));
+}
+
+struct MxUnit {
+    int e, ct, nrows;
+    int64_t row0;
+};
+
+__device__ __forceinline__ MxUnit mx_unit(const MxArgs &a, const MxCtl &ctl, int64_t u) {
+    const int t = (int)(u / a.nct);
+    int lo = 0, hi = a.E;  // the last e with first[e] <= t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (ctl.first[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    MxUnit x;
+    x.e = lo;
+    x.ct = (int)(u - (int64_t)t * a.nct);
+    x.row0 = (int64_t)ctl.begin[lo] + (int64_t)(t - ctl.first[lo]) * kMxRows;
+    const int64_t left = (int64_t)ctl.begin[lo + 1] - x.row0;
+    x.nrows = left < kMxRows ? (int)left : kMxRows;
+    return x;
+}
+
+// kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
+template <int kN, int kOut>
+__global__ void __launch_bounds__(kMxThreads, 1)
+microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_small,
+                       const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sa_small,
+                       const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sb,
+                       const MxArgs a) {
+    using G = MxTile<kN>;
+    constexpr bool kGated = kOut == 3;
+    constexpr int kHalf = kN / 2;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *stages = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ MxCtl ctl;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+            mbar_init(&ctl.sfull[s], 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.tfull[b], 1);
+            mbar_init(&ctl.tempty[b], 4);
+        }
+        mbar_init(&ctl.done, 1);
+        ctl.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(&ctl.tmem, G::kTmemCols);
+    if (warp == 8 && lane == 0) {
+        prefetch_tensormap(&tm_b);
+        prefetch_tensormap(&tm_sb);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // row tiles before each expert; offsets outside [0, rows] or running backwards are clamped
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kMxThreads) {
+        const int e = e0 + threadIdx.x;
+        int64_t lo = 0, hi = 0;
+        if (e < a.E) {
+            lo = a.offsets ? a.offsets[e] : 0;
+            hi = a.offsets ? a.offsets[e + 1] : a.rows;
+            lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
+            hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
+        }
+        const int tiles = (int)((hi - lo + kMxRows - 1) / kMxRows);
+        int inc = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += t;
+        }
+        if (lane == 31) ctl.wsum[warp] = inc;
+        __syncthreads();
+        int off = carry, chunk = 0;
+        for (int w = 0; w < kMxThreads / 32; ++w) {
+            const int t = ctl.wsum[w];
+            if (w < warp) off += t;
+            chunk += t;
+        }
+        if (e < a.E) {
+            ctl.first[e] = off + inc - tiles;
+            ctl.begin[e] = (int)lo;
+            if (e == a.E - 1) {
+                ctl.begin[a.E] = (int)hi;
+                ctl.valid_rows = (int)hi;
+            }
+        }
+        carry += chunk;
+        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const int64_t T = (int64_t)carry * a.nct;
+    const int nks = (a.K + kMxStageK - 1) / kMxStageK;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_normal();
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, par = 0;
+            for (int64_t u = blockIdx.x; u < T && !ctl.abort; u += gridDim.x) {
+                const MxUnit x = mx_unit(a, ctl, u);
+                const bool full_tile = x.nrows > kMxRows - kMxSmallBox;
+                const int nbox = (x.nrows + kMxSmallBox - 1) / kMxSmallBox;
+                const uint32_t bytes = (full_tile ? kMxRows : nbox * kMxSmallBox) * (128 + 16) + G::kBBytes + G::kSBBytes;
+                // weight rows of the two halves of the N side
+                const int b0 = x.e * a.N + x.ct * (kGated ? kHalf : kN);
+                const int b1 = kGated ? x.e * a.N + a.N / 2 + x.ct * kHalf : b0 + kHalf;
+                for (int s = 0; s < nks; ++s) {
+                    if (!gwait(&ctl.empty[stage], phase ^ 1u, ctl)) break;
+                    uint64_t *bar = &ctl.full[stage];
+                    unsigned char *A = stages + stage * G::kStageBytes;
+                    unsigned char *B = A + G::kABytes, *SA = B + G::kBBytes, *SB = SA + G::kSABytes;
+                    mbar_arrive_expect_tx(bar, bytes);
+                    const int xk = s * 128, xs = (s >> 1) * 16;
+                    tma_load_2d(B, &tm_b, xk, b0, bar, pol);
+                    tma_load_2d(B + kHalf * 128, &tm_b, xk, b1, bar, pol);
+                    tma_load_2d(SB, &tm_sb, xs, b0, bar, pol);
+                    tma_load_2d(SB + kHalf * 16, &tm_sb, xs, b1, bar, pol);
+                    if (full_tile) {
+                        tma_load_2d(A, &tm_a, xk, (int)x.row0, bar, pol);
+                        tma_load_2d(SA, &tm_sa, xs, (int)x.row0, bar, pol);
+                    } else {
+                        for (int q = 0; q < nbox; ++q) {
+                            tma_load_2d(A + q * kMxSmallBox * 128, &tm_a_small, xk, (int)x.row0 + q * kMxSmallBox, bar, pol);
+                            tma_load_2d(SA + q * kMxSmallBox * 16, &tm_sa_small, xs, (int)x.row0 + q * kMxSmallBox, bar, pol);
+                        }
+                    }
+                    issued |= 1u << stage;
+                    par = (par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == G::kStages) stage = 0, phase ^= 1u;
+                }
+            }
+            // every copy has landed before the CTA can exit
+            for (int s = 0; s < G::kStages; ++s)
+                if ((issued >> s) & 1u)
+                    if (!mbar_wait_bounded(&ctl.full[s], (par >> s) & 1u)) ctl.abort = 1;
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        if (lane == 0) {
+            int stage = 0, local = 0;
+            uint32_t phase = 0;
+            for (int64_t u = blockIdx.x; u < T && !ctl.abort; u += gridDim.x, ++local) {
+                const int buf = local & 1;
+                if (!gwait(&ctl.tempty[buf], ((local >> 1) & 1) ^ 1u, ctl)) break;
+                const uint32_t d = ctl.tmem + (uint32_t)(buf * kN);
+                bool ok = true;
+                for (int s = 0; s < nks; ++s) {
+                    if (!gwait(&ctl.full[stage], phase, ctl) || !gwait(&ctl.sfull[stage], phase, ctl)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t A = smem_u32(stages + stage * G::kStageBytes);
+                    const uint32_t B = A + G::kABytes;
+                    const uint32_t sf = ctl.tmem + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
+#pragma unroll
+                    for (int ks = 0; ks < kMxStageK / 64; ++ks) {
+                        if (s * kMxStageK + ks * 64 >= a.K) break;
+                        // K-major, 128-byte swizzle: 32 bytes per K step, 8-row atoms 1 KB apart
+                        const uint64_t ad = umma_smem_desc(A + ks * 32, 16, 1024, 2);
+                        const uint64_t bd = umma_smem_desc(B + ks * 32, 16, 1024, 2);
+                        const uint32_t sfa = sf + (uint32_t)((ks >> 1) * G::kACols);
+                        const uint32_t sfb = sf + (uint32_t)(2 * G::kACols + (ks >> 1) * G::kBPad);
+                        umma_mxf4(d, ad, bd, mx_idesc(kN, (ks & 1) ? 2u : 0u), sfa, sfb, s > 0 || ks > 0);
+                    }
+                    umma_commit(&ctl.empty[stage]);
+                    if (++stage == G::kStages) stage = 0, phase ^= 1u;
+                }
+                if (!ok) break;
+                umma_commit(&ctl.tfull[buf]);
+            }
+            // every issued MMA has completed before the CTA frees its tensor memory
+            umma_commit(&ctl.done);
+            if (!mbar_wait_bounded(&ctl.done, 0)) ctl.abort = 1;
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const uint32_t quad = (uint32_t)(32 * (warp - 4)) << 16;
+        const int nb = a.K / 32;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < T && ok; u += gridDim.x)
+            for (int s = 0; s < nks; ++s) {
+                if (!(ok = gwait(&ctl.full[stage], phase, ctl))) break;
+                const unsigned char *SA = stages + stage * G::kStageBytes + G::kABytes + G::kBBytes;
+                const unsigned char *SB = SA + G::kSABytes;
+                uint32_t wa[2 * G::kACols], wb[2 * G::kBPad] = {};
+                // blocks past K have zero codes; their scale must not be a NaN
+                uint32_t mask[2];
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const int left = nb - (s * 8 + kk * 4);
+                    mask[kk] = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
+                }
+#pragma unroll
+                for (int c = 0; c < G::kACols; ++c) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(SA + (c * 32 + lane) * 16 + (s & 1) * 8);
+                    wa[c] = v.x & mask[0];
+                    wa[G::kACols + c] = v.y & mask[1];
+                }
+#pragma unroll
+                for (int c = 0; c < G::kBCols; ++c) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(SB + (c * 32 + lane) * 16 + (s & 1) * 8);
+                    wb[c] = v.x & mask[0];
+                    wb[G::kBPad + c] = v.y & mask[1];
+                }
+                const uint32_t sf = ctl.tmem + quad + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
+                tmem_st8(sf, wa);
+#pragma unroll
+                for (int c = 0; c < 2 * G::kBPad; c += 4) tmem_st4(sf + 2 * G::kACols + c, wb + c);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.sfull[stage]);
+                if (++stage == G::kStages) stage = 0, phase ^= 1u;
+            }
+    } else {
+        const uint32_t quad = (uint32_t)(32 * warp) << 16;
+        int local = 0;
+        for (int64_t u = blockIdx.x; u < T; u += gridDim.x, ++local) {
+            const MxUnit x = mx_unit(a, ctl, u);
+            const int buf = local & 1;
+            if (!gwait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
+            tc_fence_after();
+            const int64_t row = x.row0 + 32 * warp + lane;
+            const bool live = 32 * warp + lane < x.nrows;
+            const uint32_t d = ctl.tmem + quad + (uint32_t)(buf * kN);
+            if constexpr (!kGated) {
+                using T_ = typename std::conditional<kOut == 0, __nv_bfloat16,
+                                                     typename std::conditional<kOut == 1, __half, float>::type>::type;
+#pragma unroll 1
+                for (int c = 0; c < kN; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(d + c, v);
+                    tmem_ld_wait(v);
+                    if (live && x.ct * kN + c < a.N) store_row32<T_>(a, row, x.ct * kN + c, v);
+                }
+            } else {
+                const int I = a.N / 2;
+#pragma unroll 1
+                for (int c = 0; c < kHalf; c += 32) {
+                    uint32_t g[32], up[32];
+                    tmem_ld32(d + c, g);
+                    tmem_ld32(d + kHalf + c, up);
+                    tmem_ld_wait(g);
+                    tmem_ld_wait(up);
+                    const int n = x.ct * kHalf + c;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        g[i] = __float_as_uint(silu_f32(__uint_as_float(g[i])) * __uint_as_float(up[i]));
+                        const uint32_t b = g[i] & 0x7fffffffu;
+                        top = b > top ? b : top;
+                    }
+                    const uint32_t byte = microscale_byte(top);
+                    const float inv = microscale_inverse(byte);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(g[8 * q + i]) * inv;
+                        o[q] = byte == 255u ? 0u : fp4x8(f);
+                    }
+                    if (live && n < I) {
+                        *reinterpret_cast<uint4 *>(a.codes + row * (I / 2) + n / 2) = make_uint4(o[0], o[1], o[2], o[3]);
+                        a.scales[row * a.pitch + n / 32] = (uint8_t)byte;
+                    }
+                }
+                if (live && x.ct == a.nct - 1)
+                    for (int b = I / 32; b < a.pitch; ++b) a.scales[row * a.pitch + b] = 0;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.tempty[buf]);
+        }
+        // rows past the last group (dropped routes): zeros
+        for (int64_t r = ctl.valid_rows + (int64_t)blockIdx.x; r < a.rows; r += gridDim.x) {
+            if constexpr (kGated) {
+                for (int i = threadIdx.x; i < a.N / 64; i += 128)
+                    *reinterpret_cast<uint4 *>(a.codes + r * (a.N / 4) + 16 * i) = uint4{0, 0, 0, 0};
+                for (int i = threadIdx.x; i < a.pitch; i += 128) a.scales[r * a.pitch + i] = 0;
+            } else {
+                using T_ = typename std::conditional<kOut == 0, __nv_bfloat16,
+                                                     typename std::conditional<kOut == 1, __half, float>::type>::type;
+                for (int i = threadIdx.x; i < a.N; i += 128) put_f32(static_cast<T_ *>(a.y) + r * a.ldy + i, 0.0f);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(ctl.tmem, G::kTmemCols);
+    if (threadIdx.x == 0 && ctl.abort) atomicOr(a.status, MOE_DEV_WAIT_TIMEOUT);
+}
+
+// ----------------------------------------------------------------------------------- launcher
+template <int kN, int kOut>
+static cudaError_t gemm_as(const MicroscaleMaps &tm, MxArgs a, cudaStream_t stream) {
+    using G = MxTile<kN>;
+    a.nct = kOut == 3 ? (a.N / 2 + kN / 2 - 1) / (kN / 2) : (a.N + kN - 1) / kN;
+    const int64_t tiles = a.rows < a.E ? a.rows : a.rows / kMxRows + a.E;
+    const int64_t units = tiles * a.nct, sms = num_sms();
+    const int64_t grid = units < 1 ? 1 : (units < sms ? units : sms);
+    const auto fn = microscale_gemm_kernel<kN, kOut>;
+    cudaError_t err = ensure_smem((const void *)fn, G::kSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)grid), dim3(kMxThreads), G::kSmem, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, fn, tm.a, tm.a_small, tm.sa, tm.sa_small, tm.b, tm.sb, a);
+}
+
+template <int kN>
+static cudaError_t gemm_width(const MicroscaleMaps &tm, const MxArgs &a, int out, cudaStream_t stream) {
+    switch (out) {
+        case MOE_DT_BF16: return gemm_as<kN, 0>(tm, a, stream);
+        case MOE_DT_F16: return gemm_as<kN, 1>(tm, a, stream);
+        case MOE_DT_F32: return gemm_as<kN, 2>(tm, a, stream);
+        default: return gemm_as<kN, 3>(tm, a, stream);
+    }
+}
+
+int microscale_tile_n(int64_t rows, int E) { return rows >= 32 * (int64_t)E ? 192 : 64; }
+
+cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const int32_t *offsets, int E,
+                                   int N, int K, int dtype, void *y, int64_t ldy, uint8_t *codes,
+                                   uint8_t *scales, int32_t *status, cudaStream_t stream) {
+    MxArgs a{};
+    a.offsets = offsets, a.rows = rows, a.E = E, a.N = N, a.K = K;
+    a.y = y, a.ldy = ldy, a.codes = codes, a.scales = scales, a.status = status;
+    a.pitch = microscale_pitch(N / 2);
+    const int elem = dtype == MOE_DT_F32 ? 4 : 2;
+    a.vec = y && (reinterpret_cast<uintptr_t>(y) | (uint64_t)(ldy * elem)) % 32 == 0;
+    const int out = codes ? 3 : dtype;
+    return microscale_tile_n(rows, E) == 192 ? gemm_width<192>(tm, a, out, stream)
+                                             : gemm_width<64>(tm, a, out, stream);
+}
+
+}  // namespace moe

@@ -379,6 +379,46 @@ int block_for(const moe_expert_weights_t *w, int M, int k, int b);  // b, or the
 // on every launch costs host time that small decode blocks cannot hide.
 cudaError_t ensure_smem(const void *func, size_t bytes);
 
+// 2-D row-major tensor map [outer][inner] of `elem` bytes, box [box_outer][box_inner];
+// out-of-range box elements read as zeros.
+bool make_tmap_2d(CUtensorMap *tm, const void *base, CUtensorMapDataType dt, int elem,
+                  uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
+                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
+
+// Tokens sorted by expert and back (token_sort.cu).  dtype: MOE_DT_*; ld*: row pitch in
+// elements; w == NULL: weights of one.
+constexpr int kPlanMaxExperts = 1024;
+cudaError_t launch_token_plan(const int32_t *ids, int M, int k, int E, int32_t *offsets,
+                              int32_t *row_route, int32_t *route_row, cudaStream_t stream);
+cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k, int H,
+                              const int32_t *route_row, void *rows, int64_t ldr, cudaStream_t stream);
+cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
+                                const int32_t *route_row, const float *w, const void *residual,
+                                int64_t ldres, void *out, int64_t ldo, cudaStream_t stream);
+cudaError_t launch_token_unsort_grad(const void *gout, int64_t ldo, const void *rows, int64_t ldr,
+                                     int dtype, int M, int k, int H, const int32_t *route_row,
+                                     const float *w, void *grows, int64_t ldg, float *gw,
+                                     cudaStream_t stream);
+
+// 4-bit block floating point (microscale.cu, microscale_gemm.cu).
+constexpr int kMicroscaleMaxExperts = 1024;
+__host__ __device__ constexpr int microscale_pitch(int cols) { return (cols / 32 + 15) / 16 * 16; }
+cudaError_t launch_microscale_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int cols,
+                                       const int32_t *route_row, int k, uint8_t *codes, uint8_t *scales,
+                                       cudaStream_t stream);
+cudaError_t launch_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                                         int cols, void *x, int64_t ldx, int dtype, cudaStream_t stream);
+// Tensor maps of one grouped product: codes and scales of the rows (128- and 32-row boxes) and
+// of the weights (boxes of half a column tile).
+struct MicroscaleMaps {
+    CUtensorMap a, a_small, sa, sa_small, b, sb;
+};
+int microscale_tile_n(int64_t rows, int E);  // column tile of the grouped product
+// codes == NULL: y [rows][N] of dtype; else the gated form, codes and scales of [rows][N / 2].
+cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const int32_t *offsets, int E,
+                                   int N, int K, int dtype, void *y, int64_t ldy, uint8_t *codes,
+                                   uint8_t *scales, int32_t *status, cudaStream_t stream);
+
 // Shared launch helper: programmatic dependent launch on, optional cluster dims.
 cudaLaunchConfig_t launch_config(dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                                  cudaLaunchAttribute *attrs, int cluster_x);

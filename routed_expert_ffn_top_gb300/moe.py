@@ -33,6 +33,11 @@ MOE_W_DENSE_BF16 = 0
 MOE_W_VQ_GATEUP = 1
 MOE_W_VQLR_GATEUP = 2
 
+MOE_DT_BF16 = 0
+MOE_DT_F16 = 1
+MOE_DT_F32 = 2
+MOE_MICROSCALE_STATUS_BYTES = 256
+
 # Every symbol include/moe.h declares (checked against the header by the tests).
 EXPORTS = (
     "moe_status_string", "moe_route_topk", "moe_align_capacity", "moe_align_block_size",
@@ -40,6 +45,10 @@ EXPORTS = (
     "moe_read_device_status", "moe_set_trace_events", "moe_decode_block_noalloc",
     "moe_selftest_wait_timeout", "moe_reader_build", "moe_reader_workspace_bytes",
     "moe_reader_ffn", "moe_library_block_size", "moe_workspace_layout",
+    "moe_token_plan", "moe_token_sort", "moe_token_sort_grad", "moe_token_unsort",
+    "moe_token_unsort_grad", "moe_microscale_pitch", "moe_microscale_quantize",
+    "moe_microscale_dequantize", "moe_microscale_product", "moe_microscale_gated_product",
+    "moe_microscale_workspace_bytes", "moe_microscale_ffn",
 )
 
 
@@ -85,6 +94,15 @@ class ReaderStruct(ctypes.Structure):
         ("w_down", ctypes.c_void_p), ("g_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
         ("g_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("dnorm", ctypes.c_void_p),
         ("U", ctypes.c_void_p), ("coef", ctypes.c_void_p),
+    ]
+
+
+class MicroscaleWeights(ctypes.Structure):
+    _fields_ = [
+        ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("gate_up_codes", ctypes.c_void_p), ("gate_up_scales", ctypes.c_void_p),
+        ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
     ]
 
 
@@ -135,6 +153,30 @@ def lib():
             L.moe_reader_workspace_bytes.argtypes = [rp, ci, ci, ci]
             L.moe_reader_workspace_bytes.restype = sz
             L.moe_reader_ffn.argtypes = [vp, rp, ci, ci, vp, vp, ci, ci, vp, vp, vp, vp, vp, sz, vp]
+            i64 = ctypes.c_int64
+            mp = ctypes.POINTER(MicroscaleWeights)
+            L.moe_token_plan.argtypes = [vp, ci, ci, ci, vp, vp, vp, vp]
+            L.moe_token_sort.argtypes = [vp, i64, ci, ci, ci, ci, vp, vp, i64, vp]
+            L.moe_token_sort_grad.argtypes = [vp, i64, ci, ci, ci, ci, vp, vp, i64, vp]
+            L.moe_token_unsort.argtypes = [vp, i64, ci, ci, ci, ci, vp, vp, vp, i64, vp, i64, vp]
+            L.moe_token_unsort_grad.argtypes = [vp, i64, vp, i64, ci, ci, ci, ci, vp, vp, vp, i64,
+                                                vp, vp]
+            L.moe_microscale_pitch.argtypes = [ci]
+            L.moe_microscale_quantize.argtypes = [vp, i64, ci, i64, ci, vp, ci, vp, vp, vp]
+            L.moe_microscale_dequantize.argtypes = [vp, vp, i64, ci, vp, i64, ci, vp]
+            L.moe_microscale_product.argtypes = [vp, vp, i64, vp, vp, vp, ci, ci, ci, ci, vp, i64,
+                                                 vp, sz, vp]
+            L.moe_microscale_gated_product.argtypes = [vp, vp, i64, vp, vp, vp, ci, ci, ci, vp, vp,
+                                                       vp, sz, vp]
+            L.moe_microscale_workspace_bytes.argtypes = [mp, ci, ci]
+            L.moe_microscale_workspace_bytes.restype = sz
+            L.moe_microscale_ffn.argtypes = [vp, mp, ci, ci, vp, vp, vp, vp, vp, sz, vp]
+            for f in ("moe_token_plan", "moe_token_sort", "moe_token_sort_grad",
+                      "moe_token_unsort", "moe_token_unsort_grad", "moe_microscale_pitch",
+                      "moe_microscale_quantize", "moe_microscale_dequantize",
+                      "moe_microscale_product", "moe_microscale_gated_product",
+                      "moe_microscale_ffn"):
+                getattr(L, f).restype = ci
             for f in ("moe_route_topk", "moe_align_block_size", "moe_expert_ffn",
                       "moe_decode_block", "moe_decode_block_host", "moe_read_device_status",
                       "moe_set_trace_events", "moe_decode_block_noalloc",
@@ -518,4 +560,324 @@ def moe_reader_ffn(h, rd: dict, topk_ids, topk_weights, K: int, nscan: int = 80,
            "moe_reader_ffn")
     if want_decisions:
         return out, sel[:, :K], xr
+    return out
+
+
+# ---------------------------------------------------------- tokens sorted by expert and back
+_ROW_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
+
+
+def _rows(t, name, device, dtype=None, shape=None):
+    """A matrix with contiguous columns (any row pitch); returns its row pitch in elements."""
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    if dtype is None:
+        if t.dtype not in _ROW_DTYPES:
+            raise TypeError("%s must be bfloat16, float16 or float32, got %s" % (name, t.dtype))
+    elif t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    rows, cols = t.shape
+    sr, sc = t.stride()
+    if cols > 1 and sc != 1:
+        raise ValueError("%s must have contiguous columns" % name)
+    if rows > 1 and sr < cols:
+        raise ValueError("%s must not have overlapping rows" % name)
+    return sr if rows > 1 else cols
+
+
+def _vector(t, name, dtype, device, shape):
+    _need(t, dtype, name, device)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    return t
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_token_plan(topk_ids, E, offsets=None, row_route=None, route_row=None, stream=None):
+    """(offsets [E+1], row_route [M*k], route_row [M,k]) of topk_ids [M,k] (include/moe.h)."""
+    dev = topk_ids.device
+    _need(topk_ids, torch.int32, "topk_ids", dev)
+    M, k = topk_ids.shape
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+    if row_route is None:
+        row_route = torch.empty((M * k,), dtype=torch.int32, device=dev)
+    if route_row is None:
+        route_row = torch.empty((M, k), dtype=torch.int32, device=dev)
+    _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
+    _vector(row_route, "row_route", torch.int32, dev, (M * k,))
+    _vector(route_row, "route_row", torch.int32, dev, (M, k))
+    _check(lib().moe_token_plan(topk_ids.data_ptr(), M, k, E, offsets.data_ptr(),
+                                row_route.data_ptr(), route_row.data_ptr(), _stream(stream)),
+           "moe_token_plan")
+    return offsets, row_route, route_row
+
+
+def moe_token_sort(x, route_row, rows=None, stream=None):
+    """The token rows x [M,H] in sorted order: rows [M*k,H]."""
+    dev = x.device
+    _need(route_row, torch.int32, "route_row", dev)
+    M, k = route_row.shape
+    H = x.shape[1]
+    ldx = _rows(x, "x", dev, shape=(M, H))
+    if rows is None:
+        rows = torch.empty((M * k, H), dtype=x.dtype, device=dev)
+    ldr = _rows(rows, "rows", dev, x.dtype, (M * k, H))
+    _check(lib().moe_token_sort(x.data_ptr(), ldx, _ROW_DTYPES[x.dtype], M, k, H,
+                                route_row.data_ptr(), rows.data_ptr(), ldr, _stream(stream)),
+           "moe_token_sort")
+    return rows
+
+
+def moe_token_sort_grad(grad_rows, route_row, grad_x=None, stream=None):
+    """Gradient of moe_token_sort: grad_x [M,H] of grad_rows [M*k,H]."""
+    dev = grad_rows.device
+    _need(route_row, torch.int32, "route_row", dev)
+    M, k = route_row.shape
+    H = grad_rows.shape[1]
+    ldr = _rows(grad_rows, "grad_rows", dev, shape=(M * k, H))
+    if grad_x is None:
+        grad_x = torch.empty((M, H), dtype=grad_rows.dtype, device=dev)
+    ldx = _rows(grad_x, "grad_x", dev, grad_rows.dtype, (M, H))
+    _check(lib().moe_token_sort_grad(grad_rows.data_ptr(), ldr, _ROW_DTYPES[grad_rows.dtype], M, k,
+                                     H, route_row.data_ptr(), grad_x.data_ptr(), ldx,
+                                     _stream(stream)), "moe_token_sort_grad")
+    return grad_x
+
+
+def moe_token_unsort(rows, route_row, topk_weights=None, residual=None, out=None, stream=None):
+    """out [M,H] = residual + the weighted sum of each token's rows (include/moe.h)."""
+    dev = rows.device
+    _need(route_row, torch.int32, "route_row", dev)
+    M, k = route_row.shape
+    H = rows.shape[1]
+    ldr = _rows(rows, "rows", dev, shape=(M * k, H))
+    if topk_weights is not None:
+        _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
+    ldres = 0 if residual is None else _rows(residual, "residual", dev, rows.dtype, (M, H))
+    if out is None:
+        out = torch.empty((M, H), dtype=rows.dtype, device=dev)
+    ldo = _rows(out, "out", dev, rows.dtype, (M, H))
+    _check(lib().moe_token_unsort(rows.data_ptr(), ldr, _ROW_DTYPES[rows.dtype], M, k, H,
+                                  route_row.data_ptr(), _addr(topk_weights), _addr(residual),
+                                  ldres, out.data_ptr(), ldo, _stream(stream)),
+           "moe_token_unsort")
+    return out
+
+
+def moe_token_unsort_grad(grad_out, rows, route_row, topk_weights=None, grad_rows=None,
+                          grad_weights=None, stream=None):
+    """Gradients of moe_token_unsort: (grad_rows [M*k,H], grad_weights [M,k] fp32)."""
+    dev = rows.device
+    _need(route_row, torch.int32, "route_row", dev)
+    M, k = route_row.shape
+    H = rows.shape[1]
+    ldr = _rows(rows, "rows", dev, shape=(M * k, H))
+    ldo = _rows(grad_out, "grad_out", dev, rows.dtype, (M, H))
+    if topk_weights is not None:
+        _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
+    if grad_rows is None:
+        grad_rows = torch.empty((M * k, H), dtype=rows.dtype, device=dev)
+    if grad_weights is None:
+        grad_weights = torch.empty((M, k), dtype=torch.float32, device=dev)
+    ldg = _rows(grad_rows, "grad_rows", dev, rows.dtype, (M * k, H))
+    _vector(grad_weights, "grad_weights", torch.float32, dev, (M, k))
+    _check(lib().moe_token_unsort_grad(grad_out.data_ptr(), ldo, rows.data_ptr(), ldr,
+                                       _ROW_DTYPES[rows.dtype], M, k, H, route_row.data_ptr(),
+                                       _addr(topk_weights), grad_rows.data_ptr(), ldg,
+                                       grad_weights.data_ptr(), _stream(stream)),
+           "moe_token_unsort_grad")
+    return grad_rows, grad_weights
+
+
+# ------------------------------------------------------------- 4-bit block floating point
+def moe_microscale_pitch(cols) -> int:
+    return int(lib().moe_microscale_pitch(cols))
+
+
+def _microscaled(codes, scales, device, name):
+    """Checks a pair of codes [..., cols/2] and scales [..., pitch]; returns cols."""
+    _need(codes, torch.uint8, name + "_codes", device)
+    _need(scales, torch.uint8, name + "_scales", device)
+    cols = 2 * codes.shape[-1]
+    want = tuple(codes.shape[:-1]) + (-(-cols // 512) * 16,)
+    if tuple(scales.shape) != want:
+        raise ValueError("%s_scales must have shape %s, got %s" % (name, want, tuple(scales.shape)))
+    return cols
+
+
+def moe_microscale_quantize(x, route_row=None, codes=None, scales=None, stream=None):
+    """x [rows,cols] as 4-bit codes and scales; with route_row [rows,k] (a token plan's) in
+    sorted order, rows * k of them."""
+    dev = x.device
+    rows, cols = x.shape
+    ldx = _rows(x, "x", dev)
+    k = 1
+    if route_row is not None:
+        k = route_row.shape[1]
+        _vector(route_row, "route_row", torch.int32, dev, (rows, k))
+    if codes is None:
+        codes = torch.empty((rows * k, cols // 2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((rows * k, -(-cols // 512) * 16), dtype=torch.uint8, device=dev)
+    if _microscaled(codes, scales, dev, "x") != cols or codes.shape[0] != rows * k:
+        raise ValueError("codes must have shape %s" % ((rows * k, cols // 2),))
+    _check(lib().moe_microscale_quantize(x.data_ptr(), ldx, _ROW_DTYPES[x.dtype], rows, cols,
+                                         _addr(route_row), k, codes.data_ptr(), scales.data_ptr(),
+                                         _stream(stream)), "moe_microscale_quantize")
+    return codes, scales
+
+
+def moe_microscale_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values [rows,cols] of codes [rows,cols/2] and scales."""
+    dev = codes.device
+    cols = _microscaled(codes, scales, dev, "x")
+    rows = codes.shape[0]
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+    ldx = _rows(out, "out", dev, shape=(rows, cols))
+    _check(lib().moe_microscale_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols,
+                                           out.data_ptr(), ldx, _ROW_DTYPES[out.dtype],
+                                           _stream(stream)), "moe_microscale_dequantize")
+    return out
+
+
+def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
+    """Checks of the grouped products; returns (rows, E, N, K, workspace)."""
+    dev = x_codes.device
+    K = _microscaled(x_codes, x_scales, dev, "x")
+    if _microscaled(w_codes, w_scales, dev, "w") != K:
+        raise ValueError("x and w must have the same number of columns")
+    if w_codes.dim() == 2:
+        E, N = 1, w_codes.shape[0]
+    else:
+        E, N = w_codes.shape[:2]
+    if offsets is not None:
+        _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
+    if workspace is None:
+        workspace = torch.zeros((MOE_MICROSCALE_STATUS_BYTES,), dtype=torch.uint8, device=dev)
+    return x_codes.shape[0], E, N, K, workspace
+
+
+def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
+                           dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """y [rows,N] of 4-bit rows and 4-bit weights [E,N,K] (or [N,K]), rows grouped by offsets
+    [E+1]; rows past the last group are zero."""
+    rows, E, N, K, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
+                                             workspace)
+    dev = x_codes.device
+    if out is None:
+        out = torch.empty((rows, N), dtype=dtype, device=dev)
+    ldy = _rows(out, "out", dev, shape=(rows, N))
+    _check(lib().moe_microscale_product(x_codes.data_ptr(), x_scales.data_ptr(), rows,
+                                        _addr(offsets), w_codes.data_ptr(), w_scales.data_ptr(), E,
+                                        N, K, _ROW_DTYPES[out.dtype], out.data_ptr(), ldy,
+                                        workspace.data_ptr(), workspace.numel(),
+                                        _stream(stream)), "moe_microscale_product")
+    return out
+
+
+def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=None, codes=None,
+                                 scales=None, workspace=None, stream=None):
+    """SiLU(g) * u of the gate and up halves of w [E,N,K], quantised: (codes, scales) of
+    [rows,N/2]."""
+    rows, E, N, K, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
+                                             workspace)
+    dev = x_codes.device
+    I = N // 2
+    if codes is None:
+        codes = torch.empty((rows, I // 2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((rows, -(-I // 512) * 16), dtype=torch.uint8, device=dev)
+    if tuple(codes.shape) != (rows, I // 2):
+        raise ValueError("codes must have shape %s" % ((rows, I // 2),))
+    _microscaled(codes, scales, dev, "p")
+    _check(lib().moe_microscale_gated_product(x_codes.data_ptr(), x_scales.data_ptr(), rows,
+                                              _addr(offsets), w_codes.data_ptr(),
+                                              w_scales.data_ptr(), E, N, K, codes.data_ptr(),
+                                              scales.data_ptr(), workspace.data_ptr(),
+                                              workspace.numel(), _stream(stream)),
+           "moe_microscale_gated_product")
+    return codes, scales
+
+
+def microscale_weights(layer: dict) -> MicroscaleWeights:
+    """C descriptor of a layer's 4-bit weights: H, I, E and gate_up_codes [E,2I,H/2],
+    gate_up_scales, down_codes [E,H,I/2], down_scales (the caller keeps the tensors alive)."""
+    H, I, E = layer["H"], layer["I"], layer["E"]
+    dev = layer["down_codes"].device
+    w = MicroscaleWeights()
+    w.H, w.I, w.E = H, I, E
+    for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
+        c, s = layer[name + "_codes"], layer[name + "_scales"]
+        if _microscaled(c, s, dev, name) != cols or tuple(c.shape[:-1]) != (E, n):
+            raise ValueError("%s_codes must have shape %s" % (name, (E, n, cols // 2)))
+        setattr(w, name + "_codes", c.data_ptr())
+        setattr(w, name + "_scales", s.data_ptr())
+    return w
+
+
+def microscale_layer(layer: dict, stream=None) -> dict:
+    """4-bit weights of a dense layer (w_gate, w_up [E,H,I], w_down [E,I,H] bf16): each
+    projection's output channels become rows, quantised along the summed dimension."""
+    H, I, E = layer["H"], layer["I"], layer["E"]
+    dev = layer["w_down"].device
+    if H % 32 or I % 32:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "microscale_layer")
+    out = {"H": H, "I": I, "E": E}
+    for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
+        out[name + "_codes"] = torch.empty((E, n, cols // 2), dtype=torch.uint8, device=dev)
+        out[name + "_scales"] = torch.empty((E, n, -(-cols // 512) * 16), dtype=torch.uint8,
+                                            device=dev)
+    for e in range(E):
+        for name, w, at in (("gate_up", layer["w_gate"][e], 0), ("gate_up", layer["w_up"][e], I),
+                            ("down", layer["w_down"][e], 0)):
+            rows = w.t().contiguous()
+            moe_microscale_quantize(rows, codes=out[name + "_codes"][e, at:at + len(rows)],
+                                    scales=out[name + "_scales"][e, at:at + len(rows)],
+                                    stream=stream)
+    return out
+
+
+def moe_microscale_workspace_bytes(layer: dict, M, k) -> int:
+    return int(lib().moe_microscale_workspace_bytes(ctypes.byref(microscale_weights(layer)), M, k))
+
+
+def microscale_workspace(layer: dict, M, k) -> torch.Tensor:
+    """A zero-filled workspace of moe_microscale_ffn."""
+    n = moe_microscale_workspace_bytes(layer, M, k)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_workspace_bytes")
+    return torch.zeros((n,), dtype=torch.uint8, device=layer["down_codes"].device)
+
+
+def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None, workspace=None,
+                       stream=None):
+    """The 4-bit expert step (include/moe.h) for given routes; `layer` as microscale_weights
+    takes it."""
+    dev = h.device
+    w = microscale_weights(layer)
+    _need(h, torch.bfloat16, "h", dev)
+    M, k = topk_ids.shape
+    _vector(h, "h", torch.bfloat16, dev, (M, w.H))
+    _need(topk_ids, torch.int32, "topk_ids", dev)
+    _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
+    if residual is not None:
+        _vector(residual, "residual", torch.bfloat16, dev, (M, w.H))
+    if out is None:
+        out = torch.empty((M, w.H), dtype=torch.bfloat16, device=dev)
+    _vector(out, "out", torch.bfloat16, dev, (M, w.H))
+    if workspace is None:
+        workspace = microscale_workspace(layer, M, k)
+    _check(lib().moe_microscale_ffn(h.data_ptr(), ctypes.byref(w), M, k, topk_ids.data_ptr(),
+                                    topk_weights.data_ptr(), _addr(residual), out.data_ptr(),
+                                    workspace.data_ptr(), workspace.numel(), _stream(stream)),
+           "moe_microscale_ffn")
     return out
