@@ -70,6 +70,14 @@ struct MxCtl {
     int32_t begin[kMicroscaleMaxExperts + 1];  // first row of expert e
 };
 
+// gwait with the first tries made without reading the timer, whose latency would add to
+// every wait that is short.
+__device__ __forceinline__ bool mx_wait(uint64_t *bar, uint32_t parity, MxCtl &ctl) {
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return gwait(bar, parity, ctl);
+}
+
 struct MxArgs {
     const int32_t *offsets;  // NULL: one group of all rows
     int64_t rows;
@@ -180,6 +188,10 @@ __device__ __forceinline__ void store_row32(const MxArgs &a, int64_t row, int n,
     for (int i = 0; i < 32; ++i)
         if (n + i < a.N) put_f32(dst + i, __uint_as_float(v[i]));
 }
+
+// SiLU with the approximate division (2 units in the last place): p goes to 4 bits next.  Below
+// g = -87 it gives 0 for values under 2^-119.
+__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + expf(-g)); }
 
 struct MxUnit {
     int e, ct, nrows;
@@ -298,7 +310,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                 const int b0 = x.e * a.N + x.ct * (kGated ? kHalf : kN);
                 const int b1 = kGated ? x.e * a.N + a.N / 2 + x.ct * kHalf : b0 + kHalf;
                 for (int s = 0; s < nks; ++s) {
-                    if (!gwait(&ctl.empty[stage], phase ^ 1u, ctl)) break;
+                    if (!mx_wait(&ctl.empty[stage], phase ^ 1u, ctl)) break;
                     uint64_t *bar = &ctl.full[stage];
                     unsigned char *A = stages + stage * G::kStageBytes;
                     unsigned char *B = A + G::kABytes, *SA = B + G::kBBytes, *SB = SA + G::kSABytes;
@@ -334,11 +346,11 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             uint32_t phase = 0;
             for (int64_t u = blockIdx.x; u < T && !ctl.abort; u += gridDim.x, ++local) {
                 const int buf = local & 1;
-                if (!gwait(&ctl.tempty[buf], ((local >> 1) & 1) ^ 1u, ctl)) break;
+                if (!mx_wait(&ctl.tempty[buf], ((local >> 1) & 1) ^ 1u, ctl)) break;
                 const uint32_t d = ctl.tmem + (uint32_t)(buf * kN);
                 bool ok = true;
                 for (int s = 0; s < nks; ++s) {
-                    if (!gwait(&ctl.full[stage], phase, ctl) || !gwait(&ctl.sfull[stage], phase, ctl)) {
+                    if (!mx_wait(&ctl.full[stage], phase, ctl) || !mx_wait(&ctl.sfull[stage], phase, ctl)) {
                         ok = false;
                         break;
                     }
@@ -375,7 +387,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         bool ok = true;
         for (int64_t u = blockIdx.x; u < T && ok; u += gridDim.x)
             for (int s = 0; s < nks; ++s) {
-                if (!(ok = gwait(&ctl.full[stage], phase, ctl))) break;
+                if (!(ok = mx_wait(&ctl.full[stage], phase, ctl))) break;
                 const unsigned char *SA = stages + stage * G::kStageBytes + G::kABytes + G::kBBytes;
                 const unsigned char *SB = SA + G::kSABytes;
                 uint32_t wa[2 * G::kACols], wb[2 * G::kBPad] = {};
@@ -414,12 +426,14 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         for (int64_t u = blockIdx.x; u < T; u += gridDim.x, ++local) {
             const MxUnit x = mx_unit(a, ctl, u);
             const int buf = local & 1;
-            if (!gwait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
+            if (!mx_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
             tc_fence_after();
             const int64_t row = x.row0 + 32 * warp + lane;
             const bool live = 32 * warp + lane < x.nrows;
             const uint32_t d = ctl.tmem + quad + (uint32_t)(buf * kN);
-            if constexpr (!kGated) {
+            if (32 * warp >= x.nrows) {
+                // no row of this warp's lanes: the accumulator holds nothing of the tile here
+            } else if constexpr (!kGated) {
                 using T_ = typename std::conditional<kOut == 0, __nv_bfloat16,
                                                      typename std::conditional<kOut == 1, __half, float>::type>::type;
 #pragma unroll 1
@@ -442,7 +456,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                     uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        g[i] = __float_as_uint(silu_f32(__uint_as_float(g[i])) * __uint_as_float(up[i]));
+                        g[i] = __float_as_uint(silu_fast(__uint_as_float(g[i])) * __uint_as_float(up[i]));
                         const uint32_t b = g[i] & 0x7fffffffu;
                         top = b > top ? b : top;
                     }
