@@ -157,18 +157,32 @@ static int check_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_
     return MOE_OK;
 }
 
+// The gated form's weights are seen as [chunk][gate/up][row]: one box takes a run of gate rows
+// and the up rows beside it.  Without whole chunks the chunk dimension has one entry, and a
+// row's bytes past its end read as zeros.
 static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
-                         const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K) {
-    const int pitch = microscale_pitch(K);
-    const uint32_t half = (uint32_t)microscale_tile_n(rows, E) / 2;
-    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    return make_tmap_2d(&tm->a, x_codes, u8, 1, K / 2, rows, 128, 128, sw) &&
-           make_tmap_2d(&tm->a_small, x_codes, u8, 1, K / 2, rows, 128, 32, sw) &&
-           make_tmap_2d(&tm->sa, x_scales, u8, 1, pitch, rows, 16, 128) &&
-           make_tmap_2d(&tm->sa_small, x_scales, u8, 1, pitch, rows, 16, 32) &&
-           make_tmap_2d(&tm->b, w_codes, u8, 1, K / 2, (uint64_t)E * N, 128, half, sw) &&
-           make_tmap_2d(&tm->sb, w_scales, u8, 1, pitch, (uint64_t)E * N, 16, half);
+                         const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K, bool gated) {
+    const MicroscaleTile t = microscale_tile(rows, E);
+    const uint64_t row = (uint64_t)K / 2, pitch = (uint64_t)microscale_pitch(K);
+    const uint64_t inner = K % 256 == 0 ? 128 : row, chunks = K % 256 == 0 ? K / 256 : 1;
+    const uint32_t depth = K % 256 == 0 ? t.chunks : 1;
+    const uint64_t halves = gated ? 2 : 1, wrows = (uint64_t)E * N - (gated ? N / 2 : 0);
+    const uint64_t up = (uint64_t)(gated ? N / 2 : N);  // rows from gate to up
+    const uint32_t bn = (uint32_t)(t.n / halves), m = (uint32_t)t.m, two = (uint32_t)halves;
+    const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    tm->deep = K % 256 == 0;
+    const uint64_t ad[3] = {inner, (uint64_t)rows, chunks}, as[2] = {row, 128};
+    const uint32_t ab[3] = {128, m, depth};
+    const uint64_t bd[4] = {inner, wrows, halves, chunks}, bs[3] = {row, up * row, 128};
+    const uint32_t bb[4] = {128, bn, two, depth};
+    const uint64_t sad[2] = {pitch, (uint64_t)rows}, sas[1] = {pitch};
+    const uint32_t sab[2] = {64, m};
+    const uint64_t sbd[3] = {pitch, wrows, halves}, sbs[2] = {pitch, up * pitch};
+    const uint32_t sbb[3] = {64, bn, two};
+    return make_tmap_bytes(&tm->a, x_codes, 3, ad, as, ab, sw128) &&
+           make_tmap_bytes(&tm->b, w_codes, 4, bd, bs, bb, sw128) &&
+           make_tmap_bytes(&tm->sa, x_scales, 2, sad, sas, sab, sw64) &&
+           make_tmap_bytes(&tm->sb, w_scales, 3, sbd, sbs, sbb, sw64);
 }
 
 extern "C" int moe_microscale_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
@@ -181,7 +195,7 @@ extern "C" int moe_microscale_product(const uint8_t *x_codes, const uint8_t *x_s
     if (rows == 0) return MOE_OK;
     if ((rc = check_matrix(y, ldy, N, dtype_bytes(dtype))) != MOE_OK) return rc;
     MicroscaleMaps tm;
-    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K)) return MOE_ERR_CUDA;
+    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K, false)) return MOE_ERR_CUDA;
     return cuda_status(launch_microscale_gemm(tm, rows, offsets, E, N, K, dtype, y, ldy, nullptr, nullptr,
                                               static_cast<int32_t *>(workspace),
                                               static_cast<cudaStream_t>(stream)));
@@ -197,7 +211,7 @@ extern "C" int moe_microscale_gated_product(const uint8_t *x_codes, const uint8_
     if (rows == 0) return MOE_OK;
     if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_INVALID_ARG;
     MicroscaleMaps tm;
-    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K)) return MOE_ERR_CUDA;
+    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K, true)) return MOE_ERR_CUDA;
     return cuda_status(launch_microscale_gemm(tm, rows, offsets, E, N, K, MOE_DT_BF16, nullptr, 0, codes, scales,
                                               static_cast<int32_t *>(workspace),
                                               static_cast<cudaStream_t>(stream)));

@@ -30,35 +30,49 @@
 namespace moe {
 
 constexpr int kMxThreads = 320;
-constexpr int kMxStageK = 256;
-constexpr int kMxRows = 128;
 constexpr int kMxMaxStages = 8;
-constexpr int kMxSmallBox = 32;  // rows per copy for tiles that are not full
+constexpr int kMxMaxScaleBufs = 4;
+constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
 
-template <int kN>
+// kM: rows per tile that are copied and stored (128, or 32 for small groups: the MMA still
+// reads 128 rows, the others whatever follows in shared memory, and their results are
+// dropped); kN: channels per tile; kChunks: 256-wide chunks of K per stage.
+template <int kM, int kN>
 struct MxTile {
-    static constexpr int kABytes = kMxRows * 128;
-    static constexpr int kBBytes = kN * 128;
-    static constexpr int kSABytes = kMxRows * 16;
-    static constexpr int kSBBytes = kN * 16;
-    static constexpr int kStageBytes = kABytes + kBBytes + kSABytes + kSBBytes;
-    static constexpr int kStages = kN == 192 ? 4 : 8;
-    static constexpr int kACols = kMxRows / 32;  // scale columns per 128 of K
+    static_assert(kM == 32 || kM == 128, "row tiles");
+    static_assert(kN % 64 == 0 && kN <= 192, "column tiles");
+    static constexpr int kChunks = kM == 32 ? 2 : 1;
+    static constexpr int kStageK = 256 * kChunks;
+    static constexpr int kAChunk = kM * 128;               // one 256-wide chunk of the rows
+    static constexpr int kBChunk = kN * 128;
+    static constexpr int kABytes = kChunks * kAChunk;
+    static constexpr int kBBytes = kChunks * kBChunk;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kScaleBytes = (kM + kN) * 64;     // one copy of scales, rows then channels
+    static constexpr int kScaleBufs = kM == 32 ? 4 : 2;
+    static constexpr int kStages = kM == 128 ? 4 : (kN == 64 ? 7 : 4);
+    static constexpr int kACols = 4;                       // scale columns per 128 of K
+    static constexpr int kAUsed = kM / 32;                 // those whose rows exist
     static constexpr int kBCols = kN / 32;
     static constexpr int kBPad = (kBCols + 3) / 4 * 4;     // every set starts at a multiple of 4
-    static constexpr int kSfCols = 2 * (kACols + kBPad);   // per stage
+    static constexpr int kGroups = 2 * kChunks;            // 128-wide groups of K per stage
+    static constexpr int kSfCols = kGroups * (kACols + kBPad);  // per stage
     static constexpr int kSfCol0 = 2 * kN;                 // after the two accumulators
     static constexpr uint32_t kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
-    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
-    static_assert(kStageBytes % 1024 == 0, "stage alignment");
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kScaleBufs * kScaleBytes + 1024;
+    static_assert(kStageBytes % 1024 == 0 && kScaleBytes % 512 == 0, "stage alignment");
     static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
-    static_assert(kStages <= kMxMaxStages, "barriers");
+    static_assert(kStages <= kMxMaxStages && kScaleBufs <= kMxMaxScaleBufs, "barriers");
+    // the MMA's reads past a 32-row chunk stay inside the stage
+    static_assert(kABytes - kAChunk + 128 * 128 <= kStageBytes, "A reads");
 };
 
 struct MxCtl {
     uint64_t full[kMxMaxStages];
     uint64_t empty[kMxMaxStages];
-    uint64_t sfull[kMxMaxStages];
+    uint64_t sfull[kMxMaxStages];      // the stage's scales are in tensor memory
+    uint64_t cfull[kMxMaxScaleBufs];   // a copy of scales has landed
+    uint64_t cempty[kMxMaxScaleBufs];
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t done;
@@ -79,6 +93,7 @@ __device__ __forceinline__ bool mx_wait(uint64_t *bar, uint32_t parity, MxCtl &c
 }
 
 struct MxArgs {
+    int deep;                // the maps' third dimension is K's 256-wide chunks, a stage a copy
     const int32_t *offsets;  // NULL: one group of all rows
     int64_t rows;
     int E, N, K;
@@ -95,7 +110,7 @@ struct MxArgs {
 // scale ids pick the 16-bit half of the scale columns (0: bytes 0-1, 2: bytes 2-3).
 __device__ __forceinline__ constexpr uint32_t mx_idesc(int N, uint32_t sf_id) {
     return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(kMxRows >> 4) << 24) | (sf_id << 29);
+           ((uint32_t)(128 >> 4) << 24) | (sf_id << 29);
 }
 
 __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
@@ -112,12 +127,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
-
 // 32 consecutive fp32 columns of this warp's lanes; complete after tmem_ld_wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -198,6 +207,27 @@ struct MxUnit {
     int64_t row0;
 };
 
+// The scale words of stage `part` of a copy for one row: word q of 128 of K to w[q * kStep].
+// Rows are 64 bytes, their 16-byte pieces exchanged as the 64-byte swizzle does.
+template <int kGroups, int kStep>
+__device__ __forceinline__ void mx_scale_words(const unsigned char *base, int row, int part,
+                                               const uint32_t (&mask)[kGroups], uint32_t *w) {
+    const int piece = kGroups == 4 ? part : part >> 1;
+    const unsigned char *p = base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+    if constexpr (kGroups == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x & mask[0];
+        w[kStep] = v.y & mask[1];
+        w[2 * kStep] = v.z & mask[2];
+        w[3 * kStep] = v.w & mask[3];
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p + (part & 1) * 8);
+        w[0] = v.x & mask[0];
+        w[kStep] = v.y & mask[1];
+    }
+}
+
+template <int kM>
 __device__ __forceinline__ MxUnit mx_unit(const MxArgs &a, const MxCtl &ctl, int64_t u) {
     const int t = (int)(u / a.nct);
     int lo = 0, hi = a.E;  // the last e with first[e] <= t
@@ -209,25 +239,25 @@ __device__ __forceinline__ MxUnit mx_unit(const MxArgs &a, const MxCtl &ctl, int
     MxUnit x;
     x.e = lo;
     x.ct = (int)(u - (int64_t)t * a.nct);
-    x.row0 = (int64_t)ctl.begin[lo] + (int64_t)(t - ctl.first[lo]) * kMxRows;
+    x.row0 = (int64_t)ctl.begin[lo] + (int64_t)(t - ctl.first[lo]) * kM;
     const int64_t left = (int64_t)ctl.begin[lo + 1] - x.row0;
-    x.nrows = left < kMxRows ? (int)left : kMxRows;
+    x.nrows = left < kM ? (int)left : kM;
     return x;
 }
 
 // kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
-template <int kN, int kOut>
+template <int kM, int kN, int kOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
-microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_small,
-                       const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sa_small,
+microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_sa,
                        const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sb,
                        const MxArgs a) {
-    using G = MxTile<kN>;
+    using G = MxTile<kM, kN>;
     constexpr bool kGated = kOut == 3;
     constexpr int kHalf = kN / 2;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *stages = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *scales = stages + G::kStages * G::kStageBytes;
     __shared__ MxCtl ctl;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
@@ -236,6 +266,10 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             mbar_init(&ctl.full[s], 1);
             mbar_init(&ctl.empty[s], 1);
             mbar_init(&ctl.sfull[s], 4);
+        }
+        for (int b = 0; b < G::kScaleBufs; ++b) {
+            mbar_init(&ctl.cfull[b], 1);
+            mbar_init(&ctl.cempty[b], 4);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl.tfull[b], 1);
@@ -264,7 +298,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
             hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
         }
-        const int tiles = (int)((hi - lo + kMxRows - 1) / kMxRows);
+        const int tiles = (int)((hi - lo + kM - 1) / kM);
         int inc = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -294,40 +328,43 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     __syncthreads();
     tc_fence_after();
     const int64_t T = (int64_t)carry * a.nct;
-    const int nks = (a.K + kMxStageK - 1) / kMxStageK;
+    const int nks = (a.K + G::kStageK - 1) / G::kStageK;  // stages per unit
+    constexpr int kPerScale = kMxScaleK / G::kStageK;         // stages per copy of scales
 
     if (warp == 8) {
         if (lane == 0) {
             const uint64_t pol = policy_evict_normal();
-            int stage = 0;
+            int stage = 0, buf = 0;
             uint32_t phase = 0, issued = 0, par = 0;
+            uint32_t cphase = 0, cissued = 0, cpar = 0;
             for (int64_t u = blockIdx.x; u < T && !ctl.abort; u += gridDim.x) {
-                const MxUnit x = mx_unit(a, ctl, u);
-                const bool full_tile = x.nrows > kMxRows - kMxSmallBox;
-                const int nbox = (x.nrows + kMxSmallBox - 1) / kMxSmallBox;
-                const uint32_t bytes = (full_tile ? kMxRows : nbox * kMxSmallBox) * (128 + 16) + G::kBBytes + G::kSBBytes;
-                // weight rows of the two halves of the N side
+                const MxUnit x = mx_unit<kM>(a, ctl, u);
+                // first weight row of the N side; a gated tile's box also takes the up rows beside it
                 const int b0 = x.e * a.N + x.ct * (kGated ? kHalf : kN);
-                const int b1 = kGated ? x.e * a.N + a.N / 2 + x.ct * kHalf : b0 + kHalf;
                 for (int s = 0; s < nks; ++s) {
+                    if (s % kPerScale == 0) {
+                        if (!mx_wait(&ctl.cempty[buf], cphase ^ 1u, ctl)) break;
+                        uint64_t *bar = &ctl.cfull[buf];
+                        unsigned char *SA = scales + buf * G::kScaleBytes, *SB = SA + kM * 64;
+                        mbar_arrive_expect_tx(bar, G::kScaleBytes);
+                        const int xs = s / kPerScale * 64;
+                        tma_load_3d(SB, &tm_sb, xs, b0, 0, bar, pol);
+                        tma_load_2d(SA, &tm_sa, xs, (int)x.row0, bar, pol);
+                        cissued |= 1u << buf;
+                        cpar = (cpar & ~(1u << buf)) | (cphase << buf);
+                        if (++buf == G::kScaleBufs) buf = 0, cphase ^= 1u;
+                    }
                     if (!mx_wait(&ctl.empty[stage], phase ^ 1u, ctl)) break;
                     uint64_t *bar = &ctl.full[stage];
-                    unsigned char *A = stages + stage * G::kStageBytes;
-                    unsigned char *B = A + G::kABytes, *SA = B + G::kBBytes, *SB = SA + G::kSABytes;
-                    mbar_arrive_expect_tx(bar, bytes);
-                    const int xk = s * 128, xs = (s >> 1) * 16;
-                    tma_load_2d(B, &tm_b, xk, b0, bar, pol);
-                    tma_load_2d(B + kHalf * 128, &tm_b, xk, b1, bar, pol);
-                    tma_load_2d(SB, &tm_sb, xs, b0, bar, pol);
-                    tma_load_2d(SB + kHalf * 16, &tm_sb, xs, b1, bar, pol);
-                    if (full_tile) {
-                        tma_load_2d(A, &tm_a, xk, (int)x.row0, bar, pol);
-                        tma_load_2d(SA, &tm_sa, xs, (int)x.row0, bar, pol);
-                    } else {
-                        for (int q = 0; q < nbox; ++q) {
-                            tma_load_2d(A + q * kMxSmallBox * 128, &tm_a_small, xk, (int)x.row0 + q * kMxSmallBox, bar, pol);
-                            tma_load_2d(SA + q * kMxSmallBox * 16, &tm_sa_small, xs, (int)x.row0 + q * kMxSmallBox, bar, pol);
-                        }
+                    unsigned char *A = stages + stage * G::kStageBytes, *B = A + G::kABytes;
+                    // one copy brings the whole stage, or one per chunk (past K: none)
+                    const int left = (a.K - s * G::kStageK + 255) / 256;
+                    const int copies = a.deep ? 1 : (left < G::kChunks ? left : G::kChunks);
+                    mbar_arrive_expect_tx(bar, a.deep ? G::kStageBytes : copies * (G::kAChunk + G::kBChunk));
+                    for (int c = 0; c < copies; ++c) {
+                        const int cx = a.deep ? 0 : (s * G::kChunks + c) * 128, cz = a.deep ? s * G::kChunks : 0;
+                        tma_load_4d(B + c * G::kBChunk, &tm_b, cx, b0, 0, cz, bar, pol);
+                        tma_load_3d(A + c * G::kAChunk, &tm_a, cx, (int)x.row0, cz, bar, pol);
                     }
                     issued |= 1u << stage;
                     par = (par & ~(1u << stage)) | (phase << stage);
@@ -338,6 +375,9 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             for (int s = 0; s < G::kStages; ++s)
                 if ((issued >> s) & 1u)
                     if (!mbar_wait_bounded(&ctl.full[s], (par >> s) & 1u)) ctl.abort = 1;
+            for (int b = 0; b < G::kScaleBufs; ++b)
+                if ((cissued >> b) & 1u)
+                    if (!mbar_wait_bounded(&ctl.cfull[b], (cpar >> b) & 1u)) ctl.abort = 1;
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -359,13 +399,13 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                     const uint32_t B = A + G::kABytes;
                     const uint32_t sf = ctl.tmem + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
 #pragma unroll
-                    for (int ks = 0; ks < kMxStageK / 64; ++ks) {
-                        if (s * kMxStageK + ks * 64 >= a.K) break;
+                    for (int ks = 0; ks < G::kStageK / 64; ++ks) {
+                        if (s * G::kStageK + ks * 64 >= a.K) break;
                         // K-major, 128-byte swizzle: 32 bytes per K step, 8-row atoms 1 KB apart
-                        const uint64_t ad = umma_smem_desc(A + ks * 32, 16, 1024, 2);
-                        const uint64_t bd = umma_smem_desc(B + ks * 32, 16, 1024, 2);
+                        const uint64_t ad = umma_smem_desc(A + (ks >> 2) * G::kAChunk + (ks & 3) * 32, 16, 1024, 2);
+                        const uint64_t bd = umma_smem_desc(B + (ks >> 2) * G::kBChunk + (ks & 3) * 32, 16, 1024, 2);
                         const uint32_t sfa = sf + (uint32_t)((ks >> 1) * G::kACols);
-                        const uint32_t sfb = sf + (uint32_t)(2 * G::kACols + (ks >> 1) * G::kBPad);
+                        const uint32_t sfb = sf + (uint32_t)(G::kGroups * G::kACols + (ks >> 1) * G::kBPad);
                         umma_mxf4(d, ad, bd, mx_idesc(kN, (ks & 1) ? 2u : 0u), sfa, sfb, s > 0 || ks > 0);
                     }
                     umma_commit(&ctl.empty[stage]);
@@ -382,38 +422,39 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     } else if (warp >= 4) {
         const uint32_t quad = (uint32_t)(32 * (warp - 4)) << 16;
         const int nb = a.K / 32;
-        int stage = 0;
-        uint32_t phase = 0;
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, cphase = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < T && ok; u += gridDim.x)
             for (int s = 0; s < nks; ++s) {
-                if (!(ok = mx_wait(&ctl.full[stage], phase, ctl))) break;
-                const unsigned char *SA = stages + stage * G::kStageBytes + G::kABytes + G::kBBytes;
-                const unsigned char *SB = SA + G::kSABytes;
-                uint32_t wa[2 * G::kACols], wb[2 * G::kBPad] = {};
+                const int part = s % kPerScale;
+                if (part == 0 && !(ok = mx_wait(&ctl.cfull[buf], cphase, ctl))) break;
                 // blocks past K have zero codes; their scale must not be a NaN
-                uint32_t mask[2];
+                uint32_t mask[G::kGroups];
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    const int left = nb - (s * 8 + kk * 4);
-                    mask[kk] = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
+                for (int q = 0; q < G::kGroups; ++q) {
+                    const int left = nb - (s * G::kGroups + q) * 4;
+                    mask[q] = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
                 }
+                const unsigned char *SA = scales + buf * G::kScaleBytes, *SB = SA + kM * 64;
+                uint32_t wa[G::kGroups * G::kACols] = {}, wb[G::kGroups * G::kBPad] = {};
 #pragma unroll
-                for (int c = 0; c < G::kACols; ++c) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(SA + (c * 32 + lane) * 16 + (s & 1) * 8);
-                    wa[c] = v.x & mask[0];
-                    wa[G::kACols + c] = v.y & mask[1];
-                }
+                for (int c = 0; c < G::kAUsed; ++c) mx_scale_words<G::kGroups, G::kACols>(SA, c * 32 + lane, part, mask, wa + c);
 #pragma unroll
-                for (int c = 0; c < G::kBCols; ++c) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(SB + (c * 32 + lane) * 16 + (s & 1) * 8);
-                    wb[c] = v.x & mask[0];
-                    wb[G::kBPad + c] = v.y & mask[1];
+                for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kGroups, G::kBPad>(SB, c * 32 + lane, part, mask, wb + c);
+                if (part == kPerScale - 1 || s == nks - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.cempty[buf]);
+                    if (++buf == G::kScaleBufs) buf = 0, cphase ^= 1u;
                 }
+                // the MMAs that read this slot's scales have completed
+                if (!(ok = mx_wait(&ctl.empty[stage], phase ^ 1u, ctl))) break;
+                tc_fence_after();
                 const uint32_t sf = ctl.tmem + quad + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
-                tmem_st8(sf, wa);
 #pragma unroll
-                for (int c = 0; c < 2 * G::kBPad; c += 4) tmem_st4(sf + 2 * G::kACols + c, wb + c);
+                for (int i = 0; i < G::kGroups * G::kACols; i += 8) tmem_st8(sf + i, wa + i);
+#pragma unroll
+                for (int i = 0; i < G::kGroups * G::kBPad; i += 8) tmem_st8(sf + G::kGroups * G::kACols + i, wb + i);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -424,7 +465,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         const uint32_t quad = (uint32_t)(32 * warp) << 16;
         int local = 0;
         for (int64_t u = blockIdx.x; u < T; u += gridDim.x, ++local) {
-            const MxUnit x = mx_unit(a, ctl, u);
+            const MxUnit x = mx_unit<kM>(a, ctl, u);
             const int buf = local & 1;
             if (!mx_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
             tc_fence_after();
@@ -504,45 +545,49 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
 }
 
 // ----------------------------------------------------------------------------------- launcher
-template <int kN, int kOut>
+MicroscaleTile microscale_tile(int64_t rows, int E) {
+    return rows >= 32 * (int64_t)E ? MicroscaleTile{128, 192, 1} : MicroscaleTile{32, rows > E / 4 ? 128 : 64, 2};
+}
+
+template <int kM, int kN, int kOut>
 static cudaError_t gemm_as(const MicroscaleMaps &tm, MxArgs a, cudaStream_t stream) {
-    using G = MxTile<kN>;
+    using G = MxTile<kM, kN>;
     a.nct = kOut == 3 ? (a.N / 2 + kN / 2 - 1) / (kN / 2) : (a.N + kN - 1) / kN;
-    const int64_t tiles = a.rows < a.E ? a.rows : a.rows / kMxRows + a.E;
+    const int64_t tiles = a.rows < a.E ? a.rows : a.rows / kM + a.E;
     const int64_t units = tiles * a.nct, sms = num_sms();
     const int64_t grid = units < 1 ? 1 : (units < sms ? units : sms);
-    const auto fn = microscale_gemm_kernel<kN, kOut>;
+    const auto fn = microscale_gemm_kernel<kM, kN, kOut>;
     cudaError_t err = ensure_smem((const void *)fn, G::kSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)grid), dim3(kMxThreads), G::kSmem, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, fn, tm.a, tm.a_small, tm.sa, tm.sa_small, tm.b, tm.sb, a);
+    return cudaLaunchKernelEx(&cfg, fn, tm.a, tm.sa, tm.b, tm.sb, a);
 }
 
-template <int kN>
-static cudaError_t gemm_width(const MicroscaleMaps &tm, const MxArgs &a, int out, cudaStream_t stream) {
+template <int kM, int kN>
+static cudaError_t gemm_tile(const MicroscaleMaps &tm, const MxArgs &a, int out, cudaStream_t stream) {
     switch (out) {
-        case MOE_DT_BF16: return gemm_as<kN, 0>(tm, a, stream);
-        case MOE_DT_F16: return gemm_as<kN, 1>(tm, a, stream);
-        case MOE_DT_F32: return gemm_as<kN, 2>(tm, a, stream);
-        default: return gemm_as<kN, 3>(tm, a, stream);
+        case MOE_DT_BF16: return gemm_as<kM, kN, 0>(tm, a, stream);
+        case MOE_DT_F16: return gemm_as<kM, kN, 1>(tm, a, stream);
+        case MOE_DT_F32: return gemm_as<kM, kN, 2>(tm, a, stream);
+        default: return gemm_as<kM, kN, 3>(tm, a, stream);
     }
 }
-
-int microscale_tile_n(int64_t rows, int E) { return rows >= 32 * (int64_t)E ? 192 : 64; }
 
 cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const int32_t *offsets, int E,
                                    int N, int K, int dtype, void *y, int64_t ldy, uint8_t *codes,
                                    uint8_t *scales, int32_t *status, cudaStream_t stream) {
     MxArgs a{};
+    a.deep = tm.deep;
     a.offsets = offsets, a.rows = rows, a.E = E, a.N = N, a.K = K;
     a.y = y, a.ldy = ldy, a.codes = codes, a.scales = scales, a.status = status;
     a.pitch = microscale_pitch(N / 2);
     const int elem = dtype == MOE_DT_F32 ? 4 : 2;
     a.vec = y && (reinterpret_cast<uintptr_t>(y) | (uint64_t)(ldy * elem)) % 32 == 0;
     const int out = codes ? 3 : dtype;
-    return microscale_tile_n(rows, E) == 192 ? gemm_width<192>(tm, a, out, stream)
-                                             : gemm_width<64>(tm, a, out, stream);
+    const MicroscaleTile t = microscale_tile(rows, E);
+    if (t.m == 128) return gemm_tile<128, 192>(tm, a, out, stream);
+    return t.n == 128 ? gemm_tile<32, 128>(tm, a, out, stream) : gemm_tile<32, 64>(tm, a, out, stream);
 }
 
 }  // namespace moe

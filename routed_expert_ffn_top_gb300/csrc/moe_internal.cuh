@@ -379,11 +379,10 @@ int block_for(const moe_expert_weights_t *w, int M, int k, int b);  // b, or the
 // on every launch costs host time that small decode blocks cannot hide.
 cudaError_t ensure_smem(const void *func, size_t bytes);
 
-// 2-D row-major tensor map [outer][inner] of `elem` bytes, box [box_outer][box_inner];
+// Tensor map of bytes: dims and box innermost first, strides (bytes) of dimensions 1 and up;
 // out-of-range box elements read as zeros.
-bool make_tmap_2d(CUtensorMap *tm, const void *base, CUtensorMapDataType dt, int elem,
-                  uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
-                  CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
+bool make_tmap_bytes(CUtensorMap *tm, const void *base, int rank, const uint64_t *dims,
+                     const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle swizzle);
 
 // Tokens sorted by expert and back (token_sort.cu).  dtype: MOE_DT_*; ld*: row pitch in
 // elements; w == NULL: weights of one.
@@ -408,12 +407,18 @@ cudaError_t launch_microscale_quantize(const void *x, int64_t ldx, int dtype, in
                                        cudaStream_t stream);
 cudaError_t launch_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                          int cols, void *x, int64_t ldx, int dtype, cudaStream_t stream);
-// Tensor maps of one grouped product: codes and scales of the rows (128- and 32-row boxes) and
-// of the weights (boxes of half a column tile).
-struct MicroscaleMaps {
-    CUtensorMap a, a_small, sa, sa_small, b, sb;
+// Tile of the grouped product for these sizes: rows, channels, 256-wide chunks of K a stage.
+struct MicroscaleTile {
+    int m, n, chunks;
 };
-int microscale_tile_n(int64_t rows, int E);  // column tile of the grouped product
+MicroscaleTile microscale_tile(int64_t rows, int E);
+// Tensor maps of one grouped product: codes and scales of the rows and of the weights.  Codes
+// have a chunk dimension of K (128 bytes each) when K is a multiple of 256 (`deep`); the
+// weights' have a gate/up dimension.
+struct MicroscaleMaps {
+    CUtensorMap a, sa, b, sb;
+    int deep;
+};
 // codes == NULL: y [rows][N] of dtype; else the gated form, codes and scales of [rows][N / 2].
 cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const int32_t *offsets, int E,
                                    int N, int K, int dtype, void *y, int64_t ldy, uint8_t *codes,
