@@ -52,15 +52,12 @@ struct QuantArgs {
 // quantised once and stored k times (tail rows of dropped routes as zeros).
 // Memory bound: elem + 1/2 + 1/32 bytes a value.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(256) microscale_quantize_kernel(const QuantArgs a, int nchunk) {
+__global__ void __launch_bounds__(256) microscale_quantize_kernel(const QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t units = a.rows * nchunk;
+    const int lane = threadIdx.x & 31, c0 = blockIdx.y * 512;
     const int64_t stride = (int64_t)gridDim.x * 8;
-    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += stride) {
-        const int64_t m = u / nchunk;
-        const int c0 = (int)(u - m * nchunk) * 512;
+    for (int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows; m += stride) {
         const T *x = static_cast<const T *>(a.x) + m * a.ldx + c0 + lane * 8;
         const bool in[2] = {c0 + lane * 8 < a.cols, c0 + 256 + lane * 8 < a.cols};
         float v[2][8];
@@ -133,22 +130,56 @@ struct DequantArgs {
     int64_t ldx;
 };
 
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+// Eight codes to four bf16 pairs: the two bytes of a magnitude's bf16 come from two eight-entry
+// byte tables indexed by the code, the sign bits are moved in.
+__device__ __forceinline__ void decode_bf16(uint32_t code, uint32_t (&v)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t c = code >> (16 * h), sel = c & 0x7777u;
+        const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, sel);
+        const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, sel);
+        v[2 * h] = __byte_perm(lo, hi, 0x5140) | ((c & 0x8u) << 12) | ((c & 0x80u) << 24);
+        v[2 * h + 1] = __byte_perm(lo, hi, 0x7362) | ((c & 0x800u) << 4) | ((c & 0x8000u) << 16);
+    }
+}
+
+// Eight values of a block: the products with 2^X are exact in bf16 and fp32.
+__device__ __forceinline__ void decode8(uint32_t code, uint32_t byte, __nv_bfloat16 (&o)[8]) {
+    uint32_t v[4];
+    decode_bf16(code, v);
+    const uint32_t s = byte == 255u ? 0x7fffu : (byte == 0u ? 0x0040u : byte << 7);
+    const uint32_t ss = s | (s << 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<__nv_bfloat162 *>(&o[2 * i]) = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i]),
+                                                                 *reinterpret_cast<const __nv_bfloat162 *>(&ss));
+}
+__device__ __forceinline__ void decode8(uint32_t code, uint32_t byte, float (&o)[8]) {
+    uint32_t v[4];
+    decode_bf16(code, v);
+    const float s = microscale_value(byte);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = bf16_lo(v[i]) * s;
+        o[2 * i + 1] = bf16_hi(v[i]) * s;
+    }
+}
+__device__ __forceinline__ void decode8(uint32_t code, uint32_t byte, __half (&o)[8]) {
+    float f[8];
+    decode8(code, byte, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = __float2half_rn(f[i]);
+}
 
 // A unit is 512 columns of one row, as above.  A code's value times 2^X is exact in fp32 and
 // in bf16; fp16 rounds it (to infinity past its range).
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(256) microscale_dequantize_kernel(const DequantArgs a, int nchunk) {
+__global__ void __launch_bounds__(256) microscale_dequantize_kernel(const DequantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t units = a.rows * nchunk;
+    const int lane = threadIdx.x & 31, c0 = blockIdx.y * 512 + lane * 8;
     const int64_t stride = (int64_t)gridDim.x * 8;
-    for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += stride) {
-        const int64_t m = u / nchunk;
-        const int c0 = (int)(u - m * nchunk) * 512 + lane * 8;
+    for (int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows; m += stride) {
         uint32_t code[2], byte[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -160,16 +191,8 @@ __global__ void __launch_bounds__(256) microscale_dequantize_kernel(const Dequan
         for (int h = 0; h < 2; ++h) {
             const int c = c0 + 256 * h;
             if (c >= a.cols) continue;
-            const float s = microscale_value(byte[h]);
             alignas(16) T o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // magnitude bits eem: 0.5 m for ee = 0, else (2 + m) 2^(ee - 2)
-                const uint32_t q = code[h] >> (4 * i);
-                const uint32_t ee = (q >> 1) & 3u, mm = q & 1u;
-                const float mag = ee == 0 ? 0.5f * (float)mm : __uint_as_float(((ee + 126u) << 23) | (mm << 22));
-                put(&o[i], ((q & 8u) ? -mag : mag) * s);
-            }
+            decode8(code[h], byte[h], o);
             T *dst = static_cast<T *>(a.x) + m * a.ldx + c;
             if constexpr (kVec) {
                 constexpr int n = 16 / sizeof(T);
@@ -184,27 +207,26 @@ __global__ void __launch_bounds__(256) microscale_dequantize_kernel(const Dequan
     }
 }
 
-static unsigned ctas_for(int64_t units) {
-    const int64_t n = (units + 7) / 8, most = (int64_t)num_sms() * 64;
-    return (unsigned)(n < 1 ? 1 : n < most ? n : most);
+// Grid: rows along x, 512-column chunks along y; up to 64 CTAs an SM in all.
+static dim3 rows_by_chunks(int64_t rows, int cols) {
+    const int64_t nchunk = (cols + 511) / 512, n = (rows + 7) / 8, most = (int64_t)num_sms() * 64 / nchunk + 1;
+    return dim3((unsigned)(n < most ? n : most), (unsigned)nchunk);
 }
 
 template <typename T>
 static cudaError_t quantize_as(const QuantArgs &a, cudaStream_t stream) {
-    const int nchunk = (a.cols + 511) / 512;
     const bool vec = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.ldx * sizeof(T))) % 16 == 0;
     cudaLaunchAttribute attrs[2];
-    cudaLaunchConfig_t cfg = launch_config(dim3(ctas_for(a.rows * nchunk)), dim3(256), 0, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, vec ? microscale_quantize_kernel<T, true> : microscale_quantize_kernel<T, false>, a, nchunk);
+    cudaLaunchConfig_t cfg = launch_config(rows_by_chunks(a.rows, a.cols), dim3(256), 0, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, vec ? microscale_quantize_kernel<T, true> : microscale_quantize_kernel<T, false>, a);
 }
 
 template <typename T>
 static cudaError_t dequantize_as(const DequantArgs &a, cudaStream_t stream) {
-    const int nchunk = (a.cols + 511) / 512;
     const bool vec = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.ldx * sizeof(T))) % 16 == 0;
     cudaLaunchAttribute attrs[2];
-    cudaLaunchConfig_t cfg = launch_config(dim3(ctas_for(a.rows * nchunk)), dim3(256), 0, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, vec ? microscale_dequantize_kernel<T, true> : microscale_dequantize_kernel<T, false>, a, nchunk);
+    cudaLaunchConfig_t cfg = launch_config(rows_by_chunks(a.rows, a.cols), dim3(256), 0, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, vec ? microscale_dequantize_kernel<T, true> : microscale_dequantize_kernel<T, false>, a);
 }
 
 cudaError_t launch_microscale_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int cols,

@@ -354,6 +354,256 @@ __global__ void __launch_bounds__(kGradThreads) token_unsort_grad_kernel(const R
     }
 }
 
+// ------------------------------------------------------------------- row kernels, 16-byte rows
+// The same two operators where every row is whole 16-byte pieces.  What bounds the form above
+// is latency: a warp loads its indices, then its rows, then stores, and holds one unit's rows in
+// registers.  Here each lane copies its own pieces of the next kDepth units into its own slots
+// of shared memory (cp.async), so a warp has kDepth units in flight and no thread waits for
+// another.  The arithmetic and its order per element are those of the form above.
+constexpr int kRingWarps = 4;
+constexpr int kRingBytes = 74 * 1024;  // of a CTA's slots at most: three CTAs an SM
+
+// One unit of the ring: the k rows' pieces, then the token's own (residual or gradient).
+struct RingUnit {
+    int64_t m;
+    int vi;  // this lane's 16-byte piece of the row
+};
+
+template <typename T>
+__device__ __forceinline__ void ring_issue(const RowArgs &a, const void *rows, int64_t ldrows, const void *own,
+                                           int64_t ldown, const RingUnit &u, int nvec, int row_l, uint4 *slot) {
+    constexpr int n = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+    const bool in = u.vi < nvec;
+    for (int j = 0; j < a.k; ++j) {
+        const int row = __shfl_sync(0xffffffffu, row_l, j);
+        if (in && row >= 0)
+            cp_async_16(slot + j * 32 + lane, static_cast<const T *>(rows) + (int64_t)row * ldrows + (int64_t)u.vi * n);
+    }
+    if (own && in) cp_async_16(slot + a.k * 32 + lane, static_cast<const T *>(own) + u.m * ldown + (int64_t)u.vi * n);
+}
+
+// route_row entry of lane j < k for token m, -1 for a dropped or unknown row.
+__device__ __forceinline__ int ring_row(const RowArgs &a, int64_t m) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= a.k) return -1;
+    const int v = a.route_row[m * a.k + lane];
+    return row_of(v, (int64_t)a.M * a.k) < 0 ? -1 : v;
+}
+
+// A warp's sequence of units: chunks q, q + wpt, ... of tokens m, m + step, ... (no division:
+// at 600 instructions a unit the 64-bit ones alone cost a third of the kernel's time).
+struct RingCursor {
+    int64_t m;
+    int c;
+    __device__ __forceinline__ void advance(int q, int wpt, int nchunk, int64_t step) {
+        c += wpt;
+        if (c >= nchunk) c = q, m += step;
+    }
+};
+
+template <typename T, int kDepth>
+__global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(const RowArgs a, int nvec, int nchunk, int wpt) {
+    constexpr int n = 16 / sizeof(T);
+    using P = Pack<T, n>;
+    extern __shared__ uint4 ring[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (a.k + (a.res ? 1 : 0)) * 32;
+    uint4 *mine = ring + (size_t)warp * kDepth * per;
+    const int q = warp % wpt, tokens = kRingWarps / wpt;
+    const int64_t step = (int64_t)gridDim.x * tokens;
+    RingCursor now{(int64_t)blockIdx.x * tokens + warp / wpt, q}, ahead = now;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // indices and weights of the token the copies are at and of the one the sums are at
+    int row_a = -1, row = -1;
+    float w = 1.0f, w_n = 1.0f;
+    int row_n = -1;
+    auto weight = [&](int64_t m) { return a.w && lane < a.k ? a.w[m * a.k + lane] : 1.0f; };
+    if (now.m < a.M) {
+        row = row_a = ring_row(a, now.m);
+        w = weight(now.m);
+        if (now.m + step < a.M) row_n = ring_row(a, now.m + step), w_n = weight(now.m + step);
+    }
+    int slot_in = 0, slot_out = 0;
+    auto issue = [&]() {
+        if (ahead.m < a.M) {
+            ring_issue<T>(a, a.a, a.lda, a.res, a.ldres, RingUnit{ahead.m, ahead.c * 32 + lane}, nvec, row_a, mine + slot_in * per);
+            const int64_t m = ahead.m;
+            ahead.advance(q, wpt, nchunk, step);
+            if (ahead.m != m) row_a = ahead.m < a.M ? ring_row(a, ahead.m) : -1;
+        }
+        cp_async_commit();
+        if (++slot_in == kDepth) slot_in = 0;
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) issue();
+    while (now.m < a.M) {
+        cp_async_wait_group<kDepth - 1>();
+        const int vi = now.c * 32 + lane;
+        const uint4 *slot = mine + slot_out * per;
+        const bool in = vi < nvec;
+        float acc[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) acc[i] = 0.0f;
+        if (a.res && in) {
+            const P r = *reinterpret_cast<const P *>(slot + a.k * 32 + lane);
+#pragma unroll
+            for (int i = 0; i < n; ++i) acc[i] = Elem<T>::load(r.v[i]);
+        }
+#pragma unroll 8
+        for (int j = 0; j < a.k; ++j) {
+            const int rj = __shfl_sync(0xffffffffu, row, j);
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            if (in && rj >= 0) {
+                const P p = *reinterpret_cast<const P *>(slot + j * 32 + lane);
+#pragma unroll
+                for (int i = 0; i < n; ++i) acc[i] = fmaf(wj, Elem<T>::load(p.v[i]), acc[i]);
+            }
+        }
+        if (in) {
+            P o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) o.v[i] = Elem<T>::store(acc[i]);
+            *reinterpret_cast<P *>(static_cast<T *>(a.out) + now.m * a.ldout + (int64_t)vi * n) = o;
+        }
+        if (++slot_out == kDepth) slot_out = 0;
+        issue();
+        const int64_t m = now.m;
+        now.advance(q, wpt, nchunk, step);
+        if (now.m != m) {
+            row = row_n, w = w_n;
+            if (now.m + step < a.M) row_n = ring_row(a, now.m + step), w_n = weight(now.m + step);
+        }
+    }
+    cp_async_wait_all();
+}
+
+// One CTA per token (grid-stride): warp q takes chunks q, q + 4, ... of the row, a running
+// sequence of units over all its tokens; the k <= 8 products are summed over the lanes, then
+// over the warps, in fixed trees.
+constexpr int kRingSlots = 8;
+
+template <typename T, int kDepth>
+__global__ void __launch_bounds__(32 * kRingWarps) token_unsort_grad_ring_kernel(const RowArgs a, int nvec, int nchunk) {
+    constexpr int n = 16 / sizeof(T);
+    using P = Pack<T, n>;
+    extern __shared__ uint4 ring[];
+    __shared__ float part[2][kRingWarps][kRingSlots];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (a.k + 1) * 32;
+    uint4 *mine = ring + (size_t)warp * kDepth * per;
+    const int mychunks = nchunk > warp ? (nchunk - warp + kRingWarps - 1) / kRingWarps : 0;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // the unit `steps` after (m, c)
+    struct Cursor {
+        int64_t m;
+        int c;
+    };
+    auto advance = [&](Cursor &x) {
+        if (++x.c == mychunks) x.c = 0, x.m += gridDim.x;
+    };
+    auto unit = [&](const Cursor &x) { return RingUnit{x.m, (warp + x.c * kRingWarps) * 32 + lane}; };
+    Cursor ahead{(int64_t)blockIdx.x, 0};
+    int slot_in = 0, slot_out = 0;
+    int row_ahead = -1;
+    if (mychunks > 0 && ahead.m < a.M) row_ahead = ring_row(a, ahead.m);
+    auto issue = [&]() {
+        if (mychunks > 0 && ahead.m < a.M) {
+            ring_issue<T>(a, a.b, a.ldb, a.a, a.lda, unit(ahead), nvec, row_ahead, mine + slot_in * per);
+            const int64_t m = ahead.m;
+            advance(ahead);
+            if (ahead.m != m) row_ahead = ahead.m < a.M ? ring_row(a, ahead.m) : -1;
+        }
+        cp_async_commit();
+        if (++slot_in == kDepth) slot_in = 0;
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) issue();
+
+    int parity = 0;
+    int v_next = 0;
+    float w_next = 1.0f;
+    if (lane < a.k && (int64_t)blockIdx.x < a.M) {
+        v_next = a.route_row[(int64_t)blockIdx.x * a.k + lane];
+        if (a.w) w_next = a.w[(int64_t)blockIdx.x * a.k + lane];
+    }
+    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x, parity ^= 1) {
+        const int v_l = v_next;
+        const float w_l = w_next;
+        const int64_t mn = m + gridDim.x;
+        if (lane < a.k && mn < a.M) {
+            v_next = a.route_row[mn * a.k + lane];
+            if (a.w) w_next = a.w[mn * a.k + lane];
+        }
+        float dot[kRingSlots];
+#pragma unroll
+        for (int s = 0; s < kRingSlots; ++s) dot[s] = 0.0f;
+        for (int c = 0; c < mychunks; ++c) {
+            cp_async_wait_group<kDepth - 1>();
+            const int vi = (warp + c * kRingWarps) * 32 + lane;
+            const uint4 *slot = mine + slot_out * per;
+            const bool in = vi < nvec;
+            float g[n];
+            if (in) {
+                const P p = *reinterpret_cast<const P *>(slot + a.k * 32 + lane);
+#pragma unroll
+                for (int i = 0; i < n; ++i) g[i] = Elem<T>::load(p.v[i]);
+            }
+#pragma unroll
+            for (int s = 0; s < kRingSlots; ++s) {
+                if (s >= a.k) break;
+                const int v = __shfl_sync(0xffffffffu, v_l, s);
+                const float w = __shfl_sync(0xffffffffu, w_l, s);
+                const int64_t at = row_of(v, (int64_t)a.M * a.k);
+                if (in && at >= 0) {
+                    P o;
+                    if (v >= 0) {
+                        const P y = *reinterpret_cast<const P *>(slot + s * 32 + lane);
+#pragma unroll
+                        for (int i = 0; i < n; ++i) {
+                            dot[s] = fmaf(g[i], Elem<T>::load(y.v[i]), dot[s]);
+                            o.v[i] = Elem<T>::store(w * g[i]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < n; ++i) o.v[i] = Elem<T>::store(0.0f);
+                    }
+                    *reinterpret_cast<P *>(static_cast<T *>(a.out) + at * a.ldout + (int64_t)vi * n) = o;
+                }
+            }
+            if (++slot_out == kDepth) slot_out = 0;
+            issue();
+        }
+        // 8 sums over 32 lanes: halves exchanged until a lane holds one slot, then added
+#pragma unroll
+        for (int h = 4; h >= 1; h >>= 1) {
+            const bool up = lane & (4 * h);
+#pragma unroll
+            for (int i = 0; i < h; ++i) {
+                const float send = up ? dot[i] : dot[i + h];
+                const float keep = up ? dot[i + h] : dot[i];
+                dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4 * h);
+            }
+        }
+        float t = dot[0];
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        // lane bits 4, 3, 2 chose the slot's bits 2, 1, 0
+        if ((lane & 3) == 0) part[parity][warp][lane >> 2] = t;
+        __syncthreads();
+        if ((int)threadIdx.x < a.k) {
+            float sum = 0.0f;
+            for (int q = 0; q < kRingWarps; ++q) sum += part[parity][q][threadIdx.x];
+            static_cast<float *>(a.out2)[m * a.k + threadIdx.x] = sum;
+        }
+    }
+    cp_async_wait_all();
+}
+
 // ----------------------------------------------------------------------------------- launchers
 static int64_t cap_grid(int64_t ctas, int per_sm) {
     const int64_t most = (int64_t)num_sms() * per_sm;
@@ -423,6 +673,60 @@ static cudaError_t unsort_grad_as(const RowArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, token_unsort_grad_kernel<T, V>, a, a.H / V);
 }
 
+// CTAs an SM for a ring of `smem` bytes (its grids are persistent).
+static int ring_ctas(size_t smem) {
+    const int n = (int)(222 * 1024 / (smem + 1024));
+    return n < 1 ? 1 : (n > 8 ? 8 : n);
+}
+
+// Units in flight a warp: as many of 8, 4, 2, 1 as fit.
+static int ring_depth(int rows) {
+    int d = 8;
+    while (d > 1 && kRingWarps * d * rows * 512 > kRingBytes) d /= 2;
+    return d;
+}
+
+template <typename T, int kDepth>
+static cudaError_t unsort_ring_as(const RowArgs &a, cudaStream_t stream) {
+    const int nvec = a.H / (16 / (int)sizeof(T)), nchunk = (nvec + 31) / 32;
+    const size_t smem = (size_t)kRingWarps * kDepth * (a.k + (a.res ? 1 : 0)) * 512;
+    const auto fn = token_unsort_ring_kernel<T, kDepth>;
+    cudaError_t err = ensure_smem((const void *)fn, smem);
+    if (err != cudaSuccess) return err;
+    const int wpt = nchunk >= 4 ? 4 : nchunk >= 2 ? 2 : 1;  // warps a token
+    const int64_t ctas = ((int64_t)a.M * wpt + kRingWarps - 1) / kRingWarps;
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(ctas, ring_ctas(smem))), dim3(32 * kRingWarps), smem, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, fn, a, nvec, nchunk, wpt);
+}
+
+template <typename T, int kDepth>
+static cudaError_t unsort_grad_ring_as(const RowArgs &a, cudaStream_t stream) {
+    const int nvec = a.H / (16 / (int)sizeof(T)), nchunk = (nvec + 31) / 32;
+    const size_t smem = (size_t)kRingWarps * kDepth * (a.k + 1) * 512;
+    const auto fn = token_unsort_grad_ring_kernel<T, kDepth>;
+    cudaError_t err = ensure_smem((const void *)fn, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(a.M, ring_ctas(smem))), dim3(32 * kRingWarps), smem, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, fn, a, nvec, nchunk);
+}
+
+template <typename T>
+static cudaError_t unsort_ring(const RowArgs &a, cudaStream_t stream) {
+    switch (ring_depth(a.k + (a.res ? 1 : 0))) {
+        case 8: return unsort_ring_as<T, 8>(a, stream);
+        case 4: return unsort_ring_as<T, 4>(a, stream);
+        case 2: return unsort_ring_as<T, 2>(a, stream);
+        default: return unsort_ring_as<T, 1>(a, stream);
+    }
+}
+
+template <typename T>
+static cudaError_t unsort_grad_ring(const RowArgs &a, cudaStream_t stream) {
+    return ring_depth(a.k + 1) == 8 ? unsort_grad_ring_as<T, 8>(a, stream) : unsort_grad_ring_as<T, 4>(a, stream);
+}
+
 cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k, int H,
                               const int32_t *route_row, void *rows, int64_t ldr, cudaStream_t stream) {
     RowArgs a{};
@@ -435,16 +739,17 @@ cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k
     }
 }
 
-// Calls F<T, V>(args, stream) for the element type and the widest access.
-#define MOE_ROW_DISPATCH(F)                                                       \
-    const int elem = dtype == MOE_DT_F32 ? 4 : 2;                                 \
-    const int vb = vec_bytes(a, elem);                                            \
-    if (dtype == MOE_DT_F32) return vb == 16 ? F<float, 4>(a, stream) : F<float, 1>(a, stream); \
-    if (dtype == MOE_DT_F16)                                                      \
-        return vb == 16 ? F<__half, 8>(a, stream)                                 \
-                        : vb == 4 ? F<__half, 2>(a, stream) : F<__half, 1>(a, stream); \
-    return vb == 16 ? F<__nv_bfloat16, 8>(a, stream)                              \
-                    : vb == 4 ? F<__nv_bfloat16, 2>(a, stream) : F<__nv_bfloat16, 1>(a, stream);
+// Calls F<T, V>(args, stream) for the element type and an access of vb bytes; 16-byte rows go to
+// the ring forms where `RING` takes them.
+#define MOE_ROW_DISPATCH(F, RING, takes)                                                             \
+    const int vb = vec_bytes(a, dtype == MOE_DT_F32 ? 4 : 2);                                        \
+    if (vb == 16 && (takes)) {                                                                       \
+        if (dtype == MOE_DT_F32) return RING<float>(a, stream);                                      \
+        return dtype == MOE_DT_F16 ? RING<__half>(a, stream) : RING<__nv_bfloat16>(a, stream);       \
+    }                                                                                                \
+    if (dtype == MOE_DT_F32) return F<float, 1>(a, stream);                                          \
+    if (dtype == MOE_DT_F16) return vb >= 4 ? F<__half, 2>(a, stream) : F<__half, 1>(a, stream);     \
+    return vb >= 4 ? F<__nv_bfloat16, 2>(a, stream) : F<__nv_bfloat16, 1>(a, stream);
 
 cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
                                 const int32_t *route_row, const float *w, const void *residual,
@@ -452,7 +757,7 @@ cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M,
     RowArgs a{};
     a.a = rows, a.res = residual, a.out = out, a.lda = ldr, a.ldres = ldres, a.ldout = ldo;
     a.route_row = route_row, a.w = w, a.M = M, a.k = k, a.H = H;
-    MOE_ROW_DISPATCH(unsort_as)
+    MOE_ROW_DISPATCH(unsort_as, unsort_ring, true)
 }
 
 cudaError_t launch_token_unsort_grad(const void *gout, int64_t ldo, const void *rows, int64_t ldr,
@@ -462,7 +767,7 @@ cudaError_t launch_token_unsort_grad(const void *gout, int64_t ldo, const void *
     RowArgs a{};
     a.a = gout, a.b = rows, a.out = grows, a.out2 = gw, a.lda = ldo, a.ldb = ldr, a.ldout = ldg;
     a.route_row = route_row, a.w = w, a.M = M, a.k = k, a.H = H;
-    MOE_ROW_DISPATCH(unsort_grad_as)
+    MOE_ROW_DISPATCH(unsort_grad_as, unsort_grad_ring, k <= kRingSlots)
 }
 
 }  // namespace moe
