@@ -193,7 +193,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     return ctypes.c_void_p(int(stream))
@@ -564,23 +564,29 @@ def moe_reader_ffn(h, rd: dict, topk_ids, topk_weights, K: int, nscan: int = 80,
 
 
 # ---------------------------------------------------------- tokens sorted by expert and back
+# These calls are short (2 to 5 us of GPU time for a few tokens), so their argument checks
+# test the usual case -- right type, shape and device, contiguous -- in one expression.
 _ROW_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
 
 
-def _rows(t, name, device, dtype=None, shape=None):
-    """A matrix with contiguous columns (any row pitch); returns its row pitch in elements."""
-    if t.dim() != 2:
-        raise ValueError("%s must be a matrix" % name)
-    if dtype is None:
-        if t.dtype not in _ROW_DTYPES:
-            raise TypeError("%s must be bfloat16, float16 or float32, got %s" % (name, t.dtype))
-    elif t.dtype != dtype:
+def _raw_stream(stream, device):
+    """The stream's handle; the device's current stream when none is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _rows(t, name, device, dtype, shape):
+    """Checks a matrix with contiguous columns (any row pitch); returns its pitch in elements."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return shape[1]
+    if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    if shape is not None and tuple(t.shape) != shape:
+    if tuple(t.shape) != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    rows, cols = t.shape
+    rows, cols = shape
     sr, sc = t.stride()
     if cols > 1 and sc != 1:
         raise ValueError("%s must have contiguous columns" % name)
@@ -589,15 +595,31 @@ def _rows(t, name, device, dtype=None, shape=None):
     return sr if rows > 1 else cols
 
 
+def _row_dtype(t, name):
+    """MOE_DT_* of a matrix."""
+    code = _ROW_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16, float16 or float32, got %s" % (name, t.dtype))
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    return code
+
+
 def _vector(t, name, dtype, device, shape):
-    _need(t, dtype, name, device)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    return t
+    """Checks a contiguous tensor; returns its address."""
+    if not (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        _need(t, dtype, name, device)
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    return t.data_ptr()
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _routes(t, device):
+    """Checks route_row [M,k]; returns (address, M, k)."""
+    if t.dim() != 2:
+        raise ValueError("route_row must be a matrix")
+    M, k = t.shape
+    return _vector(t, "route_row", torch.int32, device, (M, k)), M, k
 
 
 def moe_token_plan(topk_ids, E, offsets=None, row_route=None, route_row=None, stream=None):
@@ -605,69 +627,75 @@ def moe_token_plan(topk_ids, E, offsets=None, row_route=None, route_row=None, st
     dev = topk_ids.device
     _need(topk_ids, torch.int32, "topk_ids", dev)
     M, k = topk_ids.shape
+    i32 = torch.int32
     if offsets is None:
-        offsets = torch.empty((E + 1,), dtype=torch.int32, device=dev)
+        offsets = torch.empty(E + 1, dtype=i32, device=dev)
     if row_route is None:
-        row_route = torch.empty((M * k,), dtype=torch.int32, device=dev)
+        row_route = torch.empty(M * k, dtype=i32, device=dev)
     if route_row is None:
-        route_row = torch.empty((M, k), dtype=torch.int32, device=dev)
-    _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
-    _vector(row_route, "row_route", torch.int32, dev, (M * k,))
-    _vector(route_row, "route_row", torch.int32, dev, (M, k))
-    _check(lib().moe_token_plan(topk_ids.data_ptr(), M, k, E, offsets.data_ptr(),
-                                row_route.data_ptr(), route_row.data_ptr(), _stream(stream)),
-           "moe_token_plan")
+        route_row = torch.empty((M, k), dtype=i32, device=dev)
+    rc = lib().moe_token_plan(topk_ids.data_ptr(), M, k, E,
+                              _vector(offsets, "offsets", i32, dev, (E + 1,)),
+                              _vector(row_route, "row_route", i32, dev, (M * k,)),
+                              _vector(route_row, "route_row", i32, dev, (M, k)),
+                              _raw_stream(stream, dev))
+    _check(rc, "moe_token_plan")
     return offsets, row_route, route_row
 
 
 def moe_token_sort(x, route_row, rows=None, stream=None):
     """The token rows x [M,H] in sorted order: rows [M*k,H]."""
-    dev = x.device
-    _need(route_row, torch.int32, "route_row", dev)
-    M, k = route_row.shape
+    dev, dt = x.device, x.dtype
+    code = _row_dtype(x, "x")
+    rr, M, k = _routes(route_row, dev)
     H = x.shape[1]
-    ldx = _rows(x, "x", dev, shape=(M, H))
+    ldx = _rows(x, "x", dev, dt, (M, H))
     if rows is None:
-        rows = torch.empty((M * k, H), dtype=x.dtype, device=dev)
-    ldr = _rows(rows, "rows", dev, x.dtype, (M * k, H))
-    _check(lib().moe_token_sort(x.data_ptr(), ldx, _ROW_DTYPES[x.dtype], M, k, H,
-                                route_row.data_ptr(), rows.data_ptr(), ldr, _stream(stream)),
-           "moe_token_sort")
+        rows, ldr = torch.empty((M * k, H), dtype=dt, device=dev), H
+    else:
+        ldr = _rows(rows, "rows", dev, dt, (M * k, H))
+    _check(lib().moe_token_sort(x.data_ptr(), ldx, code, M, k, H, rr, rows.data_ptr(), ldr,
+                                _raw_stream(stream, dev)), "moe_token_sort")
     return rows
 
 
 def moe_token_sort_grad(grad_rows, route_row, grad_x=None, stream=None):
     """Gradient of moe_token_sort: grad_x [M,H] of grad_rows [M*k,H]."""
-    dev = grad_rows.device
-    _need(route_row, torch.int32, "route_row", dev)
-    M, k = route_row.shape
+    dev, dt = grad_rows.device, grad_rows.dtype
+    code = _row_dtype(grad_rows, "grad_rows")
+    rr, M, k = _routes(route_row, dev)
     H = grad_rows.shape[1]
-    ldr = _rows(grad_rows, "grad_rows", dev, shape=(M * k, H))
+    ldr = _rows(grad_rows, "grad_rows", dev, dt, (M * k, H))
     if grad_x is None:
-        grad_x = torch.empty((M, H), dtype=grad_rows.dtype, device=dev)
-    ldx = _rows(grad_x, "grad_x", dev, grad_rows.dtype, (M, H))
-    _check(lib().moe_token_sort_grad(grad_rows.data_ptr(), ldr, _ROW_DTYPES[grad_rows.dtype], M, k,
-                                     H, route_row.data_ptr(), grad_x.data_ptr(), ldx,
-                                     _stream(stream)), "moe_token_sort_grad")
+        grad_x, ldx = torch.empty((M, H), dtype=dt, device=dev), H
+    else:
+        ldx = _rows(grad_x, "grad_x", dev, dt, (M, H))
+    _check(lib().moe_token_sort_grad(grad_rows.data_ptr(), ldr, code, M, k, H, rr,
+                                     grad_x.data_ptr(), ldx, _raw_stream(stream, dev)),
+           "moe_token_sort_grad")
     return grad_x
 
 
 def moe_token_unsort(rows, route_row, topk_weights=None, residual=None, out=None, stream=None):
     """out [M,H] = residual + the weighted sum of each token's rows (include/moe.h)."""
-    dev = rows.device
-    _need(route_row, torch.int32, "route_row", dev)
-    M, k = route_row.shape
+    dev, dt = rows.device, rows.dtype
+    code = _row_dtype(rows, "rows")
+    rr, M, k = _routes(route_row, dev)
     H = rows.shape[1]
-    ldr = _rows(rows, "rows", dev, shape=(M * k, H))
+    ldr = _rows(rows, "rows", dev, dt, (M * k, H))
+    w = res = None
+    ldres = 0
     if topk_weights is not None:
-        _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
-    ldres = 0 if residual is None else _rows(residual, "residual", dev, rows.dtype, (M, H))
+        w = _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
+    if residual is not None:
+        ldres = _rows(residual, "residual", dev, dt, (M, H))
+        res = residual.data_ptr()
     if out is None:
-        out = torch.empty((M, H), dtype=rows.dtype, device=dev)
-    ldo = _rows(out, "out", dev, rows.dtype, (M, H))
-    _check(lib().moe_token_unsort(rows.data_ptr(), ldr, _ROW_DTYPES[rows.dtype], M, k, H,
-                                  route_row.data_ptr(), _addr(topk_weights), _addr(residual),
-                                  ldres, out.data_ptr(), ldo, _stream(stream)),
+        out, ldo = torch.empty((M, H), dtype=dt, device=dev), H
+    else:
+        ldo = _rows(out, "out", dev, dt, (M, H))
+    _check(lib().moe_token_unsort(rows.data_ptr(), ldr, code, M, k, H, rr, w, res, ldres,
+                                  out.data_ptr(), ldo, _raw_stream(stream, dev)),
            "moe_token_unsort")
     return out
 
@@ -675,25 +703,25 @@ def moe_token_unsort(rows, route_row, topk_weights=None, residual=None, out=None
 def moe_token_unsort_grad(grad_out, rows, route_row, topk_weights=None, grad_rows=None,
                           grad_weights=None, stream=None):
     """Gradients of moe_token_unsort: (grad_rows [M*k,H], grad_weights [M,k] fp32)."""
-    dev = rows.device
-    _need(route_row, torch.int32, "route_row", dev)
-    M, k = route_row.shape
+    dev, dt = rows.device, rows.dtype
+    code = _row_dtype(rows, "rows")
+    rr, M, k = _routes(route_row, dev)
     H = rows.shape[1]
-    ldr = _rows(rows, "rows", dev, shape=(M * k, H))
-    ldo = _rows(grad_out, "grad_out", dev, rows.dtype, (M, H))
+    ldr = _rows(rows, "rows", dev, dt, (M * k, H))
+    ldo = _rows(grad_out, "grad_out", dev, dt, (M, H))
+    w = None
     if topk_weights is not None:
-        _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
+        w = _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
     if grad_rows is None:
-        grad_rows = torch.empty((M * k, H), dtype=rows.dtype, device=dev)
+        grad_rows, ldg = torch.empty((M * k, H), dtype=dt, device=dev), H
+    else:
+        ldg = _rows(grad_rows, "grad_rows", dev, dt, (M * k, H))
     if grad_weights is None:
         grad_weights = torch.empty((M, k), dtype=torch.float32, device=dev)
-    ldg = _rows(grad_rows, "grad_rows", dev, rows.dtype, (M * k, H))
-    _vector(grad_weights, "grad_weights", torch.float32, dev, (M, k))
-    _check(lib().moe_token_unsort_grad(grad_out.data_ptr(), ldo, rows.data_ptr(), ldr,
-                                       _ROW_DTYPES[rows.dtype], M, k, H, route_row.data_ptr(),
-                                       _addr(topk_weights), grad_rows.data_ptr(), ldg,
-                                       grad_weights.data_ptr(), _stream(stream)),
-           "moe_token_unsort_grad")
+    gw = _vector(grad_weights, "grad_weights", torch.float32, dev, (M, k))
+    _check(lib().moe_token_unsort_grad(grad_out.data_ptr(), ldo, rows.data_ptr(), ldr, code, M, k,
+                                       H, rr, w, grad_rows.data_ptr(), ldg, gw,
+                                       _raw_stream(stream, dev)), "moe_token_unsort_grad")
     return grad_rows, grad_weights
 
 
@@ -702,36 +730,54 @@ def moe_microscale_pitch(cols) -> int:
     return int(lib().moe_microscale_pitch(cols))
 
 
+def _pitch(cols):
+    return -(-cols // 512) * 16
+
+
 def _microscaled(codes, scales, device, name):
     """Checks a pair of codes [..., cols/2] and scales [..., pitch]; returns cols."""
-    _need(codes, torch.uint8, name + "_codes", device)
-    _need(scales, torch.uint8, name + "_scales", device)
-    cols = 2 * codes.shape[-1]
-    want = tuple(codes.shape[:-1]) + (-(-cols // 512) * 16,)
-    if tuple(scales.shape) != want:
-        raise ValueError("%s_scales must have shape %s, got %s" % (name, want, tuple(scales.shape)))
+    u8 = torch.uint8
+    cs = codes.shape
+    cols = 2 * cs[-1]
+    ss = cs[:-1] + (_pitch(cols),)
+    if not (codes.dtype is u8 and scales.dtype is u8 and codes.device == device
+            and scales.device == device and codes.is_contiguous() and scales.is_contiguous()
+            and scales.shape == ss):
+        _need(codes, u8, name + "_codes", device)
+        _need(scales, u8, name + "_scales", device)
+        raise ValueError("%s_scales must have shape %s, got %s" % (name, tuple(ss), tuple(scales.shape)))
     return cols
+
+
+def _quantised_outputs(codes, scales, rows, cols, dev):
+    """Codes and scales of a [rows, cols] result, allocated where the caller gave none."""
+    if codes is None:
+        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty((rows, _pitch(cols)), dtype=torch.uint8, device=dev)
+    if codes.shape != (rows, cols // 2):
+        raise ValueError("codes must have shape %s, got %s" % ((rows, cols // 2), tuple(codes.shape)))
+    _microscaled(codes, scales, dev, "out")
+    return codes, scales
 
 
 def moe_microscale_quantize(x, route_row=None, codes=None, scales=None, stream=None):
     """x [rows,cols] as 4-bit codes and scales; with route_row [rows,k] (a token plan's) in
     sorted order, rows * k of them."""
     dev = x.device
+    code = _row_dtype(x, "x")
     rows, cols = x.shape
-    ldx = _rows(x, "x", dev)
-    k = 1
+    ldx = _rows(x, "x", dev, x.dtype, (rows, cols))
+    if cols % 32:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_quantize")
+    rr, k = None, 1
     if route_row is not None:
         k = route_row.shape[1]
-        _vector(route_row, "route_row", torch.int32, dev, (rows, k))
-    if codes is None:
-        codes = torch.empty((rows * k, cols // 2), dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty((rows * k, -(-cols // 512) * 16), dtype=torch.uint8, device=dev)
-    if _microscaled(codes, scales, dev, "x") != cols or codes.shape[0] != rows * k:
-        raise ValueError("codes must have shape %s" % ((rows * k, cols // 2),))
-    _check(lib().moe_microscale_quantize(x.data_ptr(), ldx, _ROW_DTYPES[x.dtype], rows, cols,
-                                         _addr(route_row), k, codes.data_ptr(), scales.data_ptr(),
-                                         _stream(stream)), "moe_microscale_quantize")
+        rr = _vector(route_row, "route_row", torch.int32, dev, (rows, k))
+    codes, scales = _quantised_outputs(codes, scales, rows * k, cols, dev)
+    _check(lib().moe_microscale_quantize(x.data_ptr(), ldx, code, rows, cols, rr, k,
+                                         codes.data_ptr(), scales.data_ptr(),
+                                         _raw_stream(stream, dev)), "moe_microscale_quantize")
     return codes, scales
 
 
@@ -742,45 +788,46 @@ def moe_microscale_dequantize(codes, scales, dtype=torch.bfloat16, out=None, str
     rows = codes.shape[0]
     if out is None:
         out = torch.empty((rows, cols), dtype=dtype, device=dev)
-    ldx = _rows(out, "out", dev, shape=(rows, cols))
+    code = _row_dtype(out, "out")
+    ldx = _rows(out, "out", dev, out.dtype, (rows, cols))
     _check(lib().moe_microscale_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols,
-                                           out.data_ptr(), ldx, _ROW_DTYPES[out.dtype],
-                                           _stream(stream)), "moe_microscale_dequantize")
+                                           out.data_ptr(), ldx, code, _raw_stream(stream, dev)),
+           "moe_microscale_dequantize")
     return out
 
 
 def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
-    """Checks of the grouped products; returns (rows, E, N, K, workspace)."""
+    """Checks of the grouped products; returns (rows, E, N, K, offsets' address, workspace)."""
     dev = x_codes.device
     K = _microscaled(x_codes, x_scales, dev, "x")
     if _microscaled(w_codes, w_scales, dev, "w") != K:
         raise ValueError("x and w must have the same number of columns")
-    if w_codes.dim() == 2:
-        E, N = 1, w_codes.shape[0]
-    else:
-        E, N = w_codes.shape[:2]
+    ws = w_codes.shape
+    E, N = (1, ws[0]) if len(ws) == 2 else (ws[0], ws[1])
+    off = None
     if offsets is not None:
-        _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
+        off = _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     if workspace is None:
-        workspace = torch.zeros((MOE_MICROSCALE_STATUS_BYTES,), dtype=torch.uint8, device=dev)
-    return x_codes.shape[0], E, N, K, workspace
+        workspace = torch.zeros(MOE_MICROSCALE_STATUS_BYTES, dtype=torch.uint8, device=dev)
+    return x_codes.shape[0], E, N, K, off, workspace
 
 
 def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
                            dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """y [rows,N] of 4-bit rows and 4-bit weights [E,N,K] (or [N,K]), rows grouped by offsets
     [E+1]; rows past the last group are zero."""
-    rows, E, N, K, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
-                                             workspace)
+    rows, E, N, K, off, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
+                                                  workspace)
     dev = x_codes.device
     if out is None:
         out = torch.empty((rows, N), dtype=dtype, device=dev)
-    ldy = _rows(out, "out", dev, shape=(rows, N))
-    _check(lib().moe_microscale_product(x_codes.data_ptr(), x_scales.data_ptr(), rows,
-                                        _addr(offsets), w_codes.data_ptr(), w_scales.data_ptr(), E,
-                                        N, K, _ROW_DTYPES[out.dtype], out.data_ptr(), ldy,
-                                        workspace.data_ptr(), workspace.numel(),
-                                        _stream(stream)), "moe_microscale_product")
+    code = _row_dtype(out, "out")
+    ldy = _rows(out, "out", dev, out.dtype, (rows, N))
+    _check(lib().moe_microscale_product(x_codes.data_ptr(), x_scales.data_ptr(), rows, off,
+                                        w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, code,
+                                        out.data_ptr(), ldy, workspace.data_ptr(),
+                                        workspace.numel(), _raw_stream(stream, dev)),
+           "moe_microscale_product")
     return out
 
 
@@ -788,22 +835,17 @@ def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=N
                                  scales=None, workspace=None, stream=None):
     """SiLU(g) * u of the gate and up halves of w [E,N,K], quantised: (codes, scales) of
     [rows,N/2]."""
-    rows, E, N, K, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
-                                             workspace)
+    rows, E, N, K, off, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
+                                                  workspace)
+    if N % 64:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_gated_product")
     dev = x_codes.device
-    I = N // 2
-    if codes is None:
-        codes = torch.empty((rows, I // 2), dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty((rows, -(-I // 512) * 16), dtype=torch.uint8, device=dev)
-    if tuple(codes.shape) != (rows, I // 2):
-        raise ValueError("codes must have shape %s" % ((rows, I // 2),))
-    _microscaled(codes, scales, dev, "p")
-    _check(lib().moe_microscale_gated_product(x_codes.data_ptr(), x_scales.data_ptr(), rows,
-                                              _addr(offsets), w_codes.data_ptr(),
-                                              w_scales.data_ptr(), E, N, K, codes.data_ptr(),
-                                              scales.data_ptr(), workspace.data_ptr(),
-                                              workspace.numel(), _stream(stream)),
+    codes, scales = _quantised_outputs(codes, scales, rows, N // 2, dev)
+    _check(lib().moe_microscale_gated_product(x_codes.data_ptr(), x_scales.data_ptr(), rows, off,
+                                              w_codes.data_ptr(), w_scales.data_ptr(), E, N, K,
+                                              codes.data_ptr(), scales.data_ptr(),
+                                              workspace.data_ptr(), workspace.numel(),
+                                              _raw_stream(stream, dev)),
            "moe_microscale_gated_product")
     return codes, scales
 
@@ -812,16 +854,15 @@ def microscale_weights(layer: dict) -> MicroscaleWeights:
     """C descriptor of a layer's 4-bit weights: H, I, E and gate_up_codes [E,2I,H/2],
     gate_up_scales, down_codes [E,H,I/2], down_scales (the caller keeps the tensors alive)."""
     H, I, E = layer["H"], layer["I"], layer["E"]
-    dev = layer["down_codes"].device
-    w = MicroscaleWeights()
-    w.H, w.I, w.E = H, I, E
-    for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
-        c, s = layer[name + "_codes"], layer[name + "_scales"]
-        if _microscaled(c, s, dev, name) != cols or tuple(c.shape[:-1]) != (E, n):
-            raise ValueError("%s_codes must have shape %s" % (name, (E, n, cols // 2)))
-        setattr(w, name + "_codes", c.data_ptr())
-        setattr(w, name + "_scales", s.data_ptr())
-    return w
+    gc, gs, dc, ds = (layer["gate_up_codes"], layer["gate_up_scales"], layer["down_codes"],
+                      layer["down_scales"])
+    dev = dc.device
+    if gc.shape != (E, 2 * I, H // 2) or _microscaled(gc, gs, dev, "gate_up") != H:
+        raise ValueError("gate_up_codes must have shape %s" % ((E, 2 * I, H // 2),))
+    if dc.shape != (E, H, I // 2) or _microscaled(dc, ds, dev, "down") != I:
+        raise ValueError("down_codes must have shape %s" % ((E, H, I // 2),))
+    return MicroscaleWeights(H, I, E, 0, gc.data_ptr(), gs.data_ptr(), dc.data_ptr(),
+                             ds.data_ptr())
 
 
 def microscale_layer(layer: dict, stream=None) -> dict:
@@ -834,8 +875,7 @@ def microscale_layer(layer: dict, stream=None) -> dict:
     out = {"H": H, "I": I, "E": E}
     for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
         out[name + "_codes"] = torch.empty((E, n, cols // 2), dtype=torch.uint8, device=dev)
-        out[name + "_scales"] = torch.empty((E, n, -(-cols // 512) * 16), dtype=torch.uint8,
-                                            device=dev)
+        out[name + "_scales"] = torch.empty((E, n, _pitch(cols)), dtype=torch.uint8, device=dev)
     for e in range(E):
         for name, w, at in (("gate_up", layer["w_gate"][e], 0), ("gate_up", layer["w_up"][e], I),
                             ("down", layer["w_down"][e], 0)):
@@ -864,20 +904,19 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
     takes it."""
     dev = h.device
     w = microscale_weights(layer)
-    _need(h, torch.bfloat16, "h", dev)
     M, k = topk_ids.shape
-    _vector(h, "h", torch.bfloat16, dev, (M, w.H))
-    _need(topk_ids, torch.int32, "topk_ids", dev)
-    _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
-    if residual is not None:
-        _vector(residual, "residual", torch.bfloat16, dev, (M, w.H))
+    H = w.H
+    bf16 = torch.bfloat16
+    ph = _vector(h, "h", bf16, dev, (M, H))
+    ids = _vector(topk_ids, "topk_ids", torch.int32, dev, (M, k))
+    pw = _vector(topk_weights, "topk_weights", torch.float32, dev, (M, k))
+    res = None if residual is None else _vector(residual, "residual", bf16, dev, (M, H))
     if out is None:
-        out = torch.empty((M, w.H), dtype=torch.bfloat16, device=dev)
-    _vector(out, "out", torch.bfloat16, dev, (M, w.H))
+        out = torch.empty((M, H), dtype=bf16, device=dev)
+    po = _vector(out, "out", bf16, dev, (M, H))
     if workspace is None:
         workspace = microscale_workspace(layer, M, k)
-    _check(lib().moe_microscale_ffn(h.data_ptr(), ctypes.byref(w), M, k, topk_ids.data_ptr(),
-                                    topk_weights.data_ptr(), _addr(residual), out.data_ptr(),
-                                    workspace.data_ptr(), workspace.numel(), _stream(stream)),
-           "moe_microscale_ffn")
+    _check(lib().moe_microscale_ffn(ph, ctypes.byref(w), M, k, ids, pw, res, po,
+                                    workspace.data_ptr(), workspace.numel(),
+                                    _raw_stream(stream, dev)), "moe_microscale_ffn")
     return out
