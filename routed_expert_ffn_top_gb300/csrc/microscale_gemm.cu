@@ -29,7 +29,7 @@
 
 namespace moe {
 
-constexpr int kMxThreads = 320;
+constexpr int kMxThreads = 384;
 constexpr int kMxMaxStages = 8;
 constexpr int kMxMaxScaleBufs = 4;
 constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
@@ -202,9 +202,39 @@ __device__ __forceinline__ void store_row32(const MxArgs &a, int64_t row, int n,
 // g = -87 it gives 0 for values under 2^-119.
 __device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + expf(-g)); }
 
-struct MxUnit {
-    int e, ct, nrows;
-    int64_t row0;
+// A CTA's units: u = blockIdx.x, blockIdx.x + gridDim.x, ...; unit u is channel tile u % nct of
+// row tile u / nct.  Each role walks them without dividing: the steps are constant and the
+// expert only moves forward.
+template <int kM>
+struct MxWalk {
+    int t, ct, e;          // row tile, channel tile, expert
+    int dt, dct;           // a step
+    int nrows;             // of this row tile
+    int row0;
+
+    __device__ __forceinline__ void place(const MxCtl &ctl) {
+        while (ctl.first[e + 1] <= t) ++e;
+        row0 = ctl.begin[e] + (t - ctl.first[e]) * kM;
+        const int left = ctl.begin[e + 1] - row0;
+        nrows = left < kM ? left : kM;
+    }
+    __device__ __forceinline__ MxWalk(const MxArgs &a, const MxCtl &ctl, int tiles) {
+        t = blockIdx.x / a.nct, ct = blockIdx.x % a.nct, e = 0;
+        dt = gridDim.x / a.nct, dct = gridDim.x % a.nct;
+        if (t >= tiles) return;
+        int hi = a.E;  // the last e with first[e] <= t
+        while (hi - e > 1) {
+            const int mid = (e + hi) >> 1;
+            if (ctl.first[mid] <= t) e = mid;
+            else hi = mid;
+        }
+        place(ctl);
+    }
+    __device__ __forceinline__ void next(const MxArgs &a, const MxCtl &ctl, int tiles) {
+        t += dt, ct += dct;
+        if (ct >= a.nct) ct -= a.nct, ++t;
+        if (t < tiles) place(ctl);
+    }
 };
 
 // The scale words of stage `part` of a copy for one row: word q of 128 of K to w[q * kStep].
@@ -227,24 +257,6 @@ __device__ __forceinline__ void mx_scale_words(const unsigned char *base, int ro
     }
 }
 
-template <int kM>
-__device__ __forceinline__ MxUnit mx_unit(const MxArgs &a, const MxCtl &ctl, int64_t u) {
-    const int t = (int)(u / a.nct);
-    int lo = 0, hi = a.E;  // the last e with first[e] <= t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (ctl.first[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    MxUnit x;
-    x.e = lo;
-    x.ct = (int)(u - (int64_t)t * a.nct);
-    x.row0 = (int64_t)ctl.begin[lo] + (int64_t)(t - ctl.first[lo]) * kM;
-    const int64_t left = (int64_t)ctl.begin[lo + 1] - x.row0;
-    x.nrows = left < kM ? (int)left : kM;
-    return x;
-}
-
 // kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
 template <int kM, int kN, int kOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
@@ -263,7 +275,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
-            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.full[s], 2);  // the two code producers
             mbar_init(&ctl.empty[s], 1);
             mbar_init(&ctl.sfull[s], 4);
         }
@@ -317,6 +329,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             ctl.first[e] = off + inc - tiles;
             ctl.begin[e] = (int)lo;
             if (e == a.E - 1) {
+                ctl.first[a.E] = off + inc;
                 ctl.begin[a.E] = (int)hi;
                 ctl.valid_rows = (int)hi;
             }
@@ -327,66 +340,65 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int64_t T = (int64_t)carry * a.nct;
+    const int tiles = carry;
     const int nks = (a.K + G::kStageK - 1) / G::kStageK;  // stages per unit
     constexpr int kPerScale = kMxScaleK / G::kStageK;         // stages per copy of scales
 
-    if (warp == 8) {
+    if (warp == 8 || warp >= 10) {
+        // three producers, one thread each: weight codes, row codes, scales (a copy takes its
+        // thread 100 to 200 cycles to issue, and a small unit has few MMAs to hide them)
         if (lane == 0) {
             const uint64_t pol = policy_evict_normal();
-            int stage = 0, buf = 0;
+            uint64_t *const full = warp == 11 ? ctl.cfull : ctl.full, *const empty = warp == 11 ? ctl.cempty : ctl.empty;
+            const int ring = warp == 11 ? G::kScaleBufs : G::kStages;
+            const int steps = warp == 11 ? (nks + kPerScale - 1) / kPerScale : nks;
+            int slot = 0;
             uint32_t phase = 0, issued = 0, par = 0;
-            uint32_t cphase = 0, cissued = 0, cpar = 0;
-            for (int64_t u = blockIdx.x; u < T && !ctl.abort; u += gridDim.x) {
-                const MxUnit x = mx_unit<kM>(a, ctl, u);
+            for (MxWalk<kM> x(a, ctl, tiles); x.t < tiles && !ctl.abort; x.next(a, ctl, tiles)) {
                 // first weight row of the N side; a gated tile's box also takes the up rows beside it
                 const int b0 = x.e * a.N + x.ct * (kGated ? kHalf : kN);
-                for (int s = 0; s < nks; ++s) {
-                    if (s % kPerScale == 0) {
-                        if (!mx_wait(&ctl.cempty[buf], cphase ^ 1u, ctl)) break;
-                        uint64_t *bar = &ctl.cfull[buf];
-                        unsigned char *SA = scales + buf * G::kScaleBytes, *SB = SA + kM * 64;
+                for (int s = 0; s < steps; ++s) {
+                    if (!mx_wait(&empty[slot], phase ^ 1u, ctl)) break;
+                    uint64_t *bar = &full[slot];
+                    if (warp == 11) {
+                        unsigned char *SA = scales + slot * G::kScaleBytes;
                         mbar_arrive_expect_tx(bar, G::kScaleBytes);
-                        const int xs = s / kPerScale * 64;
-                        tma_load_3d(SB, &tm_sb, xs, b0, 0, bar, pol);
-                        tma_load_2d(SA, &tm_sa, xs, (int)x.row0, bar, pol);
-                        cissued |= 1u << buf;
-                        cpar = (cpar & ~(1u << buf)) | (cphase << buf);
-                        if (++buf == G::kScaleBufs) buf = 0, cphase ^= 1u;
+                        tma_load_3d(SA + kM * 64, &tm_sb, s * 64, b0, 0, bar, pol);
+                        tma_load_2d(SA, &tm_sa, s * 64, x.row0, bar, pol);
+                    } else {
+                        // one copy brings the whole stage, or one per chunk (past K: none)
+                        unsigned char *A = stages + slot * G::kStageBytes;
+                        const int left = (a.K - s * G::kStageK + 255) / 256;
+                        const int copies = a.deep ? 1 : (left < G::kChunks ? left : G::kChunks);
+                        const int chunk = warp == 8 ? G::kBChunk : G::kAChunk;
+                        mbar_arrive_expect_tx(bar, (a.deep ? G::kChunks : copies) * chunk);
+                        for (int c = 0; c < copies; ++c) {
+                            const int cx = a.deep ? 0 : (s * G::kChunks + c) * 128, cz = a.deep ? s * G::kChunks : 0;
+                            if (warp == 8) tma_load_4d(A + G::kABytes + c * G::kBChunk, &tm_b, cx, b0, 0, cz, bar, pol);
+                            else tma_load_3d(A + c * G::kAChunk, &tm_a, cx, x.row0, cz, bar, pol);
+                        }
                     }
-                    if (!mx_wait(&ctl.empty[stage], phase ^ 1u, ctl)) break;
-                    uint64_t *bar = &ctl.full[stage];
-                    unsigned char *A = stages + stage * G::kStageBytes, *B = A + G::kABytes;
-                    // one copy brings the whole stage, or one per chunk (past K: none)
-                    const int left = (a.K - s * G::kStageK + 255) / 256;
-                    const int copies = a.deep ? 1 : (left < G::kChunks ? left : G::kChunks);
-                    mbar_arrive_expect_tx(bar, a.deep ? G::kStageBytes : copies * (G::kAChunk + G::kBChunk));
-                    for (int c = 0; c < copies; ++c) {
-                        const int cx = a.deep ? 0 : (s * G::kChunks + c) * 128, cz = a.deep ? s * G::kChunks : 0;
-                        tma_load_4d(B + c * G::kBChunk, &tm_b, cx, b0, 0, cz, bar, pol);
-                        tma_load_3d(A + c * G::kAChunk, &tm_a, cx, (int)x.row0, cz, bar, pol);
-                    }
-                    issued |= 1u << stage;
-                    par = (par & ~(1u << stage)) | (phase << stage);
-                    if (++stage == G::kStages) stage = 0, phase ^= 1u;
+                    issued |= 1u << slot;
+                    par = (par & ~(1u << slot)) | (phase << slot);
+                    if (++slot == ring) slot = 0, phase ^= 1u;
                 }
             }
             // every copy has landed before the CTA can exit
-            for (int s = 0; s < G::kStages; ++s)
+            for (int s = 0; s < ring; ++s)
                 if ((issued >> s) & 1u)
-                    if (!mbar_wait_bounded(&ctl.full[s], (par >> s) & 1u)) ctl.abort = 1;
-            for (int b = 0; b < G::kScaleBufs; ++b)
-                if ((cissued >> b) & 1u)
-                    if (!mbar_wait_bounded(&ctl.cfull[b], (cpar >> b) & 1u)) ctl.abort = 1;
+                    if (!mbar_wait_bounded(&full[s], (par >> s) & 1u)) ctl.abort = 1;
         }
         __syncwarp();
     } else if (warp == 9) {
         if (lane == 0) {
-            int stage = 0, local = 0;
-            uint32_t phase = 0;
-            for (int64_t u = blockIdx.x; u < T && !ctl.abort; u += gridDim.x, ++local) {
-                const int buf = local & 1;
-                if (!mx_wait(&ctl.tempty[buf], ((local >> 1) & 1) ^ 1u, ctl)) break;
+            // K-major, 128-byte swizzle: 32 bytes per K step, 8-row atoms 1 KB apart.  A step
+            // only moves the address field of the descriptors (16-byte units).
+            const uint64_t a0 = umma_smem_desc(smem_u32(stages), 16, 1024, 2);
+            const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, 16, 1024, 2);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, tphase = 1;
+            for (int t = blockIdx.x / a.nct, ct = blockIdx.x % a.nct; t < tiles && !ctl.abort;) {
+                if (!mx_wait(&ctl.tempty[buf], tphase, ctl)) break;
                 const uint32_t d = ctl.tmem + (uint32_t)(buf * kN);
                 bool ok = true;
                 for (int s = 0; s < nks; ++s) {
@@ -395,24 +407,31 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t A = smem_u32(stages + stage * G::kStageBytes);
-                    const uint32_t B = A + G::kABytes;
+                    const uint64_t ad = a0 + (uint32_t)(stage * (G::kStageBytes >> 4));
+                    const uint64_t bd = b0 + (uint32_t)(stage * (G::kStageBytes >> 4));
                     const uint32_t sf = ctl.tmem + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
+                    auto step = [&](int ks) {
+                        umma_mxf4(d, ad + (ks >> 2) * (G::kAChunk >> 4) + (ks & 3) * 2,
+                                  bd + (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2, mx_idesc(kN, (ks & 1) ? 2u : 0u),
+                                  sf + (ks >> 1) * G::kACols, sf + G::kGroups * G::kACols + (ks >> 1) * G::kBPad,
+                                  s > 0 || ks > 0);
+                    };
+                    const int left = (a.K - s * G::kStageK + 63) / 64;  // K steps of this stage
+                    if (left >= G::kStageK / 64) {
 #pragma unroll
-                    for (int ks = 0; ks < G::kStageK / 64; ++ks) {
-                        if (s * G::kStageK + ks * 64 >= a.K) break;
-                        // K-major, 128-byte swizzle: 32 bytes per K step, 8-row atoms 1 KB apart
-                        const uint64_t ad = umma_smem_desc(A + (ks >> 2) * G::kAChunk + (ks & 3) * 32, 16, 1024, 2);
-                        const uint64_t bd = umma_smem_desc(B + (ks >> 2) * G::kBChunk + (ks & 3) * 32, 16, 1024, 2);
-                        const uint32_t sfa = sf + (uint32_t)((ks >> 1) * G::kACols);
-                        const uint32_t sfb = sf + (uint32_t)(G::kGroups * G::kACols + (ks >> 1) * G::kBPad);
-                        umma_mxf4(d, ad, bd, mx_idesc(kN, (ks & 1) ? 2u : 0u), sfa, sfb, s > 0 || ks > 0);
+                        for (int ks = 0; ks < G::kStageK / 64; ++ks) step(ks);
+                    } else {
+                        for (int ks = 0; ks < left; ++ks) step(ks);
                     }
                     umma_commit(&ctl.empty[stage]);
                     if (++stage == G::kStages) stage = 0, phase ^= 1u;
                 }
                 if (!ok) break;
                 umma_commit(&ctl.tfull[buf]);
+                if (buf) tphase ^= 1u;
+                buf ^= 1;
+                t += gridDim.x / a.nct, ct += gridDim.x % a.nct;
+                if (ct >= a.nct) ct -= a.nct, ++t;
             }
             // every issued MMA has completed before the CTA frees its tensor memory
             umma_commit(&ctl.done);
@@ -425,7 +444,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         int stage = 0, buf = 0;
         uint32_t phase = 0, cphase = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < T && ok; u += gridDim.x)
+        for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.nct && ok; u += gridDim.x)
             for (int s = 0; s < nks; ++s) {
                 const int part = s % kPerScale;
                 if (part == 0 && !(ok = mx_wait(&ctl.cfull[buf], cphase, ctl))) break;
@@ -464,12 +483,11 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     } else {
         const uint32_t quad = (uint32_t)(32 * warp) << 16;
         int local = 0;
-        for (int64_t u = blockIdx.x; u < T; u += gridDim.x, ++local) {
-            const MxUnit x = mx_unit<kM>(a, ctl, u);
+        for (MxWalk<kM> x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles), ++local) {
             const int buf = local & 1;
             if (!mx_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
             tc_fence_after();
-            const int64_t row = x.row0 + 32 * warp + lane;
+            const int64_t row = (int64_t)x.row0 + 32 * warp + lane;
             const bool live = 32 * warp + lane < x.nrows;
             const uint32_t d = ctl.tmem + quad + (uint32_t)(buf * kN);
             if (32 * warp >= x.nrows) {
@@ -478,11 +496,15 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                 using T_ = typename std::conditional<kOut == 0, __nv_bfloat16,
                                                      typename std::conditional<kOut == 1, __half, float>::type>::type;
 #pragma unroll 1
-                for (int c = 0; c < kN; c += 32) {
-                    uint32_t v[32];
+                for (int c = 0; c < kN; c += 64) {
+                    uint32_t v[32], w[32];
                     tmem_ld32(d + c, v);
+                    tmem_ld32(d + c + 32, w);
                     tmem_ld_wait(v);
-                    if (live && x.ct * kN + c < a.N) store_row32<T_>(a, row, x.ct * kN + c, v);
+                    tmem_ld_wait(w);
+                    const int n = x.ct * kN + c;
+                    if (live && n < a.N) store_row32<T_>(a, row, n, v);
+                    if (live && n + 32 < a.N) store_row32<T_>(a, row, n + 32, w);
                 }
             } else {
                 const int I = a.N / 2;
@@ -546,7 +568,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
 
 // ----------------------------------------------------------------------------------- launcher
 MicroscaleTile microscale_tile(int64_t rows, int E) {
-    return rows >= 32 * (int64_t)E ? MicroscaleTile{128, 192, 1} : MicroscaleTile{32, rows > E / 4 ? 128 : 64, 2};
+    return rows >= 32 * (int64_t)E ? MicroscaleTile{128, 192, 1} : MicroscaleTile{32, 128, 2};
 }
 
 template <int kM, int kN, int kOut>
