@@ -158,19 +158,21 @@ static int check_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_
 }
 
 // The gated form's weights are seen as [chunk][gate/up][row]: one box takes a run of gate rows
-// and the up rows beside it.  Without whole chunks the chunk dimension has one entry, and a
-// row's bytes past its end read as zeros.
+// and the up rows beside it.  When K is not a whole number of stages the chunk dimension has
+// one entry, a copy brings one chunk, and a row's bytes past its end read as zeros (a stage's
+// box would zero-fill whole chunks past K, which costs as much as copying them).
 static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
                          const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K, bool gated) {
     const MicroscaleTile t = microscale_tile(rows, E);
     const uint64_t row = (uint64_t)K / 2, pitch = (uint64_t)microscale_pitch(K);
-    const uint64_t inner = K % 256 == 0 ? 128 : row, chunks = K % 256 == 0 ? K / 256 : 1;
-    const uint32_t depth = K % 256 == 0 ? t.chunks : 1;
+    const bool deep = K % (256 * t.chunks) == 0;
+    const uint64_t inner = deep ? 128 : row, chunks = deep ? K / 256 : 1;
+    const uint32_t depth = deep ? t.chunks : 1;
     const uint64_t halves = gated ? 2 : 1, wrows = (uint64_t)E * N - (gated ? N / 2 : 0);
     const uint64_t up = (uint64_t)(gated ? N / 2 : N);  // rows from gate to up
     const uint32_t bn = (uint32_t)(t.n / halves), m = (uint32_t)t.m, two = (uint32_t)halves;
     const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
-    tm->deep = K % 256 == 0;
+    tm->deep = deep;
     const uint64_t ad[3] = {inner, (uint64_t)rows, chunks}, as[2] = {row, 128};
     const uint32_t ab[3] = {128, m, depth};
     const uint64_t bd[4] = {inner, wrows, halves, chunks}, bs[3] = {row, up * row, 128};

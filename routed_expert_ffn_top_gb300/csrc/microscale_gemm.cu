@@ -92,6 +92,11 @@ __device__ __forceinline__ bool mx_wait(uint64_t *bar, uint32_t parity, MxCtl &c
     return gwait(bar, parity, ctl);
 }
 
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool mx_warp_wait(uint64_t *bar, uint32_t parity, MxCtl &ctl) {
+    return __all_sync(0xffffffffu, mx_wait(bar, parity, ctl));
+}
+
 struct MxArgs {
     int deep;                // the maps' third dimension is K's 256-wide chunks, a stage a copy
     const int32_t *offsets;  // NULL: one group of all rows
@@ -203,8 +208,9 @@ __device__ __forceinline__ void store_row32(const MxArgs &a, int64_t row, int n,
 __device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + expf(-g)); }
 
 // A CTA's units: u = blockIdx.x, blockIdx.x + gridDim.x, ...; unit u is channel tile u % nct of
-// row tile u / nct.  Each role walks them without dividing: the steps are constant and the
-// expert only moves forward.
+// row tile u / nct.  Each warp walks them on its own, without dividing, and finds the next
+// expert with its 32 lanes at once: a walk by one thread took 1000 cycles a unit, as long as a
+// small unit's copies.
 template <int kM>
 struct MxWalk {
     int t, ct, e;          // row tile, channel tile, expert
@@ -212,8 +218,13 @@ struct MxWalk {
     int nrows;             // of this row tile
     int row0;
 
-    __device__ __forceinline__ void place(const MxCtl &ctl) {
-        while (ctl.first[e + 1] <= t) ++e;
+    __device__ __forceinline__ void place(const MxArgs &a, const MxCtl &ctl) {
+        unsigned past;
+        do {
+            const int i = e + 1 + (threadIdx.x & 31);
+            past = __ballot_sync(0xffffffffu, i <= a.E && ctl.first[i] <= t);
+            e += __popc(past);
+        } while (past == 0xffffffffu);
         row0 = ctl.begin[e] + (t - ctl.first[e]) * kM;
         const int left = ctl.begin[e + 1] - row0;
         nrows = left < kM ? left : kM;
@@ -221,19 +232,12 @@ struct MxWalk {
     __device__ __forceinline__ MxWalk(const MxArgs &a, const MxCtl &ctl, int tiles) {
         t = blockIdx.x / a.nct, ct = blockIdx.x % a.nct, e = 0;
         dt = gridDim.x / a.nct, dct = gridDim.x % a.nct;
-        if (t >= tiles) return;
-        int hi = a.E;  // the last e with first[e] <= t
-        while (hi - e > 1) {
-            const int mid = (e + hi) >> 1;
-            if (ctl.first[mid] <= t) e = mid;
-            else hi = mid;
-        }
-        place(ctl);
+        if (t < tiles) place(a, ctl);
     }
     __device__ __forceinline__ void next(const MxArgs &a, const MxCtl &ctl, int tiles) {
         t += dt, ct += dct;
         if (ct >= a.nct) ct -= a.nct, ++t;
-        if (t < tiles) place(ctl);
+        if (t < tiles) place(a, ctl);
     }
 };
 
@@ -345,21 +349,22 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     constexpr int kPerScale = kMxScaleK / G::kStageK;         // stages per copy of scales
 
     if (warp == 8 || warp >= 10) {
-        // three producers, one thread each: weight codes, row codes, scales (a copy takes its
-        // thread 100 to 200 cycles to issue, and a small unit has few MMAs to hide them)
-        if (lane == 0) {
-            const uint64_t pol = policy_evict_normal();
-            uint64_t *const full = warp == 11 ? ctl.cfull : ctl.full, *const empty = warp == 11 ? ctl.cempty : ctl.empty;
-            const int ring = warp == 11 ? G::kScaleBufs : G::kStages;
-            const int steps = warp == 11 ? (nks + kPerScale - 1) / kPerScale : nks;
-            int slot = 0;
-            uint32_t phase = 0, issued = 0, par = 0;
-            for (MxWalk<kM> x(a, ctl, tiles); x.t < tiles && !ctl.abort; x.next(a, ctl, tiles)) {
-                // first weight row of the N side; a gated tile's box also takes the up rows beside it
-                const int b0 = x.e * a.N + x.ct * (kGated ? kHalf : kN);
-                for (int s = 0; s < steps; ++s) {
-                    if (!mx_wait(&empty[slot], phase ^ 1u, ctl)) break;
-                    uint64_t *bar = &full[slot];
+        // three producer warps: weight codes, row codes, scales (issued one after the other, a
+        // small unit's copies took longer than the unit's MMAs)
+        const uint64_t pol = policy_evict_normal();
+        uint64_t *const full = warp == 11 ? ctl.cfull : ctl.full, *const empty = warp == 11 ? ctl.cempty : ctl.empty;
+        const int ring = warp == 11 ? G::kScaleBufs : G::kStages;
+        const int steps = warp == 11 ? (nks + kPerScale - 1) / kPerScale : nks;
+        int slot = 0;
+        uint32_t phase = 0, issued = 0, par = 0;
+        bool ok = true;
+        for (MxWalk<kM> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
+            // first weight row of the N side; a gated tile's box also takes the up rows beside it
+            const int b0 = x.e * a.N + x.ct * (kGated ? kHalf : kN);
+            for (int s = 0; s < steps; ++s) {
+                if (!(ok = mx_warp_wait(&empty[slot], phase ^ 1u, ctl))) break;
+                uint64_t *bar = &full[slot];
+                if (lane == 0) {
                     if (warp == 11) {
                         unsigned char *SA = scales + slot * G::kScaleBytes;
                         mbar_arrive_expect_tx(bar, G::kScaleBytes);
@@ -378,16 +383,17 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                             else tma_load_3d(A + c * G::kAChunk, &tm_a, cx, x.row0, cz, bar, pol);
                         }
                     }
-                    issued |= 1u << slot;
-                    par = (par & ~(1u << slot)) | (phase << slot);
-                    if (++slot == ring) slot = 0, phase ^= 1u;
                 }
+                __syncwarp();
+                issued |= 1u << slot;
+                par = (par & ~(1u << slot)) | (phase << slot);
+                if (++slot == ring) slot = 0, phase ^= 1u;
             }
-            // every copy has landed before the CTA can exit
-            for (int s = 0; s < ring; ++s)
-                if ((issued >> s) & 1u)
-                    if (!mbar_wait_bounded(&full[s], (par >> s) & 1u)) ctl.abort = 1;
         }
+        // every copy has landed before the CTA can exit
+        for (int s = 0; s < ring; ++s)
+            if ((issued >> s) & 1u)
+                if (!mbar_wait_bounded(&full[s], (par >> s) & 1u)) ctl.abort = 1;
         __syncwarp();
     } else if (warp == 9) {
         if (lane == 0) {
@@ -397,6 +403,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, 16, 1024, 2);
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 1;
+            const int dt = gridDim.x / a.nct, dct = gridDim.x % a.nct;
             for (int t = blockIdx.x / a.nct, ct = blockIdx.x % a.nct; t < tiles && !ctl.abort;) {
                 if (!mx_wait(&ctl.tempty[buf], tphase, ctl)) break;
                 const uint32_t d = ctl.tmem + (uint32_t)(buf * kN);
@@ -430,7 +437,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                 umma_commit(&ctl.tfull[buf]);
                 if (buf) tphase ^= 1u;
                 buf ^= 1;
-                t += gridDim.x / a.nct, ct += gridDim.x % a.nct;
+                t += dt, ct += dct;
                 if (ct >= a.nct) ct -= a.nct, ++t;
             }
             // every issued MMA has completed before the CTA frees its tensor memory
@@ -447,7 +454,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.nct && ok; u += gridDim.x)
             for (int s = 0; s < nks; ++s) {
                 const int part = s % kPerScale;
-                if (part == 0 && !(ok = mx_wait(&ctl.cfull[buf], cphase, ctl))) break;
+                if (part == 0 && !(ok = mx_warp_wait(&ctl.cfull[buf], cphase, ctl))) break;
                 // blocks past K have zero codes; their scale must not be a NaN
                 uint32_t mask[G::kGroups];
 #pragma unroll
@@ -467,7 +474,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                     if (++buf == G::kScaleBufs) buf = 0, cphase ^= 1u;
                 }
                 // the MMAs that read this slot's scales have completed
-                if (!(ok = mx_wait(&ctl.empty[stage], phase ^ 1u, ctl))) break;
+                if (!(ok = mx_warp_wait(&ctl.empty[stage], phase ^ 1u, ctl))) break;
                 tc_fence_after();
                 const uint32_t sf = ctl.tmem + quad + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
 #pragma unroll
@@ -485,7 +492,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         int local = 0;
         for (MxWalk<kM> x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles), ++local) {
             const int buf = local & 1;
-            if (!mx_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
+            if (!mx_warp_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
             tc_fence_after();
             const int64_t row = (int64_t)x.row0 + 32 * warp + lane;
             const bool live = 32 * warp + lane < x.nrows;

@@ -413,7 +413,7 @@ struct MicroscaleTile {
 };
 MicroscaleTile microscale_tile(int64_t rows, int E);
 // Tensor maps of one grouped product: codes and scales of the rows and of the weights.  Codes
-// have a chunk dimension of K (128 bytes each) when K is a multiple of 256 (`deep`); the
+// have a chunk dimension of K (128 bytes each) when K is a whole number of stages (`deep`); the
 // weights' have a gate/up dimension.
 struct MicroscaleMaps {
     CUtensorMap a, sa, b, sb;
