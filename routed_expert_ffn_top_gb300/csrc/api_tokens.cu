@@ -181,10 +181,10 @@ static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8
     const uint32_t sab[2] = {64, m};
     const uint64_t sbd[3] = {pitch, wrows, halves}, sbs[2] = {pitch, up * pitch};
     const uint32_t sbb[3] = {64, bn, two};
-    return make_tmap_bytes(&tm->a, x_codes, 3, ad, as, ab, sw128) &&
-           make_tmap_bytes(&tm->b, w_codes, 4, bd, bs, bb, sw128) &&
-           make_tmap_bytes(&tm->sa, x_scales, 2, sad, sas, sab, sw64) &&
-           make_tmap_bytes(&tm->sb, w_scales, 3, sbd, sbs, sbb, sw64);
+    return make_tmap_bytes(&tm->x, x_codes, 3, ad, as, ab, sw128) &&
+           make_tmap_bytes(&tm->w, w_codes, 4, bd, bs, bb, sw128) &&
+           make_tmap_bytes(&tm->sx, x_scales, 2, sad, sas, sab, sw64) &&
+           make_tmap_bytes(&tm->sw, w_scales, 3, sbd, sbs, sbb, sw64);
 }
 
 extern "C" int moe_microscale_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,

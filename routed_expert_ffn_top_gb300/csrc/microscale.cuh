@@ -37,4 +37,15 @@ __device__ __forceinline__ uint32_t fp4x8(const float (&v)[8]) {
     return r;
 }
 
+// One float to its code.
+__device__ __forceinline__ uint32_t fp4(float v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+        "cvt.u32.u8 %0, b;\n\t}"
+        : "=r"(r)
+        : "f"(v), "f"(0.0f));
+    return r;
+}
+
 }  // namespace moe

@@ -34,37 +34,38 @@ constexpr int kMxMaxStages = 8;
 constexpr int kMxMaxScaleBufs = 4;
 constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
 
-// kM: rows per tile that are copied and stored (128, or 32 for small groups: the MMA still
-// reads 128 rows, the others whatever follows in shared memory, and their results are
-// dropped); kN: channels per tile; kChunks: 256-wide chunks of K per stage.
-template <int kM, int kN>
+// Two tiles.  kTok = 128: 128 rows of x as the MMA's M side, kCh = 192 channels as its N side.
+// kTok = 32, for small groups: the sides change places, 128 channels are M and up to 32 rows
+// N, so no MMA reads rows that do not exist and the four epilogue warps share every row (with
+// the rows on the M side an MMA read 4 KB of rows for a handful, and shared memory bound it).
+template <int kTok_>
 struct MxTile {
-    static_assert(kM == 32 || kM == 128, "row tiles");
-    static_assert(kN % 64 == 0 && kN <= 192, "column tiles");
-    static constexpr int kChunks = kM == 32 ? 2 : 1;
+    static_assert(kTok_ == 32 || kTok_ == 128, "row tiles");
+    static constexpr bool kSwap = kTok_ == 32;
+    static constexpr int kTok = kTok_, kCh = kSwap ? 128 : 192;
+    static constexpr int kA = kSwap ? kCh : kTok, kB = kSwap ? kTok : kCh;  // M and N sides
+    static_assert(kA == 128, "the MMA's M");
+    static constexpr int kChunks = kSwap ? 2 : 1;          // 256-wide chunks of K per stage
     static constexpr int kStageK = 256 * kChunks;
-    static constexpr int kAChunk = kM * 128;               // one 256-wide chunk of the rows
-    static constexpr int kBChunk = kN * 128;
+    static constexpr int kAChunk = kA * 128;               // one chunk of the M side
+    static constexpr int kBChunk = kB * 128;
     static constexpr int kABytes = kChunks * kAChunk;
     static constexpr int kBBytes = kChunks * kBChunk;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kScaleBytes = (kM + kN) * 64;     // one copy of scales, rows then channels
-    static constexpr int kScaleBufs = kM == 32 ? 4 : 2;
-    static constexpr int kStages = kM == 128 ? 4 : (kN == 64 ? 7 : 4);
-    static constexpr int kACols = 4;                       // scale columns per 128 of K
-    static constexpr int kAUsed = kM / 32;                 // those whose rows exist
-    static constexpr int kBCols = kN / 32;
+    static constexpr int kScaleBytes = (kA + kB) * 64;     // one copy of scales, M side then N side
+    static constexpr int kScaleBufs = kSwap ? 4 : 2;
+    static constexpr int kStages = 4;
+    static constexpr int kACols = kA / 32;                 // scale columns per 128 of K
+    static constexpr int kBCols = kB / 32;
     static constexpr int kBPad = (kBCols + 3) / 4 * 4;     // every set starts at a multiple of 4
     static constexpr int kGroups = 2 * kChunks;            // 128-wide groups of K per stage
     static constexpr int kSfCols = kGroups * (kACols + kBPad);  // per stage
-    static constexpr int kSfCol0 = 2 * kN;                 // after the two accumulators
+    static constexpr int kSfCol0 = 2 * kB;                 // after the two accumulators
     static constexpr uint32_t kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kScaleBufs * kScaleBytes + 1024;
     static_assert(kStageBytes % 1024 == 0 && kScaleBytes % 512 == 0, "stage alignment");
     static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
     static_assert(kStages <= kMxMaxStages && kScaleBufs <= kMxMaxScaleBufs, "barriers");
-    // the MMA's reads past a 32-row chunk stay inside the stage
-    static_assert(kABytes - kAChunk + 128 * 128 <= kStageBytes, "A reads");
 };
 
 struct MxCtl {
@@ -261,20 +262,65 @@ __device__ __forceinline__ void mx_scale_words(const unsigned char *base, int ro
     }
 }
 
+// Small tile: lane's channel n of up to 32 rows (v: one per row).
+template <typename T>
+__device__ __forceinline__ void mx_store_columns(const MxArgs &a, int row0, int nrows, int n, const uint32_t (&v)[32]) {
+    if (n >= a.N) return;
+    T *dst = static_cast<T *>(a.y) + (int64_t)row0 * a.ldy + n;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j < nrows) put_f32(dst + j * a.ldy, __uint_as_float(v[j]));
+}
+
+// Small gated tile: warps 0 and 1 hold g of 64 channels, warps 2 and 3 u of the same; u goes
+// through shared memory, a block of 32 channels is a warp's lanes.
+__device__ __forceinline__ void mx_gate_columns(const MxArgs &a, float *exchange, int row0, int nrows, int n0, int warp,
+                                                int lane, const uint32_t (&v)[32], bool last) {
+    float *u = exchange + (32 * warp + lane) % 64;
+    if (warp >= 2) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < nrows) u[64 * j] = __uint_as_float(v[j]);
+    }
+    named_bar_sync(1, 128);
+    const int I = a.N / 2, n = n0 + 32 * warp;
+    if (warp < 2 && n < I) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (j >= nrows) break;
+            const float p = silu_fast(__uint_as_float(v[j])) * u[64 * j];
+            const uint32_t byte = microscale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(p) & 0x7fffffffu));
+            uint32_t c = byte == 255u ? 0u : fp4(p * microscale_inverse(byte)) << (4 * (lane & 7));
+            c |= __shfl_xor_sync(0xffffffffu, c, 1);
+            c |= __shfl_xor_sync(0xffffffffu, c, 2);
+            c |= __shfl_xor_sync(0xffffffffu, c, 4);
+            const int64_t row = row0 + j;
+            if ((lane & 7) == 0) *reinterpret_cast<uint32_t *>(a.codes + row * (I / 2) + n / 2 + lane / 2) = c;
+            if (lane == 0) a.scales[row * a.pitch + n / 32] = (uint8_t)byte;
+        }
+    }
+    if (warp == 2 && last)
+        for (int j = 0; j < nrows; ++j)
+            for (int b = I / 32 + lane; b < a.pitch; b += 32) a.scales[(int64_t)(row0 + j) * a.pitch + b] = 0;
+}
+
 // kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
-template <int kM, int kN, int kOut>
+template <int kTok, int kOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
-microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_sa,
-                       const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_sb,
+microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_sx,
+                       const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_sw,
                        const MxArgs a) {
-    using G = MxTile<kM, kN>;
+    using G = MxTile<kTok>;
     constexpr bool kGated = kOut == 3;
-    constexpr int kHalf = kN / 2;
+    constexpr int kN = G::kB, kHalf = G::kCh / 2;
+    using Out = typename std::conditional<kOut == 0, __nv_bfloat16,
+                                          typename std::conditional<kOut == 1, __half, float>::type>::type;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *stages = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *scales = stages + G::kStages * G::kStageBytes;
     __shared__ MxCtl ctl;
+    __shared__ float exchange[kGated && G::kSwap ? 2 * 32 * 64 : 1];  // u of the gated small tile, two units
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -297,8 +343,8 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     }
     if (warp == 9) tmem_alloc(&ctl.tmem, G::kTmemCols);
     if (warp == 8 && lane == 0) {
-        prefetch_tensormap(&tm_b);
-        prefetch_tensormap(&tm_sb);
+        prefetch_tensormap(&tm_w);
+        prefetch_tensormap(&tm_sw);
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -314,7 +360,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
             lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
             hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
         }
-        const int tiles = (int)((hi - lo + kM - 1) / kM);
+        const int tiles = (int)((hi - lo + kTok - 1) / kTok);
         int inc = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -358,29 +404,30 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
         int slot = 0;
         uint32_t phase = 0, issued = 0, par = 0;
         bool ok = true;
-        for (MxWalk<kM> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
-            // first weight row of the N side; a gated tile's box also takes the up rows beside it
-            const int b0 = x.e * a.N + x.ct * (kGated ? kHalf : kN);
+        for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
+            // first weight row; a gated tile's box also takes the up rows beside its gate rows
+            const int w0 = x.e * a.N + x.ct * (kGated ? kHalf : G::kCh);
             for (int s = 0; s < steps; ++s) {
                 if (!(ok = mx_warp_wait(&empty[slot], phase ^ 1u, ctl))) break;
                 uint64_t *bar = &full[slot];
                 if (lane == 0) {
                     if (warp == 11) {
-                        unsigned char *SA = scales + slot * G::kScaleBytes;
+                        unsigned char *S = scales + slot * G::kScaleBytes;
                         mbar_arrive_expect_tx(bar, G::kScaleBytes);
-                        tma_load_3d(SA + kM * 64, &tm_sb, s * 64, b0, 0, bar, pol);
-                        tma_load_2d(SA, &tm_sa, s * 64, x.row0, bar, pol);
+                        tma_load_3d(S + (G::kSwap ? 0 : G::kA * 64), &tm_sw, s * 64, w0, 0, bar, pol);
+                        tma_load_2d(S + (G::kSwap ? G::kA * 64 : 0), &tm_sx, s * 64, x.row0, bar, pol);
                     } else {
                         // one copy brings the whole stage, or one per chunk (past K: none)
-                        unsigned char *A = stages + slot * G::kStageBytes;
                         const int left = (a.K - s * G::kStageK + 255) / 256;
                         const int copies = a.deep ? 1 : (left < G::kChunks ? left : G::kChunks);
-                        const int chunk = warp == 8 ? G::kBChunk : G::kAChunk;
+                        const bool side_a = G::kSwap == (warp == 8);
+                        const int chunk = side_a ? G::kAChunk : G::kBChunk;
+                        unsigned char *dst = stages + slot * G::kStageBytes + (side_a ? 0 : G::kABytes);
                         mbar_arrive_expect_tx(bar, (a.deep ? G::kChunks : copies) * chunk);
-                        for (int c = 0; c < copies; ++c) {
+                        for (int c = 0; c < copies; ++c, dst += chunk) {
                             const int cx = a.deep ? 0 : (s * G::kChunks + c) * 128, cz = a.deep ? s * G::kChunks : 0;
-                            if (warp == 8) tma_load_4d(A + G::kABytes + c * G::kBChunk, &tm_b, cx, b0, 0, cz, bar, pol);
-                            else tma_load_3d(A + c * G::kAChunk, &tm_a, cx, x.row0, cz, bar, pol);
+                            if (warp == 8) tma_load_4d(dst, &tm_w, cx, w0, 0, cz, bar, pol);
+                            else tma_load_3d(dst, &tm_x, cx, x.row0, cz, bar, pol);
                         }
                     }
                 }
@@ -462,10 +509,10 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                     const int left = nb - (s * G::kGroups + q) * 4;
                     mask[q] = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
                 }
-                const unsigned char *SA = scales + buf * G::kScaleBytes, *SB = SA + kM * 64;
+                const unsigned char *SA = scales + buf * G::kScaleBytes, *SB = SA + G::kA * 64;
                 uint32_t wa[G::kGroups * G::kACols] = {}, wb[G::kGroups * G::kBPad] = {};
 #pragma unroll
-                for (int c = 0; c < G::kAUsed; ++c) mx_scale_words<G::kGroups, G::kACols>(SA, c * 32 + lane, part, mask, wa + c);
+                for (int c = 0; c < G::kACols; ++c) mx_scale_words<G::kGroups, G::kACols>(SA, c * 32 + lane, part, mask, wa + c);
 #pragma unroll
                 for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kGroups, G::kBPad>(SB, c * 32 + lane, part, mask, wb + c);
                 if (part == kPerScale - 1 || s == nks - 1) {
@@ -490,18 +537,27 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
     } else {
         const uint32_t quad = (uint32_t)(32 * warp) << 16;
         int local = 0;
-        for (MxWalk<kM> x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles), ++local) {
+        for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles), ++local) {
             const int buf = local & 1;
             if (!mx_warp_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
             tc_fence_after();
+            const uint32_t d = ctl.tmem + quad + (uint32_t)(buf * kN);
+            if constexpr (G::kSwap) {
+                uint32_t v[32];
+                tmem_ld32(d, v);
+                tmem_ld_wait(v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.tempty[buf]);
+                if constexpr (!kGated) mx_store_columns<Out>(a, x.row0, x.nrows, x.ct * G::kCh + 32 * warp + lane, v);
+                else mx_gate_columns(a, exchange + buf * (32 * 64), x.row0, x.nrows, x.ct * kHalf, warp, lane, v, x.ct == a.nct - 1);
+                continue;
+            }
             const int64_t row = (int64_t)x.row0 + 32 * warp + lane;
             const bool live = 32 * warp + lane < x.nrows;
-            const uint32_t d = ctl.tmem + quad + (uint32_t)(buf * kN);
             if (32 * warp >= x.nrows) {
                 // no row of this warp's lanes: the accumulator holds nothing of the tile here
             } else if constexpr (!kGated) {
-                using T_ = typename std::conditional<kOut == 0, __nv_bfloat16,
-                                                     typename std::conditional<kOut == 1, __half, float>::type>::type;
 #pragma unroll 1
                 for (int c = 0; c < kN; c += 64) {
                     uint32_t v[32], w[32];
@@ -510,8 +566,8 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                     tmem_ld_wait(v);
                     tmem_ld_wait(w);
                     const int n = x.ct * kN + c;
-                    if (live && n < a.N) store_row32<T_>(a, row, n, v);
-                    if (live && n + 32 < a.N) store_row32<T_>(a, row, n + 32, w);
+                    if (live && n < a.N) store_row32<Out>(a, row, n, v);
+                    if (live && n + 32 < a.N) store_row32<Out>(a, row, n + 32, w);
                 }
             } else {
                 const int I = a.N / 2;
@@ -559,9 +615,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
                     *reinterpret_cast<uint4 *>(a.codes + r * (a.N / 4) + 16 * i) = uint4{0, 0, 0, 0};
                 for (int i = threadIdx.x; i < a.pitch; i += 128) a.scales[r * a.pitch + i] = 0;
             } else {
-                using T_ = typename std::conditional<kOut == 0, __nv_bfloat16,
-                                                     typename std::conditional<kOut == 1, __half, float>::type>::type;
-                for (int i = threadIdx.x; i < a.N; i += 128) put_f32(static_cast<T_ *>(a.y) + r * a.ldy + i, 0.0f);
+                for (int i = threadIdx.x; i < a.N; i += 128) put_f32(static_cast<Out *>(a.y) + r * a.ldy + i, 0.0f);
             }
         }
     }
@@ -575,31 +629,35 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_co
 
 // ----------------------------------------------------------------------------------- launcher
 MicroscaleTile microscale_tile(int64_t rows, int E) {
-    return rows >= 32 * (int64_t)E ? MicroscaleTile{128, 192, 1} : MicroscaleTile{32, 128, 2};
+    using Large = MxTile<128>;
+    using Small = MxTile<32>;
+    return rows >= 32 * (int64_t)E ? MicroscaleTile{128, Large::kCh, Large::kChunks}
+                                   : MicroscaleTile{32, Small::kCh, Small::kChunks};
 }
 
-template <int kM, int kN, int kOut>
+template <int kTok, int kOut>
 static cudaError_t gemm_as(const MicroscaleMaps &tm, MxArgs a, cudaStream_t stream) {
-    using G = MxTile<kM, kN>;
-    a.nct = kOut == 3 ? (a.N / 2 + kN / 2 - 1) / (kN / 2) : (a.N + kN - 1) / kN;
-    const int64_t tiles = a.rows < a.E ? a.rows : a.rows / kM + a.E;
+    using G = MxTile<kTok>;
+    const int per = kOut == 3 ? G::kCh / 2 : G::kCh, cols = kOut == 3 ? a.N / 2 : a.N;
+    a.nct = (cols + per - 1) / per;
+    const int64_t tiles = a.rows < a.E ? a.rows : a.rows / kTok + a.E;
     const int64_t units = tiles * a.nct, sms = num_sms();
     const int64_t grid = units < 1 ? 1 : (units < sms ? units : sms);
-    const auto fn = microscale_gemm_kernel<kM, kN, kOut>;
+    const auto fn = microscale_gemm_kernel<kTok, kOut>;
     cudaError_t err = ensure_smem((const void *)fn, G::kSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)grid), dim3(kMxThreads), G::kSmem, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, fn, tm.a, tm.sa, tm.b, tm.sb, a);
+    return cudaLaunchKernelEx(&cfg, fn, tm.x, tm.sx, tm.w, tm.sw, a);
 }
 
-template <int kM, int kN>
+template <int kTok>
 static cudaError_t gemm_tile(const MicroscaleMaps &tm, const MxArgs &a, int out, cudaStream_t stream) {
     switch (out) {
-        case MOE_DT_BF16: return gemm_as<kM, kN, 0>(tm, a, stream);
-        case MOE_DT_F16: return gemm_as<kM, kN, 1>(tm, a, stream);
-        case MOE_DT_F32: return gemm_as<kM, kN, 2>(tm, a, stream);
-        default: return gemm_as<kM, kN, 3>(tm, a, stream);
+        case MOE_DT_BF16: return gemm_as<kTok, 0>(tm, a, stream);
+        case MOE_DT_F16: return gemm_as<kTok, 1>(tm, a, stream);
+        case MOE_DT_F32: return gemm_as<kTok, 2>(tm, a, stream);
+        default: return gemm_as<kTok, 3>(tm, a, stream);
     }
 }
 
@@ -614,9 +672,7 @@ cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const
     const int elem = dtype == MOE_DT_F32 ? 4 : 2;
     a.vec = y && (reinterpret_cast<uintptr_t>(y) | (uint64_t)(ldy * elem)) % 32 == 0;
     const int out = codes ? 3 : dtype;
-    const MicroscaleTile t = microscale_tile(rows, E);
-    if (t.m == 128) return gemm_tile<128, 192>(tm, a, out, stream);
-    return t.n == 128 ? gemm_tile<32, 128>(tm, a, out, stream) : gemm_tile<32, 64>(tm, a, out, stream);
+    return microscale_tile(rows, E).m == 128 ? gemm_tile<128>(tm, a, out, stream) : gemm_tile<32>(tm, a, out, stream);
 }
 
 }  // namespace moe

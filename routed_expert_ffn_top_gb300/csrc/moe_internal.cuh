@@ -416,7 +416,7 @@ MicroscaleTile microscale_tile(int64_t rows, int E);
 // have a chunk dimension of K (128 bytes each) when K is a whole number of stages (`deep`); the
 // weights' have a gate/up dimension.
 struct MicroscaleMaps {
-    CUtensorMap a, sa, b, sb;
+    CUtensorMap x, sx, w, sw;
     int deep;
 };
 // codes == NULL: y [rows][N] of dtype; else the gated form, codes and scales of [rows][N / 2].
