@@ -164,27 +164,23 @@ static int check_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_
 static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
                          const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K, bool gated) {
     const MicroscaleTile t = microscale_tile(rows, E);
-    const uint64_t row = (uint64_t)K / 2, pitch = (uint64_t)microscale_pitch(K);
+    const uint64_t row = (uint64_t)K / 2;
     const bool deep = K % (256 * t.chunks) == 0;
     const uint64_t inner = deep ? 128 : row, chunks = deep ? K / 256 : 1;
     const uint32_t depth = deep ? t.chunks : 1;
     const uint64_t halves = gated ? 2 : 1, wrows = (uint64_t)E * N - (gated ? N / 2 : 0);
     const uint64_t up = (uint64_t)(gated ? N / 2 : N);  // rows from gate to up
     const uint32_t bn = (uint32_t)(t.n / halves), m = (uint32_t)t.m, two = (uint32_t)halves;
-    const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B;
     tm->deep = deep;
+    tm->x_scales = x_scales;
+    tm->w_scales = w_scales;
     const uint64_t ad[3] = {inner, (uint64_t)rows, chunks}, as[2] = {row, 128};
     const uint32_t ab[3] = {128, m, depth};
     const uint64_t bd[4] = {inner, wrows, halves, chunks}, bs[3] = {row, up * row, 128};
     const uint32_t bb[4] = {128, bn, two, depth};
-    const uint64_t sad[2] = {pitch, (uint64_t)rows}, sas[1] = {pitch};
-    const uint32_t sab[2] = {64, m};
-    const uint64_t sbd[3] = {pitch, wrows, halves}, sbs[2] = {pitch, up * pitch};
-    const uint32_t sbb[3] = {64, bn, two};
     return make_tmap_bytes(&tm->x, x_codes, 3, ad, as, ab, sw128) &&
-           make_tmap_bytes(&tm->w, w_codes, 4, bd, bs, bb, sw128) &&
-           make_tmap_bytes(&tm->sx, x_scales, 2, sad, sas, sab, sw64) &&
-           make_tmap_bytes(&tm->sw, w_scales, 3, sbd, sbs, sbb, sw64);
+           make_tmap_bytes(&tm->w, w_codes, 4, bd, bs, bb, sw128);
 }
 
 extern "C" int moe_microscale_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,

@@ -15,8 +15,8 @@
 // computes p = SiLU(g) u in fp32 and quantises it in the epilogue, so g and u never leave the
 // chip.
 //
-// Per CTA, 10 warps: 0-3 drain the accumulators, 4-7 bring the scales from shared memory into
-// tensor memory, 8 issues the copies, 9 the MMAs.  A stage is 256 of K: 128-byte rows of
+// Per CTA, 11 warps: 0-3 drain the accumulators, 4-7 bring the scales through shared memory into
+// tensor memory, 8 and 10 issue the copies of codes, 9 the MMAs.  A stage is 256 of K: 128-byte rows of
 // codes, 128-byte swizzled, and 16-byte rows of scales (a copy's inner extent is 16 bytes at
 // least, so two stages share their scale bytes and each uses its half).  The MMA reads the
 // scale of row r at lane r % 32, column r / 32, four K blocks a 32-bit column, repeated in the
@@ -29,9 +29,8 @@
 
 namespace moe {
 
-constexpr int kMxThreads = 384;
+constexpr int kMxThreads = 352;
 constexpr int kMxMaxStages = 8;
-constexpr int kMxMaxScaleBufs = 4;
 constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
 
 // Two tiles.  kTok = 128: 128 rows of x as the MMA's M side, kCh = 192 channels as its N side.
@@ -65,15 +64,13 @@ struct MxTile {
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kScaleBufs * kScaleBytes + 1024;
     static_assert(kStageBytes % 1024 == 0 && kScaleBytes % 512 == 0, "stage alignment");
     static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
-    static_assert(kStages <= kMxMaxStages && kScaleBufs <= kMxMaxScaleBufs, "barriers");
+    static_assert(kStages <= kMxMaxStages, "barriers");
 };
 
 struct MxCtl {
     uint64_t full[kMxMaxStages];
     uint64_t empty[kMxMaxStages];
     uint64_t sfull[kMxMaxStages];      // the stage's scales are in tensor memory
-    uint64_t cfull[kMxMaxScaleBufs];   // a copy of scales has landed
-    uint64_t cempty[kMxMaxScaleBufs];
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t done;
@@ -101,6 +98,8 @@ __device__ __forceinline__ bool mx_warp_wait(uint64_t *bar, uint32_t parity, MxC
 struct MxArgs {
     int deep;                // the maps' third dimension is K's 256-wide chunks, a stage a copy
     const int32_t *offsets;  // NULL: one group of all rows
+    const uint8_t *x_scales, *w_scales;
+    int kpitch;              // their row bytes
     int64_t rows;
     int E, N, K;
     int nct;                 // column tiles
@@ -305,10 +304,16 @@ __device__ __forceinline__ void mx_gate_columns(const MxArgs &a, float *exchange
 }
 
 // kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
+// First weight row of a unit: of the tile's channels, or (gated) of its gate channels, whose up
+// rows lie N / 2 further on.
+template <bool kGated, int kCh>
+__device__ __forceinline__ int mx_first_channel(const MxArgs &a, int e, int ct) {
+    return e * a.N + ct * (kGated ? kCh / 2 : kCh);
+}
+
 template <int kTok, int kOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
-microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_sx,
-                       const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_sw,
+microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                        const MxArgs a) {
     using G = MxTile<kTok>;
     constexpr bool kGated = kOut == 3;
@@ -329,10 +334,6 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
             mbar_init(&ctl.empty[s], 1);
             mbar_init(&ctl.sfull[s], 4);
         }
-        for (int b = 0; b < G::kScaleBufs; ++b) {
-            mbar_init(&ctl.cfull[b], 1);
-            mbar_init(&ctl.cempty[b], 4);
-        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl.tfull[b], 1);
             mbar_init(&ctl.tempty[b], 4);
@@ -344,7 +345,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     if (warp == 9) tmem_alloc(&ctl.tmem, G::kTmemCols);
     if (warp == 8 && lane == 0) {
         prefetch_tensormap(&tm_w);
-        prefetch_tensormap(&tm_sw);
+        prefetch_tensormap(&tm_x);
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -394,53 +395,42 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     const int nks = (a.K + G::kStageK - 1) / G::kStageK;  // stages per unit
     constexpr int kPerScale = kMxScaleK / G::kStageK;         // stages per copy of scales
 
-    if (warp == 8 || warp >= 10) {
-        // three producer warps: weight codes, row codes, scales (issued one after the other, a
-        // small unit's copies took longer than the unit's MMAs)
+    if (warp == 8 || warp == 10) {
+        // two producer warps: weight codes and row codes
         const uint64_t pol = policy_evict_normal();
-        uint64_t *const full = warp == 11 ? ctl.cfull : ctl.full, *const empty = warp == 11 ? ctl.cempty : ctl.empty;
-        const int ring = warp == 11 ? G::kScaleBufs : G::kStages;
-        const int steps = warp == 11 ? (nks + kPerScale - 1) / kPerScale : nks;
+        const bool side_a = G::kSwap == (warp == 8);
+        const int chunk = side_a ? G::kAChunk : G::kBChunk;
+        unsigned char *const base = stages + (side_a ? 0 : G::kABytes);
         int slot = 0;
         uint32_t phase = 0, issued = 0, par = 0;
         bool ok = true;
         for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
-            // first weight row; a gated tile's box also takes the up rows beside its gate rows
-            const int w0 = x.e * a.N + x.ct * (kGated ? kHalf : G::kCh);
-            for (int s = 0; s < steps; ++s) {
-                if (!(ok = mx_warp_wait(&empty[slot], phase ^ 1u, ctl))) break;
-                uint64_t *bar = &full[slot];
+            const int w0 = mx_first_channel<kGated, G::kCh>(a, x.e, x.ct);
+            for (int s = 0; s < nks; ++s) {
+                if (!(ok = mx_warp_wait(&ctl.empty[slot], phase ^ 1u, ctl))) break;
                 if (lane == 0) {
-                    if (warp == 11) {
-                        unsigned char *S = scales + slot * G::kScaleBytes;
-                        mbar_arrive_expect_tx(bar, G::kScaleBytes);
-                        tma_load_3d(S + (G::kSwap ? 0 : G::kA * 64), &tm_sw, s * 64, w0, 0, bar, pol);
-                        tma_load_2d(S + (G::kSwap ? G::kA * 64 : 0), &tm_sx, s * 64, x.row0, bar, pol);
-                    } else {
-                        // one copy brings the whole stage, or one per chunk (past K: none)
-                        const int left = (a.K - s * G::kStageK + 255) / 256;
-                        const int copies = a.deep ? 1 : (left < G::kChunks ? left : G::kChunks);
-                        const bool side_a = G::kSwap == (warp == 8);
-                        const int chunk = side_a ? G::kAChunk : G::kBChunk;
-                        unsigned char *dst = stages + slot * G::kStageBytes + (side_a ? 0 : G::kABytes);
-                        mbar_arrive_expect_tx(bar, (a.deep ? G::kChunks : copies) * chunk);
-                        for (int c = 0; c < copies; ++c, dst += chunk) {
-                            const int cx = a.deep ? 0 : (s * G::kChunks + c) * 128, cz = a.deep ? s * G::kChunks : 0;
-                            if (warp == 8) tma_load_4d(dst, &tm_w, cx, w0, 0, cz, bar, pol);
-                            else tma_load_3d(dst, &tm_x, cx, x.row0, cz, bar, pol);
-                        }
+                    // one copy brings the whole stage, or one per chunk (past K: none)
+                    uint64_t *bar = &ctl.full[slot];
+                    const int left = (a.K - s * G::kStageK + 255) / 256;
+                    const int copies = a.deep ? 1 : (left < G::kChunks ? left : G::kChunks);
+                    unsigned char *dst = base + slot * G::kStageBytes;
+                    mbar_arrive_expect_tx(bar, (a.deep ? G::kChunks : copies) * chunk);
+                    for (int c = 0; c < copies; ++c, dst += chunk) {
+                        const int cx = a.deep ? 0 : (s * G::kChunks + c) * 128, cz = a.deep ? s * G::kChunks : 0;
+                        if (warp == 8) tma_load_4d(dst, &tm_w, cx, w0, 0, cz, bar, pol);
+                        else tma_load_3d(dst, &tm_x, cx, x.row0, cz, bar, pol);
                     }
                 }
                 __syncwarp();
                 issued |= 1u << slot;
                 par = (par & ~(1u << slot)) | (phase << slot);
-                if (++slot == ring) slot = 0, phase ^= 1u;
+                if (++slot == G::kStages) slot = 0, phase ^= 1u;
             }
         }
         // every copy has landed before the CTA can exit
-        for (int s = 0; s < ring; ++s)
+        for (int s = 0; s < G::kStages; ++s)
             if ((issued >> s) & 1u)
-                if (!mbar_wait_bounded(&full[s], (par >> s) & 1u)) ctl.abort = 1;
+                if (!mbar_wait_bounded(&ctl.full[s], (par >> s) & 1u)) ctl.abort = 1;
         __syncwarp();
     } else if (warp == 9) {
         if (lane == 0) {
@@ -493,15 +483,47 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         }
         __syncwarp();
     } else if (warp >= 4) {
+        // scales: copied kMxScaleK of K at a time, kScaleBufs copies ahead, by 16-byte cp.async
+        // (a tensor copy of 64-byte rows takes 11 cycles a row, as long as the unit's codes
+        // when K is short); every warp then needs all rows, hence the barrier
         const uint32_t quad = (uint32_t)(32 * (warp - 4)) << 16;
-        const int nb = a.K / 32;
-        int stage = 0, buf = 0;
-        uint32_t phase = 0, cphase = 0;
+        const int nb = a.K / 32, per_unit = (nks + kPerScale - 1) / kPerScale;
+        MxWalk<kTok> ahead(a, ctl, tiles);
+        int part_a = 0, slot_a = 0, slot = 0, stage = 0;
+        uint32_t phase = 0;
+        auto issue = [&]() {
+            if (ahead.t < tiles) {
+                const int w0 = mx_first_channel<kGated, G::kCh>(a, ahead.e, ahead.ct);
+                unsigned char *S = scales + slot_a * G::kScaleBytes;
+#pragma unroll
+                for (int i = 0; i < (G::kA + G::kB) * 4 / 128; ++i) {
+                    const int p = (int)threadIdx.x - 128 + 128 * i, r = p >> 2, piece = p & 3;
+                    const int rs = r < G::kA ? r : r - G::kA;  // row of its side
+                    const bool is_w = (r < G::kA) == G::kSwap;
+                    int64_t row = is_w ? w0 + rs : ahead.row0 + rs;
+                    if (kGated && is_w && rs >= kHalf) row += a.N / 2 - kHalf;
+                    const bool in = row < (is_w ? (int64_t)a.E * a.N : a.rows) && part_a * 64 + piece * 16 < a.kpitch;
+                    if (in)
+                        cp_async_16(S + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4),
+                                    (is_w ? a.w_scales : a.x_scales) + row * a.kpitch + part_a * 64 + piece * 16);
+                }
+                if (++part_a == per_unit) part_a = 0, ahead.next(a, ctl, tiles);
+            }
+            cp_async_commit();
+            if (++slot_a == G::kScaleBufs) slot_a = 0;
+        };
+        for (int i = 0; i < G::kScaleBufs - 1; ++i) issue();
+        // after a wait that gave up the loop runs on without waits, so that the barriers stay paired
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.nct && ok; u += gridDim.x)
+        for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.nct; u += gridDim.x)
             for (int s = 0; s < nks; ++s) {
                 const int part = s % kPerScale;
-                if (part == 0 && !(ok = mx_warp_wait(&ctl.cfull[buf], cphase, ctl))) break;
+                if (part == 0) {
+                    if (s > 0 || u != blockIdx.x) slot = slot + 1 == G::kScaleBufs ? 0 : slot + 1;
+                    cp_async_wait_group<G::kScaleBufs - 2>();
+                    named_bar_sync(2, 128);
+                    issue();  // into the slot that every warp has just finished with
+                }
                 // blocks past K have zero codes; their scale must not be a NaN
                 uint32_t mask[G::kGroups];
 #pragma unroll
@@ -509,37 +531,39 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                     const int left = nb - (s * G::kGroups + q) * 4;
                     mask[q] = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
                 }
-                const unsigned char *SA = scales + buf * G::kScaleBytes, *SB = SA + G::kA * 64;
+                const unsigned char *SA = scales + slot * G::kScaleBytes, *SB = SA + G::kA * 64;
                 uint32_t wa[G::kGroups * G::kACols] = {}, wb[G::kGroups * G::kBPad] = {};
 #pragma unroll
                 for (int c = 0; c < G::kACols; ++c) mx_scale_words<G::kGroups, G::kACols>(SA, c * 32 + lane, part, mask, wa + c);
 #pragma unroll
                 for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kGroups, G::kBPad>(SB, c * 32 + lane, part, mask, wb + c);
-                if (part == kPerScale - 1 || s == nks - 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.cempty[buf]);
-                    if (++buf == G::kScaleBufs) buf = 0, cphase ^= 1u;
-                }
                 // the MMAs that read this slot's scales have completed
-                if (!(ok = mx_warp_wait(&ctl.empty[stage], phase ^ 1u, ctl))) break;
-                tc_fence_after();
-                const uint32_t sf = ctl.tmem + quad + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
+                ok = ok && mx_warp_wait(&ctl.empty[stage], phase ^ 1u, ctl);
+                if (ok) {
+                    tc_fence_after();
+                    const uint32_t sf = ctl.tmem + quad + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
 #pragma unroll
-                for (int i = 0; i < G::kGroups * G::kACols; i += 8) tmem_st8(sf + i, wa + i);
+                    for (int i = 0; i < G::kGroups * G::kACols; i += 8) tmem_st8(sf + i, wa + i);
 #pragma unroll
-                for (int i = 0; i < G::kGroups * G::kBPad; i += 8) tmem_st8(sf + G::kGroups * G::kACols + i, wb + i);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.sfull[stage]);
+                    for (int i = 0; i < G::kGroups * G::kBPad; i += 8) tmem_st8(sf + G::kGroups * G::kACols + i, wb + i);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.sfull[stage]);
+                }
                 if (++stage == G::kStages) stage = 0, phase ^= 1u;
             }
+        cp_async_wait_all();
     } else {
         const uint32_t quad = (uint32_t)(32 * warp) << 16;
         int local = 0;
         for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles), ++local) {
             const int buf = local & 1;
-            if (!mx_warp_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) break;
+            if (!mx_warp_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) {
+                if constexpr (!(kGated && G::kSwap)) break;
+                named_bar_sync(1, 128);  // a warp that does not give up waits here for the others
+                continue;
+            }
             tc_fence_after();
             const uint32_t d = ctl.tmem + quad + (uint32_t)(buf * kN);
             if constexpr (G::kSwap) {
@@ -648,7 +672,7 @@ static cudaError_t gemm_as(const MicroscaleMaps &tm, MxArgs a, cudaStream_t stre
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)grid), dim3(kMxThreads), G::kSmem, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, fn, tm.x, tm.sx, tm.w, tm.sw, a);
+    return cudaLaunchKernelEx(&cfg, fn, tm.x, tm.w, a);
 }
 
 template <int kTok>
@@ -667,6 +691,7 @@ cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const
     MxArgs a{};
     a.deep = tm.deep;
     a.offsets = offsets, a.rows = rows, a.E = E, a.N = N, a.K = K;
+    a.x_scales = tm.x_scales, a.w_scales = tm.w_scales, a.kpitch = microscale_pitch(K);
     a.y = y, a.ldy = ldy, a.codes = codes, a.scales = scales, a.status = status;
     a.pitch = microscale_pitch(N / 2);
     const int elem = dtype == MOE_DT_F32 ? 4 : 2;

@@ -412,12 +412,13 @@ struct MicroscaleTile {
     int m, n, chunks;
 };
 MicroscaleTile microscale_tile(int64_t rows, int E);
-// Tensor maps of one grouped product: codes and scales of the rows and of the weights.  Codes
-// have a chunk dimension of K (128 bytes each) when K is a whole number of stages (`deep`); the
+// Operands of one grouped product: tensor maps of the codes of the rows and of the weights, and
+// their scales.  Codes have a chunk dimension of K (128 bytes each) when K is a whole number of stages (`deep`); the
 // weights' have a gate/up dimension.
 struct MicroscaleMaps {
-    CUtensorMap x, sx, w, sw;
+    CUtensorMap x, w;
     int deep;
+    const uint8_t *x_scales, *w_scales;
 };
 // codes == NULL: y [rows][N] of dtype; else the gated form, codes and scales of [rows][N / 2].
 cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const int32_t *offsets, int E,
