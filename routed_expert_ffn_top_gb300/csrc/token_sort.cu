@@ -21,22 +21,37 @@
 namespace moe {
 
 // ------------------------------------------------------------------------------------- plan
-// One cluster of C CTAs.  Each warp takes a contiguous run of routes and counts them per
-// expert in its own row of shared memory, 32 routes a step: the lanes that share an expert
-// find each other with match.any, so a route's rank inside its warp's run needs no atomics
-// and follows r.  Two scans (over the warps of a CTA, then over the CTAs of the cluster,
-// through distributed shared memory) and one over the experts turn ranks into rows.
+// Clusters of C CTAs.  Each warp of a cluster takes a contiguous run of routes and counts them
+// per expert in its own row of shared memory, 32 routes a step: the lanes that share an expert
+// find each other by one ballot per bit of its number, so a route's rank inside its warp's run
+// needs no atomics and follows r.  Two scans (over the warps of a CTA, then over the CTAs of the
+// cluster, through distributed shared memory) and one over the experts turn ranks into rows.
 // Dropped routes use bucket E, which follows the last expert.
+//
+// What bounds it is latency, and for many routes the scattered stores of row_route, one sector a
+// cycle and SM.  So several clusters count all the routes, and each writes its share of every
+// warp's steps: counting again costs less than 8 SMs' stores (65,536 routes, 128 experts: one
+// cluster 16 us).
 constexpr int kPlanMaxCluster = 8;
-constexpr int kPlanKeep = 4;  // steps whose ranks stay in registers; longer runs park them in route_row
+constexpr int kPlanMaxShares = 8;  // clusters
+constexpr int kPlanKeep = 4;       // steps of a share whose ranks stay in registers
 
 struct PlanArgs {
     const int32_t *ids;
     int32_t *offsets, *row_route, *route_row;
     int R, E;
+    int bits;      // of a bucket number
     int per_warp;  // routes per warp, a multiple of 32
     int nwarps;    // warps per CTA that hold routes
+    int C;         // CTAs per cluster
+    int share;     // steps of a warp that one cluster writes, at most kPlanKeep
 };
+
+__device__ __forceinline__ int plan_key(const PlanArgs &a, int r, int hi) {
+    if (r >= hi) return -1;
+    const int id = a.ids[r];
+    return (uint32_t)id < (uint32_t)a.E ? id : a.E;
+}
 
 __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanArgs a) {
     extern __shared__ int32_t sm[];
@@ -46,7 +61,7 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanArgs a) {
     int32_t *base = tot + kPlanMaxCluster * B;   // [B]
     __shared__ int32_t wsum[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x, C = gridDim.x;
+    const int C = a.C, c = blockIdx.x % C, first_step = blockIdx.x / C * a.share;
 
     for (int i = threadIdx.x; i < a.nwarps * B; i += blockDim.x) cnt[i] = 0;
     pdl_wait();
@@ -59,37 +74,49 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanArgs a) {
     const int hi = (int)(lo64 + a.per_warp < a.R ? lo64 + a.per_warp : a.R);
     const int steps = warp < a.nwarps ? (hi - lo + 31) / 32 : 0;
     int32_t *mine = cnt + warp * B;
-    int keep_key[kPlanKeep], keep_rank[kPlanKeep];
-    for (int s0 = 0; s0 < steps; s0 += kPlanKeep) {
+    int keep_key[kPlanKeep], keep_rank[kPlanKeep];  // of the steps this cluster writes
 #pragma unroll
-        for (int i = 0; i < kPlanKeep; ++i) {
-            const int r = lo + (s0 + i) * 32 + lane;
-            const int id = r < hi ? a.ids[r] : 0;
-            keep_key[i] = r < hi ? ((uint32_t)id < (uint32_t)a.E ? id : a.E) : -1;
-        }
+    for (int i = 0; i < kPlanKeep; ++i) keep_key[i] = -1, keep_rank[i] = 0;
+    constexpr int kAhead = 8;
+    for (int s0 = 0; s0 < steps; s0 += kAhead) {
+        int keys[kAhead];
 #pragma unroll
-        for (int i = 0; i < kPlanKeep; ++i) {
+        for (int i = 0; i < kAhead; ++i) keys[i] = plan_key(a, lo + (s0 + i) * 32 + lane, hi);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
             if (s0 + i >= steps) break;
-            const int key = keep_key[i];
-            const unsigned same = __match_any_sync(0xffffffffu, key);
+            const int key = keys[i];
+            unsigned same = __ballot_sync(0xffffffffu, key >= 0);
+            for (int b = 0; b < a.bits; ++b) {
+                const bool one = (key >> b) & 1;
+                const unsigned v = __ballot_sync(0xffffffffu, one);
+                same &= one ? v : ~v;
+            }
             const int before = key >= 0 ? mine[key] : 0;
             __syncwarp();
             const int rank = before + __popc(same & ((1u << lane) - 1u));
-            if (key >= 0 && lane == 31 - __clz(same)) mine[key] = rank + 1;
+            if (key >= 0 && (same >> lane) == 1u) mine[key] = rank + 1;  // its last lane
             __syncwarp();
-            keep_rank[i] = rank;
-            if (steps > kPlanKeep && key >= 0) a.route_row[lo + (s0 + i) * 32 + lane] = rank;
+            const int q = s0 + i - first_step;
+#pragma unroll
+            for (int t = 0; t < kPlanKeep; ++t)
+                if (q == t && t < a.share) keep_key[t] = key, keep_rank[t] = rank;
         }
     }
     __syncthreads();
 
-    // exclusive over this CTA's warps; the totals go to every CTA of the cluster
+    // exclusive over this CTA's warps, 8 counts in flight; the totals go to the whole cluster
     for (int e = threadIdx.x; e < B; e += blockDim.x) {
         int run = 0;
-        for (int w = 0; w < a.nwarps; ++w) {
-            const int t = cnt[w * B + e];
-            cnt[w * B + e] = run;
-            run += t;
+        for (int w0 = 0; w0 < a.nwarps; w0 += 8) {
+            int t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = w0 + i < a.nwarps ? cnt[(w0 + i) * B + e] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (w0 + i < a.nwarps) cnt[(w0 + i) * B + e] = run;
+                run += t[i];
+            }
         }
         tot[c * B + e] = run;
         for (int q = 0; q < C; ++q)
@@ -120,41 +147,30 @@ __global__ void __launch_bounds__(1024) token_plan_kernel(const PlanArgs a) {
         }
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
-        int off = carry, chunk = 0;
-        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-            const int t = wsum[w];
-            if (w < warp) off += t;
-            chunk += t;
+        int w = lane < (int)(blockDim.x >> 5) ? wsum[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, w, d);
+            if (lane >= d) w += t;
         }
-        const int start = off + inc - all;
+        const int below = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+        const int start = carry + (warp > 0 ? below : 0) + inc - all;
         if (e < B) {
             base[e] = start + before;
-            if (c == 0) a.offsets[e] = start;  // bucket E starts at the number of valid routes
+            if (blockIdx.x == 0) a.offsets[e] = start;  // bucket E starts at the number of valid routes
         }
-        carry += chunk;
+        carry += __shfl_sync(0xffffffffu, w, 31);
         __syncthreads();
     }
 
-    for (int s0 = 0; s0 < steps; s0 += kPlanKeep) {
-        if (steps > kPlanKeep) {
 #pragma unroll
-            for (int i = 0; i < kPlanKeep; ++i) {
-                const int r = lo + (s0 + i) * 32 + lane;
-                const int id = r < hi ? a.ids[r] : 0;
-                keep_key[i] = r < hi ? ((uint32_t)id < (uint32_t)a.E ? id : a.E) : -1;
-                keep_rank[i] = r < hi ? a.route_row[r] : 0;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kPlanKeep; ++i) {
-            if (s0 + i >= steps) break;
-            const int key = keep_key[i];
-            if (key < 0) continue;
-            const int r = lo + (s0 + i) * 32 + lane;
-            const int row = base[key] + mine[key] + keep_rank[i];
-            a.route_row[r] = key < a.E ? row : ~row;
-            a.row_route[row] = key < a.E ? r : -1;
-        }
+    for (int t = 0; t < kPlanKeep; ++t) {
+        const int key = keep_key[t];
+        if (key < 0) continue;
+        const int r = lo + (first_step + t) * 32 + lane;
+        const int row = base[key] + mine[key] + keep_rank[t];
+        a.route_row[r] = key < a.E ? row : ~row;
+        a.row_route[row] = key < a.E ? r : -1;
     }
 }
 
@@ -612,15 +628,21 @@ static int64_t cap_grid(int64_t ctas, int per_sm) {
 
 cudaError_t launch_token_plan(const int32_t *ids, int M, int k, int E, int32_t *offsets,
                               int32_t *row_route, int32_t *route_row, cudaStream_t stream) {
-    PlanArgs a{ids, offsets, row_route, route_row, M * k, E, 0, 0};
-    // 128 routes a warp where there are enough of them, up to 8 CTAs of 32 warps
+    PlanArgs a{ids, offsets, row_route, route_row, M * k, E, 0, 0, 0, 1, kPlanKeep};
+    while ((1 << a.bits) <= E) ++a.bits;
+    // runs of 128 routes a warp where there are enough of them, up to 8 CTAs of 32 warps; then
+    // runs of up to 1024 routes in 8 clusters that each write 4 of a run's 32 steps, and past
+    // 262,144 routes more clusters
     const int64_t groups = ((int64_t)a.R + 127) / 128;
-    int C = 1;
-    while (C < kPlanMaxCluster && groups > 32 * C) C *= 2;
-    const int64_t per_cta = (groups + C - 1) / C;
+    while (a.C < kPlanMaxCluster && groups > 32 * a.C) a.C *= 2;
+    const int64_t per_cta = (groups + a.C - 1) / a.C;
     a.nwarps = (int)(per_cta < 1 ? 1 : per_cta > 32 ? 32 : per_cta);
-    const int64_t per_warp = ((int64_t)a.R + (int64_t)C * a.nwarps - 1) / ((int64_t)C * a.nwarps);
+    const int64_t warps = (int64_t)a.C * a.nwarps, per_warp = ((int64_t)a.R + warps - 1) / warps;
     a.per_warp = (int)((per_warp + 31) / 32 * 32);
+    const int steps = a.per_warp / 32;
+    a.share = steps <= kPlanMaxShares ? 1 : (steps + kPlanMaxShares - 1) / kPlanMaxShares;
+    if (a.share > kPlanKeep) a.share = kPlanKeep;
+    const int clusters = steps > 0 ? (steps + a.share - 1) / a.share : 1;
     int threads = a.nwarps * 32;
     const int want = (E + 1 + 31) / 32 * 32;
     if (threads < want) threads = want < 1024 ? want : 1024;
@@ -628,7 +650,7 @@ cudaError_t launch_token_plan(const int32_t *ids, int M, int k, int E, int32_t *
     cudaError_t err = ensure_smem((const void *)token_plan_kernel, smem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
-    cudaLaunchConfig_t cfg = launch_config(dim3(C), dim3(threads), smem, stream, attrs, C > 1 ? C : 0);
+    cudaLaunchConfig_t cfg = launch_config(dim3(a.C * clusters), dim3(threads), smem, stream, attrs, a.C > 1 ? a.C : 0);
     return cudaLaunchKernelEx(&cfg, token_plan_kernel, a);
 }
 
