@@ -377,7 +377,14 @@ __global__ void __launch_bounds__(kGradThreads) token_unsort_grad_kernel(const R
 // of shared memory (cp.async), so a warp has kDepth units in flight and no thread waits for
 // another.  The arithmetic and its order per element are those of the form above.
 constexpr int kRingWarps = 4;
-constexpr int kRingBytes = 74 * 1024;  // of a CTA's slots at most: three CTAs an SM
+// Shared memory of a CTA, whatever part its slots fill: three CTAs an SM, in a grid that fills
+// the SMs once.  Every such launch asks for the same size: with sizes of their own, a grid that
+// starts while another drains found holes that fit two CTAs on a few SMs, and the third ran
+// after all others (gradients of 8192 tokens 226 against 168 us).
+constexpr int kRingBytes = 74 * 1024;
+constexpr int kRingCtas = 3;
+constexpr int kRingSlots = 8;  // slots of the gradient's dot products
+constexpr int kRingSmem = kRingBytes + 2 * kRingWarps * kRingSlots * 4;  // and their partial sums
 
 // One unit of the ring: the k rows' pieces, then the token's own (residual or gradient).
 struct RingUnit {
@@ -499,14 +506,12 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
 // One CTA per token (grid-stride): warp q takes chunks q, q + 4, ... of the row, a running
 // sequence of units over all its tokens; the k <= 8 products are summed over the lanes, then
 // over the warps, in fixed trees.
-constexpr int kRingSlots = 8;
-
 template <typename T, int kDepth>
 __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_grad_ring_kernel(const RowArgs a, int nvec, int nchunk) {
     constexpr int n = 16 / sizeof(T);
     using P = Pack<T, n>;
     extern __shared__ uint4 ring[];
-    __shared__ float part[2][kRingWarps][kRingSlots];
+    float (*part)[kRingWarps][kRingSlots] = reinterpret_cast<float (*)[kRingWarps][kRingSlots]>(ring + kRingBytes / 16);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (a.k + 1) * 32;
     uint4 *mine = ring + (size_t)warp * kDepth * per;
@@ -695,12 +700,6 @@ static cudaError_t unsort_grad_as(const RowArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, token_unsort_grad_kernel<T, V>, a, a.H / V);
 }
 
-// CTAs an SM for a ring of `smem` bytes (its grids are persistent).
-static int ring_ctas(size_t smem) {
-    const int n = (int)(222 * 1024 / (smem + 1024));
-    return n < 1 ? 1 : (n > 8 ? 8 : n);
-}
-
 // Units in flight a warp: as many of 8, 4, 2, 1 as fit.
 static int ring_depth(int rows) {
     int d = 8;
@@ -711,26 +710,24 @@ static int ring_depth(int rows) {
 template <typename T, int kDepth>
 static cudaError_t unsort_ring_as(const RowArgs &a, cudaStream_t stream) {
     const int nvec = a.H / (16 / (int)sizeof(T)), nchunk = (nvec + 31) / 32;
-    const size_t smem = (size_t)kRingWarps * kDepth * (a.k + (a.res ? 1 : 0)) * 512;
     const auto fn = token_unsort_ring_kernel<T, kDepth>;
-    cudaError_t err = ensure_smem((const void *)fn, smem);
+    cudaError_t err = ensure_smem((const void *)fn, kRingSmem);
     if (err != cudaSuccess) return err;
     const int wpt = nchunk >= 4 ? 4 : nchunk >= 2 ? 2 : 1;  // warps a token
     const int64_t ctas = ((int64_t)a.M * wpt + kRingWarps - 1) / kRingWarps;
     cudaLaunchAttribute attrs[2];
-    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(ctas, ring_ctas(smem))), dim3(32 * kRingWarps), smem, stream, attrs, 0);
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(ctas, kRingCtas)), dim3(32 * kRingWarps), kRingSmem, stream, attrs, 0);
     return cudaLaunchKernelEx(&cfg, fn, a, nvec, nchunk, wpt);
 }
 
 template <typename T, int kDepth>
 static cudaError_t unsort_grad_ring_as(const RowArgs &a, cudaStream_t stream) {
     const int nvec = a.H / (16 / (int)sizeof(T)), nchunk = (nvec + 31) / 32;
-    const size_t smem = (size_t)kRingWarps * kDepth * (a.k + 1) * 512;
     const auto fn = token_unsort_grad_ring_kernel<T, kDepth>;
-    cudaError_t err = ensure_smem((const void *)fn, smem);
+    cudaError_t err = ensure_smem((const void *)fn, kRingSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
-    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(a.M, ring_ctas(smem))), dim3(32 * kRingWarps), smem, stream, attrs, 0);
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(a.M, kRingCtas)), dim3(32 * kRingWarps), kRingSmem, stream, attrs, 0);
     return cudaLaunchKernelEx(&cfg, fn, a, nvec, nchunk);
 }
 
