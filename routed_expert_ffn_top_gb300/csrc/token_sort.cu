@@ -15,6 +15,8 @@
 //
 // All sums are fp32 in fixed orders (slots ascending; columns by thread, then a fixed tree),
 // so results are bitwise reproducible.  A value is rounded once, when it is stored.
+#include <type_traits>
+
 #include "moe_internal.cuh"
 #include "ptx.cuh"
 
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kGradThreads) token_unsort_grad_kernel(const R
 // registers.  Here each lane copies its own pieces of the next kDepth units into its own slots
 // of shared memory (cp.async), so a warp has kDepth units in flight and no thread waits for
 // another.  The arithmetic and its order per element are those of the form above.
-constexpr int kRingWarps = 4;
+constexpr int kRingWarps = 8;
 // Shared memory of a CTA, whatever part its slots fill: three CTAs an SM, in a grid that fills
 // the SMs once.  Every such launch asks for the same size: with sizes of their own, a grid that
 // starts while another drains found holes that fit two CTAs on a few SMs, and the third ran
@@ -400,10 +402,27 @@ __device__ __forceinline__ void ring_issue(const RowArgs &a, const void *rows, i
     const bool in = u.vi < nvec;
     for (int j = 0; j < a.k; ++j) {
         const int row = __shfl_sync(0xffffffffu, row_l, j);
-        if (in && row >= 0)
-            cp_async_16(slot + j * 32 + lane, static_cast<const T *>(rows) + (int64_t)row * ldrows + (int64_t)u.vi * n);
+        // a dropped route's slot is filled with zeros, from no address of its own
+        if (in)
+            cp_async_16_zfill(slot + j * 32 + lane,
+                              static_cast<const T *>(rows) + (row >= 0 ? (int64_t)row * ldrows + (int64_t)u.vi * n : 0),
+                              row >= 0 ? 16u : 0u);
     }
     if (own && in) cp_async_16(slot + a.k * 32 + lane, static_cast<const T *>(own) + u.m * ldown + (int64_t)u.vi * n);
+}
+
+// One 16-byte piece as fp32.
+template <typename T>
+__device__ __forceinline__ void ring_load(const uint4 *p, float (&v)[16 / sizeof(T)]) {
+    const uint4 u = *p;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+        v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+    } else {
+        const T *t = reinterpret_cast<const T *>(&u);
+#pragma unroll
+        for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = Elem<T>::load(t[i]);
+    }
 }
 
 // route_row entry of lane j < k for token m, -1 for a dropped or unknown row.
@@ -439,15 +458,15 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
     pdl_wait();
     pdl_launch_dependents();
 
-    // indices and weights of the token the copies are at and of the one the sums are at
-    int row_a = -1, row = -1;
-    float w = 1.0f, w_n = 1.0f;
-    int row_n = -1;
-    auto weight = [&](int64_t m) { return a.w && lane < a.k ? a.w[m * a.k + lane] : 1.0f; };
+    // rows of the token the copies are at; weights of the one the sums are at and of the next
+    int row_a = -1;
+    float w = 0.0f, w_n = 0.0f;
+    // a dropped route's weight is zero, whatever the caller's says
+    auto weight = [&](int64_t m) { return ring_row(a, m) < 0 ? 0.0f : (a.w ? a.w[m * a.k + lane] : 1.0f); };
     if (now.m < a.M) {
-        row = row_a = ring_row(a, now.m);
+        row_a = ring_row(a, now.m);
         w = weight(now.m);
-        if (now.m + step < a.M) row_n = ring_row(a, now.m + step), w_n = weight(now.m + step);
+        if (now.m + step < a.M) w_n = weight(now.m + step);
     }
     int slot_in = 0, slot_out = 0;
     auto issue = [&]() {
@@ -470,20 +489,14 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
         float acc[n];
 #pragma unroll
         for (int i = 0; i < n; ++i) acc[i] = 0.0f;
-        if (a.res && in) {
-            const P r = *reinterpret_cast<const P *>(slot + a.k * 32 + lane);
-#pragma unroll
-            for (int i = 0; i < n; ++i) acc[i] = Elem<T>::load(r.v[i]);
-        }
+        if (a.res && in) ring_load<T>(slot + a.k * 32 + lane, acc);
 #pragma unroll 8
         for (int j = 0; j < a.k; ++j) {
-            const int rj = __shfl_sync(0xffffffffu, row, j);
             const float wj = __shfl_sync(0xffffffffu, w, j);
-            if (in && rj >= 0) {
-                const P p = *reinterpret_cast<const P *>(slot + j * 32 + lane);
+            float v[n];
+            ring_load<T>(slot + j * 32 + lane, v);
 #pragma unroll
-                for (int i = 0; i < n; ++i) acc[i] = fmaf(wj, Elem<T>::load(p.v[i]), acc[i]);
-            }
+            for (int i = 0; i < n; i += 2) ffma2(acc[i], acc[i + 1], wj, v[i], v[i + 1]);
         }
         if (in) {
             P o;
@@ -496,14 +509,14 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
         const int64_t m = now.m;
         now.advance(q, wpt, nchunk, step);
         if (now.m != m) {
-            row = row_n, w = w_n;
-            if (now.m + step < a.M) row_n = ring_row(a, now.m + step), w_n = weight(now.m + step);
+            w = w_n;
+            if (now.m + step < a.M) w_n = weight(now.m + step);
         }
     }
     cp_async_wait_all();
 }
 
-// One CTA per token (grid-stride): warp q takes chunks q, q + 4, ... of the row, a running
+// One CTA per token (grid-stride): warp q takes chunks q, q + 8, ... of the row, a running
 // sequence of units over all its tokens; the k <= 8 products are summed over the lanes, then
 // over the warps, in fixed trees.
 template <typename T, int kDepth>
@@ -569,11 +582,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_grad_ring_kernel
             const uint4 *slot = mine + slot_out * per;
             const bool in = vi < nvec;
             float g[n];
-            if (in) {
-                const P p = *reinterpret_cast<const P *>(slot + a.k * 32 + lane);
-#pragma unroll
-                for (int i = 0; i < n; ++i) g[i] = Elem<T>::load(p.v[i]);
-            }
+            ring_load<T>(slot + a.k * 32 + lane, g);
 #pragma unroll
             for (int s = 0; s < kRingSlots; ++s) {
                 if (s >= a.k) break;
@@ -583,10 +592,11 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_grad_ring_kernel
                 if (in && at >= 0) {
                     P o;
                     if (v >= 0) {
-                        const P y = *reinterpret_cast<const P *>(slot + s * 32 + lane);
+                        float y[n];
+                        ring_load<T>(slot + s * 32 + lane, y);
 #pragma unroll
                         for (int i = 0; i < n; ++i) {
-                            dot[s] = fmaf(g[i], Elem<T>::load(y.v[i]), dot[s]);
+                            dot[s] = fmaf(g[i], y[i], dot[s]);
                             o.v[i] = Elem<T>::store(w * g[i]);
                         }
                     } else {
@@ -700,20 +710,25 @@ static cudaError_t unsort_grad_as(const RowArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, token_unsort_grad_kernel<T, V>, a, a.H / V);
 }
 
+// Whether `depth` units of `rows` pieces a warp fit a CTA's slots.
+static bool ring_fits(int rows, int depth) { return kRingWarps * depth * rows * 512 <= kRingBytes; }
+
 // Units in flight a warp: as many of 8, 4, 2, 1 as fit.
 static int ring_depth(int rows) {
     int d = 8;
-    while (d > 1 && kRingWarps * d * rows * 512 > kRingBytes) d /= 2;
+    while (d > 1 && !ring_fits(rows, d)) d /= 2;
     return d;
 }
 
 template <typename T, int kDepth>
 static cudaError_t unsort_ring_as(const RowArgs &a, cudaStream_t stream) {
+    if (!ring_fits(a.k + (a.res ? 1 : 0), kDepth)) return cudaErrorInvalidValue;
     const int nvec = a.H / (16 / (int)sizeof(T)), nchunk = (nvec + 31) / 32;
     const auto fn = token_unsort_ring_kernel<T, kDepth>;
     cudaError_t err = ensure_smem((const void *)fn, kRingSmem);
     if (err != cudaSuccess) return err;
-    const int wpt = nchunk >= 4 ? 4 : nchunk >= 2 ? 2 : 1;  // warps a token
+    int wpt = 1;  // warps a token
+    while (wpt < kRingWarps && wpt * 2 <= nchunk) wpt *= 2;
     const int64_t ctas = ((int64_t)a.M * wpt + kRingWarps - 1) / kRingWarps;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(ctas, kRingCtas)), dim3(32 * kRingWarps), kRingSmem, stream, attrs, 0);
@@ -722,6 +737,7 @@ static cudaError_t unsort_ring_as(const RowArgs &a, cudaStream_t stream) {
 
 template <typename T, int kDepth>
 static cudaError_t unsort_grad_ring_as(const RowArgs &a, cudaStream_t stream) {
+    if (!ring_fits(a.k + 1, kDepth)) return cudaErrorInvalidValue;
     const int nvec = a.H / (16 / (int)sizeof(T)), nchunk = (nvec + 31) / 32;
     const auto fn = token_unsort_grad_ring_kernel<T, kDepth>;
     cudaError_t err = ensure_smem((const void *)fn, kRingSmem);
@@ -743,7 +759,11 @@ static cudaError_t unsort_ring(const RowArgs &a, cudaStream_t stream) {
 
 template <typename T>
 static cudaError_t unsort_grad_ring(const RowArgs &a, cudaStream_t stream) {
-    return ring_depth(a.k + 1) == 8 ? unsort_grad_ring_as<T, 8>(a, stream) : unsort_grad_ring_as<T, 4>(a, stream);
+    switch (ring_depth(a.k + 1)) {
+        case 8: return unsort_grad_ring_as<T, 8>(a, stream);
+        case 4: return unsort_grad_ring_as<T, 4>(a, stream);
+        default: return unsort_grad_ring_as<T, 2>(a, stream);
+    }
 }
 
 cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k, int H,
@@ -759,16 +779,19 @@ cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k
 }
 
 // Calls F<T, V>(args, stream) for the element type and an access of vb bytes; 16-byte rows go to
-// the ring forms where `RING` takes them.
+// the ring forms where they fit (unsort up to 17 slots and a residual, its gradient up to 8).
 #define MOE_ROW_DISPATCH(F, RING, takes)                                                             \
     const int vb = vec_bytes(a, dtype == MOE_DT_F32 ? 4 : 2);                                        \
     if (vb == 16 && (takes)) {                                                                       \
         if (dtype == MOE_DT_F32) return RING<float>(a, stream);                                      \
         return dtype == MOE_DT_F16 ? RING<__half>(a, stream) : RING<__nv_bfloat16>(a, stream);       \
     }                                                                                                \
-    if (dtype == MOE_DT_F32) return F<float, 1>(a, stream);                                          \
-    if (dtype == MOE_DT_F16) return vb >= 4 ? F<__half, 2>(a, stream) : F<__half, 1>(a, stream);     \
-    return vb >= 4 ? F<__nv_bfloat16, 2>(a, stream) : F<__nv_bfloat16, 1>(a, stream);
+    if (dtype == MOE_DT_F32) return vb == 16 ? F<float, 4>(a, stream) : F<float, 1>(a, stream);      \
+    if (dtype == MOE_DT_F16)                                                                         \
+        return vb == 16 ? F<__half, 8>(a, stream)                                                    \
+                        : vb == 4 ? F<__half, 2>(a, stream) : F<__half, 1>(a, stream);               \
+    return vb == 16 ? F<__nv_bfloat16, 8>(a, stream)                                                 \
+                    : vb == 4 ? F<__nv_bfloat16, 2>(a, stream) : F<__nv_bfloat16, 1>(a, stream);
 
 cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
                                 const int32_t *route_row, const float *w, const void *residual,
@@ -776,7 +799,7 @@ cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M,
     RowArgs a{};
     a.a = rows, a.res = residual, a.out = out, a.lda = ldr, a.ldres = ldres, a.ldout = ldo;
     a.route_row = route_row, a.w = w, a.M = M, a.k = k, a.H = H;
-    MOE_ROW_DISPATCH(unsort_as, unsort_ring, true)
+    MOE_ROW_DISPATCH(unsort_as, unsort_ring, ring_fits(k + (residual ? 1 : 0), 1))
 }
 
 cudaError_t launch_token_unsort_grad(const void *gout, int64_t ldo, const void *rows, int64_t ldr,

@@ -81,7 +81,8 @@ def strided(t, pad):
 
 ROWS = [(1, 8, 128, 2048, 0, 0), (5, 3, 8, 1, 0.2, 0), (21, 8, 128, 2048, 0, 0), (64, 2, 16, 255, 0.1, 0),
         (77, 5, 24, 1033, 0.05, 0), (40, 32, 64, 514, 0.05, 2), (33, 9, 16, 8192 + 8, 0, 8), (300, 8, 32, 96, 1.0, 0),
-        (19, 6, 8, 640, 0.1, 1), (700, 1, 8, 130, 0, 3)]
+        (19, 6, 8, 640, 0.1, 1), (700, 1, 8, 130, 0, 3), (30, 17, 32, 520, 0.05, 0), (30, 18, 32, 520, 0.05, 8),
+        (9, 32, 64, 1024, 0.05, 0), (50, 9, 16, 776, 0, 0), (60, 2, 8, 4096, 0.1, 0)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
