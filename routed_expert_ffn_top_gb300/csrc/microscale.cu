@@ -20,21 +20,29 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 
-// Eight consecutive elements; kVec: 16-byte accesses.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
-    if constexpr (kVec) {
-        constexpr int n = 16 / sizeof(T);
+// Sixteen consecutive elements by accesses of kBytes (32, 16, or the element's).
+template <typename T, int kBytes>
+__device__ __forceinline__ void load16(const T *p, float (&v)[16]) {
+    if constexpr (kBytes >= 16) {
+        alignas(32) uint32_t u[4 * sizeof(T)];
+        constexpr int words = kBytes / 4;
 #pragma unroll
-        for (int i = 0; i < 8; i += n) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p + i);
-            const T *t = reinterpret_cast<const T *>(&u);
-#pragma unroll
-            for (int q = 0; q < n; ++q) v[i + q] = to_f32(t[q]);
+        for (int i = 0; i < (int)(4 * sizeof(T)); i += words) {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(p) + i;
+            if constexpr (kBytes == 32)
+                asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                             : "=r"(u[i]), "=r"(u[i + 1]), "=r"(u[i + 2]), "=r"(u[i + 3]), "=r"(u[i + 4]),
+                               "=r"(u[i + 5]), "=r"(u[i + 6]), "=r"(u[i + 7])
+                             : "l"(q));
+            else
+                *reinterpret_cast<uint4 *>(&u[i]) = *reinterpret_cast<const uint4 *>(q);
         }
+        const T *t = reinterpret_cast<const T *>(u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = to_f32(t[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+        for (int i = 0; i < 16; ++i) v[i] = to_f32(p[i]);
     }
 }
 
@@ -47,61 +55,45 @@ struct QuantArgs {
     uint8_t *codes, *scales;
 };
 
-// A unit is 512 columns of one row, one warp: lane l takes columns 8 l and 256 + 8 l, four
-// lanes share a block.  512 columns are 16 scale bytes, one store.  With route_row a token is
+// A unit is 512 columns of one row, one warp: lane l takes columns 16 l to 16 l + 15, two lanes
+// share a block.  512 columns are 16 scale bytes, one store.  With route_row a token is
 // quantised once and stored k times (tail rows of dropped routes as zeros).
 // Memory bound: elem + 1/2 + 1/32 bytes a value.
-template <typename T, bool kVec>
+template <typename T, int kBytes>
 __global__ void __launch_bounds__(256) microscale_quantize_kernel(const QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, c0 = blockIdx.y * 512;
+    const bool in = c0 + lane * 16 < a.cols;
     const int64_t stride = (int64_t)gridDim.x * 8;
     for (int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows; m += stride) {
-        const T *x = static_cast<const T *>(a.x) + m * a.ldx + c0 + lane * 8;
-        const bool in[2] = {c0 + lane * 8 < a.cols, c0 + 256 + lane * 8 < a.cols};
-        float v[2][8];
+        float v[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[h][i] = 0.0f;
-            if (in[h]) load8<T, kVec>(x + 256 * h, v[h]);
-        }
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        if (in) load16<T, kBytes>(static_cast<const T *>(a.x) + m * a.ldx + c0 + lane * 16, v);
         const int row_l = a.route_row && lane < a.k ? a.route_row[m * a.k + lane] : 0;
-        uint32_t code[2];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+            top = b > top ? b : top;
+        }
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, top, 1);
+        const uint32_t byte = microscale_byte(other > top ? other : top);
+        const float inv = microscale_inverse(byte);
+        float f[2][8];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i / 8][i % 8] = v[i] * inv;
+        uint2 code = {fp4x8(f[0]), fp4x8(f[1])};
+        if (byte == 255u) code = {0u, 0u};
+        // the warp's 16 scale bytes, block b's in lane 2 b: pairs, then fours, then all in lane 0
+        uint32_t s4 = byte | __shfl_down_sync(0xffffffffu, byte, 2) << 8;
+        s4 |= __shfl_down_sync(0xffffffffu, s4, 4) << 16;
         uint4 sc;
-        uint32_t sb[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t b = __float_as_uint(v[h][i]) & 0x7fffffffu;
-                top = b > top ? b : top;
-            }
-            uint32_t o = __shfl_xor_sync(0xffffffffu, top, 1);
-            top = o > top ? o : top;
-            o = __shfl_xor_sync(0xffffffffu, top, 2);
-            top = o > top ? o : top;
-            const uint32_t byte = microscale_byte(top);
-            const float inv = microscale_inverse(byte);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[h][i] *= inv;
-            code[h] = byte == 255u ? 0u : fp4x8(v[h]);
-            sb[h] = byte;
-        }
-        // the warp's 16 scale bytes: block b of half h in lane 4 b
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t lo = 0, hi = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                lo |= __shfl_sync(0xffffffffu, sb[h], 4 * b) << (8 * b);
-                hi |= __shfl_sync(0xffffffffu, sb[h], 16 + 4 * b) << (8 * b);
-            }
-            if (h == 0) sc.x = lo, sc.y = hi;
-            else sc.z = lo, sc.w = hi;
-        }
+        sc.x = s4;
+        sc.y = __shfl_down_sync(0xffffffffu, s4, 8);
+        sc.z = __shfl_down_sync(0xffffffffu, s4, 16);
+        sc.w = __shfl_down_sync(0xffffffffu, s4, 24);
         const int n = a.route_row ? a.k : 1;
         for (int j = 0; j < n; ++j) {
             int64_t at = m;
@@ -112,10 +104,8 @@ __global__ void __launch_bounds__(256) microscale_quantize_kernel(const QuantArg
                 at = live ? row : ~row;
                 if (at >= a.rows * a.k) continue;
             }
-            uint8_t *dst = a.codes + at * (a.cols / 2) + (c0 + lane * 8) / 2;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (in[h]) *reinterpret_cast<uint32_t *>(dst + 128 * h) = live ? code[h] : 0u;
+            if (in)
+                *reinterpret_cast<uint2 *>(a.codes + at * (a.cols / 2) + (c0 + lane * 16) / 2) = live ? code : uint2{0u, 0u};
             if (lane == 0)
                 *reinterpret_cast<uint4 *>(a.scales + at * a.pitch + c0 / 32) = live ? sc : uint4{0, 0, 0, 0};
         }
@@ -215,10 +205,13 @@ static dim3 rows_by_chunks(int64_t rows, int cols) {
 
 template <typename T>
 static cudaError_t quantize_as(const QuantArgs &a, cudaStream_t stream) {
-    const bool vec = (reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.ldx * sizeof(T))) % 16 == 0;
+    const uint64_t bits = reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.ldx * sizeof(T));
+    const auto fn = bits % 32 == 0   ? microscale_quantize_kernel<T, 32>
+                    : bits % 16 == 0 ? microscale_quantize_kernel<T, 16>
+                                     : microscale_quantize_kernel<T, (int)sizeof(T)>;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(rows_by_chunks(a.rows, a.cols), dim3(256), 0, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, vec ? microscale_quantize_kernel<T, true> : microscale_quantize_kernel<T, false>, a);
+    return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
 template <typename T>
