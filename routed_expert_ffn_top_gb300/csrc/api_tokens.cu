@@ -1,5 +1,7 @@
 // api_tokens.cu -- C entry points (include/moe.h) of the token sort and of 4-bit block
 // floating point: argument validation, tensor maps, and the 4-bit expert step.
+#include <string.h>
+
 #include "moe_internal.cuh"
 
 using namespace moe;
@@ -162,7 +164,8 @@ static int check_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_
 // one entry, a copy brings one chunk, and a row's bytes past its end read as zeros (a stage's
 // box would zero-fill whole chunks past K, which costs as much as copying them).
 static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
-                         const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K, bool gated) {
+                         const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K, bool gated,
+                         void *y, int64_t ldy, int elem) {
     const MicroscaleTile t = microscale_tile(rows, E);
     const uint64_t row = (uint64_t)K / 2;
     const bool deep = K % (256 * t.chunks) == 0;
@@ -179,6 +182,12 @@ static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8
     const uint32_t ab[3] = {128, m, depth};
     const uint64_t bd[4] = {inner, wrows, halves, chunks}, bs[3] = {row, up * row, 128};
     const uint32_t bb[4] = {128, bn, two, depth};
+    // y in bytes, boxes of 64 bytes x 32 rows, where its pointer and pitch allow tensor stores
+    tm->bulk = y && t.m == 128 && (reinterpret_cast<uintptr_t>(y) | (uint64_t)(ldy * elem)) % 16 == 0;
+    const uint64_t yd[2] = {(uint64_t)N * elem, (uint64_t)rows}, ys[1] = {(uint64_t)(ldy * elem)};
+    const uint32_t yb[2] = {64, 32};
+    if (!tm->bulk) memset(&tm->y, 0, sizeof tm->y);
+    else if (!make_tmap_bytes(&tm->y, y, 2, yd, ys, yb, CU_TENSOR_MAP_SWIZZLE_64B)) return false;
     return make_tmap_bytes(&tm->x, x_codes, 3, ad, as, ab, sw128) &&
            make_tmap_bytes(&tm->w, w_codes, 4, bd, bs, bb, sw128);
 }
@@ -193,7 +202,7 @@ extern "C" int moe_microscale_product(const uint8_t *x_codes, const uint8_t *x_s
     if (rows == 0) return MOE_OK;
     if ((rc = check_matrix(y, ldy, N, dtype_bytes(dtype))) != MOE_OK) return rc;
     MicroscaleMaps tm;
-    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K, false)) return MOE_ERR_CUDA;
+    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K, false, y, ldy, dtype_bytes(dtype))) return MOE_ERR_CUDA;
     return cuda_status(launch_microscale_gemm(tm, rows, offsets, E, N, K, dtype, y, ldy, nullptr, nullptr,
                                               static_cast<int32_t *>(workspace),
                                               static_cast<cudaStream_t>(stream)));
@@ -209,7 +218,7 @@ extern "C" int moe_microscale_gated_product(const uint8_t *x_codes, const uint8_
     if (rows == 0) return MOE_OK;
     if (!codes || !scales || !aligned(codes, 16) || !aligned(scales, 16)) return MOE_ERR_INVALID_ARG;
     MicroscaleMaps tm;
-    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K, true)) return MOE_ERR_CUDA;
+    if (!product_maps(&tm, x_codes, x_scales, rows, w_codes, w_scales, E, N, K, true, nullptr, 0, 0)) return MOE_ERR_CUDA;
     return cuda_status(launch_microscale_gemm(tm, rows, offsets, E, N, K, MOE_DT_BF16, nullptr, 0, codes, scales,
                                               static_cast<int32_t *>(workspace),
                                               static_cast<cudaStream_t>(stream)));

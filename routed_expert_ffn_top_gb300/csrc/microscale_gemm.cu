@@ -15,8 +15,9 @@
 // computes p = SiLU(g) u in fp32 and quantises it in the epilogue, so g and u never leave the
 // chip.
 //
-// Per CTA, 11 warps: 0-3 drain the accumulators, 4-7 bring the scales through shared memory into
-// tensor memory, 8 and 10 issue the copies of codes, 9 the MMAs.  A stage is 256 of K: 128-byte rows of
+// Per CTA, 16 warps: 0-3 and 12-15 drain the accumulators, 4-7 bring the scales through shared
+// memory into tensor memory, 8 and 10 issue the copies of codes, 9 the MMAs, 11 is idle (a warp
+// reads the tensor-memory lanes of its number modulo 4).  A stage is 256 of K: 128-byte rows of
 // codes, 128-byte swizzled, and 16-byte rows of scales (a copy's inner extent is 16 bytes at
 // least, so two stages share their scale bytes and each uses its half).  The MMA reads the
 // scale of row r at lane r % 32, column r / 32, four K blocks a 32-bit column, repeated in the
@@ -29,9 +30,10 @@
 
 namespace moe {
 
-constexpr int kMxThreads = 352;
+constexpr int kMxThreads = 512;
 constexpr int kMxMaxStages = 8;
 constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
+constexpr int kMxStaging = 2048;  // bytes a warp stages for its stores: 32 rows of 64
 
 // Two tiles.  kTok = 128: 128 rows of x as the MMA's M side, kCh = 192 channels as its N side.
 // kTok = 32, for small groups: the sides change places, 128 channels are M and up to 32 rows
@@ -61,7 +63,8 @@ struct MxTile {
     static constexpr int kSfCols = kGroups * (kACols + kBPad);  // per stage
     static constexpr int kSfCol0 = 2 * kB;                 // after the two accumulators
     static constexpr uint32_t kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
-    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kScaleBufs * kScaleBytes + 1024;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + kScaleBufs * kScaleBytes + 1024 +
+                                    (kSwap ? 0 : 8 * kMxStaging);
     static_assert(kStageBytes % 1024 == 0 && kScaleBytes % 512 == 0, "stage alignment");
     static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
     static_assert(kStages <= kMxMaxStages, "barriers");
@@ -103,7 +106,7 @@ struct MxArgs {
     int64_t rows;
     int E, N, K;
     int nct;                 // column tiles
-    int vec;                 // y rows allow 32-byte stores
+    int vec, bulk;           // y rows allow 32-byte stores, tensor stores
     void *y;
     int64_t ldy;
     uint8_t *codes, *scales;  // gated output
@@ -203,9 +206,13 @@ __device__ __forceinline__ void store_row32(const MxArgs &a, int64_t row, int n,
         if (n + i < a.N) put_f32(dst + i, __uint_as_float(v[i]));
 }
 
-// SiLU with the approximate division (2 units in the last place): p goes to 4 bits next.  Below
-// g = -87 it gives 0 for values under 2^-119.
-__device__ __forceinline__ float silu_fast(float g) { return __fdividef(g, 1.0f + expf(-g)); }
+// SiLU(g) u by the approximate reciprocal (one unit in the last place): p goes to 4 bits next.
+// Below g = -87 it gives 0 for values under 2^-119.
+__device__ __forceinline__ float gate(float g, float u) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-g)));
+    return g * r * u;
+}
 
 // A CTA's units: u = blockIdx.x, blockIdx.x + gridDim.x, ...; unit u is channel tile u % nct of
 // row tile u / nct.  Each warp walks them on its own, without dividing, and finds the next
@@ -241,23 +248,64 @@ struct MxWalk {
     }
 };
 
-// The scale words of stage `part` of a copy for one row: word q of 128 of K to w[q * kStep].
-// Rows are 64 bytes, their 16-byte pieces exchanged as the 64-byte swizzle does.
+// The 16 scale bytes (512 of K) number `piece` of a row of a copy.  Rows are 64 bytes, their
+// 16-byte pieces exchanged as the 64-byte swizzle does.
+__device__ __forceinline__ uint4 mx_scale_piece(const unsigned char *base, int row, int piece) {
+    return *reinterpret_cast<const uint4 *>(base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+
+// The words of a stage to w[0], w[kStep], ...: all four of a piece, or one half of it.
 template <int kGroups, int kStep>
-__device__ __forceinline__ void mx_scale_words(const unsigned char *base, int row, int part,
-                                               const uint32_t (&mask)[kGroups], uint32_t *w) {
-    const int piece = kGroups == 4 ? part : part >> 1;
-    const unsigned char *p = base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+__device__ __forceinline__ void mx_scale_words(const uint4 &v, bool upper, const uint32_t (&mask)[kGroups], uint32_t *w) {
     if constexpr (kGroups == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
         w[0] = v.x & mask[0];
         w[kStep] = v.y & mask[1];
         w[2 * kStep] = v.z & mask[2];
         w[3 * kStep] = v.w & mask[3];
     } else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p + (part & 1) * 8);
-        w[0] = v.x & mask[0];
-        w[kStep] = v.y & mask[1];
+        w[0] = (upper ? v.z : v.x) & mask[0];
+        w[kStep] = (upper ? v.w : v.y) & mask[1];
+    }
+}
+
+// 32 rows x 32 columns of a warp by tensor stores of 64-byte rows through its staging memory (a
+// lane's own 32 bytes of a row at a time, 32 rows an instruction, took up to a third of a
+// product's time).  byte0: of the first column in its row.
+template <bool kRead>
+__device__ __forceinline__ void bulk_store_wait() {
+    if constexpr (kRead) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    else asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mx_store_bulk(const CUtensorMap &tm_y, unsigned char *staging, int byte0, int row0,
+                                              int lane, const uint32_t (&v)[32]) {
+    constexpr int kParts = sizeof(T) / 2;  // 64-byte rows: 32 columns of 16 bits, 16 of 32
+#pragma unroll
+    for (int q = 0; q < kParts; ++q) {
+        if (lane == 0) bulk_store_wait<true>();  // the staging memory's last store has been read
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 o;
+            if constexpr (sizeof(T) == 4) {
+                o = make_uint4(v[16 * q + 4 * i], v[16 * q + 4 * i + 1], v[16 * q + 4 * i + 2], v[16 * q + 4 * i + 3]);
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    w[p] = pack2<T>(__uint_as_float(v[8 * i + 2 * p]), __uint_as_float(v[8 * i + 2 * p + 1]));
+                o = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4 *>(staging + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&tm_y)),
+                "r"(byte0 + 64 * q), "r"(row0), "r"(smem_u32(staging))
+                : "memory");
     }
 }
 
@@ -273,7 +321,7 @@ __device__ __forceinline__ void mx_store_columns(const MxArgs &a, int row0, int 
 
 // Small gated tile: warps 0 and 1 hold g of 64 channels, warps 2 and 3 u of the same; u goes
 // through shared memory, a block of 32 channels is a warp's lanes.
-__device__ __forceinline__ void mx_gate_columns(const MxArgs &a, float *exchange, int row0, int nrows, int n0, int warp,
+__device__ __forceinline__ void mx_gate_columns(const MxArgs &a, float *exchange, int group, int row0, int nrows, int n0, int warp,
                                                 int lane, const uint32_t (&v)[32], bool last) {
     float *u = exchange + (32 * warp + lane) % 64;
     if (warp >= 2) {
@@ -281,13 +329,13 @@ __device__ __forceinline__ void mx_gate_columns(const MxArgs &a, float *exchange
         for (int j = 0; j < 32; ++j)
             if (j < nrows) u[64 * j] = __uint_as_float(v[j]);
     }
-    named_bar_sync(1, 128);
+    named_bar_sync(1 + 2 * group, 128);
     const int I = a.N / 2, n = n0 + 32 * warp;
     if (warp < 2 && n < I) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             if (j >= nrows) break;
-            const float p = silu_fast(__uint_as_float(v[j])) * u[64 * j];
+            const float p = gate(__uint_as_float(v[j]), u[64 * j]);
             const uint32_t byte = microscale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(p) & 0x7fffffffu));
             uint32_t c = byte == 255u ? 0u : fp4(p * microscale_inverse(byte)) << (4 * (lane & 7));
             c |= __shfl_xor_sync(0xffffffffu, c, 1);
@@ -314,7 +362,7 @@ __device__ __forceinline__ int mx_first_channel(const MxArgs &a, int e, int ct) 
 template <int kTok, int kOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
 microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                       const MxArgs a) {
+                       const __grid_constant__ CUtensorMap tm_y, const MxArgs a) {
     using G = MxTile<kTok>;
     constexpr bool kGated = kOut == 3;
     constexpr int kN = G::kB, kHalf = G::kCh / 2;
@@ -482,7 +530,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
             if (!mbar_wait_bounded(&ctl.done, 0)) ctl.abort = 1;
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // scales: copied kMxScaleK of K at a time, kScaleBufs copies ahead, by 16-byte cp.async
         // (a tensor copy of 64-byte rows takes 11 cycles a row, as long as the unit's codes
         // when K is short); every warp then needs all rows, hence the barrier
@@ -515,6 +563,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         for (int i = 0; i < G::kScaleBufs - 1; ++i) issue();
         // after a wait that gave up the loop runs on without waits, so that the barriers stay paired
         bool ok = true;
+        uint4 piece[G::kACols + G::kBCols];
         for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.nct; u += gridDim.x)
             for (int s = 0; s < nks; ++s) {
                 const int part = s % kPerScale;
@@ -531,12 +580,18 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                     const int left = nb - (s * G::kGroups + q) * 4;
                     mask[q] = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
                 }
-                const unsigned char *SA = scales + slot * G::kScaleBytes, *SB = SA + G::kA * 64;
+                const unsigned char *S = scales + slot * G::kScaleBytes;
+                const bool upper = G::kGroups == 2 && (part & 1);
+                if (!upper) {  // a piece serves two 256-deep stages
+#pragma unroll
+                    for (int c = 0; c < G::kACols + G::kBCols; ++c)
+                        piece[c] = mx_scale_piece(S, c * 32 + lane, G::kGroups == 4 ? part : part >> 1);
+                }
                 uint32_t wa[G::kGroups * G::kACols] = {}, wb[G::kGroups * G::kBPad] = {};
 #pragma unroll
-                for (int c = 0; c < G::kACols; ++c) mx_scale_words<G::kGroups, G::kACols>(SA, c * 32 + lane, part, mask, wa + c);
+                for (int c = 0; c < G::kACols; ++c) mx_scale_words<G::kGroups, G::kACols>(piece[c], upper, mask, wa + c);
 #pragma unroll
-                for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kGroups, G::kBPad>(SB, c * 32 + lane, part, mask, wb + c);
+                for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kGroups, G::kBPad>(piece[G::kACols + c], upper, mask, wb + c);
                 // the MMAs that read this slot's scales have completed
                 ok = ok && mx_warp_wait(&ctl.empty[stage], phase ^ 1u, ctl);
                 if (ok) {
@@ -554,18 +609,23 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                 if (++stage == G::kStages) stage = 0, phase ^= 1u;
             }
         cp_async_wait_all();
-    } else {
-        const uint32_t quad = (uint32_t)(32 * warp) << 16;
+    } else if (warp < 4 || warp >= 12) {
+        // two groups of four warps take the accumulators, and so the units, in turn
+        const int group = warp >> 3, w4 = warp & 3;
+        const uint32_t quad = (uint32_t)(32 * w4) << 16;
+        unsigned char *const staging = scales + G::kScaleBufs * G::kScaleBytes + (4 * group + w4) * kMxStaging;
         int local = 0;
         for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles), ++local) {
             const int buf = local & 1;
+            if (buf != group) continue;
             if (!mx_warp_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) {
                 if constexpr (!(kGated && G::kSwap)) break;
-                named_bar_sync(1, 128);  // a warp that does not give up waits here for the others
+                named_bar_sync(1 + 2 * group, 128);  // a warp that does not give up waits here for the others
                 continue;
             }
             tc_fence_after();
             const uint32_t d = ctl.tmem + quad + (uint32_t)(buf * kN);
+            const int n0 = x.ct * (kGated ? kHalf : G::kCh);
             if constexpr (G::kSwap) {
                 uint32_t v[32];
                 tmem_ld32(d, v);
@@ -573,40 +633,37 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.tempty[buf]);
-                if constexpr (!kGated) mx_store_columns<Out>(a, x.row0, x.nrows, x.ct * G::kCh + 32 * warp + lane, v);
-                else mx_gate_columns(a, exchange + buf * (32 * 64), x.row0, x.nrows, x.ct * kHalf, warp, lane, v, x.ct == a.nct - 1);
+                if constexpr (!kGated) mx_store_columns<Out>(a, x.row0, x.nrows, n0 + 32 * w4 + lane, v);
+                else mx_gate_columns(a, exchange + buf * (32 * 64), group, x.row0, x.nrows, n0, w4, lane, v, x.ct == a.nct - 1);
                 continue;
             }
-            const int64_t row = (int64_t)x.row0 + 32 * warp + lane;
-            const bool live = 32 * warp + lane < x.nrows;
-            if (32 * warp >= x.nrows) {
+            const int64_t row = (int64_t)x.row0 + 32 * w4 + lane;
+            const bool live = 32 * w4 + lane < x.nrows;
+            if (32 * w4 >= x.nrows) {
                 // no row of this warp's lanes: the accumulator holds nothing of the tile here
             } else if constexpr (!kGated) {
+                const bool bulk = a.bulk && 32 * w4 + 32 <= x.nrows;
 #pragma unroll 1
-                for (int c = 0; c < kN; c += 64) {
-                    uint32_t v[32], w[32];
+                for (int c = 0; c < kN && n0 + c < a.N; c += 32) {
+                    uint32_t v[32];
                     tmem_ld32(d + c, v);
-                    tmem_ld32(d + c + 32, w);
                     tmem_ld_wait(v);
-                    tmem_ld_wait(w);
-                    const int n = x.ct * kN + c;
-                    if (live && n < a.N) store_row32<Out>(a, row, n, v);
-                    if (live && n + 32 < a.N) store_row32<Out>(a, row, n + 32, w);
+                    if (bulk) mx_store_bulk<Out>(tm_y, staging, (n0 + c) * (int)sizeof(Out), x.row0 + 32 * w4, lane, v);
+                    else if (live) store_row32<Out>(a, row, n0 + c, v);
                 }
             } else {
                 const int I = a.N / 2;
 #pragma unroll 1
-                for (int c = 0; c < kHalf; c += 32) {
+                for (int c = 0; c < kHalf && n0 + c < I; c += 32) {
                     uint32_t g[32], up[32];
                     tmem_ld32(d + c, g);
                     tmem_ld32(d + kHalf + c, up);
                     tmem_ld_wait(g);
                     tmem_ld_wait(up);
-                    const int n = x.ct * kHalf + c;
                     uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        g[i] = __float_as_uint(silu_fast(__uint_as_float(g[i])) * __uint_as_float(up[i]));
+                        g[i] = __float_as_uint(gate(__uint_as_float(g[i]), __uint_as_float(up[i])));
                         const uint32_t b = g[i] & 0x7fffffffu;
                         top = b > top ? b : top;
                     }
@@ -620,9 +677,9 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                         for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(g[8 * q + i]) * inv;
                         o[q] = byte == 255u ? 0u : fp4x8(f);
                     }
-                    if (live && n < I) {
-                        *reinterpret_cast<uint4 *>(a.codes + row * (I / 2) + n / 2) = make_uint4(o[0], o[1], o[2], o[3]);
-                        a.scales[row * a.pitch + n / 32] = (uint8_t)byte;
+                    if (live) {
+                        *reinterpret_cast<uint4 *>(a.codes + row * (I / 2) + (n0 + c) / 2) = make_uint4(o[0], o[1], o[2], o[3]);
+                        a.scales[row * a.pitch + (n0 + c) / 32] = (uint8_t)byte;
                     }
                 }
                 if (live && x.ct == a.nct - 1)
@@ -632,8 +689,9 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.tempty[buf]);
         }
+        if (lane == 0) bulk_store_wait<false>();  // stores have left shared memory and are visible
         // rows past the last group (dropped routes): zeros
-        for (int64_t r = ctl.valid_rows + (int64_t)blockIdx.x; r < a.rows; r += gridDim.x) {
+        for (int64_t r = ctl.valid_rows + (int64_t)blockIdx.x; r < a.rows && group == 0; r += gridDim.x) {
             if constexpr (kGated) {
                 for (int i = threadIdx.x; i < a.N / 64; i += 128)
                     *reinterpret_cast<uint4 *>(a.codes + r * (a.N / 4) + 16 * i) = uint4{0, 0, 0, 0};
@@ -672,7 +730,7 @@ static cudaError_t gemm_as(const MicroscaleMaps &tm, MxArgs a, cudaStream_t stre
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)grid), dim3(kMxThreads), G::kSmem, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, fn, tm.x, tm.w, a);
+    return cudaLaunchKernelEx(&cfg, fn, tm.x, tm.w, tm.y, a);
 }
 
 template <int kTok>
@@ -696,6 +754,7 @@ cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const
     a.pitch = microscale_pitch(N / 2);
     const int elem = dtype == MOE_DT_F32 ? 4 : 2;
     a.vec = y && (reinterpret_cast<uintptr_t>(y) | (uint64_t)(ldy * elem)) % 32 == 0;
+    a.bulk = tm.bulk;
     const int out = codes ? 3 : dtype;
     return microscale_tile(rows, E).m == 128 ? gemm_tile<128>(tm, a, out, stream) : gemm_tile<32>(tm, a, out, stream);
 }

@@ -416,8 +416,8 @@ MicroscaleTile microscale_tile(int64_t rows, int E);
 // their scales.  Codes have a chunk dimension of K (128 bytes each) when K is a whole number of stages (`deep`); the
 // weights' have a gate/up dimension.
 struct MicroscaleMaps {
-    CUtensorMap x, w;
-    int deep;
+    CUtensorMap x, w, y;
+    int deep, bulk;
     const uint8_t *x_scales, *w_scales;
 };
 // codes == NULL: y [rows][N] of dtype; else the gated form, codes and scales of [rows][N / 2].
