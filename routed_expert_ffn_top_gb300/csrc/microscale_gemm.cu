@@ -206,12 +206,22 @@ __device__ __forceinline__ void store_row32(const MxArgs &a, int64_t row, int n,
         if (n + i < a.N) put_f32(dst + i, __uint_as_float(v[i]));
 }
 
-// SiLU(g) u by the approximate reciprocal (one unit in the last place): p goes to 4 bits next.
-// Below g = -87 it gives 0 for values under 2^-119.
+// SiLU(g) u = g u / (1 + 2^(-g log2 e)) by the approximate power and reciprocal: within 2^-21
+// (1 + |g| / 4) of its value for negative g, 2^-21 for others, and p goes to 4 bits next.  Below
+// g = -87 it gives 0 for values under 2^-119.  (expf and the division took the gated epilogue's
+// instructions from 8 to 16 a value.)
 __device__ __forceinline__ float gate(float g, float u) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-g)));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return g * r * u;
+}
+
+// The larger of t, |a| and |b|, a NaN if any is one.
+__device__ __forceinline__ float max_abs(float t, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(t), "f"(a), "f"(b));
+    return r;
 }
 
 // A CTA's units: u = blockIdx.x, blockIdx.x + gridDim.x, ...; unit u is channel tile u % nct of
@@ -660,21 +670,19 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                     tmem_ld32(d + kHalf + c, up);
                     tmem_ld_wait(g);
                     tmem_ld_wait(up);
-                    uint32_t top = 0;
+                    float p[32], top = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        g[i] = __float_as_uint(gate(__uint_as_float(g[i]), __uint_as_float(up[i])));
-                        const uint32_t b = g[i] & 0x7fffffffu;
-                        top = b > top ? b : top;
-                    }
-                    const uint32_t byte = microscale_byte(top);
+                    for (int i = 0; i < 32; ++i) p[i] = gate(__uint_as_float(g[i]), __uint_as_float(up[i]));
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) top = max_abs(top, p[i], p[i + 1]);
+                    const uint32_t byte = microscale_byte(__float_as_uint(top) & 0x7fffffffu);
                     const float inv = microscale_inverse(byte);
                     uint32_t o[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float f[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(g[8 * q + i]) * inv;
+                        for (int i = 0; i < 8; ++i) f[i] = p[8 * q + i] * inv;
                         o[q] = byte == 255u ? 0u : fp4x8(f);
                     }
                     if (live) {
