@@ -271,7 +271,7 @@ extern "C" int moe_microscale_ffn(const void *h, const moe_microscale_weights_t 
     if ((rc = check_routes(M, k)) != MOE_OK) return rc;
     if (M == 0) return MOE_OK;
     if (!h || !topk_ids || !topk_weights || !out || !workspace || !aligned(workspace, 256) ||
-        !aligned(h, 16) || !aligned(out, 16) || (residual && !aligned(residual, 16)))
+        !aligned(topk_ids, 4) || !aligned(h, 16) || !aligned(out, 16) || (residual && !aligned(residual, 16)))
         return MOE_ERR_INVALID_ARG;
     const int64_t R = (int64_t)M * k;
     const MicroscaleWs L = microscale_ws(w->E, w->H, w->I, R);
@@ -279,9 +279,16 @@ extern "C" int moe_microscale_ffn(const void *h, const moe_microscale_weights_t 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     int32_t *offsets = reinterpret_cast<int32_t *>(ws + L.offsets);
     int32_t *route_row = reinterpret_cast<int32_t *>(ws + L.route_row);
-    rc = moe_token_plan(topk_ids, M, k, w->E, offsets, reinterpret_cast<int32_t *>(ws + L.row_route), route_row, stream);
-    if (rc != MOE_OK) return rc;
-    rc = moe_microscale_quantize(h, w->H, MOE_DT_BF16, M, w->H, route_row, k, ws + L.x_codes, ws + L.x_scales, stream);
+    int32_t *row_route = reinterpret_cast<int32_t *>(ws + L.row_route);
+    if (R <= kPlanQuantizeRoutes) {
+        rc = cuda_status(launch_microscale_plan_quantize(static_cast<const __nv_bfloat16 *>(h), M, w->H, topk_ids, k, w->E,
+                                                         offsets, row_route, route_row, ws + L.x_codes, ws + L.x_scales,
+                                                         static_cast<cudaStream_t>(stream)));
+    } else {
+        rc = moe_token_plan(topk_ids, M, k, w->E, offsets, row_route, route_row, stream);
+        if (rc != MOE_OK) return rc;
+        rc = moe_microscale_quantize(h, w->H, MOE_DT_BF16, M, w->H, route_row, k, ws + L.x_codes, ws + L.x_scales, stream);
+    }
     if (rc != MOE_OK) return rc;
     rc = moe_microscale_gated_product(ws + L.x_codes, ws + L.x_scales, R, offsets, w->gate_up_codes,
                                       w->gate_up_scales, w->E, 2 * w->I, w->H, ws + L.p_codes, ws + L.p_scales,

@@ -59,57 +59,102 @@ struct QuantArgs {
 // share a block.  512 columns are 16 scale bytes, one store.  With route_row a token is
 // quantised once and stored k times (tail rows of dropped routes as zeros).
 // Memory bound: elem + 1/2 + 1/32 bytes a value.
+// row_l: in lane j < k, the route_row entry of slot j (with a.k == 1 and whole == true: row m).
+template <typename T, int kBytes>
+__device__ __forceinline__ void quantize_unit(const QuantArgs &a, int64_t m, int c0, int row_l, bool whole) {
+    const int lane = threadIdx.x & 31;
+    const bool in = c0 + lane * 16 < a.cols;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    if (in) load16<T, kBytes>(static_cast<const T *>(a.x) + m * a.ldx + c0 + lane * 16, v);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+        top = b > top ? b : top;
+    }
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, top, 1);
+    const uint32_t byte = microscale_byte(other > top ? other : top);
+    const float inv = microscale_inverse(byte);
+    float f[2][8];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i / 8][i % 8] = v[i] * inv;
+    uint2 code = {fp4x8(f[0]), fp4x8(f[1])};
+    if (byte == 255u) code = {0u, 0u};
+    // the warp's 16 scale bytes, block b's in lane 2 b: pairs, then fours, then all in lane 0
+    uint32_t s4 = byte | __shfl_down_sync(0xffffffffu, byte, 2) << 8;
+    s4 |= __shfl_down_sync(0xffffffffu, s4, 4) << 16;
+    uint4 sc;
+    sc.x = s4;
+    sc.y = __shfl_down_sync(0xffffffffu, s4, 8);
+    sc.z = __shfl_down_sync(0xffffffffu, s4, 16);
+    sc.w = __shfl_down_sync(0xffffffffu, s4, 24);
+    for (int j = 0; j < a.k; ++j) {
+        const int row = whole ? 0 : __shfl_sync(0xffffffffu, row_l, j);
+        const bool live = row >= 0;
+        const int64_t at = whole ? m : (live ? row : ~row);
+        if (at >= a.rows * a.k) continue;
+        if (in)
+            *reinterpret_cast<uint2 *>(a.codes + at * (a.cols / 2) + (c0 + lane * 16) / 2) = live ? code : uint2{0u, 0u};
+        if (lane == 0)
+            *reinterpret_cast<uint4 *>(a.scales + at * a.pitch + c0 / 32) = live ? sc : uint4{0, 0, 0, 0};
+    }
+}
+
 template <typename T, int kBytes>
 __global__ void __launch_bounds__(256) microscale_quantize_kernel(const QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, c0 = blockIdx.y * 512;
-    const bool in = c0 + lane * 16 < a.cols;
+    const int lane = threadIdx.x & 31;
     const int64_t stride = (int64_t)gridDim.x * 8;
     for (int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows; m += stride) {
-        float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-        if (in) load16<T, kBytes>(static_cast<const T *>(a.x) + m * a.ldx + c0 + lane * 16, v);
         const int row_l = a.route_row && lane < a.k ? a.route_row[m * a.k + lane] : 0;
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
-            top = b > top ? b : top;
+        quantize_unit<T, kBytes>(a, m, blockIdx.y * 512, row_l, a.route_row == nullptr);
+    }
+}
+
+// The token plan and the quantisation into sorted rows of few routes in one launch: every CTA
+// ranks the routes by comparing each with all others (the plan's order: expert, then route;
+// dropped ones last), the first one writes the plan.
+__global__ void __launch_bounds__(kPlanQuantizeRoutes)
+microscale_plan_quantize_kernel(const QuantArgs a, const int32_t *ids, int E, int32_t *offsets,
+                                int32_t *row_route, int32_t *route_row) {
+    __shared__ int4 key4[kPlanQuantizeRoutes / 4];
+    __shared__ int row[kPlanQuantizeRoutes];
+    int *key = reinterpret_cast<int *>(key4);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, r = threadIdx.x, R = (int)a.rows * a.k;
+    const int id = r < R ? ids[r] : 0;
+    const int mine = r < R ? ((uint32_t)id < (uint32_t)E ? id : E) : E + 1;
+    key[r] = mine;
+    __syncthreads();
+    int at = 0;
+    for (int i = 0; i < (R + 3) / 4; ++i) {
+        const int4 q = key4[i];
+        at += (q.x < mine || (q.x == mine && 4 * i < r)) + (q.y < mine || (q.y == mine && 4 * i + 1 < r)) +
+              (q.z < mine || (q.z == mine && 4 * i + 2 < r)) + (q.w < mine || (q.w == mine && 4 * i + 3 < r));
+    }
+    row[r] = mine < E ? at : ~at;
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        if (r < R) {
+            route_row[r] = mine < E ? at : ~at;
+            row_route[at] = mine < E ? r : -1;
         }
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, top, 1);
-        const uint32_t byte = microscale_byte(other > top ? other : top);
-        const float inv = microscale_inverse(byte);
-        float f[2][8];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i / 8][i % 8] = v[i] * inv;
-        uint2 code = {fp4x8(f[0]), fp4x8(f[1])};
-        if (byte == 255u) code = {0u, 0u};
-        // the warp's 16 scale bytes, block b's in lane 2 b: pairs, then fours, then all in lane 0
-        uint32_t s4 = byte | __shfl_down_sync(0xffffffffu, byte, 2) << 8;
-        s4 |= __shfl_down_sync(0xffffffffu, s4, 4) << 16;
-        uint4 sc;
-        sc.x = s4;
-        sc.y = __shfl_down_sync(0xffffffffu, s4, 8);
-        sc.z = __shfl_down_sync(0xffffffffu, s4, 16);
-        sc.w = __shfl_down_sync(0xffffffffu, s4, 24);
-        const int n = a.route_row ? a.k : 1;
-        for (int j = 0; j < n; ++j) {
-            int64_t at = m;
-            bool live = true;
-            if (a.route_row) {
-                const int row = __shfl_sync(0xffffffffu, row_l, j);
-                live = row >= 0;
-                at = live ? row : ~row;
-                if (at >= a.rows * a.k) continue;
+        for (int e = r; e <= E; e += kPlanQuantizeRoutes) {
+            int n = 0;
+            for (int i = 0; i < (R + 3) / 4; ++i) {
+                const int4 q = key4[i];
+                n += (q.x < e) + (q.y < e) + (q.z < e) + (q.w < e);
             }
-            if (in)
-                *reinterpret_cast<uint2 *>(a.codes + at * (a.cols / 2) + (c0 + lane * 16) / 2) = live ? code : uint2{0u, 0u};
-            if (lane == 0)
-                *reinterpret_cast<uint4 *>(a.scales + at * a.pitch + c0 / 32) = live ? sc : uint4{0, 0, 0, 0};
+            offsets[e] = n;
         }
     }
+    __syncthreads();
+    const int64_t stride = (int64_t)gridDim.x * (kPlanQuantizeRoutes / 32);
+    for (int64_t m = (int64_t)blockIdx.x * (kPlanQuantizeRoutes / 32) + (threadIdx.x >> 5); m < a.rows; m += stride)
+        quantize_unit<__nv_bfloat16, 16>(a, m, blockIdx.y * 512, lane < a.k ? row[m * a.k + lane] : 0, false);
 }
 
 struct DequantArgs {
@@ -229,6 +274,15 @@ cudaError_t launch_microscale_quantize(const void *x, int64_t ldx, int dtype, in
     if (dtype == MOE_DT_F32) return quantize_as<float>(a, stream);
     if (dtype == MOE_DT_F16) return quantize_as<__half>(a, stream);
     return quantize_as<__nv_bfloat16>(a, stream);
+}
+
+cudaError_t launch_microscale_plan_quantize(const __nv_bfloat16 *x, int M, int cols, const int32_t *ids, int k,
+                                            int E, int32_t *offsets, int32_t *row_route, int32_t *route_row,
+                                            uint8_t *codes, uint8_t *scales, cudaStream_t stream) {
+    const QuantArgs a{x, cols, M, cols, microscale_pitch(cols), k, route_row, codes, scales};
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = launch_config(rows_by_chunks(M, cols), dim3(kPlanQuantizeRoutes), 0, stream, attrs, 0);
+    return cudaLaunchKernelEx(&cfg, microscale_plan_quantize_kernel, a, ids, E, offsets, row_route, route_row);
 }
 
 cudaError_t launch_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,

@@ -405,6 +405,12 @@ __host__ __device__ constexpr int microscale_pitch(int cols) { return (cols / 32
 cudaError_t launch_microscale_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int cols,
                                        const int32_t *route_row, int k, uint8_t *codes, uint8_t *scales,
                                        cudaStream_t stream);
+// The token plan and the quantisation of bf16 rows (16-byte aligned, pitch cols) into sorted
+// order in one launch, for up to kPlanQuantizeRoutes routes.
+constexpr int kPlanQuantizeRoutes = 256;
+cudaError_t launch_microscale_plan_quantize(const __nv_bfloat16 *x, int M, int cols, const int32_t *ids, int k,
+                                            int E, int32_t *offsets, int32_t *row_route, int32_t *route_row,
+                                            uint8_t *codes, uint8_t *scales, cudaStream_t stream);
 cudaError_t launch_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                          int cols, void *x, int64_t ldx, int dtype, cudaStream_t stream);
 // Tile of the grouped product for these sizes: rows, channels, 256-wide chunks of K a stage.

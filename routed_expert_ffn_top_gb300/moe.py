@@ -751,6 +751,9 @@ def _microscaled(codes, scales, device, name):
 
 def _quantised_outputs(codes, scales, rows, cols, dev):
     """Codes and scales of a [rows, cols] result, allocated where the caller gave none."""
+    if codes is None and scales is None:
+        return (torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev),
+                torch.empty((rows, _pitch(cols)), dtype=torch.uint8, device=dev))
     if codes is None:
         codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
     if scales is None:
