@@ -271,7 +271,7 @@ extern "C" int moe_microscale_ffn(const void *h, const moe_microscale_weights_t 
     if ((rc = check_routes(M, k)) != MOE_OK) return rc;
     if (M == 0) return MOE_OK;
     if (!h || !topk_ids || !topk_weights || !out || !workspace || !aligned(workspace, 256) ||
-        !aligned(topk_ids, 4) || !aligned(h, 16) || !aligned(out, 16) || (residual && !aligned(residual, 16)))
+        !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(h, 16) || !aligned(out, 16) || (residual && !aligned(residual, 16)))
         return MOE_ERR_INVALID_ARG;
     const int64_t R = (int64_t)M * k;
     const MicroscaleWs L = microscale_ws(w->E, w->H, w->I, R);

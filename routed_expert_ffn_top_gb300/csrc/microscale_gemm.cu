@@ -359,6 +359,7 @@ __device__ __forceinline__ void mx_gate_columns(const MxArgs &a, float *exchange
     if (warp == 2 && last)
         for (int j = 0; j < nrows; ++j)
             for (int b = I / 32 + lane; b < a.pitch; b += 32) a.scales[(int64_t)(row0 + j) * a.pitch + b] = 0;
+    named_bar_sync(1 + 2 * group, 128);  // u may be written over
 }
 
 // kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
@@ -383,7 +384,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *scales = stages + G::kStages * G::kStageBytes;
     __shared__ MxCtl ctl;
-    __shared__ float exchange[kGated && G::kSwap ? 2 * 32 * 64 : 1];  // u of the gated small tile, two units
+    __shared__ float exchange[kGated && G::kSwap ? 2 * 32 * 64 : 1];  // u of the gated small tile, one unit a group
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
@@ -630,7 +631,8 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
             if (buf != group) continue;
             if (!mx_warp_wait(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl)) {
                 if constexpr (!(kGated && G::kSwap)) break;
-                named_bar_sync(1 + 2 * group, 128);  // a warp that does not give up waits here for the others
+                named_bar_sync(1 + 2 * group, 128);  // a warp that does not give up waits there for the others
+                named_bar_sync(1 + 2 * group, 128);
                 continue;
             }
             tc_fence_after();
@@ -644,7 +646,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.tempty[buf]);
                 if constexpr (!kGated) mx_store_columns<Out>(a, x.row0, x.nrows, n0 + 32 * w4 + lane, v);
-                else mx_gate_columns(a, exchange + buf * (32 * 64), group, x.row0, x.nrows, n0, w4, lane, v, x.ct == a.nct - 1);
+                else mx_gate_columns(a, exchange + group * (32 * 64), group, x.row0, x.nrows, n0, w4, lane, v, x.ct == a.nct - 1);
                 continue;
             }
             const int64_t row = (int64_t)x.row0 + 32 * w4 + lane;

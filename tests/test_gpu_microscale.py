@@ -251,3 +251,51 @@ def test_expert_step(M, k, E, H, I, drop):
         assert torch.equal(out[M // 2].cpu(), res[M // 2])
     again = moe.moe_microscale_ffn(h.cuda(), q, ids.cuda(), w.cuda(), residual=res.cuda(), workspace=work)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("M,k,E,H,I,drop", [(1, 8, 128, 2048, 768, 0), (21, 8, 128, 2048, 768, 0), (40, 6, 16, 320, 96, 0.1),
+                                            (300, 8, 128, 544, 224, 0.05), (400, 8, 16, 512, 256, 0.02)])
+def test_expert_step_is_its_parts(M, k, E, H, I, drop):
+    """The step's launches (plan and quantisation in one, at the sizes that take them) give the
+    bits of the separate calls; calls share a workspace."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    ids = torch.randint(0, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    if drop:
+        ids[torch.rand((M, k), generator=g, device="cuda") < drop] = -1
+    w = torch.rand((M, k), generator=g, device="cuda")
+    h, res = (torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    layer = {"H": H, "I": I, "E": E}
+    for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
+        c, s = moe.moe_microscale_quantize((torch.randn((E * n, cols), generator=g, device="cuda") * 0.05).to(torch.bfloat16))
+        layer[name + "_codes"], layer[name + "_scales"] = c.view(E, n, -1), s.view(E, n, -1)
+    offsets, _, rr = moe.moe_token_plan(ids, E)
+    x = moe.moe_microscale_quantize(h, route_row=rr)
+    p = moe.moe_microscale_gated_product(*x, layer["gate_up_codes"], layer["gate_up_scales"], offsets=offsets)
+    y = moe.moe_microscale_product(*p, layer["down_codes"], layer["down_scales"], offsets=offsets)
+    want = moe.moe_token_unsort(y, rr, w, residual=res)
+    work = moe.microscale_workspace(layer, M, k)
+    for _ in range(5):
+        out = moe.moe_microscale_ffn(h, layer, ids, w, residual=res, workspace=work)
+        assert torch.equal(out, want)
+    assert moe.moe_read_device_status(work) == 0
+
+
+def test_many_small_gated_units():
+    """Many units a CTA with little to do in each: every unit's u is its own."""
+    g = gen(11)
+    E, I, K = 200, 160, 32
+    sizes = [(7 * e) % 33 for e in range(E)]
+    R = sum(sizes)
+    offsets = groups(sizes).cuda()
+    xc, xs = (t.cuda() for t in codes_and_scales((R, K), g, 125, 128))
+    wc, ws = (t.cuda() for t in codes_and_scales((E, 2 * I, K), g, 126, 127))
+    first = moe.moe_microscale_gated_product(xc, xs, wc, ws, offsets=offsets)
+    y = moe.moe_microscale_product(xc, xs, wc, ws, offsets=offsets, dtype=torch.float32)
+    gate, up = y[:, :I].double(), y[:, I:].double()
+    want = ref.values(*ref.pack(*ref.quantise((gate / (1 + torch.exp(-gate)) * up).cpu())))
+    got = ref.values(first[0].cpu(), first[1].cpu())
+    assert float(((got - want).abs() > 1e-12).double().mean()) < 1e-4  # values at a code's boundary
+    for _ in range(20):
+        again = moe.moe_microscale_gated_product(xc, xs, wc, ws, offsets=offsets)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
