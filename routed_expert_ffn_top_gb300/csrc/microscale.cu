@@ -59,9 +59,9 @@ struct QuantArgs {
 // share a block.  512 columns are 16 scale bytes, one store.  With route_row a token is
 // quantised once and stored k times (tail rows of dropped routes as zeros).
 // Memory bound: elem + 1/2 + 1/32 bytes a value.
-// row_l: in lane j < k, the route_row entry of slot j (with a.k == 1 and whole == true: row m).
-template <typename T, int kBytes>
-__device__ __forceinline__ void quantize_unit(const QuantArgs &a, int64_t m, int c0, int row_l, bool whole) {
+// kRouted: row_l holds in lane j < k the route_row entry of slot j; else the unit goes to row m.
+template <typename T, int kBytes, bool kRouted>
+__device__ __forceinline__ void quantize_unit(const QuantArgs &a, int64_t m, int c0, int row_l) {
     const int lane = threadIdx.x & 31;
     const bool in = c0 + lane * 16 < a.cols;
     float v[16];
@@ -90,27 +90,34 @@ __device__ __forceinline__ void quantize_unit(const QuantArgs &a, int64_t m, int
     sc.y = __shfl_down_sync(0xffffffffu, s4, 8);
     sc.z = __shfl_down_sync(0xffffffffu, s4, 16);
     sc.w = __shfl_down_sync(0xffffffffu, s4, 24);
-    for (int j = 0; j < a.k; ++j) {
-        const int row = whole ? 0 : __shfl_sync(0xffffffffu, row_l, j);
-        const bool live = row >= 0;
-        const int64_t at = whole ? m : (live ? row : ~row);
-        if (at >= a.rows * a.k) continue;
-        if (in)
-            *reinterpret_cast<uint2 *>(a.codes + at * (a.cols / 2) + (c0 + lane * 16) / 2) = live ? code : uint2{0u, 0u};
-        if (lane == 0)
-            *reinterpret_cast<uint4 *>(a.scales + at * a.pitch + c0 / 32) = live ? sc : uint4{0, 0, 0, 0};
+    uint8_t *codes = a.codes + (c0 + lane * 16) / 2, *scales = a.scales + c0 / 32;
+    const uint32_t half = (uint32_t)a.cols / 2, pitch = (uint32_t)a.pitch;
+    if constexpr (!kRouted) {
+        if (in) *reinterpret_cast<uint2 *>(codes + (uint64_t)m * half) = code;
+        if (lane == 0) *reinterpret_cast<uint4 *>(scales + (uint64_t)m * pitch) = sc;
+    } else {
+        const uint32_t R = (uint32_t)a.rows * (uint32_t)a.k;  // below 2^24
+#pragma unroll 4
+        for (int j = 0; j < a.k; ++j) {
+            const int row = __shfl_sync(0xffffffffu, row_l, j);
+            const bool live = row >= 0;
+            const uint32_t at = (uint32_t)(live ? row : ~row);
+            if (at >= R) continue;
+            if (in) *reinterpret_cast<uint2 *>(codes + (uint64_t)at * half) = live ? code : uint2{0u, 0u};
+            if (lane == 0) *reinterpret_cast<uint4 *>(scales + (uint64_t)at * pitch) = live ? sc : uint4{0, 0, 0, 0};
+        }
     }
 }
 
-template <typename T, int kBytes>
+template <typename T, int kBytes, bool kRouted>
 __global__ void __launch_bounds__(256) microscale_quantize_kernel(const QuantArgs a) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t stride = (int64_t)gridDim.x * 8;
     for (int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); m < a.rows; m += stride) {
-        const int row_l = a.route_row && lane < a.k ? a.route_row[m * a.k + lane] : 0;
-        quantize_unit<T, kBytes>(a, m, blockIdx.y * 512, row_l, a.route_row == nullptr);
+        const int row_l = kRouted && lane < a.k ? a.route_row[m * a.k + lane] : 0;
+        quantize_unit<T, kBytes, kRouted>(a, m, blockIdx.y * 512, row_l);
     }
 }
 
@@ -154,7 +161,7 @@ microscale_plan_quantize_kernel(const QuantArgs a, const int32_t *ids, int E, in
     __syncthreads();
     const int64_t stride = (int64_t)gridDim.x * (kPlanQuantizeRoutes / 32);
     for (int64_t m = (int64_t)blockIdx.x * (kPlanQuantizeRoutes / 32) + (threadIdx.x >> 5); m < a.rows; m += stride)
-        quantize_unit<__nv_bfloat16, 16>(a, m, blockIdx.y * 512, lane < a.k ? row[m * a.k + lane] : 0, false);
+        quantize_unit<__nv_bfloat16, 16, true>(a, m, blockIdx.y * 512, lane < a.k ? row[m * a.k + lane] : 0);
 }
 
 struct DequantArgs {
@@ -248,12 +255,12 @@ static dim3 rows_by_chunks(int64_t rows, int cols) {
     return dim3((unsigned)(n < most ? n : most), (unsigned)nchunk);
 }
 
-template <typename T>
+template <typename T, bool kRouted>
 static cudaError_t quantize_as(const QuantArgs &a, cudaStream_t stream) {
     const uint64_t bits = reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(a.ldx * sizeof(T));
-    const auto fn = bits % 32 == 0   ? microscale_quantize_kernel<T, 32>
-                    : bits % 16 == 0 ? microscale_quantize_kernel<T, 16>
-                                     : microscale_quantize_kernel<T, (int)sizeof(T)>;
+    const auto fn = bits % 32 == 0   ? microscale_quantize_kernel<T, 32, kRouted>
+                    : bits % 16 == 0 ? microscale_quantize_kernel<T, 16, kRouted>
+                                     : microscale_quantize_kernel<T, (int)sizeof(T), kRouted>;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(rows_by_chunks(a.rows, a.cols), dim3(256), 0, stream, attrs, 0);
     return cudaLaunchKernelEx(&cfg, fn, a);
@@ -271,9 +278,9 @@ cudaError_t launch_microscale_quantize(const void *x, int64_t ldx, int dtype, in
                                        const int32_t *route_row, int k, uint8_t *codes, uint8_t *scales,
                                        cudaStream_t stream) {
     const QuantArgs a{x, ldx, rows, cols, microscale_pitch(cols), k, route_row, codes, scales};
-    if (dtype == MOE_DT_F32) return quantize_as<float>(a, stream);
-    if (dtype == MOE_DT_F16) return quantize_as<__half>(a, stream);
-    return quantize_as<__nv_bfloat16>(a, stream);
+    if (dtype == MOE_DT_F32) return route_row ? quantize_as<float, true>(a, stream) : quantize_as<float, false>(a, stream);
+    if (dtype == MOE_DT_F16) return route_row ? quantize_as<__half, true>(a, stream) : quantize_as<__half, false>(a, stream);
+    return route_row ? quantize_as<__nv_bfloat16, true>(a, stream) : quantize_as<__nv_bfloat16, false>(a, stream);
 }
 
 cudaError_t launch_microscale_plan_quantize(const __nv_bfloat16 *x, int M, int cols, const int32_t *ids, int k,
