@@ -58,7 +58,8 @@ struct QuantArgs {
 // A unit is 512 columns of one row, one warp: lane l takes columns 16 l to 16 l + 15, two lanes
 // share a block.  512 columns are 16 scale bytes, one store.  With route_row a token is
 // quantised once and stored k times (tail rows of dropped routes as zeros).
-// Memory bound: elem + 1/2 + 1/32 bytes a value.
+// Memory bound: elem + 1/2 + 1/32 bytes a value.  128 x 1536 rows of 2048 bf16: 156 us, 6.5 TB/s,
+// 0.96 of the copy rate; 8192 tokens into 65,536 sorted rows: 19.6 us, 0.79.
 // kRouted: row_l holds in lane j < k the route_row entry of slot j; else the unit goes to row m.
 template <typename T, int kBytes, bool kRouted>
 __device__ __forceinline__ void quantize_unit(const QuantArgs &a, int64_t m, int c0, int row_l) {
@@ -214,7 +215,8 @@ __device__ __forceinline__ void decode8(uint32_t code, uint32_t byte, __half (&o
 }
 
 // A unit is 512 columns of one row, as above.  A code's value times 2^X is exact in fp32 and
-// in bf16; fp16 rounds it (to infinity past its range).
+// in bf16; fp16 rounds it (to infinity past its range).  128 x 1536 rows of 2048 to bf16: 160 us,
+// 0.94 of the copy rate (269 with a code's value worked out bit by bit).
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(256) microscale_dequantize_kernel(const DequantArgs a) {
     pdl_wait();

@@ -8,21 +8,32 @@
 // Products and scales are exact; the sums over K run in the tensor core's fp32 accumulators in
 // K order, so a row's result does not depend on its group, its tile or the grid.
 //
-// A unit is a tile of up to 128 rows of one expert (the MMA's M side) times kN of its output
-// channels (the N side).  Groups need no padding: a tile's row box may run into the next
-// expert's rows, whose results are dropped by the epilogue (a row of A only reaches its own
-// row of D).  The gated form takes kN/2 gate channels and the kN/2 up channels beside them,
-// computes p = SiLU(g) u in fp32 and quantises it in the epilogue, so g and u never leave the
-// chip.
+// A unit is a tile of rows of one expert times a tile of its output channels (MxTile gives the
+// two shapes).  Groups need no padding: a tile's row box may run into the next expert's rows,
+// whose results are dropped by the epilogue (a row only reaches its own results).  The gated
+// form takes a run of gate channels and the up channels beside them, computes p = SiLU(g) u in
+// fp32 and quantises it in the epilogue, so g and u never leave the chip.
 //
-// Per CTA, 16 warps: 0-3 and 12-15 drain the accumulators, 4-7 bring the scales through shared
-// memory into tensor memory, 8 and 10 issue the copies of codes, 9 the MMAs, 11 is idle (a warp
-// reads the tensor-memory lanes of its number modulo 4).  A stage is 256 of K: 128-byte rows of
-// codes, 128-byte swizzled, and 16-byte rows of scales (a copy's inner extent is 16 bytes at
-// least, so two stages share their scale bytes and each uses its half).  The MMA reads the
-// scale of row r at lane r % 32, column r / 32, four K blocks a 32-bit column, repeated in the
-// four lane quadrants.  Accumulators are double-buffered, so a tile's epilogue overlaps the
+// Per CTA (persistent, one an SM), 16 warps: 0-3 and 12-15 drain the accumulators in turn, 4-7
+// bring the scales through shared memory into tensor memory, 8 and 10 issue the copies of codes,
+// 9 the MMAs, 11 is idle (a warp reads the tensor-memory lanes of its number modulo 4).  A stage
+// is 256 or 512 of K: chunks of 256 as 128-byte rows of codes, 128-byte swizzled.  The MMA reads
+// the scale of row r at lane r % 32, column r / 32, four K blocks a 32-bit column, repeated in
+// the four lane quadrants.  Accumulators are double-buffered, so a tile's epilogue overlaps the
 // next one's MMAs.
+//
+// What bounds it, on a GB300 (H = 2048, I = 768, 128 experts, top 8 unless said):
+//   few rows     HBM.  21 tokens (75 experts reached): gated 22.4 us for 126 MB (0.82 of the copy
+//                rate), down 16.1 us for 63 MB (0.58: 4 us of a launch are not copies, and a unit
+//                has only 48 KB).  One token: 7.2 and 6.2 us, start-up and one pass of latency.
+//   many rows    shared memory's 128 bytes a cycle: per 256 of K a 128 x 192 tile writes 40 KB
+//                and its MMAs read 40 KB (640 cycles for 384 of MMAs), then the scale reads and
+//                the epilogue.  8192 tokens: gated 132 us (3.1 PFLOP/s), down 84 us; 16384 x 8192
+//                x 8192 in one group 446 us (4.9 PFLOP/s, 2.5 of the bf16 rate), where the clock
+//                also falls.  Two CTAs a tile (cta_group::2) measured the same and were left out.
+// Measured and left out for few rows: both products of an expert step in one grid, the second
+// waiting for the first row tile by row tile (8 tokens 44 against 38 us, 21 the same); 256-deep
+// stages (21 tokens' gated product 26.6); an L2 promotion of 256 bytes (down 19.1 to 21.0).
 #include <type_traits>
 
 #include "gemm_core.cuh"
@@ -35,10 +46,12 @@ constexpr int kMxMaxStages = 8;
 constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
 constexpr int kMxStaging = 2048;  // bytes a warp stages for its stores: 32 rows of 64
 
-// Two tiles.  kTok = 128: 128 rows of x as the MMA's M side, kCh = 192 channels as its N side.
-// kTok = 32, for small groups: the sides change places, 128 channels are M and up to 32 rows
-// N, so no MMA reads rows that do not exist and the four epilogue warps share every row (with
-// the rows on the M side an MMA read 4 KB of rows for a handful, and shared memory bound it).
+// Two tiles.
+//   kTok = 128: 128 rows of x as the MMA's M side, 192 channels as its N side (two accumulators
+//     of 192 columns leave tensor memory for the scales of four stages; 256 would not).
+//   kTok = 32, for small groups: the sides change places, 128 channels are M and up to 32 rows
+//     N, so no MMA reads rows that do not exist and four epilogue warps share every row (with
+//     the rows on the M side one token's gated product took 8.4 us for 7.2).
 template <int kTok_>
 struct MxTile {
     static_assert(kTok_ == 32 || kTok_ == 128, "row tiles");

@@ -32,8 +32,8 @@ namespace moe {
 //
 // What bounds it is latency, and for many routes the scattered stores of row_route, one sector a
 // cycle and SM.  So several clusters count all the routes, and each writes its share of every
-// warp's steps: counting again costs less than 8 SMs' stores (65,536 routes, 128 experts: one
-// cluster 16 us).
+// warp's steps: counting again costs less than 8 SMs' stores (65,536 routes, 128 experts: 9.1 us,
+// one cluster 16; 8 routes 2.0 us; 262,144 routes 26 us).
 constexpr int kPlanMaxCluster = 8;
 constexpr int kPlanMaxShares = 8;  // clusters
 constexpr int kPlanKeep = 4;       // steps of a share whose ranks stay in registers
@@ -220,7 +220,8 @@ struct RowArgs {
 // Sort: a unit is 32 * kSortVecs vectors of one token, read once and written k times.  The
 // sorted rows are written in full and the token rows read once: the bytes the operator
 // cannot do without, whatever the order (reading the rows in sorted order instead reads each
-// token k times, from L2 at best).
+// token k times, from L2 at best).  8192 tokens x 8 routes x 2048 bf16: 46.2 us, 6.5 TB/s, 0.96 of
+// the copy rate.
 constexpr int kSortVecs = 4;
 constexpr int kRowWarps = 8;
 
@@ -377,7 +378,9 @@ __global__ void __launch_bounds__(kGradThreads) token_unsort_grad_kernel(const R
 // is latency: a warp loads its indices, then its rows, then stores, and holds one unit's rows in
 // registers.  Here each lane copies its own pieces of the next kDepth units into its own slots
 // of shared memory (cp.async), so a warp has kDepth units in flight and no thread waits for
-// another.  The arithmetic and its order per element are those of the form above.
+// another.  The arithmetic and its order per element are those of the form above.  8192 tokens x
+// 8 routes x 2048 bf16 (form above): unsort 54.9 us, 0.90 of the copy rate (161); without weights
+// and residual, as the gradient of sort, 47.5 us, 0.94 (157); one token 2.5 us (3.5).
 constexpr int kRingWarps = 8;
 // Shared memory of a CTA, whatever part its slots fill: three CTAs an SM, in a grid that fills
 // the SMs once.  Every such launch asks for the same size: with sizes of their own, a grid that
@@ -433,8 +436,8 @@ __device__ __forceinline__ int ring_row(const RowArgs &a, int64_t m) {
     return row_of(v, (int64_t)a.M * a.k) < 0 ? -1 : v;
 }
 
-// A warp's sequence of units: chunks q, q + wpt, ... of tokens m, m + step, ... (no division:
-// at 600 instructions a unit the 64-bit ones alone cost a third of the kernel's time).
+// A warp's sequence of units: chunks q, q + wpt, ... of tokens m, m + step, ... (no
+// division: the 64-bit ones were a tenth of the kernel's time, 81 against 73 us).
 struct RingCursor {
     int64_t m;
     int c;
@@ -518,7 +521,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
 
 // One CTA per token (grid-stride): warp q takes chunks q, q + 8, ... of the row, a running
 // sequence of units over all its tokens; the k <= 8 products are summed over the lanes, then
-// over the warps, in fixed trees.
+// over the warps, in fixed trees.  8192 tokens x 8 routes x 2048 bf16: 88.9 us, 0.94 of the copy
+// rate (form above 207); one token 3.3 us.
 template <typename T, int kDepth>
 __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_grad_ring_kernel(const RowArgs a, int nvec, int nchunk) {
     constexpr int n = 16 / sizeof(T);
