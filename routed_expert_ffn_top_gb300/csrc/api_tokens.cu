@@ -160,8 +160,8 @@ static int check_product(const uint8_t *x_codes, const uint8_t *x_scales, int64_
 }
 
 // The gated form's weights are seen as [chunk][gate/up][row]: one box takes a run of gate rows
-// and the up rows beside it.  When K is not a whole number of stages the chunk dimension has
-// one entry, a copy brings one chunk, and a row's bytes past its end read as zeros (a stage's
+// and the up rows beside it.  When K is not a whole number of copies the chunk dimension has
+// one entry, a copy brings one chunk, and a row's bytes past its end read as zeros (a deeper
 // box would zero-fill whole chunks past K, which costs as much as copying them).
 static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
                          const uint8_t *w_codes, const uint8_t *w_scales, int E, int N, int K, bool gated,

@@ -17,7 +17,7 @@
 // Per CTA (persistent, one an SM), 16 warps: 0-3 and 12-15 drain the accumulators in turn, 4-7
 // bring the scales through shared memory into tensor memory, 8 and 10 issue the copies of codes,
 // 9 the MMAs, 11 is idle (a warp reads the tensor-memory lanes of its number modulo 4).  A stage
-// is 256 or 512 of K: chunks of 256 as 128-byte rows of codes, 128-byte swizzled.  The MMA reads
+// is 512 of K: two chunks of 256 as 128-byte rows of codes, 128-byte swizzled.  The MMA reads
 // the scale of row r at lane r % 32, column r / 32, four K blocks a 32-bit column, repeated in
 // the four lane quadrants.  Accumulators are double-buffered, so a tile's epilogue overlaps the
 // next one's MMAs.
@@ -42,7 +42,7 @@
 namespace moe {
 
 constexpr int kMxThreads = 512;
-constexpr int kMxMaxStages = 8;
+constexpr int kMxMaxSlots = 8;
 constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
 constexpr int kMxStaging = 2048;  // bytes a warp stages for its stores: 32 rows of 64
 
@@ -59,7 +59,12 @@ struct MxTile {
     static constexpr int kTok = kTok_, kCh = kSwap ? 128 : 192;
     static constexpr int kA = kSwap ? kCh : kTok, kB = kSwap ? kTok : kCh;  // M and N sides
     static_assert(kA == 128, "the MMA's M");
-    static constexpr int kChunks = kSwap ? 2 : 1;          // 256-wide chunks of K per stage
+    static constexpr int kChunks = 2;                      // 256-wide chunks of K per stage
+    // Copies per stage, each behind barriers of its own: the scales and the MMA issuer go by 512
+    // of K (at 256, beside the gated epilogue's instructions, they fell behind: 132 us for 118),
+    // the large tile's memory is refilled by 256.
+    static constexpr int kSub = kSwap ? 1 : 2;
+    static constexpr int kPer = kChunks / kSub;            // chunks per copy
     static constexpr int kStageK = 256 * kChunks;
     static constexpr int kAChunk = kA * 128;               // one chunk of the M side
     static constexpr int kBChunk = kB * 128;
@@ -68,7 +73,7 @@ struct MxTile {
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kScaleBytes = (kA + kB) * 64;     // one copy of scales, M side then N side
     static constexpr int kScaleBufs = kSwap ? 4 : 2;
-    static constexpr int kStages = 4;
+    static constexpr int kStages = kSwap ? 4 : 2;
     static constexpr int kACols = kA / 32;                 // scale columns per 128 of K
     static constexpr int kBCols = kB / 32;
     static constexpr int kBPad = (kBCols + 3) / 4 * 4;     // every set starts at a multiple of 4
@@ -80,13 +85,14 @@ struct MxTile {
                                     (kSwap ? 0 : 8 * kMxStaging);
     static_assert(kStageBytes % 1024 == 0 && kScaleBytes % 512 == 0, "stage alignment");
     static_assert(kSfCol0 + kStages * kSfCols <= 512, "tensor memory");
-    static_assert(kStages <= kMxMaxStages, "barriers");
+    static constexpr int kSlots = kStages * kSub;
+    static_assert(kSlots <= kMxMaxSlots, "barriers");
 };
 
 struct MxCtl {
-    uint64_t full[kMxMaxStages];
-    uint64_t empty[kMxMaxStages];
-    uint64_t sfull[kMxMaxStages];      // the stage's scales are in tensor memory
+    uint64_t full[kMxMaxSlots];        // per copy slot
+    uint64_t empty[kMxMaxSlots];
+    uint64_t sfull[kMxMaxSlots];      // the stage's scales are in tensor memory
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t done;
@@ -401,11 +407,11 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < G::kStages; ++s) {
+        for (int s = 0; s < G::kSlots; ++s) {
             mbar_init(&ctl.full[s], 2);  // the two code producers
             mbar_init(&ctl.empty[s], 1);
-            mbar_init(&ctl.sfull[s], 4);
         }
+        for (int s = 0; s < G::kStages; ++s) mbar_init(&ctl.sfull[s], 4);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl.tfull[b], 1);
             mbar_init(&ctl.tempty[b], 4);
@@ -473,34 +479,38 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         const bool side_a = G::kSwap == (warp == 8);
         const int chunk = side_a ? G::kAChunk : G::kBChunk;
         unsigned char *const base = stages + (side_a ? 0 : G::kABytes);
-        int slot = 0;
+        int stage = 0;
         uint32_t phase = 0, issued = 0, par = 0;
         bool ok = true;
         for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
             const int w0 = mx_first_channel<kGated, G::kCh>(a, x.e, x.ct);
-            for (int s = 0; s < nks; ++s) {
-                if (!(ok = mx_warp_wait(&ctl.empty[slot], phase ^ 1u, ctl))) break;
-                if (lane == 0) {
-                    // one copy brings the whole stage, or one per chunk (past K: none)
-                    uint64_t *bar = &ctl.full[slot];
-                    const int left = (a.K - s * G::kStageK + 255) / 256;
-                    const int copies = a.deep ? 1 : (left < G::kChunks ? left : G::kChunks);
-                    unsigned char *dst = base + slot * G::kStageBytes;
-                    mbar_arrive_expect_tx(bar, (a.deep ? G::kChunks : copies) * chunk);
-                    for (int c = 0; c < copies; ++c, dst += chunk) {
-                        const int cx = a.deep ? 0 : (s * G::kChunks + c) * 128, cz = a.deep ? s * G::kChunks : 0;
-                        if (warp == 8) tma_load_4d(dst, &tm_w, cx, w0, 0, cz, bar, pol);
-                        else tma_load_3d(dst, &tm_x, cx, x.row0, cz, bar, pol);
+            for (int s = 0; s < nks && ok; ++s) {
+#pragma unroll
+                for (int b = 0; b < G::kSub; ++b) {
+                    const int slot = stage * G::kSub + b;
+                    if (!(ok = mx_warp_wait(&ctl.empty[slot], phase ^ 1u, ctl))) break;
+                    if (lane == 0) {
+                        // one copy brings the slot's chunks, or one a chunk (past K: none)
+                        uint64_t *bar = &ctl.full[slot];
+                        const int c0 = s * G::kChunks + b * G::kPer, left = (a.K + 255) / 256 - c0;
+                        const int copies = left <= 0 ? 0 : a.deep ? 1 : (left < G::kPer ? left : G::kPer);
+                        unsigned char *dst = base + stage * G::kStageBytes + b * G::kPer * chunk;
+                        mbar_arrive_expect_tx(bar, (a.deep && copies ? G::kPer : copies) * chunk);
+                        for (int c = 0; c < copies; ++c, dst += chunk) {
+                            const int cx = a.deep ? 0 : (c0 + c) * 128, cz = a.deep ? c0 : 0;
+                            if (warp == 8) tma_load_4d(dst, &tm_w, cx, w0, 0, cz, bar, pol);
+                            else tma_load_3d(dst, &tm_x, cx, x.row0, cz, bar, pol);
+                        }
                     }
+                    __syncwarp();
+                    issued |= 1u << slot;
+                    par = (par & ~(1u << slot)) | (phase << slot);
                 }
-                __syncwarp();
-                issued |= 1u << slot;
-                par = (par & ~(1u << slot)) | (phase << slot);
-                if (++slot == G::kStages) slot = 0, phase ^= 1u;
+                if (++stage == G::kStages) stage = 0, phase ^= 1u;
             }
         }
         // every copy has landed before the CTA can exit
-        for (int s = 0; s < G::kStages; ++s)
+        for (int s = 0; s < G::kSlots; ++s)
             if ((issued >> s) & 1u)
                 if (!mbar_wait_bounded(&ctl.full[s], (par >> s) & 1u)) ctl.abort = 1;
         __syncwarp();
@@ -517,29 +527,32 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                 if (!mx_wait(&ctl.tempty[buf], tphase, ctl)) break;
                 const uint32_t d = ctl.tmem + (uint32_t)(buf * kN);
                 bool ok = true;
-                for (int s = 0; s < nks; ++s) {
-                    if (!mx_wait(&ctl.full[stage], phase, ctl) || !mx_wait(&ctl.sfull[stage], phase, ctl)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                for (int s = 0; s < nks && ok; ++s) {
                     const uint64_t ad = a0 + (uint32_t)(stage * (G::kStageBytes >> 4));
                     const uint64_t bd = b0 + (uint32_t)(stage * (G::kStageBytes >> 4));
                     const uint32_t sf = ctl.tmem + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
+                    const int left = (a.K - s * G::kStageK + 63) / 64;  // K steps of this stage
                     auto step = [&](int ks) {
                         umma_mxf4(d, ad + (ks >> 2) * (G::kAChunk >> 4) + (ks & 3) * 2,
                                   bd + (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2, mx_idesc(kN, (ks & 1) ? 2u : 0u),
                                   sf + (ks >> 1) * G::kACols, sf + G::kGroups * G::kACols + (ks >> 1) * G::kBPad,
                                   s > 0 || ks > 0);
                     };
-                    const int left = (a.K - s * G::kStageK + 63) / 64;  // K steps of this stage
-                    if (left >= G::kStageK / 64) {
 #pragma unroll
-                        for (int ks = 0; ks < G::kStageK / 64; ++ks) step(ks);
-                    } else {
-                        for (int ks = 0; ks < left; ++ks) step(ks);
+                    for (int b = 0; b < G::kSub; ++b) {
+                        const int slot = stage * G::kSub + b;
+                        constexpr int kSteps = G::kPer * 4;  // K steps a slot
+                        if (!(ok = mx_wait(&ctl.full[slot], phase, ctl) && (b > 0 || mx_wait(&ctl.sfull[stage], phase, ctl))))
+                            break;
+                        tc_fence_after();
+                        if (left >= (b + 1) * kSteps) {
+#pragma unroll
+                            for (int ks = 0; ks < kSteps; ++ks) step(b * kSteps + ks);
+                        } else {
+                            for (int ks = b * kSteps; ks < left; ++ks) step(ks);
+                        }
+                        umma_commit(&ctl.empty[slot]);
                     }
-                    umma_commit(&ctl.empty[stage]);
                     if (++stage == G::kStages) stage = 0, phase ^= 1u;
                 }
                 if (!ok) break;
@@ -617,7 +630,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 #pragma unroll
                 for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kGroups, G::kBPad>(piece[G::kACols + c], upper, mask, wb + c);
                 // the MMAs that read this slot's scales have completed
-                ok = ok && mx_warp_wait(&ctl.empty[stage], phase ^ 1u, ctl);
+                ok = ok && mx_warp_wait(&ctl.empty[stage * G::kSub + G::kSub - 1], phase ^ 1u, ctl);
                 if (ok) {
                     tc_fence_after();
                     const uint32_t sf = ctl.tmem + quad + (uint32_t)(G::kSfCol0 + stage * G::kSfCols);
@@ -740,8 +753,8 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 MicroscaleTile microscale_tile(int64_t rows, int E) {
     using Large = MxTile<128>;
     using Small = MxTile<32>;
-    return rows > 32 && rows >= 4 * (int64_t)E ? MicroscaleTile{128, Large::kCh, Large::kChunks}
-                                               : MicroscaleTile{32, Small::kCh, Small::kChunks};
+    return rows > 32 && rows >= 4 * (int64_t)E ? MicroscaleTile{128, Large::kCh, Large::kPer}
+                                               : MicroscaleTile{32, Small::kCh, Small::kPer};
 }
 
 template <int kTok, int kOut>

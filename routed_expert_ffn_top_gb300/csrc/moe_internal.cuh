@@ -413,13 +413,13 @@ cudaError_t launch_microscale_plan_quantize(const __nv_bfloat16 *x, int M, int c
                                             uint8_t *codes, uint8_t *scales, cudaStream_t stream);
 cudaError_t launch_microscale_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows,
                                          int cols, void *x, int64_t ldx, int dtype, cudaStream_t stream);
-// Tile of the grouped product for these sizes: rows, channels, 256-wide chunks of K a stage.
+// Tile of the grouped product for these sizes: rows, channels, 256-wide chunks of K a copy.
 struct MicroscaleTile {
     int m, n, chunks;
 };
 MicroscaleTile microscale_tile(int64_t rows, int E);
 // Operands of one grouped product: tensor maps of the codes of the rows and of the weights, and
-// their scales.  Codes have a chunk dimension of K (128 bytes each) when K is a whole number of stages (`deep`); the
+// their scales.  Codes have a chunk dimension of K (128 bytes each) when K is a whole number of copies (`deep`); the
 // weights' have a gate/up dimension.
 struct MicroscaleMaps {
     CUtensorMap x, w, y;
