@@ -475,7 +475,11 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 
     if (warp == 8 || warp == 10) {
         // two producer warps: weight codes and row codes
-        const uint64_t pol = policy_evict_normal();
+        // weights that one row tile reads leave L2 first, rows (read by every channel tile) last:
+        // with layers' weights in turn, 21 tokens' gated product 23.2 to 21.5 us, 256 tokens' down
+        // product 23.2 to 20.0
+        const uint64_t keep = warp == 8 ? policy_evict_normal() : policy_evict_last();
+        const uint64_t once = warp == 8 ? policy_evict_first() : keep;
         const bool side_a = G::kSwap == (warp == 8);
         const int chunk = side_a ? G::kAChunk : G::kBChunk;
         unsigned char *const base = stages + (side_a ? 0 : G::kABytes);
@@ -484,6 +488,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         bool ok = true;
         for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
             const int w0 = mx_first_channel<kGated, G::kCh>(a, x.e, x.ct);
+            const uint64_t pol = ctl.first[x.e + 1] - ctl.first[x.e] == 1 ? once : keep;
             for (int s = 0; s < nks && ok; ++s) {
 #pragma unroll
                 for (int b = 0; b < G::kSub; ++b) {
