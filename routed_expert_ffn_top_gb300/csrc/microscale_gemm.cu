@@ -125,6 +125,7 @@ struct MxArgs {
     int64_t rows;
     int E, N, K;
     int nct;                 // column tiles
+    int dt, dct;             // a step of a CTA's units in row tiles and column tiles
     int vec, bulk;           // y rows allow 32-byte stores, tensor stores
     void *y;
     int64_t ldy;
@@ -267,7 +268,7 @@ struct MxWalk {
     }
     __device__ __forceinline__ MxWalk(const MxArgs &a, const MxCtl &ctl, int tiles) {
         t = blockIdx.x / a.nct, ct = blockIdx.x % a.nct, e = 0;
-        dt = gridDim.x / a.nct, dct = gridDim.x % a.nct;
+        dt = a.dt, dct = a.dct;
         if (t < tiles) place(a, ctl);
     }
     __device__ __forceinline__ void next(const MxArgs &a, const MxCtl &ctl, int tiles) {
@@ -527,7 +528,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
             const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, 16, 1024, 2);
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 1;
-            const int dt = gridDim.x / a.nct, dct = gridDim.x % a.nct;
+            const int dt = a.dt, dct = a.dct;
             for (int t = blockIdx.x / a.nct, ct = blockIdx.x % a.nct; t < tiles && !ctl.abort;) {
                 if (!mx_wait(&ctl.tempty[buf], tphase, ctl)) break;
                 const uint32_t d = ctl.tmem + (uint32_t)(buf * kN);
@@ -770,6 +771,7 @@ static cudaError_t gemm_as(const MicroscaleMaps &tm, MxArgs a, cudaStream_t stre
     const int64_t tiles = a.rows < a.E ? a.rows : a.rows / kTok + a.E;
     const int64_t units = tiles * a.nct, sms = num_sms();
     const int64_t grid = units < 1 ? 1 : (units < sms ? units : sms);
+    a.dt = (int)(grid / a.nct), a.dct = (int)(grid % a.nct);
     const auto fn = microscale_gemm_kernel<kTok, kOut>;
     cudaError_t err = ensure_smem((const void *)fn, G::kSmem);
     if (err != cudaSuccess) return err;
