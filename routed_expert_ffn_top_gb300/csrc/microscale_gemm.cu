@@ -43,7 +43,7 @@ namespace moe {
 
 constexpr int kMxThreads = 512;
 constexpr int kMxMaxSlots = 8;
-constexpr int kMxScaleK = 2048;  // K per copy of scales: 64-byte rows
+constexpr int kMxScaleK = 1024;  // K per copy of scales: 32-byte rows
 constexpr int kMxStaging = 2048;  // bytes a warp stages for its stores: 32 rows of 64
 
 // Two tiles.
@@ -71,8 +71,8 @@ struct MxTile {
     static constexpr int kABytes = kChunks * kAChunk;
     static constexpr int kBBytes = kChunks * kBChunk;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kScaleBytes = (kA + kB) * 64;     // one copy of scales, M side then N side
-    static constexpr int kScaleBufs = kSwap ? 4 : 2;
+    static constexpr int kScaleBytes = (kA + kB) * 32;     // one copy of scales, M side then N side
+    static constexpr int kScaleBufs = kSwap ? 6 : 4;
     static constexpr int kStages = kSwap ? 4 : 2;
     static constexpr int kACols = kA / 32;                 // scale columns per 128 of K
     static constexpr int kBCols = kB / 32;
@@ -278,10 +278,11 @@ struct MxWalk {
     }
 };
 
-// The 16 scale bytes (512 of K) number `piece` of a row of a copy.  Rows are 64 bytes, their
-// 16-byte pieces exchanged as the 64-byte swizzle does.
+// The 16 scale bytes (512 of K) number `piece` of a row of a copy.  Rows are 32 bytes, their two
+// pieces exchanged in every other four rows, so that 8 lanes reading a piece each take all banks.
+__device__ __forceinline__ int mx_scale_at(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
 __device__ __forceinline__ uint4 mx_scale_piece(const unsigned char *base, int row, int piece) {
-    return *reinterpret_cast<const uint4 *>(base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+    return *reinterpret_cast<const uint4 *>(base + mx_scale_at(row, piece));
 }
 
 // The words of a stage to w[0], w[kStep], ...: all four of a piece, or one half of it.
@@ -587,16 +588,17 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                 const int w0 = mx_first_channel<kGated, G::kCh>(a, ahead.e, ahead.ct);
                 unsigned char *S = scales + slot_a * G::kScaleBytes;
 #pragma unroll
-                for (int i = 0; i < (G::kA + G::kB) * 4 / 128; ++i) {
-                    const int p = (int)threadIdx.x - 128 + 128 * i, r = p >> 2, piece = p & 3;
+                for (int i = 0; i < ((G::kA + G::kB) * 2 + 127) / 128; ++i) {
+                    const int p = (int)threadIdx.x - 128 + 128 * i, r = p >> 1, c = p & 1;
                     const int rs = r < G::kA ? r : r - G::kA;  // row of its side
                     const bool is_w = (r < G::kA) == G::kSwap;
                     int64_t row = is_w ? w0 + rs : ahead.row0 + rs;
                     if (kGated && is_w && rs >= kHalf) row += a.N / 2 - kHalf;
-                    const bool in = row < (is_w ? (int64_t)a.E * a.N : a.rows) && part_a * 64 + piece * 16 < a.kpitch;
+                    const bool in = r < G::kA + G::kB && row < (is_w ? (int64_t)a.E * a.N : a.rows) &&
+                                    part_a * 32 + c * 16 < a.kpitch;
                     if (in)
-                        cp_async_16(S + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4),
-                                    (is_w ? a.w_scales : a.x_scales) + row * a.kpitch + part_a * 64 + piece * 16);
+                        cp_async_16(S + mx_scale_at(r, c),
+                                    (is_w ? a.w_scales : a.x_scales) + row * a.kpitch + part_a * 32 + c * 16);
                 }
                 if (++part_a == per_unit) part_a = 0, ahead.next(a, ctl, tiles);
             }
