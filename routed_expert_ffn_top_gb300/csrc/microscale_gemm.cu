@@ -118,6 +118,10 @@ __device__ __forceinline__ bool mx_warp_wait(uint64_t *bar, uint32_t parity, MxC
 }
 
 struct MxArgs {
+    // early: offsets, ids and weights were complete before the kernel ahead began.  ids: the
+    // groups' sizes are counted from nids <= kMxThreads routes' experts instead.
+    int early, nids;
+    const int32_t *ids;
     int deep;                // the maps' third dimension is K's 256-wide chunks, a stage a copy
     const int32_t *offsets;  // NULL: one group of all rows
     const uint8_t *x_scales, *w_scales;
@@ -427,21 +431,35 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         prefetch_tensormap(&tm_w);
         prefetch_tensormap(&tm_x);
     }
-    pdl_wait();
-    pdl_launch_dependents();
+    // Early, nothing of the kernel ahead is needed before the rows: the tiles are counted and the
+    // first weights copied while it runs.
+    if (!a.early) pdl_wait();
+    if (a.ids) {
+        for (int e = threadIdx.x; e < a.E; e += kMxThreads) ctl.begin[e] = 0;
+        __syncthreads();
+        const int id = (int)threadIdx.x < a.nids ? __ldcg(a.ids + threadIdx.x) : -1;
+        if (id >= 0 && id < a.E) atomicAdd(&ctl.begin[id], 1);
+        __syncthreads();
+    }
 
-    // row tiles before each expert; offsets outside [0, rows] or running backwards are clamped
+    // row tiles before each expert; offsets outside [0, rows] or running backwards are clamped.
+    // Counted groups' rows are summed along, in the upper half of the same words.
+    const int low = a.ids ? 0xffff : -1;
     int carry = 0;
     for (int e0 = 0; e0 < a.E; e0 += kMxThreads) {
         const int e = e0 + threadIdx.x;
         int64_t lo = 0, hi = 0;
         if (e < a.E) {
-            lo = a.offsets ? a.offsets[e] : 0;
-            hi = a.offsets ? a.offsets[e + 1] : a.rows;
-            lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
-            hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
+            if (a.ids) {
+                hi = ctl.begin[e];
+            } else {
+                lo = a.offsets ? __ldcg(a.offsets + e) : 0;
+                hi = a.offsets ? __ldcg(a.offsets + e + 1) : a.rows;
+                lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
+                hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
+            }
         }
-        const int tiles = (int)((hi - lo + kTok - 1) / kTok);
+        const int tiles = (int)((hi - lo + kTok - 1) / kTok) | (a.ids ? (int)hi << 16 : 0);
         int inc = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -457,12 +475,12 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
             chunk += t;
         }
         if (e < a.E) {
-            ctl.first[e] = off + inc - tiles;
-            ctl.begin[e] = (int)lo;
+            const int end = off + inc, at = end - tiles;
+            ctl.first[e] = at & low;
+            ctl.begin[e] = a.ids ? at >> 16 : (int)lo;
             if (e == a.E - 1) {
-                ctl.first[a.E] = off + inc;
-                ctl.begin[a.E] = (int)hi;
-                ctl.valid_rows = (int)hi;
+                ctl.first[a.E] = end & low;
+                ctl.valid_rows = ctl.begin[a.E] = a.ids ? end >> 16 : (int)hi;
             }
         }
         carry += chunk;
@@ -471,7 +489,13 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int tiles = carry;
+    // (warp 8 reads weights only.)  The next kernel may begin once this one need not wait: so its
+    // beginning says that the kernel ahead of this one is complete.
+    if (warp != 8) {
+        if (a.early) pdl_wait();
+        pdl_launch_dependents();
+    }
+    const int tiles = carry & low;
     const int nks = (a.K + G::kStageK - 1) / G::kStageK;  // stages per unit
     constexpr int kPerScale = kMxScaleK / G::kStageK;         // stages per copy of scales
 
@@ -794,8 +818,9 @@ static cudaError_t gemm_tile(const MicroscaleMaps &tm, const MxArgs &a, int out,
 
 cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const int32_t *offsets, int E,
                                    int N, int K, int dtype, void *y, int64_t ldy, uint8_t *codes,
-                                   uint8_t *scales, int32_t *status, cudaStream_t stream) {
+                                   uint8_t *scales, MicroscaleEarly early, int32_t *status, cudaStream_t stream) {
     MxArgs a{};
+    a.early = early.on, a.ids = early.ids, a.nids = early.nids;
     a.deep = tm.deep;
     a.offsets = offsets, a.rows = rows, a.E = E, a.N = N, a.K = K;
     a.x_scales = tm.x_scales, a.w_scales = tm.w_scales, a.kpitch = microscale_pitch(K);

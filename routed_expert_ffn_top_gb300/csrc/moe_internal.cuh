@@ -391,9 +391,10 @@ cudaError_t launch_token_plan(const int32_t *ids, int M, int k, int E, int32_t *
                               int32_t *row_route, int32_t *route_row, cudaStream_t stream);
 cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k, int H,
                               const int32_t *route_row, void *rows, int64_t ldr, cudaStream_t stream);
+// early: all but the rows were complete before the kernel ahead in the stream began.
 cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
                                 const int32_t *route_row, const float *w, const void *residual,
-                                int64_t ldres, void *out, int64_t ldo, cudaStream_t stream);
+                                int64_t ldres, void *out, int64_t ldo, bool early, cudaStream_t stream);
 cudaError_t launch_token_unsort_grad(const void *gout, int64_t ldo, const void *rows, int64_t ldr,
                                      int dtype, int M, int k, int H, const int32_t *route_row,
                                      const float *w, void *grows, int64_t ldg, float *gw,
@@ -427,9 +428,17 @@ struct MicroscaleMaps {
     const uint8_t *x_scales, *w_scales;
 };
 // codes == NULL: y [rows][N] of dtype; else the gated form, codes and scales of [rows][N / 2].
+// early.on: the offsets and weights were complete before the kernel ahead in the stream began;
+// with early.ids the groups are counted from up to kPlanQuantizeRoutes routes' experts, and it
+// is these that were.
+struct MicroscaleEarly {
+    bool on;
+    const int32_t *ids;
+    int nids;
+};
 cudaError_t launch_microscale_gemm(const MicroscaleMaps &tm, int64_t rows, const int32_t *offsets, int E,
                                    int N, int K, int dtype, void *y, int64_t ldy, uint8_t *codes,
-                                   uint8_t *scales, int32_t *status, cudaStream_t stream);
+                                   uint8_t *scales, MicroscaleEarly early, int32_t *status, cudaStream_t stream);
 
 // Shared launch helper: programmatic dependent launch on, optional cluster dims.
 cudaLaunchConfig_t launch_config(dim3 grid, dim3 block, size_t smem, cudaStream_t stream,

@@ -215,6 +215,7 @@ struct RowArgs {
     const int32_t *route_row;
     const float *w;              // NULL: weights of one
     int M, k, H;
+    int early;                   // unsort: all but the rows were complete before the kernel ahead began
 };
 
 // Sort: a unit is 32 * kSortVecs vectors of one token, read once and written k times.  The
@@ -432,7 +433,8 @@ __device__ __forceinline__ void ring_load(const uint4 *p, float (&v)[16 / sizeof
 __device__ __forceinline__ int ring_row(const RowArgs &a, int64_t m) {
     const int lane = threadIdx.x & 31;
     if (lane >= a.k) return -1;
-    const int v = a.route_row[m * a.k + lane];
+    const int32_t *at = a.route_row + m * a.k + lane;
+    const int v = a.early ? __ldcg(at) : *at;
     return row_of(v, (int64_t)a.M * a.k) < 0 ? -1 : v;
 }
 
@@ -458,8 +460,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
     const int q = warp % wpt, tokens = kRingWarps / wpt;
     const int64_t step = (int64_t)gridDim.x * tokens;
     RingCursor now{(int64_t)blockIdx.x * tokens + warp / wpt, q}, ahead = now;
-    pdl_wait();
-    pdl_launch_dependents();
+    if (!a.early) pdl_wait();
 
     // rows of the token the copies are at; weights of the one the sums are at and of the next
     int row_a = -1;
@@ -471,6 +472,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
         w = weight(now.m);
         if (now.m + step < a.M) w_n = weight(now.m + step);
     }
+    if (a.early) pdl_wait();
+    pdl_launch_dependents();
     int slot_in = 0, slot_out = 0;
     auto issue = [&]() {
         if (ahead.m < a.M) {
@@ -799,8 +802,9 @@ cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k
 
 cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
                                 const int32_t *route_row, const float *w, const void *residual,
-                                int64_t ldres, void *out, int64_t ldo, cudaStream_t stream) {
+                                int64_t ldres, void *out, int64_t ldo, bool early, cudaStream_t stream) {
     RowArgs a{};
+    a.early = early;
     a.a = rows, a.res = residual, a.out = out, a.lda = ldr, a.ldres = ldres, a.ldout = ldo;
     a.route_row = route_row, a.w = w, a.M = M, a.k = k, a.H = H;
     MOE_ROW_DISPATCH(unsort_as, unsort_ring, ring_fits(k + (residual ? 1 : 0), 1))

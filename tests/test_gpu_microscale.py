@@ -281,6 +281,56 @@ def test_expert_step_is_its_parts(M, k, E, H, I, drop):
     assert moe.moe_read_device_status(work) == 0
 
 
+@pytest.mark.parametrize("M,k,E,H,I", [(1, 8, 128, 512, 256), (3, 4, 600, 256, 96), (32, 8, 24, 320, 160),
+                                       (33, 8, 24, 320, 160), (256, 1, 16, 512, 256), (700, 4, 40, 512, 256)])
+def test_steps_in_a_row_with_routes_of_their_own(M, k, E, H, I):
+    """Steps of two layers in a row, each with the rows and routes that the last one's output
+    gives and one workspace: the bits of the separate calls, each waited for.  (A step's products
+    begin before the kernel ahead has ended: groups or rows of the step before would show.)"""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + k)
+    layers = []
+    for _ in range(2):
+        layer = {"H": H, "I": I, "E": E, "router": torch.randn((H, E), generator=g, device="cuda")}
+        for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
+            c, s = moe.moe_microscale_quantize((torch.randn((E * n, cols), generator=g, device="cuda") * 0.1).to(torch.bfloat16))
+            layer[name + "_codes"], layer[name + "_scales"] = c.view(E, n, -1), s.view(E, n, -1)
+        layers.append(layer)
+    x0 = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+
+    def chain(step):
+        x, seen = x0, []
+        ids = torch.empty((M, k), dtype=torch.int32, device="cuda")
+        for i in range(8):
+            layer = layers[i % 2]
+            score, idx = torch.topk((x.float() @ layer["router"]) / x.float().norm(dim=1, keepdim=True), k, dim=1)
+            ids.copy_(idx)
+            if i == 5:
+                ids[0, 0] = -1
+            x = step(x, layer, ids, torch.softmax(score, dim=1))
+            seen.append(x)
+            # the step is quadratic in x, so without a norm between the layers eight overflow
+            x = torch.nn.functional.rms_norm(x, (H,))
+        return torch.stack(seen)
+
+    def parts(x, layer, ids, w):
+        offsets, _, rr = moe.moe_token_plan(ids, E)
+        q = moe.moe_microscale_quantize(x, route_row=rr)
+        torch.cuda.synchronize()
+        p = moe.moe_microscale_gated_product(*q, layer["gate_up_codes"], layer["gate_up_scales"], offsets=offsets)
+        torch.cuda.synchronize()
+        y = moe.moe_microscale_product(*p, layer["down_codes"], layer["down_scales"], offsets=offsets)
+        torch.cuda.synchronize()
+        return moe.moe_token_unsort(y, rr, w, residual=x)
+
+    work = moe.microscale_workspace(layers[0], M, k)
+    want = chain(parts)
+    got = chain(lambda x, layer, ids, w: moe.moe_microscale_ffn(x, layer, ids, w, residual=x, workspace=work))
+    assert bool(torch.isfinite(want.float()).all())
+    assert torch.equal(got, want)
+    assert moe.moe_read_device_status(work) == 0
+
+
 def test_many_small_gated_units():
     """Many units a CTA with little to do in each: every unit's u is its own."""
     g = gen(11)
