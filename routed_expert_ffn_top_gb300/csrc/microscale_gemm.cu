@@ -23,17 +23,21 @@
 // next one's MMAs.
 //
 // What bounds it, on a GB300 (H = 2048, I = 768, 128 experts, top 8 unless said):
-//   few rows     HBM.  21 tokens (75 experts reached): gated 22.4 us for 126 MB (0.82 of the copy
-//                rate), down 16.1 us for 63 MB (0.58: 4 us of a launch are not copies, and a unit
-//                has only 48 KB).  One token: 7.2 and 6.2 us, start-up and one pass of latency.
-//   many rows    shared memory's 128 bytes a cycle: per 256 of K a 128 x 192 tile writes 40 KB
-//                and its MMAs read 40 KB (640 cycles for 384 of MMAs), then the scale reads and
-//                the epilogue.  8192 tokens: gated 132 us (3.1 PFLOP/s), down 84 us; 16384 x 8192
-//                x 8192 in one group 446 us (4.9 PFLOP/s, 2.5 of the bf16 rate), where the clock
-//                also falls.  Two CTAs a tile (cta_group::2) measured the same and were left out.
-// Measured and left out for few rows: both products of an expert step in one grid, the second
-// waiting for the first row tile by row tile (8 tokens 44 against 38 us, 21 the same); 256-deep
-// stages (21 tokens' gated product 26.6); an L2 promotion of 256 bytes (down 19.1 to 21.0).
+//   few rows     HBM.  21 tokens (75 experts reached): gated 21.8 us for 126 MB (0.85 of the copy
+//                rate), down 15.3 us for 63 MB (0.61: 4 us of a launch are not copies, and a unit
+//                has only 48 KB).  One token: 6.8 and 5.6 us, start-up and one pass of latency.
+//                In an expert step both begin while the kernel ahead runs (MxArgs::early).
+//   many rows    the way into the SM.  16384 x 8192 x 8192 in one group takes 379 us (5.8 PFLOP/s,
+//                3.0 of the bf16 rate), the same with the copies of codes alone 364: 64 bytes a
+//                cycle and SM, 40 KB per 256 of K for 384 cycles of MMAs.
+//                8192 tokens: gated 105 us (3.9 PFLOP/s; 512 rows an expert, four row tiles),
+//                down 85 us, of which 16 go with the stores of y (268 MB) not issued and 7 more
+//                with their staging.
+// Two CTAs a tile (cta_group::2, 256 x 192) take a third less in, but gated 113 us, down 93, and
+// the large product 374: left out.  So were, for few rows, both products of an expert step in
+// one grid, the second waiting for the first row tile by row tile (8 tokens 44 against 38 us, 21
+// the same); 256-deep stages (21 tokens' gated product 26.6 against 22.1); an L2 promotion of 256
+// bytes (down 21.0 against 19.1).  Stores of y by 128-byte rows take the time of the 64-byte ones.
 #include <type_traits>
 
 #include "gemm_core.cuh"
@@ -50,8 +54,8 @@ constexpr int kMxStaging = 2048;  // bytes a warp stages for its stores: 32 rows
 //   kTok = 128: 128 rows of x as the MMA's M side, 192 channels as its N side (two accumulators
 //     of 192 columns leave tensor memory for the scales of four stages; 256 would not).
 //   kTok = 32, for small groups: the sides change places, 128 channels are M and up to 32 rows
-//     N, so no MMA reads rows that do not exist and four epilogue warps share every row (with
-//     the rows on the M side one token's gated product took 8.4 us for 7.2).
+//     N, so no MMA reads rows that do not exist and four epilogue warps share every row N, so no MMA reads rows that do not exist and four epilogue warps share every row (with
+//     the rows on the M side one token's gated product took 8.4 us, this way 7.2)..
 template <int kTok_>
 struct MxTile {
     static_assert(kTok_ == 32 || kTok_ == 128, "row tiles");
@@ -779,9 +783,9 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
 
 // ----------------------------------------------------------------------------------- launcher
 // Small tiles while the groups are small: up to 32 rows, or under 4 rows an expert on average.
-// Both tiles measured over an expert step's two products (H = 2048, I = 768, 128 experts, top 8,
-// us, large / small): 8 tokens 63 / 39, 21 62 / 53, 32 67 / 61, 64 (4 rows an expert) 66 / 67, 128
-// 70 / 75, 256 74 / 85, 512 82 / 114.
+// Both tiles measured over an expert step (H = 2048, I = 768, 128 experts, top 8, us, large /
+// small): 1 token 17.6 / 15.8, 8 34.7 / 31.4, 21 45.4 / 44.5, 32 50.7 / 50.7, 64 (4 rows an
+// expert) 55.6 / 56.4, 128 61.6 / 64.7, 256 67.1 / 75.0, 512 74.3 / 107.
 MicroscaleTile microscale_tile(int64_t rows, int E) {
     using Large = MxTile<128>;
     using Small = MxTile<32>;
