@@ -437,7 +437,10 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     }
     // Early, nothing of the kernel ahead is needed before the rows: the tiles are counted and the
     // first weights copied while it runs.
-    if (!a.early) pdl_wait();
+    if (!a.early) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     if (a.ids) {
         for (int e = threadIdx.x; e < a.E; e += kMxThreads) ctl.begin[e] = 0;
         __syncthreads();
@@ -457,8 +460,9 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
             if (a.ids) {
                 hi = ctl.begin[e];
             } else {
-                lo = a.offsets ? __ldcg(a.offsets + e) : 0;
-                hi = a.offsets ? __ldcg(a.offsets + e + 1) : a.rows;
+                if (!a.offsets) hi = a.rows;
+                else if (a.early) lo = __ldcg(a.offsets + e), hi = __ldcg(a.offsets + e + 1);
+                else lo = a.offsets[e], hi = a.offsets[e + 1];
                 lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
                 hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
             }
@@ -493,10 +497,10 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // (warp 8 reads weights only.)  The next kernel may begin once this one need not wait: so its
-    // beginning says that the kernel ahead of this one is complete.
-    if (warp != 8) {
-        if (a.early) pdl_wait();
+    // (Warp 8 reads weights only.)  Either way the next kernel may begin only after this one's
+    // wait: its beginning says that the kernel ahead of this one is complete.
+    if (a.early && warp != 8) {
+        pdl_wait();
         pdl_launch_dependents();
     }
     const int tiles = carry & low;
@@ -515,7 +519,7 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         unsigned char *const base = stages + (side_a ? 0 : G::kABytes);
         int stage = 0;
         uint32_t phase = 0, issued = 0, par = 0;
-        bool ok = true;
+        bool ok = true, ahead = a.early && warp == 8;
         for (MxWalk<kTok> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
             const int w0 = mx_first_channel<kGated, G::kCh>(a, x.e, x.ct);
             const uint64_t pol = ctl.first[x.e + 1] - ctl.first[x.e] == 1 ? once : keep;
@@ -541,7 +545,11 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                     issued |= 1u << slot;
                     par = (par & ~(1u << slot)) | (phase << slot);
                 }
-                if (++stage == G::kStages) stage = 0, phase ^= 1u;
+                if (++stage == G::kStages) {
+                    stage = 0, phase ^= 1u;
+                    // all slots full: the kernel ahead is waited for outside the bounded waits
+                    if (ahead) pdl_wait(), ahead = false;
+                }
             }
         }
         // every copy has landed before the CTA can exit
