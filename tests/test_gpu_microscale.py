@@ -331,6 +331,46 @@ def test_steps_in_a_row_with_routes_of_their_own(M, k, E, H, I):
     assert moe.moe_read_device_status(work) == 0
 
 
+@pytest.mark.parametrize("M,k", [(1, 4), (20, 8), (90, 5)])
+def test_steps_in_a_graph(M, k):
+    """Three steps captured in a graph on a stream of their own, replayed with other rows and
+    routes: the bits of calls outside it."""
+    E, H, I = 32, 256, 128
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    layer = {"H": H, "I": I, "E": E}
+    for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
+        c, s = moe.moe_microscale_quantize((torch.randn((E * n, cols), generator=g, device="cuda") * 0.05).to(torch.bfloat16))
+        layer[name + "_codes"], layer[name + "_scales"] = c.view(E, n, -1), s.view(E, n, -1)
+    x = torch.zeros((M, H), dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros((3, M, k), dtype=torch.int32, device="cuda")
+    w = torch.full((M, k), 1.0 / k, device="cuda")
+    work = moe.microscale_workspace(layer, M, k)
+
+    def steps(ws):
+        y = x
+        for i in range(3):
+            y = moe.moe_microscale_ffn(y, layer, ids[i], w, residual=y, workspace=ws)
+        return y
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        steps(work)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = steps(work)
+    other = moe.microscale_workspace(layer, M, k)
+    for _ in range(4):
+        x.copy_(torch.randn((M, H), generator=g, device="cuda"))
+        ids.copy_(torch.randint(-1, E, (3, M, k), generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, steps(other))
+    assert moe.moe_read_device_status(work) == 0
+
+
 def test_many_small_gated_units():
     """Many units a CTA with little to do in each: every unit's u is its own."""
     g = gen(11)
