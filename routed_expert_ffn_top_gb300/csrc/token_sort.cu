@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kGradThreads) token_unsort_grad_kernel(const R
 // registers.  Here each lane copies its own pieces of the next kDepth units into its own slots
 // of shared memory (cp.async), so a warp has kDepth units in flight and no thread waits for
 // another.  The arithmetic and its order per element are those of the form above.  8192 tokens x
-// 8 routes x 2048 bf16 (form above): unsort 54.9 us, 0.90 of the copy rate (161); without weights
-// and residual, as the gradient of sort, 47.5 us, 0.94 (157); one token 2.5 us (3.5).
+// 8 routes x 2048 bf16 (form above): unsort 54.9 us, 0.90 of the copy rate (75); without weights
+// and residual, as the gradient of sort, 47.5 us, 0.94 (64); one token 2.4 us (2.3).
 constexpr int kRingWarps = 8;
 // Shared memory of a CTA, whatever part its slots fill: three CTAs an SM, in a grid that fills
 // the SMs once.  Every such launch asks for the same size: with sizes of their own, a grid that
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
 // One CTA per token (grid-stride): warp q takes chunks q, q + 8, ... of the row, a running
 // sequence of units over all its tokens; the k <= 8 products are summed over the lanes, then
 // over the warps, in fixed trees.  8192 tokens x 8 routes x 2048 bf16: 88.9 us, 0.94 of the copy
-// rate (form above 207); one token 3.3 us.
+// rate (form above 100); one token 3.5 us (2.9).
 template <typename T, int kDepth>
 __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_grad_ring_kernel(const RowArgs a, int nvec, int nchunk) {
     constexpr int n = 16 / sizeof(T);
