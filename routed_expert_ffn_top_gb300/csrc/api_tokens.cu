@@ -182,8 +182,10 @@ static bool product_maps(MicroscaleMaps *tm, const uint8_t *x_codes, const uint8
     const uint32_t ab[3] = {128, m, depth};
     const uint64_t bd[4] = {inner, wrows, halves, chunks}, bs[3] = {row, up * row, 128};
     const uint32_t bb[4] = {128, bn, two, depth};
-    // y in bytes, boxes of 64 bytes x 32 rows, where its pointer and pitch allow tensor stores
-    tm->bulk = y && t.m == 128 && (reinterpret_cast<uintptr_t>(y) | (uint64_t)(ldy * elem)) % 16 == 0;
+    // y in bytes, boxes of 64 bytes x 32 rows, where its pointer and pitch allow tensor stores and
+    // a row's bytes lie within their 32-bit signed coordinates
+    tm->bulk = y && t.m == 128 && (reinterpret_cast<uintptr_t>(y) | (uint64_t)(ldy * elem)) % 16 == 0 &&
+               (int64_t)N * elem <= INT32_MAX - 64;
     const uint64_t yd[2] = {(uint64_t)N * elem, (uint64_t)rows}, ys[1] = {(uint64_t)(ldy * elem)};
     const uint32_t yb[2] = {64, 32};
     if (!tm->bulk) memset(&tm->y, 0, sizeof tm->y);
