@@ -552,6 +552,8 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                 }
             }
         }
+        // fewer stages than the ring holds: the other producer's copies come after the kernel ahead
+        if (ahead) pdl_wait();
         // every copy has landed before the CTA can exit
         for (int s = 0; s < G::kSlots; ++s)
             if ((issued >> s) & 1u)

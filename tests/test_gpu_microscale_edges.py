@@ -42,3 +42,45 @@ def test_product_of_rows_past_2_gb():
             assert int(torch.count_nonzero(y[r, lo:hi])) == 0  # a NaN counts
     del y, wc, ws
     torch.cuda.empty_cache()
+
+
+def make_layer(E, H, I, seed, gain=0.05):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    layer = {"H": H, "I": I, "E": E}
+    for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
+        c, s = moe.moe_microscale_quantize((torch.randn((E * n, cols), generator=g, device="cuda") * gain).to(torch.bfloat16))
+        layer[name + "_codes"], layer[name + "_scales"] = c.view(E, n, -1), s.view(E, n, -1)
+    return layer
+
+
+def parts(h, layer, ids, w, residual=None):
+    """The expert step by its separate calls, each waited for."""
+    offsets, _, rr = moe.moe_token_plan(ids, layer["E"])
+    q = moe.moe_microscale_quantize(h, route_row=rr)
+    torch.cuda.synchronize()
+    p = moe.moe_microscale_gated_product(*q, layer["gate_up_codes"], layer["gate_up_scales"], offsets=offsets)
+    torch.cuda.synchronize()
+    y = moe.moe_microscale_product(*p, layer["down_codes"], layer["down_scales"], offsets=offsets)
+    torch.cuda.synchronize()
+    return moe.moe_token_unsort(y, rr, w, residual=residual)
+
+
+@pytest.mark.parametrize("M,k,I", [(1, 8, 96), (21, 8, 768), (300, 4, 96)])
+def test_step_behind_work_longer_than_its_waits(M, k, I):
+    """Queued behind work that takes longer than a bounded wait, with units of few stages (a
+    CTA's copies then never come round its ring): no wait runs out."""
+    E, H = 64, 256
+    layer = make_layer(E, H, I, seed=M)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    ids = torch.randint(0, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((M, k), generator=g, device="cuda")
+    h = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    want = parts(h, layer, ids, w)
+    work = moe.microscale_workspace(layer, M, k)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(3_500_000_000)  # over a second and a half at any SM clock
+    out = moe.moe_microscale_ffn(h, layer, ids, w, workspace=work)
+    assert moe.moe_read_device_status(work) == 0
+    assert torch.equal(out, want)
