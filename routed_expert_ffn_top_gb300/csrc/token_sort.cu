@@ -505,7 +505,12 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
     int row_a = -1;
     float w = 0.0f, w_n = 0.0f;
     // a dropped route's weight is zero, whatever the caller's says
-    auto weight = [&](int64_t m) { return ring_row(a, m) < 0 ? 0.0f : (a.w ? a.w[m * a.k + lane] : 1.0f); };
+    auto weight = [&](int64_t m) {
+        if (ring_row(a, m) < 0) return 0.0f;
+        if (!a.w) return 1.0f;
+        const float *at = a.w + m * a.k + lane;
+        return a.early ? __ldcg(at) : *at;
+    };
     if (now.m < a.M) {
         row_a = ring_row(a, now.m);
         w = weight(now.m);

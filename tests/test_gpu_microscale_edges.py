@@ -84,3 +84,42 @@ def test_step_behind_work_longer_than_its_waits(M, k, I):
     out = moe.moe_microscale_ffn(h, layer, ids, w, workspace=work)
     assert moe.moe_read_device_status(work) == 0
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M,k", [(1, 4), (20, 8), (90, 5)])
+def test_replayed_steps_with_other_weights(M, k):
+    """Steps in a graph whose route weights change in place, from replay to replay and within
+    one: what the way back reads before the kernel ahead has ended is this step's."""
+    E, H, I = 32, 256, 128
+    layer = make_layer(E, H, I, seed=M)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + 1)
+    x = torch.zeros((M, H), dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros((M, k), dtype=torch.int32, device="cuda")
+    scale, w = torch.zeros((4, M, k), device="cuda"), torch.zeros((M, k), device="cuda")
+
+    def steps(ws):
+        outs = []
+        for i in range(4):
+            w.copy_(scale[i])
+            outs.append(moe.moe_microscale_ffn(x, layer, ids, w, residual=x, workspace=ws))
+        return torch.stack(outs)
+
+    work = moe.microscale_workspace(layer, M, k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        steps(work)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = steps(work)
+    for _ in range(6):
+        x.copy_(torch.randn((M, H), generator=g, device="cuda"))
+        ids.copy_(torch.randint(-1, E, (M, k), generator=g, device="cuda"))
+        scale.copy_(torch.rand((4, M, k), generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.stack([parts(x, layer, ids, scale[i], residual=x) for i in range(4)])
+        assert torch.equal(out, want)
+    assert moe.moe_read_device_status(work) == 0
