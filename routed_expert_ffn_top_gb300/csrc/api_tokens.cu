@@ -289,6 +289,8 @@ extern "C" int moe_microscale_ffn(const void *h, const moe_microscale_weights_t 
     if (!h || !topk_ids || !topk_weights || !out || !workspace || !aligned(workspace, 256) ||
         !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(h, 16) || !aligned(out, 16) || (residual && !aligned(residual, 16)))
         return MOE_ERR_INVALID_ARG;
+    for (const uint8_t *p : {w->gate_up_codes, w->gate_up_scales, w->down_codes, w->down_scales})
+        if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
     const int64_t R = (int64_t)M * k;
     const MicroscaleWs L = microscale_ws(w->E, w->H, w->I, R);
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
