@@ -801,8 +801,16 @@ def moe_microscale_dequantize(codes, scales, dtype=torch.bfloat16, out=None, str
     return out
 
 
+def _workspace(t, device):
+    """Checks a workspace: contiguous bytes on the device.  Returns (address, bytes)."""
+    if not (t.dtype is torch.uint8 and t.device == device and t.is_contiguous()):
+        _need(t, torch.uint8, "workspace", device)
+    return t.data_ptr(), t.numel()
+
+
 def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
-    """Checks of the grouped products; returns (rows, E, N, K, offsets' address, workspace)."""
+    """Checks of the grouped products; returns (rows, E, N, K, offsets' address, workspace,
+    (its address, its bytes))."""
     dev = x_codes.device
     K = _microscaled(x_codes, x_scales, dev, "x")
     if _microscaled(w_codes, w_scales, dev, "w") != K:
@@ -814,15 +822,15 @@ def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
         off = _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     if workspace is None:
         workspace = torch.zeros(MOE_MICROSCALE_STATUS_BYTES, dtype=torch.uint8, device=dev)
-    return x_codes.shape[0], E, N, K, off, workspace
+    return x_codes.shape[0], E, N, K, off, workspace, _workspace(workspace, dev)
 
 
 def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
                            dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """y [rows,N] of 4-bit rows and 4-bit weights [E,N,K] (or [N,K]), rows grouped by offsets
     [E+1]; rows past the last group are zero."""
-    rows, E, N, K, off, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
-                                                  workspace)
+    rows, E, N, K, off, workspace, ws = _product_args(x_codes, x_scales, w_codes, w_scales,
+                                                      offsets, workspace)
     dev = x_codes.device
     if out is None:
         out = torch.empty((rows, N), dtype=dtype, device=dev)
@@ -830,8 +838,7 @@ def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
     ldy = _rows(out, "out", dev, out.dtype, (rows, N))
     _check(lib().moe_microscale_product(x_codes.data_ptr(), x_scales.data_ptr(), rows, off,
                                         w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, code,
-                                        out.data_ptr(), ldy, workspace.data_ptr(),
-                                        workspace.numel(), _raw_stream(stream, dev)),
+                                        out.data_ptr(), ldy, *ws, _raw_stream(stream, dev)),
            "moe_microscale_product")
     return out
 
@@ -840,28 +847,28 @@ def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=N
                                  scales=None, workspace=None, stream=None):
     """SiLU(g) * u of the gate and up halves of w [E,N,K], quantised: (codes, scales) of
     [rows,N/2]."""
-    rows, E, N, K, off, workspace = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
-                                                  workspace)
+    rows, E, N, K, off, workspace, ws = _product_args(x_codes, x_scales, w_codes, w_scales,
+                                                      offsets, workspace)
     if N % 64:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_gated_product")
     dev = x_codes.device
     codes, scales = _quantised_outputs(codes, scales, rows, N // 2, dev)
     _check(lib().moe_microscale_gated_product(x_codes.data_ptr(), x_scales.data_ptr(), rows, off,
                                               w_codes.data_ptr(), w_scales.data_ptr(), E, N, K,
-                                              codes.data_ptr(), scales.data_ptr(),
-                                              workspace.data_ptr(), workspace.numel(),
+                                              codes.data_ptr(), scales.data_ptr(), *ws,
                                               _raw_stream(stream, dev)),
            "moe_microscale_gated_product")
     return codes, scales
 
 
-def microscale_weights(layer: dict) -> MicroscaleWeights:
+def microscale_weights(layer: dict, device=None) -> MicroscaleWeights:
     """C descriptor of a layer's 4-bit weights: H, I, E and gate_up_codes [E,2I,H/2],
-    gate_up_scales, down_codes [E,H,I/2], down_scales (the caller keeps the tensors alive)."""
+    gate_up_scales, down_codes [E,H,I/2], down_scales (the caller keeps the tensors alive), all
+    on one device, `device` if given."""
     H, I, E = layer["H"], layer["I"], layer["E"]
     gc, gs, dc, ds = (layer["gate_up_codes"], layer["gate_up_scales"], layer["down_codes"],
                       layer["down_scales"])
-    dev = dc.device
+    dev = dc.device if device is None else device
     if gc.shape != (E, 2 * I, H // 2) or _microscaled(gc, gs, dev, "gate_up") != H:
         raise ValueError("gate_up_codes must have shape %s" % ((E, 2 * I, H // 2),))
     if dc.shape != (E, H, I // 2) or _microscaled(dc, ds, dev, "down") != I:
@@ -908,7 +915,7 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
     """The 4-bit expert step (include/moe.h) for given routes; `layer` as microscale_weights
     takes it."""
     dev = h.device
-    w = microscale_weights(layer)
+    w = microscale_weights(layer, dev)
     M, k = topk_ids.shape
     H = w.H
     bf16 = torch.bfloat16
@@ -922,6 +929,6 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
     if workspace is None:
         workspace = microscale_workspace(layer, M, k)
     _check(lib().moe_microscale_ffn(ph, ctypes.byref(w), M, k, ids, pw, res, po,
-                                    workspace.data_ptr(), workspace.numel(),
-                                    _raw_stream(stream, dev)), "moe_microscale_ffn")
+                                    *_workspace(workspace, dev), _raw_stream(stream, dev)),
+           "moe_microscale_ffn")
     return out
