@@ -602,8 +602,7 @@ def _row_dtype(t, name):
     code = _ROW_DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("%s must be bfloat16, float16 or float32, got %s" % (name, t.dtype))
-    if t.dim() != 2:
-        raise ValueError("%s must be a matrix" % name)
+    _matrix(t, name)
     return code
 
 
@@ -616,11 +615,16 @@ def _vector(t, name, dtype, device, shape):
     return t.data_ptr()
 
 
+def _matrix(t, name):
+    """The two sizes of a matrix."""
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix, got shape %s" % (name, tuple(t.shape)))
+    return t.shape
+
+
 def _routes(t, device):
     """Checks route_row [M,k]; returns (address, M, k)."""
-    if t.dim() != 2:
-        raise ValueError("route_row must be a matrix")
-    M, k = t.shape
+    M, k = _matrix(t, "route_row")
     return _vector(t, "route_row", torch.int32, device, (M, k)), M, k
 
 
@@ -628,7 +632,7 @@ def moe_token_plan(topk_ids, E, offsets=None, row_route=None, route_row=None, st
     """(offsets [E+1], row_route [M*k], route_row [M,k]) of topk_ids [M,k] (include/moe.h)."""
     dev = topk_ids.device
     _need(topk_ids, torch.int32, "topk_ids", dev)
-    M, k = topk_ids.shape
+    M, k = _matrix(topk_ids, "topk_ids")
     i32 = torch.int32
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=i32, device=dev)
@@ -777,7 +781,7 @@ def moe_microscale_quantize(x, route_row=None, codes=None, scales=None, stream=N
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_quantize")
     rr, k = None, 1
     if route_row is not None:
-        k = route_row.shape[1]
+        k = _matrix(route_row, "route_row")[1]
         rr = _vector(route_row, "route_row", torch.int32, dev, (rows, k))
     codes, scales = _quantised_outputs(codes, scales, rows * k, cols, dev)
     _check(lib().moe_microscale_quantize(x.data_ptr(), ldx, code, rows, cols, rr, k,
@@ -789,8 +793,8 @@ def moe_microscale_quantize(x, route_row=None, codes=None, scales=None, stream=N
 def moe_microscale_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values [rows,cols] of codes [rows,cols/2] and scales."""
     dev = codes.device
+    rows = _matrix(codes, "codes")[0]
     cols = _microscaled(codes, scales, dev, "x")
-    rows = codes.shape[0]
     if out is None:
         out = torch.empty((rows, cols), dtype=dtype, device=dev)
     code = _row_dtype(out, "out")
@@ -812,17 +816,20 @@ def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
     """Checks of the grouped products; returns (rows, E, N, K, offsets' address, workspace,
     (its address, its bytes))."""
     dev = x_codes.device
+    rows = _matrix(x_codes, "x_codes")[0]
     K = _microscaled(x_codes, x_scales, dev, "x")
     if _microscaled(w_codes, w_scales, dev, "w") != K:
         raise ValueError("x and w must have the same number of columns")
     ws = w_codes.shape
+    if len(ws) != 2 and len(ws) != 3:
+        raise ValueError("w_codes must have shape [N,K/2] or [E,N,K/2], got %s" % (tuple(ws),))
     E, N = (1, ws[0]) if len(ws) == 2 else (ws[0], ws[1])
     off = None
     if offsets is not None:
         off = _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     if workspace is None:
         workspace = torch.zeros(MOE_MICROSCALE_STATUS_BYTES, dtype=torch.uint8, device=dev)
-    return x_codes.shape[0], E, N, K, off, workspace, _workspace(workspace, dev)
+    return rows, E, N, K, off, workspace, _workspace(workspace, dev)
 
 
 def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
@@ -916,7 +923,7 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
     takes it."""
     dev = h.device
     w = microscale_weights(layer, dev)
-    M, k = topk_ids.shape
+    M, k = _matrix(topk_ids, "topk_ids")
     H = w.H
     bf16 = torch.bfloat16
     ph = _vector(h, "h", bf16, dev, (M, H))

@@ -103,3 +103,31 @@ def test_a_workspace_is_contiguous_bytes_of_the_device(fake, work, error):
     with pytest.raises(error):
         moe.moe_microscale_gated_product(*x, *wt, offsets=offsets, workspace=work)
     assert launches(fake) == []
+
+
+def test_rows_are_matrices(fake):
+    """Codes [E,n,cols/2] of a layer are not rows: E of its E * n rows would come back."""
+    layer, (c, s), wt = four_bit_layer(), quantised(3, 64), quantised(2, 64, 64)
+    off = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="matrix"):
+        moe.moe_microscale_dequantize(layer["gate_up_codes"], layer["gate_up_scales"])
+    for call in (moe.moe_microscale_product, moe.moe_microscale_gated_product):
+        with pytest.raises(ValueError, match="matrix"):
+            call(layer["gate_up_codes"], layer["gate_up_scales"], *wt, offsets=off)
+        with pytest.raises(ValueError, match="matrix"):
+            call(c[0], s[0], *wt, offsets=off)
+        for w in (quantised(64), quantised(2, 3, 64, 64)):
+            with pytest.raises(ValueError, match="w_codes"):
+                call(c, s, *w)
+    with pytest.raises(ValueError, match="route_row"):
+        moe.moe_microscale_quantize(torch.zeros(3, 64), route_row=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="topk_ids"):
+        moe.moe_token_plan(torch.zeros(3, dtype=torch.int32), 4)
+    with pytest.raises(ValueError, match="topk_ids"):
+        h, _, w = step_args()
+        moe.moe_microscale_ffn(h, layer, torch.zeros(3, dtype=torch.int32), w)
+    assert launches(fake) == []
+    moe.moe_microscale_dequantize(c, s)
+    moe.moe_microscale_product(c, s, *wt, offsets=off)
+    moe.moe_microscale_product(c, s, wt[0][0], wt[1][0])
+    assert len(launches(fake)) == 3
