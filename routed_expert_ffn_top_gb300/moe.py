@@ -570,9 +570,12 @@ _ROW_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.flo
 
 
 def _raw_stream(stream, device):
-    """The stream's handle; the device's current stream when none is given."""
+    """The stream's handle; the device's current stream when none is given.  The library launches
+    on the current device, which has to be the tensors'."""
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device, got %s" % device)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, torch.cuda.current_device()))
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)

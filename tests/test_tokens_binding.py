@@ -131,3 +131,14 @@ def test_rows_are_matrices(fake):
     moe.moe_microscale_product(c, s, *wt, offsets=off)
     moe.moe_microscale_product(c, s, wt[0][0], wt[1][0])
     assert len(launches(fake)) == 3
+
+
+def test_tensors_of_a_device_that_is_not_current_are_refused(monkeypatch):
+    """The library launches on the current device; the other's default stream has the same
+    handle, 0."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    assert moe._raw_stream(None, torch.device("cuda", 0)) == 0
+    for stream in (None, 0, 1 << 20):
+        with pytest.raises(ValueError, match="current device"):
+            moe._raw_stream(stream, torch.device("cuda", 1))
