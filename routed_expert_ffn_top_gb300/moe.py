@@ -191,9 +191,17 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _current_stream(index) -> int:
+    """Handle of a device's current stream: without a Stream object where torch allows it."""
+    try:
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return ctypes.c_void_p(_current_stream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     return ctypes.c_void_p(int(stream))
@@ -577,7 +585,7 @@ def _raw_stream(stream, device):
     if device.index != torch.cuda.current_device():
         raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, torch.cuda.current_device()))
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return _current_stream(device.index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 

@@ -142,3 +142,14 @@ def test_tensors_of_a_device_that_is_not_current_are_refused(monkeypatch):
     for stream in (None, 0, 1 << 20):
         with pytest.raises(ValueError, match="current device"):
             moe._raw_stream(stream, torch.device("cuda", 1))
+
+
+def test_the_current_stream_without_the_raw_handle(monkeypatch):
+    """Where torch has no call for the raw handle the public one serves."""
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert moe._raw_stream(None, torch.device("cuda", 0)) == 77
+    assert moe._stream(None).value == 77
