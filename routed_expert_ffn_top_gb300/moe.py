@@ -191,12 +191,11 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _current_stream(index) -> int:
-    """Handle of a device's current stream: without a Stream object where torch allows it."""
-    try:
-        return torch._C._cuda_getCurrentRawStream(index)
-    except AttributeError:
-        return torch.cuda.current_stream(index).cuda_stream
+# The current device, and the handle of its current stream without a Stream object, by torch's own
+# short calls where it has them (the public ones take a microsecond each of calls that take 5).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -577,16 +576,33 @@ def moe_reader_ffn(h, rd: dict, topk_ids, topk_weights, K: int, nscan: int = 80,
 _ROW_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
 
 
-def _raw_stream(stream, device):
-    """The stream's handle; the device's current stream when none is given.  The library launches
-    on the current device, which has to be the tensors'."""
+def _need_cuda(device):
     if device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device, got %s" % device)
-    if device.index != torch.cuda.current_device():
-        raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, torch.cuda.current_device()))
-    if stream is None:
-        return _current_stream(device.index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _launch_stream(stream, device):
+    """Makes a given stream (an object or a handle) the current one.  The calls below run whole
+    under it, so that the outputs and temporaries they allocate are that stream's: memory of
+    another stream may still be in use there, and a temporary would be given away there while
+    the launches use it."""
+    _need_cuda(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)  # 0 and 1 name the default stream
+        stream = (torch.cuda.ExternalStream(handle, device) if handle > 1 else
+                  torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream(device):
+    """Handle of the current stream.  The library launches on the current device, which has to be
+    the tensors'."""
+    index = device.index
+    if index is None:
+        _need_cuda(device)
+    if index != _current_device():
+        raise ValueError("tensors on %s, but the current device is cuda:%d" % (device, _current_device()))
+    return _current_stream(index)
 
 
 def _rows(t, name, device, dtype, shape):
@@ -613,7 +629,8 @@ def _row_dtype(t, name):
     code = _ROW_DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("%s must be bfloat16, float16 or float32, got %s" % (name, t.dtype))
-    _matrix(t, name)
+    if t.dim() != 2:
+        _not_a_matrix(t, name)
     return code
 
 
@@ -626,42 +643,52 @@ def _vector(t, name, dtype, device, shape):
     return t.data_ptr()
 
 
-def _matrix(t, name):
-    """The two sizes of a matrix."""
-    if t.dim() != 2:
-        raise ValueError("%s must be a matrix, got shape %s" % (name, tuple(t.shape)))
-    return t.shape
+def _not_a_matrix(t, name):
+    raise ValueError("%s must be a matrix, got shape %s" % (name, tuple(t.shape)))
 
 
 def _routes(t, device):
     """Checks route_row [M,k]; returns (address, M, k)."""
-    M, k = _matrix(t, "route_row")
+    if t.dim() != 2:
+        _not_a_matrix(t, "route_row")
+    M, k = t.shape
     return _vector(t, "route_row", torch.int32, device, (M, k)), M, k
 
 
 def moe_token_plan(topk_ids, E, offsets=None, row_route=None, route_row=None, stream=None):
     """(offsets [E+1], row_route [M*k], route_row [M,k]) of topk_ids [M,k] (include/moe.h)."""
+    if stream is not None:
+        with _launch_stream(stream, topk_ids.device):
+            return moe_token_plan(topk_ids, E, offsets, row_route, route_row)
     dev = topk_ids.device
-    _need(topk_ids, torch.int32, "topk_ids", dev)
-    M, k = _matrix(topk_ids, "topk_ids")
     i32 = torch.int32
+    if topk_ids.dim() != 2:
+        _not_a_matrix(topk_ids, "topk_ids")
+    M, k = topk_ids.shape
+    ids = _vector(topk_ids, "topk_ids", i32, dev, (M, k))
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=i32, device=dev)
+    else:
+        _vector(offsets, "offsets", i32, dev, (E + 1,))
     if row_route is None:
         row_route = torch.empty(M * k, dtype=i32, device=dev)
+    else:
+        _vector(row_route, "row_route", i32, dev, (M * k,))
     if route_row is None:
         route_row = torch.empty((M, k), dtype=i32, device=dev)
-    rc = lib().moe_token_plan(topk_ids.data_ptr(), M, k, E,
-                              _vector(offsets, "offsets", i32, dev, (E + 1,)),
-                              _vector(row_route, "row_route", i32, dev, (M * k,)),
-                              _vector(route_row, "route_row", i32, dev, (M, k)),
-                              _raw_stream(stream, dev))
+    else:
+        _vector(route_row, "route_row", i32, dev, (M, k))
+    rc = lib().moe_token_plan(ids, M, k, E, offsets.data_ptr(), row_route.data_ptr(),
+                              route_row.data_ptr(), _raw_stream(dev))
     _check(rc, "moe_token_plan")
     return offsets, row_route, route_row
 
 
 def moe_token_sort(x, route_row, rows=None, stream=None):
     """The token rows x [M,H] in sorted order: rows [M*k,H]."""
+    if stream is not None:
+        with _launch_stream(stream, x.device):
+            return moe_token_sort(x, route_row, rows)
     dev, dt = x.device, x.dtype
     code = _row_dtype(x, "x")
     rr, M, k = _routes(route_row, dev)
@@ -672,12 +699,15 @@ def moe_token_sort(x, route_row, rows=None, stream=None):
     else:
         ldr = _rows(rows, "rows", dev, dt, (M * k, H))
     _check(lib().moe_token_sort(x.data_ptr(), ldx, code, M, k, H, rr, rows.data_ptr(), ldr,
-                                _raw_stream(stream, dev)), "moe_token_sort")
+                                _raw_stream(dev)), "moe_token_sort")
     return rows
 
 
 def moe_token_sort_grad(grad_rows, route_row, grad_x=None, stream=None):
     """Gradient of moe_token_sort: grad_x [M,H] of grad_rows [M*k,H]."""
+    if stream is not None:
+        with _launch_stream(stream, grad_rows.device):
+            return moe_token_sort_grad(grad_rows, route_row, grad_x)
     dev, dt = grad_rows.device, grad_rows.dtype
     code = _row_dtype(grad_rows, "grad_rows")
     rr, M, k = _routes(route_row, dev)
@@ -688,13 +718,16 @@ def moe_token_sort_grad(grad_rows, route_row, grad_x=None, stream=None):
     else:
         ldx = _rows(grad_x, "grad_x", dev, dt, (M, H))
     _check(lib().moe_token_sort_grad(grad_rows.data_ptr(), ldr, code, M, k, H, rr,
-                                     grad_x.data_ptr(), ldx, _raw_stream(stream, dev)),
+                                     grad_x.data_ptr(), ldx, _raw_stream(dev)),
            "moe_token_sort_grad")
     return grad_x
 
 
 def moe_token_unsort(rows, route_row, topk_weights=None, residual=None, out=None, stream=None):
     """out [M,H] = residual + the weighted sum of each token's rows (include/moe.h)."""
+    if stream is not None:
+        with _launch_stream(stream, rows.device):
+            return moe_token_unsort(rows, route_row, topk_weights, residual, out)
     dev, dt = rows.device, rows.dtype
     code = _row_dtype(rows, "rows")
     rr, M, k = _routes(route_row, dev)
@@ -712,7 +745,7 @@ def moe_token_unsort(rows, route_row, topk_weights=None, residual=None, out=None
     else:
         ldo = _rows(out, "out", dev, dt, (M, H))
     _check(lib().moe_token_unsort(rows.data_ptr(), ldr, code, M, k, H, rr, w, res, ldres,
-                                  out.data_ptr(), ldo, _raw_stream(stream, dev)),
+                                  out.data_ptr(), ldo, _raw_stream(dev)),
            "moe_token_unsort")
     return out
 
@@ -720,6 +753,10 @@ def moe_token_unsort(rows, route_row, topk_weights=None, residual=None, out=None
 def moe_token_unsort_grad(grad_out, rows, route_row, topk_weights=None, grad_rows=None,
                           grad_weights=None, stream=None):
     """Gradients of moe_token_unsort: (grad_rows [M*k,H], grad_weights [M,k] fp32)."""
+    if stream is not None:
+        with _launch_stream(stream, rows.device):
+            return moe_token_unsort_grad(grad_out, rows, route_row, topk_weights, grad_rows,
+                                         grad_weights)
     dev, dt = rows.device, rows.dtype
     code = _row_dtype(rows, "rows")
     rr, M, k = _routes(route_row, dev)
@@ -735,10 +772,11 @@ def moe_token_unsort_grad(grad_out, rows, route_row, topk_weights=None, grad_row
         ldg = _rows(grad_rows, "grad_rows", dev, dt, (M * k, H))
     if grad_weights is None:
         grad_weights = torch.empty((M, k), dtype=torch.float32, device=dev)
-    gw = _vector(grad_weights, "grad_weights", torch.float32, dev, (M, k))
+    else:
+        _vector(grad_weights, "grad_weights", torch.float32, dev, (M, k))
     _check(lib().moe_token_unsort_grad(grad_out.data_ptr(), ldo, rows.data_ptr(), ldr, code, M, k,
-                                       H, rr, w, grad_rows.data_ptr(), ldg, gw,
-                                       _raw_stream(stream, dev)), "moe_token_unsort_grad")
+                                       H, rr, w, grad_rows.data_ptr(), ldg, grad_weights.data_ptr(),
+                                       _raw_stream(dev)), "moe_token_unsort_grad")
     return grad_rows, grad_weights
 
 
@@ -784,6 +822,9 @@ def _quantised_outputs(codes, scales, rows, cols, dev):
 def moe_microscale_quantize(x, route_row=None, codes=None, scales=None, stream=None):
     """x [rows,cols] as 4-bit codes and scales; with route_row [rows,k] (a token plan's) in
     sorted order, rows * k of them."""
+    if stream is not None:
+        with _launch_stream(stream, x.device):
+            return moe_microscale_quantize(x, route_row, codes, scales)
     dev = x.device
     code = _row_dtype(x, "x")
     rows, cols = x.shape
@@ -792,26 +833,34 @@ def moe_microscale_quantize(x, route_row=None, codes=None, scales=None, stream=N
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_quantize")
     rr, k = None, 1
     if route_row is not None:
-        k = _matrix(route_row, "route_row")[1]
+        if route_row.dim() != 2:
+            _not_a_matrix(route_row, "route_row")
+        k = route_row.shape[1]
         rr = _vector(route_row, "route_row", torch.int32, dev, (rows, k))
     codes, scales = _quantised_outputs(codes, scales, rows * k, cols, dev)
     _check(lib().moe_microscale_quantize(x.data_ptr(), ldx, code, rows, cols, rr, k,
                                          codes.data_ptr(), scales.data_ptr(),
-                                         _raw_stream(stream, dev)), "moe_microscale_quantize")
+                                         _raw_stream(dev)), "moe_microscale_quantize")
     return codes, scales
 
 
 def moe_microscale_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values [rows,cols] of codes [rows,cols/2] and scales."""
+    if stream is not None:
+        with _launch_stream(stream, codes.device):
+            return moe_microscale_dequantize(codes, scales, dtype, out)
     dev = codes.device
-    rows = _matrix(codes, "codes")[0]
     cols = _microscaled(codes, scales, dev, "x")
+    if codes.dim() != 2:
+        _not_a_matrix(codes, "codes")
+    rows = codes.shape[0]
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        out, ldx = torch.empty((rows, cols), dtype=dtype, device=dev), cols
+    else:
+        ldx = _rows(out, "out", dev, out.dtype, (rows, cols))
     code = _row_dtype(out, "out")
-    ldx = _rows(out, "out", dev, out.dtype, (rows, cols))
     _check(lib().moe_microscale_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols,
-                                           out.data_ptr(), ldx, code, _raw_stream(stream, dev)),
+                                           out.data_ptr(), ldx, code, _raw_stream(dev)),
            "moe_microscale_dequantize")
     return out
 
@@ -827,7 +876,8 @@ def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
     """Checks of the grouped products; returns (rows, E, N, K, offsets' address, workspace,
     (its address, its bytes))."""
     dev = x_codes.device
-    rows = _matrix(x_codes, "x_codes")[0]
+    if x_codes.dim() != 2:
+        _not_a_matrix(x_codes, "x_codes")
     K = _microscaled(x_codes, x_scales, dev, "x")
     if _microscaled(w_codes, w_scales, dev, "w") != K:
         raise ValueError("x and w must have the same number of columns")
@@ -840,23 +890,28 @@ def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
         off = _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     if workspace is None:
         workspace = torch.zeros(MOE_MICROSCALE_STATUS_BYTES, dtype=torch.uint8, device=dev)
-    return rows, E, N, K, off, workspace, _workspace(workspace, dev)
+    return x_codes.shape[0], E, N, K, off, workspace, _workspace(workspace, dev)
 
 
 def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
                            dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """y [rows,N] of 4-bit rows and 4-bit weights [E,N,K] (or [N,K]), rows grouped by offsets
     [E+1]; rows past the last group are zero."""
+    if stream is not None:
+        with _launch_stream(stream, x_codes.device):
+            return moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets, dtype,
+                                          out, workspace)
     rows, E, N, K, off, workspace, ws = _product_args(x_codes, x_scales, w_codes, w_scales,
                                                       offsets, workspace)
     dev = x_codes.device
     if out is None:
-        out = torch.empty((rows, N), dtype=dtype, device=dev)
+        out, ldy = torch.empty((rows, N), dtype=dtype, device=dev), N
+    else:
+        ldy = _rows(out, "out", dev, out.dtype, (rows, N))
     code = _row_dtype(out, "out")
-    ldy = _rows(out, "out", dev, out.dtype, (rows, N))
     _check(lib().moe_microscale_product(x_codes.data_ptr(), x_scales.data_ptr(), rows, off,
                                         w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, code,
-                                        out.data_ptr(), ldy, *ws, _raw_stream(stream, dev)),
+                                        out.data_ptr(), ldy, *ws, _raw_stream(dev)),
            "moe_microscale_product")
     return out
 
@@ -865,6 +920,10 @@ def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=N
                                  scales=None, workspace=None, stream=None):
     """SiLU(g) * u of the gate and up halves of w [E,N,K], quantised: (codes, scales) of
     [rows,N/2]."""
+    if stream is not None:
+        with _launch_stream(stream, x_codes.device):
+            return moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets,
+                                                codes, scales, workspace)
     rows, E, N, K, off, workspace, ws = _product_args(x_codes, x_scales, w_codes, w_scales,
                                                       offsets, workspace)
     if N % 64:
@@ -874,7 +933,7 @@ def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=N
     _check(lib().moe_microscale_gated_product(x_codes.data_ptr(), x_scales.data_ptr(), rows, off,
                                               w_codes.data_ptr(), w_scales.data_ptr(), E, N, K,
                                               codes.data_ptr(), scales.data_ptr(), *ws,
-                                              _raw_stream(stream, dev)),
+                                              _raw_stream(dev)),
            "moe_microscale_gated_product")
     return codes, scales
 
@@ -898,6 +957,9 @@ def microscale_weights(layer: dict, device=None) -> MicroscaleWeights:
 def microscale_layer(layer: dict, stream=None) -> dict:
     """4-bit weights of a dense layer (w_gate, w_up [E,H,I], w_down [E,I,H] bf16): each
     projection's output channels become rows, quantised along the summed dimension."""
+    if stream is not None:
+        with _launch_stream(stream, layer["w_down"].device):
+            return microscale_layer(layer)
     H, I, E = layer["H"], layer["I"], layer["E"]
     dev = layer["w_down"].device
     if H % 32 or I % 32:
@@ -911,8 +973,7 @@ def microscale_layer(layer: dict, stream=None) -> dict:
                             ("down", layer["w_down"][e], 0)):
             rows = w.t().contiguous()
             moe_microscale_quantize(rows, codes=out[name + "_codes"][e, at:at + len(rows)],
-                                    scales=out[name + "_scales"][e, at:at + len(rows)],
-                                    stream=stream)
+                                    scales=out[name + "_scales"][e, at:at + len(rows)])
     return out
 
 
@@ -932,9 +993,14 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
                        stream=None):
     """The 4-bit expert step (include/moe.h) for given routes; `layer` as microscale_weights
     takes it."""
+    if stream is not None:
+        with _launch_stream(stream, h.device):
+            return moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual, out, workspace)
     dev = h.device
     w = microscale_weights(layer, dev)
-    M, k = _matrix(topk_ids, "topk_ids")
+    if topk_ids.dim() != 2:
+        _not_a_matrix(topk_ids, "topk_ids")
+    M, k = topk_ids.shape
     H = w.H
     bf16 = torch.bfloat16
     ph = _vector(h, "h", bf16, dev, (M, H))
@@ -943,10 +1009,11 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
     res = None if residual is None else _vector(residual, "residual", bf16, dev, (M, H))
     if out is None:
         out = torch.empty((M, H), dtype=bf16, device=dev)
-    po = _vector(out, "out", bf16, dev, (M, H))
+    else:
+        _vector(out, "out", bf16, dev, (M, H))
     if workspace is None:
         workspace = microscale_workspace(layer, M, k)
-    _check(lib().moe_microscale_ffn(ph, ctypes.byref(w), M, k, ids, pw, res, po,
-                                    *_workspace(workspace, dev), _raw_stream(stream, dev)),
+    _check(lib().moe_microscale_ffn(ph, ctypes.byref(w), M, k, ids, pw, res, out.data_ptr(),
+                                    *_workspace(workspace, dev), _raw_stream(dev)),
            "moe_microscale_ffn")
     return out

@@ -123,3 +123,61 @@ def test_replayed_steps_with_other_weights(M, k):
         want = torch.stack([parts(x, layer, ids, scale[i], residual=x) for i in range(4)])
         assert torch.equal(out, want)
     assert moe.moe_read_device_status(work) == 0
+
+
+def test_calls_on_a_stream_that_is_not_current():
+    """Calls given a busy stream, with outputs and workspaces of their own, while the current
+    stream allocates and overwrites as much memory right after each."""
+    M, k, E, H, I = 300, 4, 16, 512, 256
+    layer = make_layer(E, H, I, seed=3)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    ids = torch.randint(0, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((M, k), generator=g, device="cuda")
+    h = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    offsets, row_route, rr = moe.moe_token_plan(ids, E)
+    rows = moe.moe_token_sort(h, rr)
+    q = moe.moe_microscale_quantize(h, route_row=rr)
+    p = moe.moe_microscale_gated_product(*q, layer["gate_up_codes"], layer["gate_up_scales"], offsets=offsets)
+    y = moe.moe_microscale_product(*p, layer["down_codes"], layer["down_scales"], offsets=offsets)
+    dense = {"H": H, "I": I, "E": E}
+    for name, n, cols in (("w_gate", H, I), ("w_up", H, I), ("w_down", I, H)):
+        dense[name] = torch.randn((E, n, cols), generator=g, device="cuda").to(torch.bfloat16)
+    four = moe.microscale_layer(dense)
+    calls = [(lambda s: moe.moe_token_plan(ids, E, stream=s), (offsets, row_route, rr)),
+             (lambda s: moe.moe_token_sort(h, rr, stream=s), rows),
+             (lambda s: moe.moe_token_sort_grad(rows, rr, stream=s), moe.moe_token_sort_grad(rows, rr)),
+             (lambda s: moe.moe_token_unsort(y, rr, w, residual=h, stream=s), moe.moe_token_unsort(y, rr, w, residual=h)),
+             (lambda s: moe.moe_token_unsort_grad(h, y, rr, w, stream=s), moe.moe_token_unsort_grad(h, y, rr, w)),
+             (lambda s: moe.moe_microscale_quantize(h, route_row=rr, stream=s), q),
+             (lambda s: moe.moe_microscale_dequantize(*q, stream=s), moe.moe_microscale_dequantize(*q)),
+             (lambda s: moe.moe_microscale_gated_product(*q, layer["gate_up_codes"], layer["gate_up_scales"],
+                                                         offsets=offsets, stream=s), p),
+             (lambda s: moe.moe_microscale_product(*p, layer["down_codes"], layer["down_scales"], offsets=offsets, stream=s), y),
+             (lambda s: moe.microscale_layer(dense, stream=s), four),
+             (lambda s: moe.moe_microscale_ffn(h, layer, ids, w, residual=h, stream=s),
+              moe.moe_microscale_ffn(h, layer, ids, w, residual=h))]
+
+    def tensors(v):
+        if isinstance(v, torch.Tensor):
+            return [v]
+        return [t for t in (v.values() if isinstance(v, dict) else v) if isinstance(t, torch.Tensor)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream, 0):
+        for call, want in calls:
+            torch.cuda.synchronize()
+            # this stream's pool holds freed blocks of every size that the call might take
+            free = [torch.zeros(t.numel() * t.element_size(), dtype=torch.uint8, device="cuda") for t in tensors(want)]
+            free.append(moe.microscale_workspace(layer, M, k))
+            sizes = [f.numel() for f in free]
+            del free
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+            got = call(stream)
+            junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes]
+            torch.cuda.synchronize()
+            for a, b in zip(tensors(got), tensors(want)):
+                assert torch.equal(a, b)
+            del junk, got

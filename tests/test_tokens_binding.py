@@ -45,7 +45,7 @@ def fake(monkeypatch):
     """The binding with host tensors in the place of the GPU's and the library recorded."""
     r = Recorder()
     monkeypatch.setattr(moe, "lib", lambda: r)
-    monkeypatch.setattr(moe, "_raw_stream", lambda stream, device: 0)
+    monkeypatch.setattr(moe, "_raw_stream", lambda device: 0)
     return r
 
 
@@ -136,20 +136,93 @@ def test_rows_are_matrices(fake):
 def test_tensors_of_a_device_that_is_not_current_are_refused(monkeypatch):
     """The library launches on the current device; the other's default stream has the same
     handle, 0."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
-    assert moe._raw_stream(None, torch.device("cuda", 0)) == 0
-    for stream in (None, 0, 1 << 20):
-        with pytest.raises(ValueError, match="current device"):
-            moe._raw_stream(stream, torch.device("cuda", 1))
+    monkeypatch.setattr(moe, "_current_device", lambda: 0)
+    monkeypatch.setattr(moe, "_current_stream", lambda index: 0)
+    assert moe._raw_stream(torch.device("cuda", 0)) == 0
+    with pytest.raises(ValueError, match="current device"):
+        moe._raw_stream(torch.device("cuda", 1))
 
 
-def test_the_current_stream_without_the_raw_handle(monkeypatch):
+def test_the_current_stream_without_the_raw_handle(lib, monkeypatch):
     """Where torch has no call for the raw handle the public one serves."""
+    import importlib.util
+
     class Stream:
         cuda_stream = 77
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
-    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    assert moe._raw_stream(None, torch.device("cuda", 0)) == 77
-    assert moe._stream(None).value == 77
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("routed_expert_ffn_top_gb300.moe_again", moe.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert again._raw_stream(torch.device("cuda", 0)) == 77
+    assert again._stream(None).value == 77
+
+
+def calls_with_stream(stream):
+    """Every call that allocates, given a stream."""
+    h, ids, w = step_args()
+    layer, (c, s), wt = four_bit_layer(), quantised(3, 64), quantised(2, 64, 64)
+    off = torch.zeros(3, dtype=torch.int32)
+    x, rows = torch.zeros(3, 64), torch.zeros(6, 64)
+    dense = {"H": 64, "I": 32, "E": 2, "w_gate": torch.zeros(2, 64, 32), "w_up": torch.zeros(2, 64, 32),
+             "w_down": torch.zeros(2, 32, 64)}
+    return [lambda: moe.moe_token_plan(ids, 4, stream=stream), lambda: moe.moe_token_sort(x, ids, stream=stream),
+            lambda: moe.moe_token_sort_grad(rows, ids, stream=stream),
+            lambda: moe.moe_token_unsort(rows, ids, w, residual=x, stream=stream),
+            lambda: moe.moe_token_unsort_grad(x, rows, ids, w, stream=stream),
+            lambda: moe.moe_microscale_quantize(x, stream=stream),
+            lambda: moe.moe_microscale_quantize(x, route_row=ids, stream=stream),
+            lambda: moe.moe_microscale_dequantize(c, s, stream=stream),
+            lambda: moe.moe_microscale_product(c, s, *wt, offsets=off, stream=stream),
+            lambda: moe.moe_microscale_gated_product(c, s, *wt, offsets=off, stream=stream),
+            lambda: moe.microscale_layer(dense, stream=stream),
+            lambda: moe.moe_microscale_ffn(h, layer, ids, w, residual=h, stream=stream)]
+
+
+@pytest.mark.parametrize("i", range(12))
+def test_allocations_are_the_launch_streams(fake, monkeypatch, i):
+    """What a call allocates, fills or copies itself belongs to the stream that it launches on:
+    memory of another stream may still be in use there, and is given away there too soon."""
+    depth, seen = [0], []
+
+    class On:
+        def __enter__(self):
+            depth[0] += 1
+
+        def __exit__(self, *_):
+            depth[0] -= 1
+
+    def watch(owner, name):
+        real = getattr(owner, name)
+
+        def call(*args, **kw):
+            seen.append((name, depth[0]))
+            return real(*args, **kw)
+        monkeypatch.setattr(owner, name, call)
+
+    call = calls_with_stream(5)[i]
+    monkeypatch.setattr(moe, "_launch_stream", lambda stream, device: On(), raising=False)
+    monkeypatch.setattr(moe, "_check", lambda rc, where: seen.append((where, depth[0])))
+    for owner, name in ((torch, "empty"), (torch, "zeros"), (torch.Tensor, "contiguous")):
+        watch(owner, name)
+    call()
+    assert len(seen) > 1 and all(d == 1 for _, d in seen), seen
+
+
+def test_a_stream_is_taken_as_an_object_or_a_handle(monkeypatch):
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.handle, self.device = handle, device
+    cuda = torch.device("cuda", 0)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: Stream("default", device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    mine = Stream(3)
+    assert moe._launch_stream(mine, cuda) is mine
+    assert moe._launch_stream(1 << 20, cuda).handle == 1 << 20
+    assert moe._launch_stream(0, cuda).handle == "default"
+    with pytest.raises(ValueError):
+        moe._launch_stream(mine, torch.device("cpu"))
