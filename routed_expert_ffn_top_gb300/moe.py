@@ -872,9 +872,18 @@ def _workspace(t, device):
     return t.data_ptr(), t.numel()
 
 
+def _own_status(workspace, where):
+    """After a call that made its own workspace, whose status word has no other reader: waits for
+    the result and raises if a device wait ran out.  (A call that a graph captures cannot wait.)"""
+    if not torch.cuda.is_current_stream_capturing():
+        status = ctypes.c_int32(0)
+        _check(lib().moe_read_device_status(workspace.data_ptr(), _raw_stream(workspace.device),
+                                            ctypes.byref(status)), where)
+
+
 def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
-    """Checks of the grouped products; returns (rows, E, N, K, offsets' address, workspace,
-    (its address, its bytes))."""
+    """Checks of the grouped products; returns (rows, E, N, K, offsets' address, the workspace
+    made here or None, (the workspace's address, its bytes))."""
     dev = x_codes.device
     if x_codes.dim() != 2:
         _not_a_matrix(x_codes, "x_codes")
@@ -888,21 +897,23 @@ def _product_args(x_codes, x_scales, w_codes, w_scales, offsets, workspace):
     off = None
     if offsets is not None:
         off = _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
+    own = None
     if workspace is None:
-        workspace = torch.zeros(MOE_MICROSCALE_STATUS_BYTES, dtype=torch.uint8, device=dev)
-    return x_codes.shape[0], E, N, K, off, workspace, _workspace(workspace, dev)
+        workspace = own = torch.zeros(MOE_MICROSCALE_STATUS_BYTES, dtype=torch.uint8, device=dev)
+    return x_codes.shape[0], E, N, K, off, own, _workspace(workspace, dev)
 
 
 def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
                            dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """y [rows,N] of 4-bit rows and 4-bit weights [E,N,K] (or [N,K]), rows grouped by offsets
-    [E+1]; rows past the last group are zero."""
+    [E+1]; rows past the last group are zero.  The workspace holds the status word; without one
+    the call makes its own, waits for the result and raises what the device found."""
     if stream is not None:
         with _launch_stream(stream, x_codes.device):
             return moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets, dtype,
                                           out, workspace)
-    rows, E, N, K, off, workspace, ws = _product_args(x_codes, x_scales, w_codes, w_scales,
-                                                      offsets, workspace)
+    rows, E, N, K, off, own, ws = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
+                                                workspace)
     dev = x_codes.device
     if out is None:
         out, ldy = torch.empty((rows, N), dtype=dtype, device=dev), N
@@ -913,19 +924,21 @@ def moe_microscale_product(x_codes, x_scales, w_codes, w_scales, offsets=None,
                                         w_codes.data_ptr(), w_scales.data_ptr(), E, N, K, code,
                                         out.data_ptr(), ldy, *ws, _raw_stream(dev)),
            "moe_microscale_product")
+    if own is not None:
+        _own_status(own, "moe_microscale_product")
     return out
 
 
 def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=None, codes=None,
                                  scales=None, workspace=None, stream=None):
     """SiLU(g) * u of the gate and up halves of w [E,N,K], quantised: (codes, scales) of
-    [rows,N/2]."""
+    [rows,N/2].  Workspace as for moe_microscale_product."""
     if stream is not None:
         with _launch_stream(stream, x_codes.device):
             return moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets,
                                                 codes, scales, workspace)
-    rows, E, N, K, off, workspace, ws = _product_args(x_codes, x_scales, w_codes, w_scales,
-                                                      offsets, workspace)
+    rows, E, N, K, off, own, ws = _product_args(x_codes, x_scales, w_codes, w_scales, offsets,
+                                                workspace)
     if N % 64:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_gated_product")
     dev = x_codes.device
@@ -935,6 +948,8 @@ def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=N
                                               codes.data_ptr(), scales.data_ptr(), *ws,
                                               _raw_stream(dev)),
            "moe_microscale_gated_product")
+    if own is not None:
+        _own_status(own, "moe_microscale_gated_product")
     return codes, scales
 
 
@@ -992,7 +1007,8 @@ def microscale_workspace(layer: dict, M, k) -> torch.Tensor:
 def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None, workspace=None,
                        stream=None):
     """The 4-bit expert step (include/moe.h) for given routes; `layer` as microscale_weights
-    takes it."""
+    takes it.  Without a workspace (microscale_workspace) the call makes its own, waits for the
+    result and raises what the device found."""
     if stream is not None:
         with _launch_stream(stream, h.device):
             return moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual, out, workspace)
@@ -1011,9 +1027,12 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
         out = torch.empty((M, H), dtype=bf16, device=dev)
     else:
         _vector(out, "out", bf16, dev, (M, H))
-    if workspace is None:
+    own = workspace is None
+    if own:
         workspace = microscale_workspace(layer, M, k)
     _check(lib().moe_microscale_ffn(ph, ctypes.byref(w), M, k, ids, pw, res, out.data_ptr(),
                                     *_workspace(workspace, dev), _raw_stream(dev)),
            "moe_microscale_ffn")
+    if own:
+        _own_status(workspace, "moe_microscale_ffn")
     return out

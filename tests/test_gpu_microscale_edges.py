@@ -181,3 +181,34 @@ def test_calls_on_a_stream_that_is_not_current():
             for a, b in zip(tensors(got), tensors(want)):
                 assert torch.equal(a, b)
             del junk, got
+
+
+def test_calls_without_a_workspace():
+    """They wait for their result and raise what the status word says; in a graph's capture they
+    do neither."""
+    M, k, E, H, I = 5, 3, 8, 256, 128
+    layer = make_layer(E, H, I, seed=5)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    ids = torch.randint(0, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((M, k), generator=g, device="cuda")
+    h = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    want = parts(h, layer, ids, w)
+    done = torch.cuda.Event()
+    torch.cuda._sleep(10_000_000)
+    done.record()
+    assert torch.equal(moe.moe_microscale_ffn(h, layer, ids, w), want)
+    assert done.query()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = moe.moe_microscale_ffn(h, layer, ids, w)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    zeros = torch.zeros
+    torch.zeros = lambda *a, **kw: zeros(*a, **kw).fill_(moe.MOE_DEV_WAIT_TIMEOUT)  # a word that is set
+    try:
+        with pytest.raises(moe.MoeError):
+            moe.moe_microscale_product(*moe.moe_microscale_quantize(h), layer["gate_up_codes"][0], layer["gate_up_scales"][0])
+    finally:
+        torch.zeros = zeros

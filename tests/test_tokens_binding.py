@@ -36,7 +36,7 @@ class Recorder:
     def __getattr__(self, name):
         def call(*args):
             self.calls.append((name, args))
-            return 4096 if name.endswith("_bytes") else moe.MOE_OK
+            return 4096 if name.endswith("_bytes") else b"status" if name == "moe_status_string" else moe.MOE_OK
         return call
 
 
@@ -46,6 +46,7 @@ def fake(monkeypatch):
     r = Recorder()
     monkeypatch.setattr(moe, "lib", lambda: r)
     monkeypatch.setattr(moe, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return r
 
 
@@ -130,7 +131,7 @@ def test_rows_are_matrices(fake):
     moe.moe_microscale_dequantize(c, s)
     moe.moe_microscale_product(c, s, *wt, offsets=off)
     moe.moe_microscale_product(c, s, wt[0][0], wt[1][0])
-    assert len(launches(fake)) == 3
+    assert len([n for n in launches(fake) if n != "moe_read_device_status"]) == 3
 
 
 def test_tensors_of_a_device_that_is_not_current_are_refused(monkeypatch):
@@ -226,3 +227,34 @@ def test_a_stream_is_taken_as_an_object_or_a_handle(monkeypatch):
     assert moe._launch_stream(0, cuda).handle == "default"
     with pytest.raises(ValueError):
         moe._launch_stream(mine, torch.device("cpu"))
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_call_without_a_workspace_reports_what_the_device_found(fake, monkeypatch, capturing):
+    """Its status word has no other reader: the call waits and raises.  A call that is being
+    captured in a graph cannot wait."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    h, ids, w = step_args()
+    layer, x, wt = four_bit_layer(), quantised(3, 64), quantised(2, 64, 64)
+    off = torch.zeros(3, dtype=torch.int32)
+    work = torch.zeros(8192, dtype=torch.uint8)
+    calls = [lambda ws: moe.moe_microscale_product(*x, *wt, offsets=off, workspace=ws),
+             lambda ws: moe.moe_microscale_gated_product(*x, *wt, offsets=off, workspace=ws),
+             lambda ws: moe.moe_microscale_ffn(h, layer, ids, w, workspace=ws)]
+    for call in calls:
+        fake.calls.clear()
+        call(work)
+        assert "moe_read_device_status" not in launches(fake)
+        call(None)
+        assert launches(fake).count("moe_read_device_status") == (0 if capturing else 1)
+    if capturing:
+        return
+
+    def status(*args):
+        ctypes.cast(args[2], ctypes.POINTER(ctypes.c_int32))[0] = moe.MOE_DEV_WAIT_TIMEOUT
+        return moe.MOE_ERR_DEVICE
+    fake.moe_read_device_status = status
+    for call in calls:
+        call(work)
+        with pytest.raises(moe.MoeError):
+            call(None)
