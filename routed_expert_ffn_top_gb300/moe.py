@@ -997,11 +997,13 @@ def moe_microscale_workspace_bytes(layer: dict, M, k) -> int:
 
 
 def microscale_workspace(layer: dict, M, k) -> torch.Tensor:
-    """A zero-filled workspace of moe_microscale_ffn."""
+    """A workspace of moe_microscale_ffn, its status word zero."""
     n = moe_microscale_workspace_bytes(layer, M, k)
     if n == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_microscale_workspace_bytes")
-    return torch.zeros((n,), dtype=torch.uint8, device=layer["down_codes"].device)
+    work = torch.empty((n,), dtype=torch.uint8, device=layer["down_codes"].device)
+    work[:MOE_MICROSCALE_STATUS_BYTES].zero_()
+    return work
 
 
 def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None, workspace=None,

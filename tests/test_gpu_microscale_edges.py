@@ -212,3 +212,23 @@ def test_calls_without_a_workspace():
             moe.moe_microscale_product(*moe.moe_microscale_quantize(h), layer["gate_up_codes"][0], layer["gate_up_scales"][0])
     finally:
         torch.zeros = zeros
+
+
+@pytest.mark.parametrize("M,k", [(3, 4), (40, 8), (300, 4)])
+def test_step_reads_nothing_that_a_workspace_held(M, k):
+    """All but the status word of the workspace holds bytes that are NaN scales, dropped rows and
+    far offsets to any reader; some routes are dropped."""
+    E, H, I = 16, 320, 96
+    layer = make_layer(E, H, I, seed=M)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    ids = torch.randint(-1, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((M, k), generator=g, device="cuda")
+    h = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    want = parts(h, layer, ids, w)
+    work = moe.microscale_workspace(layer, M, k)
+    assert int(work[:256].count_nonzero()) == 0
+    for byte in (0, 255):
+        work[256:] = byte
+        assert torch.equal(moe.moe_microscale_ffn(h, layer, ids, w, workspace=work), want)
+    assert moe.moe_read_device_status(work) == 0

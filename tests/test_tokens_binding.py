@@ -258,3 +258,18 @@ def test_a_call_without_a_workspace_reports_what_the_device_found(fake, monkeypa
         call(work)
         with pytest.raises(moe.MoeError):
             call(None)
+
+
+def test_a_new_workspace_is_filled_where_it_must_be(monkeypatch):
+    """Only the status word has to be zero; a prompt's workspace is hundreds of megabytes."""
+    layer = {k: v.to("meta") if isinstance(v, torch.Tensor) else v for k, v in four_bit_layer(H=2048, I=768).items()}
+    filled = []
+    real = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: filled.append(real(*a, **kw)) or filled[-1])
+    zero_ = torch.Tensor.zero_
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda t: filled.append(t) or zero_(t))
+    monkeypatch.setattr(moe, "lib", Recorder)
+    monkeypatch.setattr(moe, "moe_microscale_workspace_bytes", lambda *a: 1 << 28)
+    work = moe.microscale_workspace(layer, 8192, 8)
+    assert work.numel() == 1 << 28 and work.dtype is torch.uint8
+    assert sum(t.numel() for t in filled) == moe.MOE_MICROSCALE_STATUS_BYTES
