@@ -931,7 +931,7 @@ extern "C" int moe_decode_block_host(const void *h_host, const void *residual_ho
 }
 
 extern "C" int moe_read_device_status(void *workspace, void *stream, int32_t *status_out) {
-    if (!workspace || !status_out || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+    if (!workspace || !status_out || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int32_t v = 0;
     if (cudaMemcpyAsync(&v, workspace, sizeof v, cudaMemcpyDeviceToHost, s) != cudaSuccess)

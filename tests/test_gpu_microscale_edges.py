@@ -232,3 +232,17 @@ def test_step_reads_nothing_that_a_workspace_held(M, k):
         work[256:] = byte
         assert torch.equal(moe.moe_microscale_ffn(h, layer, ids, w, workspace=work), want)
     assert moe.moe_read_device_status(work) == 0
+
+
+def test_status_of_a_workspace_that_only_the_products_take():
+    """A 16-byte aligned one: its status word is read back and cleared like any other."""
+    x, wt = moe.moe_microscale_quantize(torch.ones((3, 64), device="cuda")), moe.moe_microscale_quantize(torch.ones((5, 64), device="cuda"))
+    buf = torch.zeros(1024, dtype=torch.uint8, device="cuda")
+    for at in (16, 48, 256):
+        work = buf[at:at + 256]
+        y = moe.moe_microscale_product(*x, *wt, workspace=work)
+        assert bool((y == 64).all())
+        assert moe.moe_read_device_status(work) == 0
+        work[0] = moe.MOE_DEV_WAIT_TIMEOUT
+        assert moe.moe_read_device_status(work) == moe.MOE_DEV_WAIT_TIMEOUT
+        assert moe.moe_read_device_status(work) == 0

@@ -273,3 +273,9 @@ def test_a_new_workspace_is_filled_where_it_must_be(monkeypatch):
     work = moe.microscale_workspace(layer, 8192, 8)
     assert work.numel() == 1 << 28 and work.dtype is torch.uint8
     assert sum(t.numel() for t in filled) == moe.MOE_MICROSCALE_STATUS_BYTES
+
+
+def test_status_read_refuses(lib):
+    out = ctypes.c_int32(0)
+    for work, result in ((None, ctypes.byref(out)), (A + 8, ctypes.byref(out)), (A, None)):
+        assert lib.moe_read_device_status(work, None, result) == moe.MOE_ERR_INVALID_ARG
