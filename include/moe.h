@@ -503,7 +503,7 @@ int moe_microscale_gated_product(const uint8_t *x_codes, const uint8_t *x_scales
  * and down [E][H][I], each as codes and scales. */
 typedef struct moe_microscale_weights {
     int32_t H, I, E;
-    int32_t reserved;
+    int32_t y_dtype;  /* of y between the down product and the sum: MOE_DT_BF16 or MOE_DT_F32 */
     const uint8_t *gate_up_codes;
     const uint8_t *gate_up_scales;
     const uint8_t *down_codes;
@@ -516,7 +516,8 @@ size_t moe_microscale_workspace_bytes(const moe_microscale_weights_t *w, int M, 
 /*
  * The expert step with 4-bit weights and activations, for given routes: h is quantised per
  * token, p per route.  Arguments as moe_expert_ffn's; out [M,H] bf16 = bf16(residual +
- * sum_j a_j y_j) with y rounded to bf16.  H and I multiples of 32, E <= 1024, E * max(2I, H) <
+ * sum_j a_j y_j) with y of w->y_dtype: MOE_DT_F32 as in the other paths' sum, or rounded to
+ * MOE_DT_BF16, half the bytes.  H and I multiples of 32, E <= 1024, E * max(2I, H) <
  * 2^30.  workspace: 256-byte aligned, ws_bytes >= moe_microscale_workspace_bytes, its first
  * MOE_MICROSCALE_STATUS_BYTES zero before the first call.
  */

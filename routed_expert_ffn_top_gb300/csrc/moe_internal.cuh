@@ -395,6 +395,9 @@ cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k
 cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
                                 const int32_t *route_row, const float *w, const void *residual,
                                 int64_t ldres, void *out, int64_t ldo, bool early, cudaStream_t stream);
+// fp32 rows to a bf16 residual and out, all contiguous with 16-byte rows and 16-byte aligned.
+cudaError_t launch_token_unsort_f32(const float *rows, int M, int k, int H, const int32_t *route_row, const float *w,
+                                    const __nv_bfloat16 *residual, __nv_bfloat16 *out, bool early, cudaStream_t stream);
 cudaError_t launch_token_unsort_grad(const void *gout, int64_t ldo, const void *rows, int64_t ldr,
                                      int dtype, int M, int k, int H, const int32_t *route_row,
                                      const float *w, void *grows, int64_t ldg, float *gw,

@@ -150,6 +150,12 @@ __device__ __forceinline__ void cp_async_16(void *smem_dst, const void *gsrc) {
                  : "memory");
 }
 
+__device__ __forceinline__ void cp_async_8(void *smem_dst, const void *gsrc) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem_dst)),
+                 "l"(reinterpret_cast<uint64_t>(gsrc))
+                 : "memory");
+}
+
 __device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gsrc) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)),
                  "l"(reinterpret_cast<uint64_t>(gsrc))

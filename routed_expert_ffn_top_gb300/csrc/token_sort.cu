@@ -266,11 +266,12 @@ constexpr int kUnsortCtas = V * sizeof(T) >= 8 ? 2 : C > 1 ? 4 : 3;
 // one token; the k rows' vectors are loaded kSlots at a time, then added in slot order.  The next
 // unit's rows and weights are loaded meanwhile.  4096 tokens x 7 routes and a residual: 2047 bf16
 // 63 us (with C = 1 and a warp a unit 93), 2046 bf16 49 (108), 2047 fp32 76 (101); 2048 tokens x
-// 32 routes x 2048 bf16 61 us (137), 0.69 of the copy rate.
-template <typename T, int V, int C>
+// 32 routes x 2048 bf16 61 us (137), 0.69 of the copy rate.  O: type of the residual and of out.
+template <typename T, int V, int C, typename O = T>
 __global__ void __launch_bounds__(32 * kRowWarps, kUnsortCtas<T, V, C>) token_unsort_kernel(const RowArgs a, int nvec, int nchunk) {
     constexpr int kSlots = C > 1 ? 4 : 8;
     using P = Pack<T, V>;
+    using Q = Pack<O, V>;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -298,9 +299,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, kUnsortCtas<T, V, C>) token_un
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[c][i] = 0.0f;
             if (a.res && v0 + 32 * c < nvec) {
-                const P r = *reinterpret_cast<const P *>(static_cast<const T *>(a.res) + m * a.ldres + (int64_t)(v0 + 32 * c) * V);
+                const Q r = *reinterpret_cast<const Q *>(static_cast<const O *>(a.res) + m * a.ldres + (int64_t)(v0 + 32 * c) * V);
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[c][i] = Elem<T>::load(r.v[i]);
+                for (int i = 0; i < V; ++i) acc[c][i] = Elem<O>::load(r.v[i]);
             }
         }
         for (int j0 = 0; j0 < a.k; j0 += kSlots) {
@@ -329,10 +330,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, kUnsortCtas<T, V, C>) token_un
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (v0 + 32 * c < nvec) {
-                P o;
+                Q o;
 #pragma unroll
-                for (int i = 0; i < V; ++i) o.v[i] = Elem<T>::store(acc[c][i]);
-                *reinterpret_cast<P *>(static_cast<T *>(a.out) + m * a.ldout + (int64_t)(v0 + 32 * c) * V) = o;
+                for (int i = 0; i < V; ++i) o.v[i] = Elem<O>::store(acc[c][i]);
+                *reinterpret_cast<Q *>(static_cast<O *>(a.out) + m * a.ldout + (int64_t)(v0 + 32 * c) * V) = o;
             }
     }
 }
@@ -437,7 +438,8 @@ struct RingUnit {
     int vi;  // this lane's 16-byte piece of the row
 };
 
-template <typename T>
+// O: the type of the token's own piece, as many elements as a piece of the rows.
+template <typename T, typename O = T>
 __device__ __forceinline__ void ring_issue(const RowArgs &a, const void *rows, int64_t ldrows, const void *own,
                                            int64_t ldown, const RingUnit &u, int nvec, int row_l, uint4 *slot) {
     constexpr int n = 16 / sizeof(T);
@@ -451,7 +453,11 @@ __device__ __forceinline__ void ring_issue(const RowArgs &a, const void *rows, i
                               static_cast<const T *>(rows) + (row >= 0 ? (int64_t)row * ldrows + (int64_t)u.vi * n : 0),
                               row >= 0 ? 16u : 0u);
     }
-    if (own && in) cp_async_16(slot + a.k * 32 + lane, static_cast<const T *>(own) + u.m * ldown + (int64_t)u.vi * n);
+    if (own && in) {
+        const O *src = static_cast<const O *>(own) + u.m * ldown + (int64_t)u.vi * n;
+        if constexpr (sizeof(O) == sizeof(T)) cp_async_16(slot + a.k * 32 + lane, src);
+        else cp_async_8(slot + a.k * 32 + lane, src);
+    }
 }
 
 // One 16-byte piece as fp32.
@@ -466,6 +472,14 @@ __device__ __forceinline__ void ring_load(const uint4 *p, float (&v)[16 / sizeof
 #pragma unroll
         for (int i = 0; i < (int)(16 / sizeof(T)); ++i) v[i] = Elem<T>::load(t[i]);
     }
+}
+
+// A token's own piece of n elements of another type than the rows'.
+template <typename O, int n>
+__device__ __forceinline__ void ring_load_own(const uint4 *p, float (&v)[n]) {
+    const Pack<O, n> o = *reinterpret_cast<const Pack<O, n> *>(p);
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = Elem<O>::load(o.v[i]);
 }
 
 // route_row entry of lane j < k for token m, -1 for a dropped or unknown row.
@@ -488,10 +502,11 @@ struct RingCursor {
     }
 };
 
-template <typename T, int kDepth>
+// O: type of the residual and of out.
+template <typename T, typename O, int kDepth>
 __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(const RowArgs a, int nvec, int nchunk, int wpt) {
     constexpr int n = 16 / sizeof(T);
-    using P = Pack<T, n>;
+    using P = Pack<O, n>;
     extern __shared__ uint4 ring[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (a.k + (a.res ? 1 : 0)) * 32;
@@ -521,7 +536,7 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
     int slot_in = 0, slot_out = 0;
     auto issue = [&]() {
         if (ahead.m < a.M) {
-            ring_issue<T>(a, a.a, a.lda, a.res, a.ldres, RingUnit{ahead.m, ahead.c * 32 + lane}, nvec, row_a, mine + slot_in * per);
+            ring_issue<T, O>(a, a.a, a.lda, a.res, a.ldres, RingUnit{ahead.m, ahead.c * 32 + lane}, nvec, row_a, mine + slot_in * per);
             const int64_t m = ahead.m;
             ahead.advance(q, wpt, nchunk, step);
             if (ahead.m != m) row_a = ahead.m < a.M ? ring_row(a, ahead.m) : -1;
@@ -539,7 +554,10 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
         float acc[n];
 #pragma unroll
         for (int i = 0; i < n; ++i) acc[i] = 0.0f;
-        if (a.res && in) ring_load<T>(slot + a.k * 32 + lane, acc);
+        if (a.res && in) {
+            if constexpr (std::is_same<T, O>::value) ring_load<T>(slot + a.k * 32 + lane, acc);
+            else ring_load_own<O>(slot + a.k * 32 + lane, acc);
+        }
 #pragma unroll 8
         for (int j = 0; j < a.k; ++j) {
             const float wj = __shfl_sync(0xffffffffu, w, j);
@@ -551,8 +569,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) token_unsort_ring_kernel(cons
         if (in) {
             P o;
 #pragma unroll
-            for (int i = 0; i < n; ++i) o.v[i] = Elem<T>::store(acc[i]);
-            *reinterpret_cast<P *>(static_cast<T *>(a.out) + now.m * a.ldout + (int64_t)vi * n) = o;
+            for (int i = 0; i < n; ++i) o.v[i] = Elem<O>::store(acc[i]);
+            *reinterpret_cast<P *>(static_cast<O *>(a.out) + now.m * a.ldout + (int64_t)vi * n) = o;
         }
         if (++slot_out == kDepth) slot_out = 0;
         issue();
@@ -744,23 +762,23 @@ static cudaError_t sort_as(RowArgs a, int elem, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, token_sort_kernel<U>, a, nvec, nchunk);
 }
 
-template <typename T, int V, int C>
+template <typename T, int V, int C, typename O>
 static cudaError_t unsort_vecs(const RowArgs &a, cudaStream_t stream) {
     const int nvec = a.H / V;
     const int nchunk = (nvec + 32 * C - 1) / (32 * C);
     const int64_t ctas = ((int64_t)a.M * nchunk + kRowWarps - 1) / kRowWarps;
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(ctas, kUnsortCtas<T, V, C>)), dim3(32 * kRowWarps), 0, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, token_unsort_kernel<T, V, C>, a, nvec, nchunk);
+    return cudaLaunchKernelEx(&cfg, token_unsort_kernel<T, V, C, O>, a, nvec, nchunk);
 }
 
 // One vector a lane while every warp then has one unit at most (one token of 2047 bf16 2.2 us,
 // with four 3.3).
-template <typename T, int V>
+template <typename T, int V, typename O = T>
 static cudaError_t unsort_as(const RowArgs &a, cudaStream_t stream) {
     const int64_t units = (int64_t)a.M * ((a.H / V + 31) / 32);
-    if (units <= (int64_t)num_sms() * kUnsortCtas<T, V, 1> * kRowWarps) return unsort_vecs<T, V, 1>(a, stream);
-    return unsort_vecs<T, V, kRowVecs<T, V>>(a, stream);
+    if (units <= (int64_t)num_sms() * kUnsortCtas<T, V, 1> * kRowWarps) return unsort_vecs<T, V, 1, O>(a, stream);
+    return unsort_vecs<T, V, kRowVecs<T, V>, O>(a, stream);
 }
 
 template <typename T, int V>
@@ -780,11 +798,11 @@ static int ring_depth(int rows) {
     return d;
 }
 
-template <typename T, int kDepth>
+template <typename T, typename O, int kDepth>
 static cudaError_t unsort_ring_as(const RowArgs &a, cudaStream_t stream) {
     if (!ring_fits(a.k + (a.res ? 1 : 0), kDepth)) return cudaErrorInvalidValue;
     const int nvec = a.H / (16 / (int)sizeof(T)), nchunk = (nvec + 31) / 32;
-    const auto fn = token_unsort_ring_kernel<T, kDepth>;
+    const auto fn = token_unsort_ring_kernel<T, O, kDepth>;
     cudaError_t err = ensure_smem((const void *)fn, kRingSmem);
     if (err != cudaSuccess) return err;
     int wpt = 1;  // warps a token
@@ -807,13 +825,13 @@ static cudaError_t unsort_grad_ring_as(const RowArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, fn, a, nvec, nchunk);
 }
 
-template <typename T>
+template <typename T, typename O = T>
 static cudaError_t unsort_ring(const RowArgs &a, cudaStream_t stream) {
     switch (ring_depth(a.k + (a.res ? 1 : 0))) {
-        case 8: return unsort_ring_as<T, 8>(a, stream);
-        case 4: return unsort_ring_as<T, 4>(a, stream);
-        case 2: return unsort_ring_as<T, 2>(a, stream);
-        default: return unsort_ring_as<T, 1>(a, stream);
+        case 8: return unsort_ring_as<T, O, 8>(a, stream);
+        case 4: return unsort_ring_as<T, O, 4>(a, stream);
+        case 2: return unsort_ring_as<T, O, 2>(a, stream);
+        default: return unsort_ring_as<T, O, 1>(a, stream);
     }
 }
 
@@ -853,14 +871,27 @@ cudaError_t launch_token_sort(const void *x, int64_t ldx, int elem, int M, int k
     return vb == 16 ? F<__nv_bfloat16, 8>(a, stream)                                                 \
                     : vb == 4 ? F<__nv_bfloat16, 2>(a, stream) : F<__nv_bfloat16, 1>(a, stream);
 
-cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
-                                const int32_t *route_row, const float *w, const void *residual,
-                                int64_t ldres, void *out, int64_t ldo, bool early, cudaStream_t stream) {
+static RowArgs unsort_args(const void *rows, int64_t ldr, int M, int k, int H, const int32_t *route_row,
+                           const float *w, const void *residual, int64_t ldres, void *out, int64_t ldo, bool early) {
     RowArgs a{};
     a.early = early;
     a.a = rows, a.res = residual, a.out = out, a.lda = ldr, a.ldres = ldres, a.ldout = ldo;
     a.route_row = route_row, a.w = w, a.M = M, a.k = k, a.H = H;
+    return a;
+}
+
+cudaError_t launch_token_unsort(const void *rows, int64_t ldr, int dtype, int M, int k, int H,
+                                const int32_t *route_row, const float *w, const void *residual,
+                                int64_t ldres, void *out, int64_t ldo, bool early, cudaStream_t stream) {
+    const RowArgs a = unsort_args(rows, ldr, M, k, H, route_row, w, residual, ldres, out, ldo, early);
     MOE_ROW_DISPATCH(unsort_as, unsort_ring, ring_fits(k + (residual ? 1 : 0), 1))
+}
+
+cudaError_t launch_token_unsort_f32(const float *rows, int M, int k, int H, const int32_t *route_row, const float *w,
+                                    const __nv_bfloat16 *residual, __nv_bfloat16 *out, bool early, cudaStream_t stream) {
+    const RowArgs a = unsort_args(rows, H, M, k, H, route_row, w, residual, H, out, H, early);
+    if (ring_fits(k + (residual ? 1 : 0), 1)) return unsort_ring<float, __nv_bfloat16>(a, stream);
+    return unsort_as<float, 4, __nv_bfloat16>(a, stream);
 }
 
 cudaError_t launch_token_unsort_grad(const void *gout, int64_t ldo, const void *rows, int64_t ldr,

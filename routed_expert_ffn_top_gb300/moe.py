@@ -100,7 +100,7 @@ class ReaderStruct(ctypes.Structure):
 class MicroscaleWeights(ctypes.Structure):
     _fields_ = [
         ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32),
-        ("reserved", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
         ("gate_up_codes", ctypes.c_void_p), ("gate_up_scales", ctypes.c_void_p),
         ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
     ]
@@ -956,7 +956,8 @@ def moe_microscale_gated_product(x_codes, x_scales, w_codes, w_scales, offsets=N
 def microscale_weights(layer: dict, device=None) -> MicroscaleWeights:
     """C descriptor of a layer's 4-bit weights: H, I, E and gate_up_codes [E,2I,H/2],
     gate_up_scales, down_codes [E,H,I/2], down_scales (the caller keeps the tensors alive), all
-    on one device, `device` if given."""
+    on one device, `device` if given; y_dtype, torch.bfloat16 if it has none, is the type of the
+    down product's results before their sum (torch.float32 keeps them unrounded)."""
     H, I, E = layer["H"], layer["I"], layer["E"]
     gc, gs, dc, ds = (layer["gate_up_codes"], layer["gate_up_scales"], layer["down_codes"],
                       layer["down_scales"])
@@ -965,21 +966,25 @@ def microscale_weights(layer: dict, device=None) -> MicroscaleWeights:
         raise ValueError("gate_up_codes must have shape %s" % ((E, 2 * I, H // 2),))
     if dc.shape != (E, H, I // 2) or _microscaled(dc, ds, dev, "down") != I:
         raise ValueError("down_codes must have shape %s" % ((E, H, I // 2),))
-    return MicroscaleWeights(H, I, E, 0, gc.data_ptr(), gs.data_ptr(), dc.data_ptr(),
+    y = layer.get("y_dtype", torch.bfloat16)
+    if y is not torch.bfloat16 and y is not torch.float32:
+        raise TypeError("y_dtype must be bfloat16 or float32, got %s" % (y,))
+    return MicroscaleWeights(H, I, E, _ROW_DTYPES[y], gc.data_ptr(), gs.data_ptr(), dc.data_ptr(),
                              ds.data_ptr())
 
 
-def microscale_layer(layer: dict, stream=None) -> dict:
+def microscale_layer(layer: dict, stream=None, y_dtype=torch.bfloat16) -> dict:
     """4-bit weights of a dense layer (w_gate, w_up [E,H,I], w_down [E,I,H] bf16): each
-    projection's output channels become rows, quantised along the summed dimension."""
+    projection's output channels become rows, quantised along the summed dimension.  y_dtype as
+    microscale_weights takes it."""
     if stream is not None:
         with _launch_stream(stream, layer["w_down"].device):
-            return microscale_layer(layer)
+            return microscale_layer(layer, y_dtype=y_dtype)
     H, I, E = layer["H"], layer["I"], layer["E"]
     dev = layer["w_down"].device
     if H % 32 or I % 32:
         raise MoeError(MOE_ERR_UNSUPPORTED, "microscale_layer")
-    out = {"H": H, "I": I, "E": E}
+    out = {"H": H, "I": I, "E": E, "y_dtype": y_dtype}
     for name, n, cols in (("gate_up", 2 * I, H), ("down", H, I)):
         out[name + "_codes"] = torch.empty((E, n, cols // 2), dtype=torch.uint8, device=dev)
         out[name + "_scales"] = torch.empty((E, n, _pitch(cols)), dtype=torch.uint8, device=dev)

@@ -246,3 +246,38 @@ def test_status_of_a_workspace_that_only_the_products_take():
         work[0] = moe.MOE_DEV_WAIT_TIMEOUT
         assert moe.moe_read_device_status(work) == moe.MOE_DEV_WAIT_TIMEOUT
         assert moe.moe_read_device_status(work) == 0
+
+
+@pytest.mark.parametrize("M,k,E,H,I,res", [(1, 8, 128, 2048, 768, False), (21, 8, 128, 2048, 768, True), (40, 6, 16, 320, 96, True),
+                                           (300, 8, 128, 544, 224, False), (400, 8, 16, 512, 256, True),
+                                           (30, 17, 32, 96, 64, True), (30, 18, 32, 96, 64, False), (30, 18, 32, 96, 64, True),
+                                           (50, 32, 40, 160, 32, True)])
+def test_step_with_unrounded_rows(M, k, E, H, I, res):
+    """y_dtype float32: the bits of the separate calls in fp32, rounded once.  The result without
+    a residual then errs by the rounding of out alone, 2^-9 of it at most in the 2-norm."""
+    layer = make_layer(E, H, I, seed=M)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + k)
+    ids = torch.randint(0, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    if M > 30:
+        ids[torch.rand((M, k), generator=g, device="cuda") < 0.05] = -1
+    w = torch.rand((M, k), generator=g, device="cuda")
+    h = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    r = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16) if res else None
+    offsets, _, rr = moe.moe_token_plan(ids, E)
+    q = moe.moe_microscale_quantize(h, route_row=rr)
+    p = moe.moe_microscale_gated_product(*q, layer["gate_up_codes"], layer["gate_up_scales"], offsets=offsets)
+    y = moe.moe_microscale_product(*p, layer["down_codes"], layer["down_scales"], offsets=offsets, dtype=torch.float32)
+    want = moe.moe_token_unsort(y, rr, w, residual=r.float() if res else None)
+    half = moe.moe_microscale_ffn(h, layer, ids, w, residual=r, workspace=moe.microscale_workspace(layer, M, k))
+    layer["y_dtype"] = torch.float32
+    work = moe.microscale_workspace(layer, M, k)
+    for _ in range(3):
+        out = moe.moe_microscale_ffn(h, layer, ids, w, residual=r, workspace=work)
+        assert torch.equal(out, want.to(torch.bfloat16))
+    assert moe.moe_read_device_status(work) == 0
+    if not res:
+        at = torch.where(rr < 0, 0, rr).long()
+        exact = (torch.where((rr < 0).unsqueeze(-1), 0.0, y[at].double()) * w.double().unsqueeze(-1)).sum(1)
+        err = [float((v.double() - exact).norm() / exact.norm()) for v in (out, half)]
+        assert err[0] <= 2.0 ** -9 and err[0] < err[1], err

@@ -279,3 +279,21 @@ def test_status_read_refuses(lib):
     out = ctypes.c_int32(0)
     for work, result in ((None, ctypes.byref(out)), (A + 8, ctypes.byref(out)), (A, None)):
         assert lib.moe_read_device_status(work, None, result) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_type_of_the_rows_before_their_sum(lib, fake):
+    layer = four_bit_layer()
+    assert moe.microscale_weights(layer).y_dtype == moe.MOE_DT_BF16
+    layer["y_dtype"] = torch.float32
+    assert moe.microscale_weights(layer).y_dtype == moe.MOE_DT_F32
+    layer["y_dtype"] = torch.float16
+    with pytest.raises(TypeError):
+        moe.microscale_weights(layer)
+
+    def need(y):
+        return lib.moe_microscale_workspace_bytes(ctypes.byref(moe.MicroscaleWeights(64, 32, 4, y, A, A, A, A)), 40, 2)
+    assert need(moe.MOE_DT_F32) == need(moe.MOE_DT_BF16) + 80 * 64 * 2
+    for y in (moe.MOE_DT_F16, 3, -1):
+        w = moe.MicroscaleWeights(64, 32, 4, y, A, A, A, A)
+        assert need(y) == 0
+        assert lib.moe_microscale_ffn(A, ctypes.byref(w), 4, 2, A, A, None, A, A, 1 << 30, None) == moe.MOE_ERR_INVALID_ARG
