@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, kUnsortCtas<T, V, C>) token_un
 // 96 us, 0.83 of the copy rate.
 constexpr int kGradThreads = 128;
 
-template <typename T, int V>
+template <typename T, int V, int C>
 __global__ void __launch_bounds__(kGradThreads) token_unsort_grad_kernel(const RowArgs a, int nvec) {
-    constexpr int kSlots = 8, C = kRowVecs<T, V>;
+    constexpr int kSlots = 8;
     using P = Pack<T, V>;
     __shared__ float part[kGradThreads / 32][kSlots];
     pdl_wait();
@@ -781,11 +781,22 @@ static cudaError_t unsort_as(const RowArgs &a, cudaStream_t stream) {
     return unsort_vecs<T, V, kRowVecs<T, V>, O>(a, stream);
 }
 
-template <typename T, int V>
-static cudaError_t unsort_grad_as(const RowArgs &a, cudaStream_t stream) {
+template <typename T, int V, int C>
+static cudaError_t unsort_grad_vecs(const RowArgs &a, cudaStream_t stream) {
     cudaLaunchAttribute attrs[2];
     cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)cap_grid(a.M, 64)), dim3(kGradThreads), 0, stream, attrs, 0);
-    return cudaLaunchKernelEx(&cfg, token_unsort_grad_kernel<T, V>, a, a.H / V);
+    return cudaLaunchKernelEx(&cfg, token_unsort_grad_kernel<T, V, C>, a, a.H / V);
+}
+
+// As many vectors a thread as cover the row: more only take registers from other CTAs (4096 tokens
+// x 7 routes: 65 bf16 11.4 us, with four vectors 13.9; 129 fp32 17.4 with two, 22.6).
+template <typename T, int V>
+static cudaError_t unsort_grad_as(const RowArgs &a, cudaStream_t stream) {
+    constexpr int most = kRowVecs<T, V>;
+    const int need = (a.H / V + kGradThreads - 1) / kGradThreads;
+    if (need == 1) return unsort_grad_vecs<T, V, 1>(a, stream);
+    if (need == 2) return unsort_grad_vecs<T, V, most < 2 ? most : 2>(a, stream);
+    return unsort_grad_vecs<T, V, most>(a, stream);
 }
 
 // Whether `depth` units of `rows` pieces a warp fit a CTA's slots.
