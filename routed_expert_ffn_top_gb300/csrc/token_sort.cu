@@ -258,9 +258,13 @@ __global__ void __launch_bounds__(32 * kRowWarps) token_sort_kernel(const RowArg
 // in flight bound them: four of one element, two of two 16-bit ones, one of 16 bytes.
 template <typename T, int V>
 constexpr int kRowVecs = V * sizeof(T) >= 8 ? 1 : V == 1 ? 4 : 2;
-// CTAs an SM of the unsort form, in a grid that fills the SMs once.
+// CTAs an SM of the unsort form, in a grid that fills the SMs once, and slots it loads at once.
+// Four fp32 values of 8 slots at 2 CTAs left too few loads in flight: 4096 tokens x 32 routes x 1024
+// fp32 160 us, with 4 slots at 4 CTAs 88.  (Eight 16-bit ones: 61 us this way, 138 at more CTAs.)
 template <typename T, int V, int C>
-constexpr int kUnsortCtas = V * sizeof(T) >= 8 ? 2 : C > 1 ? 4 : 3;
+constexpr int kUnsortCtas = C > 1 || V == 4 ? 4 : V * sizeof(T) >= 8 ? 2 : 3;
+template <int V, int C>
+constexpr int kUnsortSlots = C > 1 || V == 4 ? 4 : 8;
 
 // Unsort, and with w == NULL and no residual the gradient of sort: a unit is 32 * C vectors of
 // one token; the k rows' vectors are loaded kSlots at a time, then added in slot order.  The next
@@ -269,7 +273,7 @@ constexpr int kUnsortCtas = V * sizeof(T) >= 8 ? 2 : C > 1 ? 4 : 3;
 // 32 routes x 2048 bf16 61 us (137), 0.69 of the copy rate.  O: type of the residual and of out.
 template <typename T, int V, int C, typename O = T>
 __global__ void __launch_bounds__(32 * kRowWarps, kUnsortCtas<T, V, C>) token_unsort_kernel(const RowArgs a, int nvec, int nchunk) {
-    constexpr int kSlots = C > 1 ? 4 : 8;
+    constexpr int kSlots = kUnsortSlots<V, C>;
     using P = Pack<T, V>;
     using Q = Pack<O, V>;
     pdl_wait();
