@@ -14,6 +14,7 @@ import sys
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from routed_expert_ffn_top_gb300 import moe, synthetic as syn
 
@@ -28,6 +29,7 @@ class SortTokens(torch.autograd.Function):
         return moe.moe_token_sort(x, route_row)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_rows):
         (route_row,) = ctx.saved_tensors
         return moe.moe_token_sort_grad(grad_rows.contiguous(), route_row), None
@@ -42,6 +44,7 @@ class UnsortTokens(torch.autograd.Function):
         return moe.moe_token_unsort(rows, route_row, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         rows, route_row, weights = ctx.saved_tensors
         grad_rows, grad_weights = moe.moe_token_unsort_grad(grad_out.contiguous(), rows, route_row, weights)
