@@ -96,8 +96,12 @@ def train(M=256, H=64, I=96, E=8, k=2, steps=60, device="cuda", seed=0):
 
 
 # ---------------------------------------------------------------------------------- serving
-def _time(fn, n=20):
+def _time(fn, n=20, replay=False):
+    """us of a call, or of its launches replayed from a graph."""
     for _ in range(3):
+        fn()
+    if replay:
+        fn = moe.capture_graph(lambda stream: fn()).replay
         fn()
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     start.record()
@@ -108,9 +112,9 @@ def _time(fn, n=20):
     return start.elapsed_time(end) / n * 1e3
 
 
-def serve(H=2048, I=768, E=128, k=8, sizes=(1, 21, 256), device="cuda", seed=0):
+def serve(H=2048, I=768, E=128, k=8, sizes=(1, 21, 256), device="cuda", seed=0, replay=False):
     """Per batch size: (tokens, relative error of the 4-bit step against the bf16 block, us of the
-    bf16 block, us of router and 4-bit step)."""
+    bf16 block, us of router and 4-bit step), called or replayed from a graph."""
     wl = syn.Workload("sorted_experts", H=H, I=I, E=E, k=k, b=0, M=max(sizes))
     dense = syn.make_layer(wl, seed=seed, device=device)
     four = moe.microscale_layer(dense)
@@ -129,13 +133,16 @@ def serve(H=2048, I=768, E=128, k=8, sizes=(1, 21, 256), device="cuda", seed=0):
         a, b = block().double(), step().double()
         if moe.moe_read_device_status(work4):
             raise RuntimeError("device status set")
-        found.append((M, float((a - b).norm() / a.norm()), _time(block), _time(step)))
+        found.append((M, float((a - b).norm() / a.norm()), _time(block, replay=replay),
+                      _time(step, replay=replay)))
     return found
 
 
 def main():
-    for M, err, t16, t4 in serve():
-        print("%5d tokens: bf16 block %7.1f us, 4-bit step %7.1f us, relative difference %.3f" % (M, t16, t4, err))
+    for replay, how in ((False, "called"), (True, "replayed")):
+        for M, err, t16, t4 in serve(replay=replay):
+            print("%5d tokens, %-8s: bf16 block %7.1f us, router and 4-bit step %7.1f us (%s is faster), "
+                  "relative difference %.3f" % (M, how, t16, t4, "bf16" if t16 < t4 else "4-bit", err))
     losses = train()
     print("training: loss %.4f -> %.4f in %d steps" % (losses[0], losses[-1], len(losses)))
 
