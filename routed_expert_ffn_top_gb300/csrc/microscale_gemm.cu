@@ -52,10 +52,11 @@ constexpr int kMxStaging = 2048;  // bytes a warp stages for its stores: 32 rows
 
 // Two tiles.
 //   kTok = 128: 128 rows of x as the MMA's M side, 192 channels as its N side (two accumulators
-//     of 192 columns leave tensor memory for the scales of four stages; 256 would not).
+//     of 192 columns leave 128 columns of tensor memory, 96 of them for the scales of two stages;
+//     256 would leave none).
 //   kTok = 32, for small groups: the sides change places, 128 channels are M and up to 32 rows
-//     N, so no MMA reads rows that do not exist and four epilogue warps share every row N, so no MMA reads rows that do not exist and four epilogue warps share every row (with
-//     the rows on the M side one token's gated product took 8.4 us, this way 7.2)..
+//     N, so no MMA reads rows that do not exist and four epilogue warps share every row (with
+//     the rows on the M side one token's gated product took 8.4 us, this way 7.2).
 template <int kTok_>
 struct MxTile {
     static_assert(kTok_ == 32 || kTok_ == 128, "row tiles");
@@ -82,6 +83,7 @@ struct MxTile {
     static constexpr int kBCols = kB / 32;
     static constexpr int kBPad = (kBCols + 3) / 4 * 4;     // every set starts at a multiple of 4
     static constexpr int kGroups = 2 * kChunks;            // 128-wide groups of K per stage
+    static_assert(kGroups == 4, "a stage's scales of a row are one 16-byte piece");
     static constexpr int kSfCols = kGroups * (kACols + kBPad);  // per stage
     static constexpr int kSfCol0 = 2 * kB;                 // after the two accumulators
     static constexpr uint32_t kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
@@ -236,7 +238,7 @@ __device__ __forceinline__ void store_row32(const MxArgs &a, int64_t row, int n,
 
 // SiLU(g) u = g u / (1 + 2^(-g log2 e)) by the approximate power and reciprocal: within 2^-21
 // (1 + |g| / 4) of its value for negative g, 2^-21 for others, and p goes to 4 bits next.  Below
-// g = -87 it gives 0 for values under 2^-119.  (expf and the division took the gated epilogue's
+// g = -87.3 the reciprocal is 0, and so is the result, whose value is under 2^-119 |u|.  (expf and the division took the gated epilogue's
 // instructions from 8 to 16 a value.)
 __device__ __forceinline__ float gate(float g, float u) {
     float e, r;
@@ -293,18 +295,13 @@ __device__ __forceinline__ uint4 mx_scale_piece(const unsigned char *base, int r
     return *reinterpret_cast<const uint4 *>(base + mx_scale_at(row, piece));
 }
 
-// The words of a stage to w[0], w[kStep], ...: all four of a piece, or one half of it.
-template <int kGroups, int kStep>
-__device__ __forceinline__ void mx_scale_words(const uint4 &v, bool upper, const uint32_t (&mask)[kGroups], uint32_t *w) {
-    if constexpr (kGroups == 4) {
-        w[0] = v.x & mask[0];
-        w[kStep] = v.y & mask[1];
-        w[2 * kStep] = v.z & mask[2];
-        w[3 * kStep] = v.w & mask[3];
-    } else {
-        w[0] = (upper ? v.z : v.x) & mask[0];
-        w[kStep] = (upper ? v.w : v.y) & mask[1];
-    }
+// The four words of a stage's piece to w[0], w[kStep], ...
+template <int kStep>
+__device__ __forceinline__ void mx_scale_words(const uint4 &v, const uint32_t (&mask)[4], uint32_t *w) {
+    w[0] = v.x & mask[0];
+    w[kStep] = v.y & mask[1];
+    w[2 * kStep] = v.z & mask[2];
+    w[3 * kStep] = v.w & mask[3];
 }
 
 // 32 rows x 32 columns of a warp by tensor stores of 64-byte rows through its staging memory (a
@@ -391,7 +388,6 @@ __device__ __forceinline__ void mx_gate_columns(const MxArgs &a, float *exchange
     named_bar_sync(1 + 2 * group, 128);  // u may be written over
 }
 
-// kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
 // First weight row of a unit: of the tile's channels, or (gated) of its gate channels, whose up
 // rows lie N / 2 further on.
 template <bool kGated, int kCh>
@@ -399,6 +395,7 @@ __device__ __forceinline__ int mx_first_channel(const MxArgs &a, int e, int ct) 
     return e * a.N + ct * (kGated ? kCh / 2 : kCh);
 }
 
+// kOut: 0 bf16, 1 f16, 2 f32, 3 gated codes and scales.
 template <int kTok, int kOut>
 __global__ void __launch_bounds__(kMxThreads, 1)
 microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -646,7 +643,6 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
         for (int i = 0; i < G::kScaleBufs - 1; ++i) issue();
         // after a wait that gave up the loop runs on without waits, so that the barriers stay paired
         bool ok = true;
-        uint4 piece[G::kACols + G::kBCols];
         for (int64_t u = blockIdx.x; u < (int64_t)tiles * a.nct; u += gridDim.x)
             for (int s = 0; s < nks; ++s) {
                 const int part = s % kPerScale;
@@ -664,17 +660,14 @@ microscale_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_co
                     mask[q] = left >= 4 ? 0xffffffffu : (left <= 0 ? 0u : (1u << (8 * left)) - 1u);
                 }
                 const unsigned char *S = scales + slot * G::kScaleBytes;
-                const bool upper = G::kGroups == 2 && (part & 1);
-                if (!upper) {  // a piece serves two 256-deep stages
+                uint4 piece[G::kACols + G::kBCols];
 #pragma unroll
-                    for (int c = 0; c < G::kACols + G::kBCols; ++c)
-                        piece[c] = mx_scale_piece(S, c * 32 + lane, G::kGroups == 4 ? part : part >> 1);
-                }
+                for (int c = 0; c < G::kACols + G::kBCols; ++c) piece[c] = mx_scale_piece(S, c * 32 + lane, part);
                 uint32_t wa[G::kGroups * G::kACols] = {}, wb[G::kGroups * G::kBPad] = {};
 #pragma unroll
-                for (int c = 0; c < G::kACols; ++c) mx_scale_words<G::kGroups, G::kACols>(piece[c], upper, mask, wa + c);
+                for (int c = 0; c < G::kACols; ++c) mx_scale_words<G::kACols>(piece[c], mask, wa + c);
 #pragma unroll
-                for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kGroups, G::kBPad>(piece[G::kACols + c], upper, mask, wb + c);
+                for (int c = 0; c < G::kBCols; ++c) mx_scale_words<G::kBPad>(piece[G::kACols + c], mask, wb + c);
                 // the MMAs that read this slot's scales have completed
                 ok = ok && mx_warp_wait(&ctl.empty[stage * G::kSub + G::kSub - 1], phase ^ 1u, ctl);
                 if (ok) {
