@@ -281,3 +281,79 @@ def test_step_with_unrounded_rows(M, k, E, H, I, res):
         exact = (torch.where((rr < 0).unsqueeze(-1), 0.0, y[at].double()) * w.double().unsqueeze(-1)).sum(1)
         err = [float((v.double() - exact).norm() / exact.norm()) for v in (out, half)]
         assert err[0] <= 2.0 ** -9 and err[0] < err[1], err
+
+
+@pytest.mark.parametrize("rows", [30, 60])
+def test_gated_product_of_blocks_without_a_value(rows):
+    """A NaN block (scale byte 255) in a row of x reaches all of that row's blocks, one in a gate or
+    an up channel that channel's block in its expert's rows: scale byte 255 and codes 0 there,
+    every other block as without them.  Both tiles."""
+    g = gen(rows)
+    E, I, K = 2, 96, 160
+    sizes = [rows // 2, rows - rows // 2]
+    offsets = torch.tensor([0, sizes[0], rows], dtype=torch.int32).cuda()
+    code = lambda *shape: torch.randint(0, 16, shape, generator=g, dtype=torch.uint8)
+    xcode, wcode = code(rows, K), code(E, 2 * I, K)
+    xbyte = torch.full((rows, K // 32), 123, dtype=torch.uint8)
+    wbyte = torch.full((E, 2 * I, K // 32), 126, dtype=torch.uint8)
+
+    def run():
+        args = [t.cuda() for t in ref.pack(xcode, xbyte) + ref.pack(wcode, wbyte)]
+        work = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        c, s = moe.moe_microscale_gated_product(*args, offsets=offsets, workspace=work)
+        assert moe.moe_read_device_status(work) == 0
+        return c.cpu().reshape(rows, I // 32, 16), s.cpu()[:, :I // 32]
+    want_c, want_s = run()
+    assert int((want_s == 255).sum()) == 0
+    xbyte[3, 4], xbyte[rows - 1, 0] = 255, 255
+    wbyte[0, 40, 1], wbyte[1, I + 95, 3] = 255, 255  # expert 0's gate 40, expert 1's up 95
+    bad = torch.zeros((rows, I // 32), dtype=torch.bool)
+    bad[3], bad[rows - 1] = True, True
+    bad[:sizes[0], 1], bad[sizes[0]:, 2] = True, True
+    got_c, got_s = run()
+    assert torch.equal(got_s == 255, bad) and int(got_c[bad].sum()) == 0
+    assert torch.equal(got_s[~bad], want_s[~bad]) and torch.equal(got_c[~bad], want_c[~bad])
+
+
+@pytest.mark.parametrize("rows", [32, 64])
+def test_gated_product_of_infinities(rows):
+    """g or u past fp32's range: the block is a NaN block; the row's others are not."""
+    I, K = 64, 32
+    xc, xs = ref.pack(torch.full((rows, K), 2, dtype=torch.uint8), torch.full((rows, 1), 127, dtype=torch.uint8))
+    byte = torch.full((2 * I, 1), 127, dtype=torch.uint8)
+    byte[3] = 252  # gate 3: 32 * 6 * 2^125 overflows; 2^125 itself does not
+    byte[I + 40] = 252
+    wc, ws = ref.pack(torch.full((2 * I, K), 7, dtype=torch.uint8), byte)
+    for gate, up, want in ((True, False, [255, None]), (False, True, [None, 255])):
+        s = ws.clone()
+        if not gate:
+            s[3] = ws[0]
+        if not up:
+            s[I + 40] = ws[0]
+        c, sc = (t.cpu() for t in moe.moe_microscale_gated_product(xc.cuda(), xs.cuda(), wc.cuda(), s.cuda()))
+        for b, w in enumerate(want):
+            if w == 255:
+                assert bool((sc[:, b] == 255).all()) and int(c[:, 16 * b:16 * b + 16].sum()) == 0
+            else:
+                v = ref.values(c[:, 16 * b:16 * b + 16].contiguous(), sc[:, b:b + 1])  # 192 * 192 = 36864 to 4 bits
+                assert bool(((v - 36864).abs() <= 0.25 * 36864).all())
+
+
+@pytest.mark.parametrize("rows", [32, 64])
+def test_gated_product_far_below_zero(rows):
+    """Row m has m ones: g = -4 m, u = 6 m 2^100.  SiLU(g) u is 4-bit rounded (a quarter of it at
+    most), or 0 where the reciprocal is: below g = -87 and under 2^-119 |u|."""
+    K, I = 32, 32
+    m = torch.arange(rows) % 32 + 1
+    code = torch.where(torch.arange(K) < m.unsqueeze(1), 2, 0).to(torch.uint8)  # 1.0
+    xc, xs = ref.pack(code, torch.full((rows, 1), 127, dtype=torch.uint8))
+    wcode = torch.cat((torch.full((I, K), 14), torch.full((I, K), 7))).to(torch.uint8)  # -4, 6
+    byte = torch.cat((torch.full((I, 1), 127), torch.full((I, 1), 227))).to(torch.uint8)
+    wc, ws = ref.pack(wcode, byte)
+    c, s = moe.moe_microscale_gated_product(xc.cuda(), xs.cuda(), wc.cuda(), ws.cuda())
+    got = ref.values(c.cpu(), s.cpu())
+    g, u = -4.0 * m.double().unsqueeze(1), 6.0 * m.double().unsqueeze(1) * 2.0 ** 100
+    p = (g * torch.exp(g) / (1 + torch.exp(g)) * u).expand(rows, I)
+    flushed = (got == 0) & (g < -87) & (p.abs() <= 2.0 ** -119 * u)
+    assert bool((((got - p).abs() <= (0.25 + 1e-4) * p.abs()) | flushed).all())
+    assert bool((got[m <= 21] != 0).all())
