@@ -357,3 +357,104 @@ def test_gated_product_far_below_zero(rows):
     flushed = (got == 0) & (g < -87) & (p.abs() <= 2.0 ** -119 * u)
     assert bool((((got - p).abs() <= (0.25 + 1e-4) * p.abs()) | flushed).all())
     assert bool((got[m <= 21] != 0).all())
+
+
+def pitched(t, pad, shift):
+    """The same matrix on the GPU with a longer pitch, NaN between the rows, and a base address off
+    by `shift` elements."""
+    R, C = t.shape
+    buf = torch.full((R * (C + pad) + shift,), float("nan"), dtype=t.dtype, device="cuda")
+    v = buf[shift:].view(R, C + pad)[:, :C]
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("M,k,E,H,pad,shift", [(1, 8, 128, 2048, 0, 0), (53, 5, 12, 608, 0, 0), (53, 5, 12, 608, 8, 8),
+                                               (29, 18, 40, 544, 3, 1), (40, 32, 8, 96, 16, 0), (700, 3, 8, 1056, 1, 0)])
+def test_quantise_into_sorted_rows_of_any_type_and_pitch(M, k, E, H, pad, shift, dtype):
+    """Bit for bit the definition's codes at the rows of a token's routes, zeros in the rows of
+    dropped ones; NaN and infinite blocks, blocks of zeros and of the largest values among them."""
+    g = gen(M * H)
+    ids = torch.randint(-1, E, (M, k), generator=g, dtype=torch.int32)
+    x = torch.randn((M, H), generator=g) * torch.exp2(torch.randint(-8, 8, (M, 1), generator=g).float())
+    x[0, :32], x[M // 2, -32:] = 0.0, torch.finfo(dtype).max
+    x[M - 1, 40], x[M // 3, 5] = float("nan"), float("-inf")
+    x = x.to(dtype)
+    route_row = ref.plan(ids, E)[2]
+    at, live = ref.at_rows(route_row)
+    codes, scales = moe.moe_microscale_quantize(pitched(x, pad, shift), route_row=route_row.cuda())
+    one_c, one_s = ref.pack(*ref.quantise(x))
+    token = torch.arange(M).repeat_interleave(k)
+    want_c = torch.zeros((M * k, H // 2), dtype=torch.uint8)
+    want_s = torch.zeros((M * k, one_s.shape[1]), dtype=torch.uint8)
+    want_c[at[live]], want_s[at[live]] = one_c[token[live]], one_s[token[live]]
+    assert torch.equal(codes.cpu(), want_c) and torch.equal(scales.cpu(), want_s)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,cols,pad,shift", [(1, 32, 0, 1), (7, 480, 3, 0), (21, 2048, 1, 3), (130, 544, 8, 8), (5, 1568, 24, 0)])
+def test_values_into_rows_of_any_pitch(rows, cols, pad, shift, dtype):
+    """All scale bytes; nothing is written between the rows."""
+    g = gen(rows * cols)
+    code = torch.randint(0, 16, (rows, cols), generator=g, dtype=torch.uint8)
+    byte = torch.randint(0, 256, (rows, cols // 32), generator=g, dtype=torch.uint8)
+    c, s = ref.pack(code, byte)
+    buf = torch.full((rows * (cols + pad) + shift + 5,), 77.0, dtype=dtype, device="cuda")
+    out = buf[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+    moe.moe_microscale_dequantize(c.cuda(), s.cuda(), out=out)
+    want = ref.values(c, s).to(dtype)
+    got = out.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(0.0, 1e30, -1e30), want.nan_to_num(0.0, 1e30, -1e30))
+    out.fill_(77.0)
+    assert bool((buf == 77.0).all())
+
+
+@pytest.mark.parametrize("M,k,res", [(20, 9, True), (7, 17, True), (12, 18, False), (20, 18, True), (9, 32, True), (64, 32, False)])
+def test_step_of_many_slots(M, k, res):
+    """More than 8 slots, and past 18 the way back's other form, which does not begin early: the
+    bits of the separate calls, in steps that follow one another."""
+    E, H, I = 40, 288, 96
+    layer = make_layer(E, H, I, seed=k)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(k)
+    work = moe.microscale_workspace(layer, M, k)
+    hs, ids = [], []
+    for _ in range(4):
+        hs.append(torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16))
+        ids.append(torch.randint(-1, E, (M, k), generator=g, device="cuda", dtype=torch.int32))
+    w = torch.rand((M, k), generator=g, device="cuda")
+    got = [moe.moe_microscale_ffn(h, layer, i, w, residual=h if res else None, workspace=work) for h, i in zip(hs, ids)]
+    assert moe.moe_read_device_status(work) == 0
+    for o, h, i in zip(got, hs, ids):
+        assert torch.equal(o, parts(h, layer, i, w, residual=h if res else None))
+
+
+@pytest.mark.parametrize("M,k", [(3, 4), (120, 8)])
+def test_step_of_tokens_without_a_value(M, k):
+    """A token with a NaN or an infinity: all of its own result is NaN, every other token's bits are
+    as without it; a token whose routes are all dropped keeps its residual."""
+    E, H, I = 16, 256, 96
+    layer = make_layer(E, H, I, seed=9)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    ids = torch.randint(0, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.rand((M, k), generator=g, device="cuda")
+    h = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    res = torch.randn((M, H), generator=g, device="cuda").to(torch.bfloat16)
+    ids[1] = -1
+    work = moe.microscale_workspace(layer, M, k)
+    want = moe.moe_microscale_ffn(h, layer, ids, w, residual=res, workspace=work)
+    assert torch.equal(want[1], res[1])
+    for value in (float("nan"), float("inf")):
+        for token in (0, 1, M - 1):
+            x = h.clone()
+            x[token, 70] = value
+            out = moe.moe_microscale_ffn(x, layer, ids, w, residual=res, workspace=work)
+            keep = torch.arange(M, device="cuda") != token
+            assert torch.equal(out[keep], want[keep])
+            assert torch.equal(out[1], res[1])
+            if token != 1:
+                assert bool(torch.isnan(out[token]).all())
+    assert moe.moe_read_device_status(work) == 0
