@@ -412,7 +412,9 @@ int moe_reader_ffn(const void *h, const moe_reader_t *rd, int M, int k, const in
  * offsets[e+1] - 1; offsets[E] = valid routes), route_row [M,k] (the row of each route; for a
  * dropped route the bitwise complement of its row, which lies past offsets[E]) and row_route
  * [M*k] (the route of each row, -1 for the rows of dropped routes).  E <= 1024.  One launch,
- * no workspace, stable: bitwise identical on every run.  M == 0 writes offsets only.
+ * no workspace, stable: bitwise identical on every run.  M == 0 writes offsets only.  Past 2^18
+ * routes its time grows with the square of their number (GB300: 2^18 26 us, 2^20 0.27 ms, 2^24
+ * 47 ms).
  */
 int moe_token_plan(const int32_t *topk_ids, int M, int k, int E, int32_t *offsets,
                    int32_t *row_route, int32_t *route_row, void *stream);

@@ -27,14 +27,15 @@
 //                rate), down 15.3 us for 63 MB (0.61: 4 us of a launch are not copies, and a unit
 //                has only 48 KB).  One token: 6.8 and 5.6 us, start-up and one pass of latency.
 //                In an expert step both begin while the kernel ahead runs (MxArgs::early).
-//   many rows    the way into the SM.  16384 x 8192 x 8192 in one group takes 379 us (5.8 PFLOP/s,
-//                3.0 of the bf16 rate), the same with the copies of codes alone 364: 64 bytes a
-//                cycle and SM, 40 KB per 256 of K for 384 cycles of MMAs.
+//   many rows    16384 x 8192 x 8192 in one group takes 379 us (5.8 PFLOP/s, 3.0 of the bf16 rate),
+//                the same with the copies of codes alone 364 (40 KB per 256 of K, which its MMAs
+//                take 384 cycles for): this form is bound by its copies.
 //                8192 tokens: gated 105 us (3.9 PFLOP/s; 512 rows an expert, four row tiles),
 //                down 85 us, of which 16 go with the stores of y (268 MB) not issued and 7 more
 //                with their staging.
-// Two CTAs a tile (cta_group::2, 256 x 192) take a third less in, but gated 113 us, down 93, and
-// the large product 374: left out.  So were, for few rows, both products of an expert step in
+// Two CTAs a tile (cta_group::2, 256 x 192) take 28 KB in for these 40, but gated 113 us, down 93, and
+// the large product 374, so something other than the copies bound them, which was not found: left
+// out.  So were, for few rows, both products of an expert step in
 // one grid, the second waiting for the first row tile by row tile (8 tokens 44 against 38 us, 21
 // the same); 256-deep stages (21 tokens' gated product 26.6 against 22.1); an L2 promotion of 256
 // bytes (down 21.0 against 19.1).  Stores of y by 128-byte rows take the time of the 64-byte ones.

@@ -33,7 +33,10 @@ namespace moe {
 // What bounds it is latency, and for many routes the scattered stores of row_route, one sector a
 // cycle and SM.  So several clusters count all the routes, and each writes its share of every
 // warp's steps: counting again costs less than 8 SMs' stores (65,536 routes, 128 experts: 9.1 us,
-// one cluster 16; 8 routes 2.0 us; 262,144 routes 26 us).
+// one cluster 16; 8 routes 2.0 us; 262,144 routes 26 us).  Eight clusters suffice up to there.  Past
+// it a cluster still writes kPlanKeep steps of a run, whose ranks its registers hold, so clusters
+// are added, all of which count all routes: 2^20 routes 0.27 ms, 2^22 3.0 ms, 2^24 47 ms, growing
+// with the square.
 constexpr int kPlanMaxCluster = 8;
 constexpr int kPlanMaxShares = 8;  // clusters
 constexpr int kPlanKeep = 4;       // steps of a share whose ranks stay in registers
