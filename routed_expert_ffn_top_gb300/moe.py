@@ -218,6 +218,25 @@ def _need(t, dtype, name, device=None):
     return t
 
 
+def _need_cuda(device):
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device, got %s" % device)
+
+
+def _workspace(t, device):
+    """Checks a workspace: contiguous bytes on the device.  Returns (address, bytes)."""
+    if not (t.dtype is torch.uint8 and t.device == device and t.is_contiguous()):
+        _need(t, torch.uint8, "workspace", device)
+    return t.data_ptr(), t.numel()
+
+
+def _one_device(device, layer):
+    """A layer's tensors (one device's, as its descriptor checks) are on the GPU of the rows."""
+    _need_cuda(device)
+    if layer["w_down"].device != device:
+        raise ValueError("the layer must be on %s, got %s" % (device, layer["w_down"].device))
+
+
 def _check(rc: int, where: str):
     if rc != MOE_OK:
         raise MoeError(rc, where)
@@ -261,6 +280,7 @@ def expert_weights(layer: dict) -> ExpertWeights:
 def moe_route_topk(h, w_router, bias, k, renormalize=True, topk_ids=None, topk_weights=None,
                    stream=None):
     dev = h.device
+    _need_cuda(dev)
     _need(h, torch.bfloat16, "h", dev)
     _need(w_router, torch.bfloat16, "w_router", dev)
     if bias is not None:
@@ -286,6 +306,7 @@ def moe_align_capacity(M, k, E, b) -> int:
 def moe_align_block_size(topk_ids, E, b, sorted_route_ids=None, expert_block_ids=None,
                          num_padded=None, stream=None):
     dev = topk_ids.device
+    _need_cuda(dev)
     _need(topk_ids, torch.int32, "topk_ids", dev)
     M, k = topk_ids.shape
     cap = moe_align_capacity(M, k, E, b)
@@ -357,6 +378,7 @@ def moe_expert_ffn(h, layer, topk_ids, topk_weights, b, alignment=None, residual
     _need(topk_weights, torch.float32, "topk_weights", dev)
     M, k = topk_ids.shape
     w = expert_weights(layer)
+    _one_device(dev, layer)
     if residual is not None:
         _need(residual, torch.bfloat16, "residual", dev)
     if out is None:
@@ -369,7 +391,7 @@ def moe_expert_ffn(h, layer, topk_ids, topk_weights, b, alignment=None, residual
         srt, blk, npad = alignment
     _check(lib().moe_expert_ffn(_ptr(h), ctypes.byref(w), M, k, _ptr(topk_ids),
                                 _ptr(topk_weights), _ptr(srt), _ptr(blk), _ptr(npad), b,
-                                _ptr(residual), _ptr(out), _ptr(workspace), workspace.numel(),
+                                _ptr(residual), _ptr(out), *_workspace(workspace, dev),
                                 _stream(stream)), "moe_expert_ffn")
     return out
 
@@ -380,6 +402,7 @@ def moe_decode_block(h, layer, k, b, residual=None, out=None, topk_ids=None, top
     _need(h, torch.bfloat16, "h", dev)
     M = h.shape[0]
     w = expert_weights(layer)
+    _one_device(dev, layer)
     w_router = _need(layer["w_router"], torch.bfloat16, "w_router", dev)
     bias = layer.get("bias")
     if bias is not None:
@@ -399,7 +422,7 @@ def moe_decode_block(h, layer, k, b, residual=None, out=None, topk_ids=None, top
     _need(topk_weights, torch.float32, "topk_weights", dev)
     _check(lib().moe_decode_block(_ptr(h), _ptr(w_router), _ptr(bias), ctypes.byref(w), M, k, b,
                                   _ptr(residual), _ptr(out), _ptr(topk_ids), _ptr(topk_weights),
-                                  _ptr(workspace), workspace.numel(), _stream(stream)),
+                                  *_workspace(workspace, dev), _stream(stream)),
            "moe_decode_block")
     return out, topk_ids, topk_weights
 
@@ -413,6 +436,7 @@ def moe_decode_block_noalloc(h, layer, k, b, residual=None, out=None, topk_ids=N
     _need(h, torch.bfloat16, "h", dev)
     M = h.shape[0]
     w = expert_weights(layer)
+    _one_device(dev, layer)
     w_router = _need(layer["w_router"], torch.bfloat16, "w_router", dev)
     bias = layer.get("bias")
     if bias is not None:
@@ -551,6 +575,7 @@ def moe_reader_ffn(h, rd: dict, topk_ids, topk_weights, K: int, nscan: int = 80,
                    out=None, workspace=None, want_decisions=False, stream=None):
     """The reader's decode (include/moe.h).  Returns out, or (out, selected [M,K] int32,
     xr [M,H] fp32) with ``want_decisions``."""
+    _one_device(h.device, rd)
     M, k = topk_ids.shape
     if out is None:
         out = torch.empty_like(h)
@@ -563,7 +588,7 @@ def moe_reader_ffn(h, rd: dict, topk_ids, topk_weights, K: int, nscan: int = 80,
     s = _reader_struct(rd)
     _check(lib().moe_reader_ffn(_ptr(h), ctypes.byref(s), M, k, _ptr(topk_ids), _ptr(topk_weights),
                                 K, nscan, _ptr(residual), _ptr(out), _ptr(sel), _ptr(xr),
-                                _ptr(workspace), workspace.numel(), _stream(stream)),
+                                *_workspace(workspace, h.device), _stream(stream)),
            "moe_reader_ffn")
     if want_decisions:
         return out, sel[:, :K], xr
@@ -574,11 +599,6 @@ def moe_reader_ffn(h, rd: dict, topk_ids, topk_weights, K: int, nscan: int = 80,
 # These calls are short (2 to 5 us of GPU time for a few tokens), so their argument checks
 # test the usual case -- right type, shape and device, contiguous -- in one expression.
 _ROW_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
-
-
-def _need_cuda(device):
-    if device.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device, got %s" % device)
 
 
 def _launch_stream(stream, device):
@@ -863,13 +883,6 @@ def moe_microscale_dequantize(codes, scales, dtype=torch.bfloat16, out=None, str
                                            out.data_ptr(), ldx, code, _raw_stream(dev)),
            "moe_microscale_dequantize")
     return out
-
-
-def _workspace(t, device):
-    """Checks a workspace: contiguous bytes on the device.  Returns (address, bytes)."""
-    if not (t.dtype is torch.uint8 and t.device == device and t.is_contiguous()):
-        _need(t, torch.uint8, "workspace", device)
-    return t.data_ptr(), t.numel()
 
 
 def _own_status(workspace, where):

@@ -297,3 +297,66 @@ def test_type_of_the_rows_before_their_sum(lib, fake):
         w = moe.MicroscaleWeights(64, 32, 4, y, A, A, A, A)
         assert need(y) == 0
         assert lib.moe_microscale_ffn(A, ctypes.byref(w), 4, 2, A, A, None, A, A, 1 << 30, None) == moe.MOE_ERR_INVALID_ARG
+
+
+def dense_layer(E=4, H=64, I=32, device="cpu"):
+    bf16 = torch.bfloat16
+    return {"H": H, "I": I, "E": E, "w_gate": torch.zeros((E, H, I), dtype=bf16, device=device),
+            "w_up": torch.zeros((E, H, I), dtype=bf16, device=device), "w_down": torch.zeros((E, I, H), dtype=bf16, device=device),
+            "w_router": torch.zeros((H, E), dtype=bf16, device=device), "bias": None}
+
+
+@pytest.fixture
+def posing(fake, monkeypatch):
+    """Host tensors in the place of the GPU's for the block's calls too."""
+    monkeypatch.setattr(moe, "_stream", lambda stream: None)
+    monkeypatch.setattr(moe, "_need_cuda", lambda device: None)
+    return fake
+
+
+def block_calls(h, ids, w, work):
+    return [lambda layer: moe.moe_expert_ffn(h, layer, ids, w, 8, workspace=work),
+            lambda layer: moe.moe_decode_block(h, layer, 2, 8, workspace=work),
+            lambda layer: moe.moe_decode_block_noalloc(h, layer, 2, 8)]
+
+
+def test_block_takes_a_layer_of_its_own_device_only(posing):
+    h, ids, w = step_args()
+    for call in block_calls(h, ids, w, torch.zeros(8192, dtype=torch.uint8)):
+        call(dense_layer())
+        assert len(launches(posing)) == 1
+        posing.calls.clear()
+        layer = dense_layer(device="meta")
+        layer["w_router"] = torch.zeros((64, 4), dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match="meta"):
+            call(layer)
+        assert launches(posing) == []
+
+
+@pytest.mark.parametrize("work,error", BAD_WORKSPACES)
+def test_a_blocks_workspace_is_contiguous_bytes_of_the_device(posing, work, error):
+    h, ids, w = step_args()
+    for call in block_calls(h, ids, w, work)[:2]:
+        with pytest.raises(error):
+            call(dense_layer())
+    rd = {"H": 64, "I": 32, "E": 4, "rank": 4}
+    for name in ("signs", "g_rows", "v_rows", "w_down", "g_codes", "v_codes", "g_scales", "v_scales", "dnorm", "U", "coef"):
+        rd[name] = torch.zeros(64)
+    with pytest.raises(error):
+        moe.moe_reader_ffn(h, rd, ids, w, 8, workspace=work)
+    assert launches(posing) == []
+
+
+def test_block_refuses_host_tensors(fake, monkeypatch):
+    monkeypatch.setattr(moe, "_stream", lambda stream: None)
+    h, ids, w = step_args()
+    work = torch.zeros(8192, dtype=torch.uint8)
+    for call in block_calls(h, ids, w, work):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(dense_layer())
+    for call in (lambda: moe.moe_route_topk(h, dense_layer()["w_router"], None, 2),
+                 lambda: moe.moe_align_block_size(ids, 4, 8),
+                 lambda: moe.moe_reader_ffn(h, {"w_down": h}, ids, w, 8, workspace=work)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    assert launches(fake) == []
