@@ -527,6 +527,94 @@ int moe_microscale_ffn(const void *h, const moe_microscale_weights_t *w, int M, 
                        const int32_t *topk_ids, const float *topk_weights, const void *residual,
                        void *out, void *workspace, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------------------------
+ * 16-bit products of rows sorted by expert, and their gradients, for prompts and training.
+ *
+ * Rows [rows][cols] (contiguous columns, pitch ld in elements) are grouped by offsets [E+1]
+ * (device), as moe_token_plan gives them: expert e owns rows offsets[e] .. offsets[e+1] - 1; NULL
+ * means one group (E == 1).  dtype, of all operands, is MOE_DT_BF16 or MOE_DT_F16.  Weights are
+ * contiguous.  Operands are 16-byte aligned, their widths and pitches multiples of 8, widths up
+ * to 2^20 (else MOE_ERR_UNSUPPORTED); E <= 1024, rows < 2^24.  Groups may be empty and of any
+ * size.  Sums are fp32 in a fixed order and each result is rounded once: a row's bits do not
+ * depend on the other rows.  Result rows past offsets[E] (dropped routes) are zero.  Outputs
+ * must not overlap inputs.  workspace: ws_bytes >= MOE_GROUPED_STATUS_BYTES, 16-byte aligned,
+ * a status word that must be zero before the first call, read back with moe_read_device_status.
+ */
+#define MOE_GROUPED_STATUS_BYTES 256
+
+/*
+ * y[r] = x[r] w[e] for the rows r of expert e: w [E][K][N]; transposed != 0: x[r] w[e]^T with w
+ * [E][N][K].  With w2 (the same shape; NULL for none) rows of x have 2K columns and y[r] =
+ * x[r][0:K] w[e] + x[r][K:2K] w2[e]: the gradient of rows that two projections read.  y [rows][N]
+ * of MOE_DT_*, any pitch ldy.
+ */
+int moe_grouped_product(const void *x, int64_t ldx, int64_t rows, int dtype, const int32_t *offsets,
+                        const void *w, const void *w2, int transposed, int E, int N, int K,
+                        int y_dtype, void *y, int64_t ldy, void *workspace, size_t ws_bytes,
+                        void *stream);
+
+/* The 8-bit forms of a checkpoint (below). */
+#define MOE_CODE_E4M3 0
+#define MOE_CODE_INT8 1
+
+/*
+ * g = x w_gate[e], u = x w_up[e] (w_gate, w_up [E][H][I], I a multiple of 32): p = SiLU(g) * u of
+ * dtype, [rows][I] with pitch ldp.  codes, scales (NULL for none): the checkpoint of g and u,
+ * as a matrix of 2I columns, g first; rounded from fp32.
+ */
+int moe_grouped_gated_product(const void *x, int64_t ldx, int64_t rows, int dtype,
+                              const int32_t *offsets, const void *w_gate, const void *w_up, int E,
+                              int I, int H, void *p, int64_t ldp, int code, uint8_t *codes,
+                              uint8_t *scales, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * The way back through the down product and the gate: grad_y [rows][H] is the gradient of
+ * y = p w_down[e] (w_down [E][I][H]).  With q = grad_y w_down[e]^T and g, u the checkpoint's values:
+ *   grad_gate_up [rows][2I] = (q u SiLU'(g), q SiLU(g)),   p [rows][I] = SiLU(g) u  (NULL: not wanted),
+ * both contiguous, of dtype, 16-byte aligned.
+ */
+int moe_grouped_gated_product_grad(const void *grad_y, int64_t ldg, int64_t rows, int dtype,
+                                   const int32_t *offsets, const void *w_down, int E, int I, int H,
+                                   int code, const uint8_t *codes, const uint8_t *scales,
+                                   void *grad_gate_up, void *p, void *workspace, size_t ws_bytes,
+                                   void *stream);
+
+/*
+ * out[e] = sum over expert e's rows of x[r]^T grads[r]: x [rows][K], grads [rows][N], out
+ * [E][K][N] of MOE_DT_*, contiguous and 16-byte aligned; zero for an expert without rows.
+ */
+int moe_grouped_weight_grad(const void *x, int64_t ldx, const void *grads, int64_t ldg,
+                            int64_t rows, int dtype, const int32_t *offsets, int E, int K, int N,
+                            int out_dtype, void *out, void *workspace, size_t ws_bytes,
+                            void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Activations kept in 8 bits between the forward and the backward pass.
+ *
+ * A matrix [rows][cols], cols a multiple of 32 up to 2^20, is held as
+ *   codes  [rows][cols] uint8: E4M3 (MOE_CODE_E4M3) or two's complement (MOE_CODE_INT8);
+ *   scales [rows][pitch] uint8: byte X + 127 of each block of 32 columns, pitch =
+ *          moe_checkpoint_pitch(cols), cols/32 rounded up to a multiple of 16, padding 0.
+ * both 16-byte aligned and contiguous.  X is the smallest integer >= -127 with max|x| <= Q 2^X, Q
+ * = 448 or 127 the largest code; a code is x / 2^X rounded to the nearest, ties to even, so no
+ * code saturates.  A block with an infinity or a NaN gets scale byte 255, whose values are NaN.
+ */
+int moe_checkpoint_pitch(int cols);  /* scale bytes of a row; 0 for unsupported cols */
+
+/* x [rows][cols] of MOE_DT_* (any pitch ldx) to codes and scales. */
+int moe_checkpoint_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int cols, int code,
+                            uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * Codes and scales back to values x of MOE_DT_* (exact in fp32, and in bf16 from 2^-126 up; fp16
+ * rounds and overflows).  route_row NULL: row by row.  Else route_row [rows][k] of a token plan: x has
+ * rows * k sorted rows, each token's values in the rows of its routes (zeros in those of dropped
+ * ones); k <= 32, rows * k < 2^24.
+ */
+int moe_checkpoint_dequantize(const uint8_t *codes, const uint8_t *scales, int code, int64_t rows,
+                              int cols, const int32_t *route_row, int k, void *x, int64_t ldx,
+                              int dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

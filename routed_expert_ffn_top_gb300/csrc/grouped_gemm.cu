@@ -1,0 +1,874 @@
+// grouped_gemm.cu -- products of 16-bit rows sorted by expert with their expert's weights, and
+// their gradients, on the tcgen05 tensor cores.
+//
+// Rows [rows][K] are grouped by offsets, as the token plan gives them.  For the rows r of expert e
+//   plain       y[r] = x[r] W[e]  (W [E][K][N]),  or x[r] W[e]^T  (W [E][N][K]),  or the sum of
+//               two such products of the two halves of x[r] with weights of their own;
+//   gated       g = x[r] Wg[e], u = x[r] Wu[e]: p = SiLU(g) u, and g and u in 8 bits;
+//   gated grad  q = d[r] Wd[e]^T is the gradient of p; with s = 1 / (1 + e^-g), g and u from 8 bits:
+//               dg = q u s (1 + g (1 - s)), du = q g s, and p again;
+//   weights     G[e] = sum_r x[r]^T d[r], a product summed over the expert's rows.
+// Operands bf16 or f16, sums in the tensor core's fp32 accumulators in the order of K (or of the
+// rows), each result rounded once: a row's result does not depend on its group, tile or grid.
+//
+// A unit is a row tile of one expert times a tile of channels.  The channels are the MMA's M side
+// and the rows its N side: N is a group's own number of rows, rounded up to 16 a CTA, so a
+// group of 300 rows costs 320, not 384 or 512, and a group's tiles are of equal size.
+// Groups need no padding: a copy may run into the next expert's rows, whose results are dropped
+// by the epilogue (a row only reaches its own results).  In a weights' gradient rows are what is
+// summed: the last rows of the last step are zeroed in shared memory before the MMA reads them.
+//
+// Large tile: two CTAs share a tile (cta_group::2): 256 channels, 128 each, times up to 256
+// rows, each CTA holding half of the rows' operand: 64 KB of shared memory a stage of 128 of K.
+// Small tile, for few rows a group: one CTA, 128 channels, up to 32 rows.
+//
+// Per CTA (persistent, one an SM) 12 warps: 0-3 and 4-7 drain the two accumulators in turn, 8 and 9
+// issue the copies of the M and N sides, 10 the MMAs (the pair's first CTA for both), 11 zeroes
+// the last rows of a weights' gradient.  The accumulators are double-buffered.  An epilogue warp
+// has 32 channels in its lanes; it turns 16 rows of them round through shared memory, so that
+// a lane then has 16 channels of one row: whole 32-byte sectors, and half of an 8-bit block.
+#include <string.h>
+
+#include "checkpoint.cuh"
+#include "gemm_core.cuh"
+#include "grouped.cuh"
+#include "row_io.cuh"
+
+namespace moe {
+
+constexpr int kGgThreads = 384;
+constexpr int kGgK = 128;             // K per stage: two chunks of 64
+constexpr int kGgChunk = 64 * 128 * 2;  // 64 x 128 elements
+constexpr int kGgTurn = 36;           // words of a row of 32 channels that is turned round
+constexpr int kGgTurnBytes = 16 * kGgTurn * 4;
+
+template <int kCtas_, int kRows_, int kStages_>
+struct GgTile {
+    static constexpr int kCtas = kCtas_, kRows = kRows_, kStages = kStages_;
+    static constexpr int kCh = 128 * kCtas;          // channels of a unit
+    static constexpr int kGran = 16 * kCtas;         // N is a multiple of this
+    static constexpr int kSide = kRows / kCtas;      // rows of the N side a CTA holds
+    static constexpr int kABytes = 2 * kGgChunk;
+    static constexpr int kBBytes = kSide * kGgK * 2;
+    static constexpr int kBChunk = kBBytes / 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr uint32_t kTmemCols = 2 * kRows;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kGgTurnBytes + 1024;
+    static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
+    static_assert(kStageBytes % 1024 == 0 && kBChunk % 1024 == 0, "stage alignment");
+};
+using GgLarge = GgTile<2, 256, 3>;
+using GgSmall = GgTile<1, 32, 4>;
+
+constexpr int kGgMaxStages = 4;
+
+struct GgCtl {
+    uint64_t full[kGgMaxStages];   // the pair's first CTA: both CTAs' copies of a stage
+    uint64_t empty[kGgMaxStages];
+    uint64_t land[kGgMaxStages];   // weights: copies of a stage whose last rows are to be zeroed
+    uint64_t tfull[2];
+    uint64_t tempty[2];            // the pair's first CTA: all epilogue warps of both
+    uint64_t done;
+    uint32_t tmem;
+    volatile int abort;
+    int32_t wsum[kGgThreads / 32];
+    int32_t valid_rows;
+    int32_t first[kGroupedMaxExperts + 1];  // row tiles before expert e
+    int32_t begin[kGroupedMaxExperts + 1];  // first row of expert e
+};
+
+struct GgMaps {
+    CUtensorMap x, x2, w, w2, y;
+};
+
+struct GgArgs {
+    const int32_t *offsets;
+    int64_t rows;
+    int E, C, K, N;   // C channels; N the weights' gradient's columns
+    int parts, nct, nnt;
+    int dt, dct;      // a step of a CTA pair's units in row tiles and channel tiles
+    uint32_t idesc;   // without N
+    int half, out32;  // f16 (else bf16) results; fp32 ones
+    int vec;          // rows of out allow stores of 32, 16 bytes or elements: 2, 1, 0
+    unsigned char *out;
+    int64_t ldo;
+    unsigned char *p;
+    int pvec;
+    int code, pitch;
+    uint8_t *codes, *scales;
+    int32_t *status;
+};
+
+// ---------------------------------------------------------------------- pairs of CTAs (PTX)
+// Address, in the cluster's window, of the pair's first CTA's copy of a barrier.
+template <int kCtas>
+__device__ __forceinline__ uint32_t gg_leader(uint64_t *bar) {
+    if constexpr (kCtas == 1) return smem_u32(bar);
+    else return map_shared_rank(bar, 0);
+}
+__device__ __forceinline__ void gg_arrive_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void gg_arrive(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool gg_try(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded; the first tries are made without reading the timer.  A whole warp gets one answer.
+__device__ __forceinline__ bool gg_wait(uint64_t *bar, uint32_t parity, GgCtl &ctl) {
+    bool ok = false;
+    for (int i = 0; i < 32 && !ok; ++i) ok = gg_try(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!(ok = gg_try(bar, parity)) && !ctl.abort)
+            if (globaltimer_ns() - t0 > kWaitLimitNs) ctl.abort = 1;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <int kCtas>
+__device__ __forceinline__ void gg_load_2d(void *dst, const CUtensorMap *tm, int x, int y, uint32_t bar, uint64_t policy) {
+    if constexpr (kCtas == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+            : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void gg_load_3d(void *dst, const CUtensorMap *tm, int x, int y, int z, uint32_t bar,
+                                           uint64_t policy) {
+    if constexpr (kCtas == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+            : "memory");
+}
+
+template <int kCtas>
+__device__ __forceinline__ void gg_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool accumulate) {
+    if constexpr (kCtas == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)accumulate)
+            : "memory");
+}
+// Arrives on the barrier, in both CTAs of a pair, when all MMAs issued so far are complete.
+template <int kCtas>
+__device__ __forceinline__ void gg_commit(uint64_t *bar) {
+    if constexpr (kCtas == 1) umma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void gg_tmem_alloc(uint32_t *slot, uint32_t cols) {
+    if constexpr (kCtas == 1) tmem_alloc(slot, cols);
+    else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int kCtas>
+__device__ __forceinline__ void gg_tmem_dealloc(uint32_t tmem, uint32_t cols) {
+    if constexpr (kCtas == 1) tmem_dealloc(tmem, cols);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+}
+
+// ------------------------------------------------------------------------------------ units
+// A pair's units: u = its number, + the number of pairs, ...; unit u is channel tile u % nct of row
+// tile u / nct (weights: of column tile (u / nct) % nnt of expert u / nct / nnt).  Each warp walks
+// them on its own, without dividing, and finds the next expert with its 32 lanes at once.
+template <Grouped kMode, typename G>
+struct GgWalk {
+    static constexpr bool kWeights = kMode == Grouped::kWeights;
+    int t, ct, e;
+    int row0, nrows;  // this row tile's (weights: the expert's) first row and number of rows
+    int n;            // the MMA's N
+    int n0;           // weights: first column
+
+    __device__ __forceinline__ void place(const GgArgs &a, const GgCtl &ctl) {
+        if constexpr (kWeights) {
+            e = t / a.nnt;
+            n0 = (t - e * a.nnt) * G::kRows;
+            row0 = ctl.begin[e];
+            const int left = ctl.begin[e + 1] - row0;
+            nrows = left < 0 ? 0 : left;
+            n = a.N - n0 < G::kRows ? a.N - n0 : G::kRows;
+        } else {
+            unsigned past;
+            do {
+                const int i = e + 1 + (threadIdx.x & 31);
+                past = __ballot_sync(0xffffffffu, i <= a.E && ctl.first[i] <= t);
+                e += __popc(past);
+            } while (past == 0xffffffffu);
+            // equal tiles: at most kRows, since a group of T tiles has at most T kRows rows
+            const int tiles = ctl.first[e + 1] - ctl.first[e], at = t - ctl.first[e];
+            const int count = ctl.begin[e + 1] - ctl.begin[e];
+            const int q = ((count + tiles - 1) / tiles + G::kGran - 1) / G::kGran * G::kGran;
+            row0 = ctl.begin[e] + at * q;
+            nrows = count - at * q < q ? count - at * q : q;
+            n = nrows;
+        }
+        n = (n + G::kGran - 1) / G::kGran * G::kGran;
+    }
+    __device__ __forceinline__ GgWalk(const GgArgs &a, const GgCtl &ctl, int tiles) {
+        const int u = blockIdx.x / G::kCtas;
+        t = u / a.nct, ct = u % a.nct, e = 0;
+        if (t < tiles) place(a, ctl);
+    }
+    __device__ __forceinline__ void next(const GgArgs &a, const GgCtl &ctl, int tiles) {
+        t += a.dt, ct += a.dct;
+        if (ct >= a.nct) ct -= a.nct, ++t;
+        if (t < tiles) place(a, ctl);
+    }
+    // Stages of a unit, and K steps of its stage s.
+    __device__ __forceinline__ int stages(const GgArgs &a) const {
+        return kWeights ? (nrows + kGgK - 1) / kGgK : a.parts * ((a.K + kGgK - 1) / kGgK);
+    }
+    // Weights: the last step's rows past the group's end are zeroed before the MMA reads them.
+    __device__ __forceinline__ bool ragged() const { return kWeights && nrows % 16 != 0; }
+};
+
+// -------------------------------------------------------------------------------- epilogues
+__device__ __forceinline__ uint32_t gg_pack(float lo, float hi, int half) {
+    return half ? pack2<__half>(lo, hi) : pack2<__nv_bfloat16>(lo, hi);
+}
+
+// kWords words of a row, by stores of 32 or 16 bytes (vec 2, 1) or as 16-bit elements; `words` of
+// them lie within the row.
+template <int kWords>
+__device__ __forceinline__ void gg_put(unsigned char *dst, const uint32_t (&o)[kWords], int words, int vec) {
+    if (vec == 2 && words == kWords && kWords % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i + 8 <= kWords; i += 8) st_global_32(dst + 4 * i, &o[i]);
+    } else if (vec) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4)
+            if (i + 4 <= words) *reinterpret_cast<uint4 *>(dst + 4 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            if (i < words) {
+                reinterpret_cast<uint16_t *>(dst)[2 * i] = (uint16_t)o[i];
+                reinterpret_cast<uint16_t *>(dst)[2 * i + 1] = (uint16_t)(o[i] >> 16);
+            }
+    }
+}
+
+// Sixteen 16-bit results to a row.
+__device__ __forceinline__ void gg_put16(unsigned char *dst, const float (&v)[16], int half, int vec) {
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = gg_pack(v[2 * i], v[2 * i + 1], half);
+    gg_put(dst, o, 8, vec);
+}
+
+// s = 1 / (1 + 2^(-g log2 e)) by the approximate power and reciprocal, within 2^-21 (1 + |g| / 4) of
+// its value for negative g, 2^-21 for others: what follows is rounded to 16 bits.  Below g = -87.3
+// the reciprocal is 0, for values under 2^-119.
+__device__ __forceinline__ float gg_sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
+// Lane's channel of 16 rows in, lane's 16 channels (16 (lane / 16) on) of row lane % 16 out.
+__device__ __forceinline__ void gg_turn_write(float *turn, int lane, const float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) turn[i * kGgTurn + lane] = v[i];
+}
+template <int kN>
+__device__ __forceinline__ void gg_turn_read(const float *turn, int row, int at, float (&v)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(turn + row * kGgTurn + at + i);
+        v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+    }
+}
+
+template <typename G>
+__device__ __forceinline__ void gg_plain(const GgArgs &a, float *turn, uint32_t d, int lane, int row0, int nrows, int ch0) {
+    const int r = lane & 15, ch = ch0 + 16 * (lane >> 4);
+    const int left = a.C - ch, elem = a.out32 ? 4 : 2;
+    unsigned char *dst = a.out + ((int64_t)row0 * a.ldo + ch) * elem;
+#pragma unroll 1
+    for (int c = 0; c < nrows; c += 16) {
+        float v[16];
+        tmem_ld16(d + c, v);
+        gg_turn_write(turn, lane, v);
+        __syncwarp();
+        gg_turn_read(turn, r, 16 * (lane >> 4), v);
+        if (c + r < nrows && left > 0) {
+            unsigned char *at = dst + (int64_t)(c + r) * a.ldo * elem;
+            if (a.out32) {
+                uint32_t o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(v[i]);
+                gg_put(at, o, left < 16 ? left : 16, a.vec);
+            } else {
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = gg_pack(v[2 * i], v[2 * i + 1], a.half);
+                gg_put(at, o, left < 16 ? left / 2 : 8, a.vec);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// Sixteen values of this lane and its neighbour's (lane ^ 16) as a block of the checkpoint.
+template <bool kInt8>
+__device__ __forceinline__ void gg_block(const GgArgs &a, const float (&v)[16], int64_t row, int col, int lane, bool live) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) top = max_abs(top, v[i], v[i + 1]);
+    const uint32_t mine = __float_as_uint(top) & 0x7fffffffu, other = __shfl_xor_sync(0xffffffffu, mine, 16);
+    const uint32_t byte = eight_byte<kInt8>(other > mine ? other : mine);
+    const uint4 code = eight_codes<kInt8>(v, byte);
+    if (!live) return;
+    *reinterpret_cast<uint4 *>(a.codes + row * (2 * a.C) + col + 16 * (lane >> 4)) = code;
+    if (lane < 16) a.scales[row * a.pitch + col / 32] = (uint8_t)byte;
+}
+
+// Two warps, of 32 gate channels and of the same 32 up channels.  Each quantises its own; p of the
+// first 16 channels is the gate warp's, of the last 16 the up warp's.
+__device__ __forceinline__ void gg_gated(const GgArgs &a, float *turn, float *other, uint32_t d, int lane, int bar,
+                                         bool up, int row0, int nrows, int ch0) {
+    const int r = lane & 15, h = lane >> 4, pch = (up ? 16 : 0) + 8 * h;
+    float *const tg = up ? other : turn, *const tu = up ? turn : other;
+    unsigned char *dst = a.out + ((int64_t)row0 * a.ldo + ch0 + pch) * 2;
+#pragma unroll 1
+    for (int c = 0; c < nrows; c += 16) {
+        float v[16];
+        tmem_ld16(d + c, v);
+        named_bar_sync(bar, 64);  // both have read the rows before
+        gg_turn_write(turn, lane, v);
+        named_bar_sync(bar, 64);
+        const bool live = c + r < nrows;
+        if (a.codes) {
+            gg_turn_read(turn, r, 16 * h, v);
+            const int col = (up ? a.C : 0) + ch0;
+            if (a.code == MOE_CODE_INT8) gg_block<true>(a, v, (int64_t)row0 + c + r, col, lane, live);
+            else gg_block<false>(a, v, (int64_t)row0 + c + r, col, lane, live);
+        }
+        float g[8], u[8];
+        gg_turn_read(tg, r, pch, g);
+        gg_turn_read(tu, r, pch, u);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = gg_pack(g[2 * i] * gg_sigmoid(g[2 * i]) * u[2 * i], g[2 * i + 1] * gg_sigmoid(g[2 * i + 1]) * u[2 * i + 1],
+                           a.half);
+        if (live) gg_put(dst + (int64_t)(c + r) * a.ldo * 2, o, 4, a.vec);
+    }
+}
+
+template <bool kInt8>
+__device__ __forceinline__ void gg_gated_grad(const GgArgs &a, float *turn, uint32_t d, int lane, int row0, int nrows,
+                                              int ch0) {
+    const int r = lane & 15, h = lane >> 4, ch = ch0 + 16 * h, I = a.C;
+#pragma unroll 1
+    for (int c = 0; c < nrows; c += 16) {
+        const bool live = c + r < nrows;
+        const int64_t row = (int64_t)row0 + c + r;
+        uint4 gc{0, 0, 0, 0}, uc{0, 0, 0, 0};
+        uint32_t gs = 0, us = 0;
+        if (live) {
+            gc = *reinterpret_cast<const uint4 *>(a.codes + row * (2 * I) + ch);
+            uc = *reinterpret_cast<const uint4 *>(a.codes + row * (2 * I) + I + ch);
+            gs = a.scales[row * a.pitch + ch / 32];
+            us = a.scales[row * a.pitch + (I + ch) / 32];
+        }
+        float q[16], g[16], u[16];
+        tmem_ld16(d + c, q);
+        gg_turn_write(turn, lane, q);
+        __syncwarp();
+        gg_turn_read(turn, r, 16 * h, q);
+        eight_values<kInt8>(gc, gs, g);
+        eight_values<kInt8>(uc, us, u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float s = gg_sigmoid(g[i]), gsi = g[i] * s, t = q[i] * u[i];
+            u[i] *= gsi;                            // p
+            q[i] *= gsi;                            // grad of u
+            g[i] = t * (s + gsi * (1.0f - s));      // grad of g
+        }
+        if (live) {
+            unsigned char *dst = a.out + (row * (2 * I) + ch) * 2;
+            gg_put16(dst, g, a.half, a.vec);
+            gg_put16(dst + 2 * I, q, a.half, a.vec);
+            if (a.p) gg_put16(a.p + (row * I + ch) * 2, u, a.half, a.pvec);
+        }
+        __syncwarp();
+    }
+}
+
+// A warp's 32 rows of the gradient times the n columns of a unit, by tensor stores of 64-byte rows
+// (clipped at the gradient's edges) through its staging memory; zeros for an expert without rows.
+__device__ __forceinline__ void gg_weights(const GgArgs &a, const CUtensorMap &tm, unsigned char *staging, uint32_t d,
+                                           int lane, int e, int ch0, int n0, int n, bool zero) {
+    const int elem = a.out32 ? 4 : 2, parts = a.out32 ? 2 : 1;
+#pragma unroll 1
+    for (int c = 0; c < n && n0 + c < a.N; c += 32) {
+        uint32_t v[32];
+        if (zero) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+        } else {
+            tmem_ld32(d + c, v);
+            tmem_ld_wait(v);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (q == parts) break;
+            if (lane == 0) bulk_store_wait<true>();  // the staging memory's last store has been read
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint4 o;
+                if (a.out32) {
+                    o = make_uint4(v[16 * q + 4 * i], v[16 * q + 4 * i + 1], v[16 * q + 4 * i + 2], v[16 * q + 4 * i + 3]);
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = gg_pack(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]), a.half);
+                    o = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                *reinterpret_cast<uint4 *>(staging + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = o;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile(
+                    "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                    "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&tm)),
+                    "r"((n0 + c) * elem + 64 * q), "r"(ch0), "r"(e), "r"(smem_u32(staging))
+                    : "memory");
+        }
+    }
+}
+
+// `bytes` (a multiple of 16; of 2 when the address is not 16-byte aligned) of zeros by 128 threads.
+__device__ __forceinline__ void gg_zero(unsigned char *p, int64_t bytes, bool wide) {
+    if (wide)
+        for (int64_t i = 16 * (int64_t)(threadIdx.x & 127); i < bytes; i += 16 * 128)
+            *reinterpret_cast<uint4 *>(p + i) = uint4{0, 0, 0, 0};
+    else
+        for (int64_t i = 2 * (int64_t)(threadIdx.x & 127); i < bytes; i += 2 * 128) *reinterpret_cast<uint16_t *>(p + i) = 0;
+}
+
+// ----------------------------------------------------------------------------------- kernel
+// kTrans: the M side's operand is K-major (weights [channels][K]), else channel-major.
+template <Grouped kMode, bool kTrans, typename G>
+__global__ void __launch_bounds__(kGgThreads, 1)
+grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
+    constexpr bool kWeights = kMode == Grouped::kWeights, kGated = kMode == Grouped::kGated;
+    constexpr int kCtas = G::kCtas;
+    extern __shared__ unsigned char smem_raw[];
+    // the same offset in both CTAs of a pair: their descriptors are the first one's
+    unsigned char *stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char *turns = stages + G::kStages * G::kStageBytes;
+    __shared__ GgCtl ctl;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = kCtas == 1 ? 0 : (int)cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(&ctl.full[s], 2 * kCtas);  // two producers a CTA
+            mbar_init(&ctl.empty[s], 1);
+            mbar_init(&ctl.land[s], 2);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.tfull[b], 1);
+            mbar_init(&ctl.tempty[b], 4 * kCtas);
+        }
+        mbar_init(&ctl.done, 1);
+        ctl.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 10) gg_tmem_alloc<kCtas>(&ctl.tmem, G::kTmemCols);
+    if (threadIdx.x == 256) {
+        prefetch_tensormap(&tm.w);
+        prefetch_tensormap(&tm.x);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // row tiles before each expert; offsets outside [0, rows] or running backwards are clamped
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kGgThreads) {
+        const int e = e0 + threadIdx.x;
+        int64_t lo = 0, hi = 0;
+        if (e < a.E) {
+            if (!a.offsets) hi = a.rows;
+            else lo = a.offsets[e], hi = a.offsets[e + 1];
+            lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
+            hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
+        }
+        const int tiles = (int)((hi - lo + G::kRows - 1) / G::kRows);
+        int inc = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += t;
+        }
+        if (lane == 31) ctl.wsum[warp] = inc;
+        __syncthreads();
+        int off = carry, chunk = 0;
+        for (int w = 0; w < kGgThreads / 32; ++w) {
+            const int t = ctl.wsum[w];
+            if (w < warp) off += t;
+            chunk += t;
+        }
+        if (e < a.E) {
+            ctl.first[e] = off + inc - tiles;
+            ctl.begin[e] = (int)lo;
+            if (e == a.E - 1) {
+                ctl.first[a.E] = off + inc;
+                ctl.valid_rows = ctl.begin[a.E] = (int)hi;
+            }
+        }
+        carry += chunk;
+        __syncthreads();
+    }
+    tc_fence_before();
+    if constexpr (kCtas == 1) __syncthreads();
+    else cluster_sync();
+    tc_fence_after();
+    const int tiles = kWeights ? a.E * a.nnt : carry;
+    const int nks = (a.K + kGgK - 1) / kGgK;  // stages of a part
+    using Walk = GgWalk<kMode, G>;
+
+    if (warp == 8 || warp == 9) {
+        // producers: 8 the M side's operand, 9 the N side's.  Weights that one row tile reads leave
+        // L2 first.
+        const bool side_m = warp == 8;
+        const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
+        unsigned char *const base = stages + (side_m ? 0 : G::kABytes);
+        const int chunk = side_m ? kGgChunk : (kWeights ? kGgChunk : G::kBChunk);
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, par = 0;
+        bool ok = true;
+        for (Walk x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
+            const int ns = x.stages(a);
+            const uint64_t pol = !kWeights && side_m && ctl.first[x.e + 1] - ctl.first[x.e] == 1 ? once : keep;
+            // this CTA's first channel, and its first row (weights: column) of the N side
+            const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128);
+            const int side = (kWeights ? x.n0 : x.row0) + rank * (x.n / kCtas);
+            const int side_end = kWeights ? a.N : x.row0 + x.nrows;
+            for (int s = 0; s < ns; ++s) {
+                if (!(ok = gg_wait(&ctl.empty[stage], phase ^ 1u, ctl))) break;
+                if (lane == 0) {
+                    const bool second = !kWeights && s >= nks;
+                    const int k0 = kWeights ? x.row0 + s * kGgK : (second ? s - nks : s) * kGgK;
+                    // copies that bring something the MMAs read, or whose results are stored
+                    int n;
+                    if (side_m) {
+                        n = kGated ? (c0 < a.C ? 2 : 0)
+                            : kTrans ? (c0 < a.C ? (a.K - k0 > 64 ? 2 : 1) : 0)
+                                     : (a.C - c0 > 64 ? 2 : (a.C > c0 ? 1 : 0));
+                    } else if (kWeights) {
+                        const int cols = side_end - side < x.n / kCtas ? side_end - side : x.n / kCtas;
+                        n = cols > 64 ? 2 : (cols > 0 ? 1 : 0);
+                    } else {
+                        n = side < side_end ? (a.K - k0 > 64 ? 2 : 1) : 0;
+                    }
+                    const bool local = kWeights && s == ns - 1 && x.ragged();
+                    const uint32_t bar = local ? smem_u32(&ctl.land[stage]) : gg_leader<kCtas>(&ctl.full[stage]);
+                    gg_arrive_tx(bar, (uint32_t)(n * chunk));
+                    unsigned char *dst = base + stage * G::kStageBytes;
+                    for (int j = 0; j < n; ++j, dst += chunk) {
+                        if (kWeights) {
+                            if (side_m) gg_load_2d<kCtas>(dst, &tm.x, (c0 + 64 * j) * 2, k0, bar, pol);
+                            else gg_load_2d<kCtas>(dst, &tm.w, (side + 64 * j) * 2, k0, bar, pol);
+                        } else if (!side_m) {
+                            gg_load_2d<kCtas>(dst, second ? &tm.x2 : &tm.x, (k0 + 64 * j) * 2, side, bar, pol);
+                        } else if (kGated) {
+                            gg_load_3d<kCtas>(dst, j ? &tm.w2 : &tm.w, c0 * 2, k0, x.e, bar, pol);
+                        } else if (kTrans) {
+                            gg_load_3d<kCtas>(dst, second ? &tm.w2 : &tm.w, (k0 + 64 * j) * 2, c0, x.e, bar, pol);
+                        } else {
+                            gg_load_3d<kCtas>(dst, second ? &tm.w2 : &tm.w, (c0 + 64 * j) * 2, k0, x.e, bar, pol);
+                        }
+                    }
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                par = (par & ~(1u << stage)) | (phase << stage);
+                if (++stage == G::kStages) stage = 0, phase ^= 1u;
+            }
+        }
+        // every copy has landed before the CTA can exit (after a wait that gave up; else the MMAs have
+        // read them all)
+        if (rank == 0)
+            for (int s = 0; s < G::kStages; ++s)
+                if ((issued >> s) & 1u)
+                    if (!mbar_wait_bounded(&ctl.full[s], (par >> s) & 1u)) ctl.abort = 1;
+        __syncwarp();
+    } else if (warp == 10) {
+        if (rank == 0) {
+            // 128-byte swizzle, 8-row atoms 1 KB apart.  K-major: a K step of 16 is 32 bytes, a chunk
+            // of 64 of K apart from the next.  Channel-major: a K step is two atoms, and channels
+            // 64 apart a chunk.  A step only moves the address field (16-byte units).
+            constexpr bool kAMajor = !kTrans, kBMajor = kWeights;  // channel-major operands
+            const uint64_t a0 = umma_smem_desc(smem_u32(stages), kAMajor ? kGgChunk : 16, 1024, 2);
+            const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, kBMajor ? kGgChunk : 16, 1024, 2);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, tphase = 1;
+            bool ok = true;
+            for (Walk x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
+                const int ns = x.stages(a);
+                if (kWeights && ns == 0) continue;
+                if (!(ok = gg_wait(&ctl.tempty[buf], tphase, ctl))) break;
+                tc_fence_after();
+                const uint32_t d = ctl.tmem + (uint32_t)(buf * G::kRows), idesc = a.idesc | (uint32_t)(x.n >> 3) << 17;
+                for (int s = 0; s < ns; ++s) {
+                    if (!(ok = gg_wait(&ctl.full[stage], phase, ctl))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t ad = a0 + (uint32_t)(stage * (G::kStageBytes >> 4));
+                        const uint64_t bd = b0 + (uint32_t)(stage * (G::kStageBytes >> 4));
+                        const int left = kWeights ? x.nrows - s * kGgK : a.K - (s < nks ? s : s - nks) * kGgK;
+                        const int steps = left >= kGgK ? kGgK / 16 : (left + 15) / 16;
+                        auto step = [&](int ks) {
+                            gg_mma<kCtas>(d, ad + (kAMajor ? ks * 128 : (ks >> 2) * (kGgChunk >> 4) + (ks & 3) * 2),
+                                          bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
+                                          s > 0 || ks > 0);
+                        };
+                        if (steps == kGgK / 16) {
+#pragma unroll
+                            for (int ks = 0; ks < kGgK / 16; ++ks) step(ks);
+                        } else {
+                            for (int ks = 0; ks < steps; ++ks) step(ks);
+                        }
+                        gg_commit<kCtas>(&ctl.empty[stage]);
+                        if (s == ns - 1) gg_commit<kCtas>(&ctl.tfull[buf]);
+                    }
+                    __syncwarp();
+                    if (++stage == G::kStages) stage = 0, phase ^= 1u;
+                }
+                if (buf) tphase ^= 1u;
+                buf ^= 1;
+            }
+            // every issued MMA has completed before the CTAs free their tensor memory
+            if (lane == 0) {
+                if constexpr (kCtas == 1) umma_commit(&ctl.done);
+                else
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                     smem_u32(&ctl.done))
+                                 : "memory");
+                if (!mbar_wait_bounded(&ctl.done, 0)) ctl.abort = 1;
+            }
+            __syncwarp();
+        }
+    } else if (warp == 11) {
+        if constexpr (kWeights) {
+            // rows past the group's end within the last K step, as zeros: both operands, since what is
+            // there may be a NaN
+            int total = 0;
+            uint32_t phase = 0;
+            for (Walk x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles)) {
+                total += x.stages(a);
+                if (!x.ragged()) continue;
+                const int stage = (total - 1) % G::kStages;
+                if (!gg_wait(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
+                phase ^= 1u << stage;
+                const int from = x.nrows % kGgK, to = (from + 15) / 16 * 16;
+                unsigned char *S = stages + stage * G::kStageBytes;
+                for (int i = lane; i < (to - from) * 32; i += 32) {
+                    const int ch = i & 3, at = i >> 2;  // four chunks, 16-byte pieces of their rows
+                    *reinterpret_cast<uint4 *>(S + ch * kGgChunk + (from + (at >> 3)) * 128 + (at & 7) * 16) = uint4{0, 0, 0, 0};
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.full[stage]), 2);
+            }
+        }
+    } else {
+        const int group = warp >> 2, quad = warp & 3;
+        float *const turn = reinterpret_cast<float *>(turns + warp * kGgTurnBytes);
+        const int bar = 1 + 2 * group + (quad & 1);  // gated: of the gate and up warps of the same channels
+        int local = 0;
+        for (Walk x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles)) {
+            const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128) + 32 * (kGated ? quad & 1 : quad);
+            if (kWeights && x.nrows == 0) {
+                if (((x.t ^ x.ct) & 1) == group && c0 < a.C)
+                    gg_weights(a, tm.y, turns + warp * 2048, 0, lane, x.e, c0, x.n0, x.n, true);
+                continue;
+            }
+            const int buf = local & 1;
+            const uint32_t parity = (uint32_t)(local >> 1) & 1u;
+            ++local;
+            if (buf != group) continue;
+            bool ok = gg_wait(&ctl.tfull[buf], parity, ctl);
+            if constexpr (kGated) ok = !named_bar_or(bar, 64, !ok);  // both go on or neither
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = ctl.tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * G::kRows);
+            if (c0 >= a.C) {
+                // no channel of this warp's lanes
+            } else if constexpr (kMode == Grouped::kPlain) {
+                gg_plain<G>(a, turn, d, lane, x.row0, x.nrows, c0);
+            } else if constexpr (kGated) {
+                gg_gated(a, turn, reinterpret_cast<float *>(turns + (warp ^ 2) * kGgTurnBytes), d, lane, bar, quad >= 2,
+                         x.row0, x.nrows, c0);
+                if (a.codes && c0 == 0 && quad == 0)  // the scale rows' padding
+                    for (int r = lane; r < x.nrows; r += 32)
+                        for (int b = a.C / 16; b < a.pitch; ++b) a.scales[((int64_t)x.row0 + r) * a.pitch + b] = 0;
+            } else if constexpr (kMode == Grouped::kGatedGrad) {
+                if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, turn, d, lane, x.row0, x.nrows, c0);
+                else gg_gated_grad<false>(a, turn, d, lane, x.row0, x.nrows, c0);
+            } else {
+                gg_weights(a, tm.y, turns + warp * 2048, d, lane, x.e, c0, x.n0, x.n, false);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.tempty[buf]), 1);
+        }
+        if (kWeights && lane == 0) bulk_store_wait<false>();  // stores have left shared memory and are visible
+        // rows past the last group (dropped routes): zeros
+        if (!kWeights && group == 0)
+            for (int64_t r = ctl.valid_rows + (int64_t)blockIdx.x; r < a.rows; r += gridDim.x) {
+                const int elem = a.out32 ? 4 : 2, width = kMode == Grouped::kGatedGrad ? 2 * a.C : a.C;
+                gg_zero(a.out + r * a.ldo * elem, (int64_t)width * elem, a.vec > 0);
+                if (kMode == Grouped::kGatedGrad && a.p) gg_zero(a.p + r * a.C * 2, (int64_t)a.C * 2, a.pvec > 0);
+                if (kGated && a.codes) {
+                    gg_zero(a.codes + r * 2 * a.C, 2 * a.C, true);
+                    gg_zero(a.scales + r * a.pitch, a.pitch, true);
+                }
+            }
+    }
+
+    tc_fence_before();
+    if constexpr (kCtas == 1) __syncthreads();
+    else __syncthreads(), cluster_sync();
+    tc_fence_after();
+    if (warp == 10) gg_tmem_dealloc<kCtas>(ctl.tmem, G::kTmemCols);
+    if (threadIdx.x == 0 && ctl.abort) atomicOr(a.status, MOE_DEV_WAIT_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------------- launcher
+template <Grouped kMode, bool kTrans, typename G>
+static cudaError_t grouped_as(const GgMaps &tm, GgArgs a, cudaStream_t stream) {
+    constexpr int per = kMode == Grouped::kGated ? G::kCh / 2 : G::kCh;
+    a.nct = (a.C + per - 1) / per;
+    a.nnt = (a.N + G::kRows - 1) / G::kRows;
+    const int64_t tiles = kMode == Grouped::kWeights ? (int64_t)a.E * a.nnt : (a.rows < a.E ? a.rows : a.rows / G::kRows + a.E);
+    const int64_t units = tiles * a.nct, most = num_sms() / G::kCtas;
+    const int64_t pairs = units < 1 ? 1 : (units < most ? units : most);
+    a.dt = (int)(pairs / a.nct), a.dct = (int)(pairs % a.nct);
+    const auto fn = grouped_gemm_kernel<kMode, kTrans, G>;
+    cudaError_t err = ensure_smem((const void *)fn, G::kSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attrs[2];
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)(pairs * G::kCtas)), dim3(kGgThreads), G::kSmem, stream, attrs,
+                                           G::kCtas > 1 ? G::kCtas : 0);
+    return cudaLaunchKernelEx(&cfg, fn, tm, a);
+}
+
+template <typename G>
+static cudaError_t grouped_tile(const GgMaps &tm, const GgArgs &a, const GroupedArgs &g, cudaStream_t stream) {
+    switch (g.mode) {
+        case Grouped::kGated: return grouped_as<Grouped::kGated, false, G>(tm, a, stream);
+        case Grouped::kGatedGrad: return grouped_as<Grouped::kGatedGrad, true, G>(tm, a, stream);
+        default:
+            return g.transposed ? grouped_as<Grouped::kPlain, true, G>(tm, a, stream)
+                                : grouped_as<Grouped::kPlain, false, G>(tm, a, stream);
+    }
+}
+
+// Bytes of a store that rows at p with this pitch allow: 2 for 32, 1 for 16, 0 for an element.
+static int store_width(const void *p, int64_t pitch_bytes) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(p) | (uint64_t)pitch_bytes;
+    return bits % 32 == 0 ? 2 : (bits % 16 == 0 ? 1 : 0);
+}
+
+cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
+    GgArgs a{};
+    const bool weights = g.mode == Grouped::kWeights, grad = g.mode == Grouped::kGatedGrad;
+    const bool small = !weights && (g.rows <= 32 || g.rows < 8 * (int64_t)g.E);
+    const uint32_t side = small ? GgSmall::kSide : GgLarge::kSide, fmt = g.half ? 0u : 1u;
+    const bool a_major = !(g.transposed || grad);  // the M side's operand is channel-major
+    const int elem = g.out_dtype == MOE_DT_F32 ? 4 : 2;
+    a.offsets = g.offsets, a.rows = g.rows, a.E = g.E, a.C = g.channels, a.K = g.K, a.N = g.N, a.parts = g.parts;
+    a.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_major ? 1u : 0u) << 15) | ((weights ? 1u : 0u) << 16) |
+              ((small ? 128u : 256u) >> 4 << 24);
+    a.half = elem == 2 && (g.mode == Grouped::kPlain || weights) ? g.out_dtype == MOE_DT_F16 : g.half;
+    a.out32 = (g.mode == Grouped::kPlain || weights) && elem == 4;
+    a.out = static_cast<unsigned char *>(g.out), a.ldo = g.ldo;
+    a.vec = store_width(g.out, g.ldo * (a.out32 ? 4 : 2));
+    a.p = static_cast<unsigned char *>(g.p), a.pvec = store_width(g.p, 2 * (int64_t)g.channels);
+    a.code = g.code, a.codes = g.codes, a.scales = g.scales, a.pitch = microscale_pitch(2 * g.channels);
+    a.status = g.status;
+
+    GgMaps tm;
+    memset(&tm, 0, sizeof tm);
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    bool ok = true;
+    auto rows_map = [&](CUtensorMap *m, const void *p, int64_t cols, int64_t ld, uint32_t box) {
+        const uint64_t d[2] = {(uint64_t)cols * 2, (uint64_t)g.rows}, s[1] = {(uint64_t)ld * 2};
+        const uint32_t b[2] = {128, box};
+        ok = ok && make_tmap_bytes(m, p, 2, d, s, b, sw);
+    };
+    auto weights_map = [&](CUtensorMap *m, const void *p) {
+        const uint64_t in = a_major ? g.channels : g.K, out = a_major ? g.K : g.channels;
+        const uint64_t d[3] = {in * 2, out, (uint64_t)g.E}, s[2] = {in * 2, in * out * 2};
+        const uint32_t b[3] = {128, 128, 1};
+        ok = ok && make_tmap_bytes(m, p, 3, d, s, b, sw);
+    };
+    if (weights) {
+        rows_map(&tm.x, g.x, g.channels, g.ldx, kGgK);
+        rows_map(&tm.w, g.w, g.N, g.ldw, kGgK);
+        const uint64_t in = (uint64_t)g.N * elem;
+        const uint64_t d[3] = {in, (uint64_t)g.channels, (uint64_t)g.E}, s[2] = {in, in * g.channels};
+        const uint32_t b[3] = {64, 32, 1};
+        ok = ok && make_tmap_bytes(&tm.y, g.out, 3, d, s, b, CU_TENSOR_MAP_SWIZZLE_64B);
+    } else {
+        rows_map(&tm.x, g.x, g.K, g.ldx, side);
+        weights_map(&tm.w, g.w);
+        if (g.parts == 2) rows_map(&tm.x2, g.x2, g.K, g.ldx, side);
+        if (g.w2) weights_map(&tm.w2, g.w2);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    if (weights) return grouped_as<Grouped::kWeights, false, GgLarge>(tm, a, stream);
+    return small ? grouped_tile<GgSmall>(tm, a, g, stream) : grouped_tile<GgLarge>(tm, a, g, stream);
+}
+
+}  // namespace moe

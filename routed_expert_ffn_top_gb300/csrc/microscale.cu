@@ -13,38 +13,9 @@
 // rows are padded to a multiple of 16 bytes, [rows][pitch] (the tensor-map rule on row
 // pitches), and the padding is written as 0.
 #include "microscale.cuh"
+#include "row_io.cuh"
 
 namespace moe {
-
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-
-// Sixteen consecutive elements by accesses of kBytes (32, 16, or the element's).
-template <typename T, int kBytes>
-__device__ __forceinline__ void load16(const T *p, float (&v)[16]) {
-    if constexpr (kBytes >= 16) {
-        alignas(32) uint32_t u[4 * sizeof(T)];
-        constexpr int words = kBytes / 4;
-#pragma unroll
-        for (int i = 0; i < (int)(4 * sizeof(T)); i += words) {
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(p) + i;
-            if constexpr (kBytes == 32)
-                asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                             : "=r"(u[i]), "=r"(u[i + 1]), "=r"(u[i + 2]), "=r"(u[i + 3]), "=r"(u[i + 4]),
-                               "=r"(u[i + 5]), "=r"(u[i + 6]), "=r"(u[i + 7])
-                             : "l"(q));
-            else
-                *reinterpret_cast<uint4 *>(&u[i]) = *reinterpret_cast<const uint4 *>(q);
-        }
-        const T *t = reinterpret_cast<const T *>(u);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = to_f32(t[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = to_f32(p[i]);
-    }
-}
 
 struct QuantArgs {
     const void *x;

@@ -37,6 +37,9 @@ MOE_DT_BF16 = 0
 MOE_DT_F16 = 1
 MOE_DT_F32 = 2
 MOE_MICROSCALE_STATUS_BYTES = 256
+MOE_GROUPED_STATUS_BYTES = 256
+MOE_CODE_E4M3 = 0
+MOE_CODE_INT8 = 1
 
 # Every symbol include/moe.h declares (checked against the header by the tests).
 EXPORTS = (
@@ -48,7 +51,9 @@ EXPORTS = (
     "moe_token_plan", "moe_token_sort", "moe_token_sort_grad", "moe_token_unsort",
     "moe_token_unsort_grad", "moe_microscale_pitch", "moe_microscale_quantize",
     "moe_microscale_dequantize", "moe_microscale_product", "moe_microscale_gated_product",
-    "moe_microscale_workspace_bytes", "moe_microscale_ffn",
+    "moe_microscale_workspace_bytes", "moe_microscale_ffn", "moe_grouped_product",
+    "moe_grouped_gated_product", "moe_grouped_gated_product_grad", "moe_grouped_weight_grad",
+    "moe_checkpoint_pitch", "moe_checkpoint_quantize", "moe_checkpoint_dequantize",
 )
 
 
@@ -171,11 +176,25 @@ def lib():
             L.moe_microscale_workspace_bytes.argtypes = [mp, ci, ci]
             L.moe_microscale_workspace_bytes.restype = sz
             L.moe_microscale_ffn.argtypes = [vp, mp, ci, ci, vp, vp, vp, vp, vp, sz, vp]
+            L.moe_grouped_product.argtypes = [vp, i64, i64, ci, vp, vp, vp, ci, ci, ci, ci, ci, vp, i64, vp,
+                                              sz, vp]
+            L.moe_grouped_gated_product.argtypes = [vp, i64, i64, ci, vp, vp, vp, ci, ci, ci, vp, i64, ci,
+                                                    vp, vp, vp, sz, vp]
+            L.moe_grouped_gated_product_grad.argtypes = [vp, i64, i64, ci, vp, vp, ci, ci, ci, ci, vp, vp,
+                                                         vp, vp, vp, sz, vp]
+            L.moe_grouped_weight_grad.argtypes = [vp, i64, vp, i64, i64, ci, vp, ci, ci, ci, ci, vp, vp, sz,
+                                                  vp]
+            L.moe_checkpoint_pitch.argtypes = [ci]
+            L.moe_checkpoint_quantize.argtypes = [vp, i64, ci, i64, ci, ci, vp, vp, vp]
+            L.moe_checkpoint_dequantize.argtypes = [vp, vp, ci, i64, ci, vp, ci, vp, i64, ci, vp]
             for f in ("moe_token_plan", "moe_token_sort", "moe_token_sort_grad",
                       "moe_token_unsort", "moe_token_unsort_grad", "moe_microscale_pitch",
                       "moe_microscale_quantize", "moe_microscale_dequantize",
                       "moe_microscale_product", "moe_microscale_gated_product",
-                      "moe_microscale_ffn"):
+                      "moe_microscale_ffn", "moe_grouped_product", "moe_grouped_gated_product",
+                      "moe_grouped_gated_product_grad", "moe_grouped_weight_grad",
+                      "moe_checkpoint_pitch", "moe_checkpoint_quantize",
+                      "moe_checkpoint_dequantize"):
                 getattr(L, f).restype = ci
             for f in ("moe_route_topk", "moe_align_block_size", "moe_expert_ffn",
                       "moe_decode_block", "moe_decode_block_host", "moe_read_device_status",
@@ -1055,4 +1074,275 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
            "moe_microscale_ffn")
     if own:
         _own_status(workspace, "moe_microscale_ffn")
+    return out
+
+
+# ------------------------------------------- 16-bit products of sorted rows, 8-bit checkpoints
+_CODE_DTYPES = {torch.float8_e4m3fn: MOE_CODE_E4M3, torch.int8: MOE_CODE_INT8}
+
+
+def _half_dtype(t, name):
+    """MOE_DT_* of a 16-bit matrix."""
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
+        raise TypeError("%s must be bfloat16 or float16, got %s" % (name, t.dtype))
+    return _row_dtype(t, name)
+
+
+def _expert_weights(w, name, device, dtype, shape):
+    """Checks expert weights [E,a,b] (None in `shape` for any size) or, of one expert, [a,b];
+    returns (E, a, b)."""
+    ws = w.shape
+    if len(ws) != 2 and len(ws) != 3:
+        raise ValueError("%s must have three dimensions, or two for one expert, got shape %s" % (name, tuple(ws)))
+    if not (w.dtype is dtype and w.device == device and w.is_contiguous()):
+        _need(w, dtype, name, device)
+    found = (1,) + tuple(ws) if len(ws) == 2 else tuple(ws)
+    if any(want is not None and want != got for want, got in zip(shape, found)):
+        raise ValueError("%s must have shape %s, got %s" % (
+            name, tuple("any" if n is None else n for n in shape), tuple(ws)))
+    return found
+
+
+def _offsets(offsets, E, device):
+    return None if offsets is None else _vector(offsets, "offsets", torch.int32, device, (E + 1,))
+
+
+def _status_workspace(workspace, device):
+    """(the workspace made here or None, (the workspace's address, its bytes))."""
+    if workspace is None:
+        workspace = torch.zeros(MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8, device=device)
+        return workspace, (workspace.data_ptr(), MOE_GROUPED_STATUS_BYTES)
+    return None, _workspace(workspace, device)
+
+
+def _code_dtype(dtype):
+    code = _CODE_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError("codes are float8_e4m3fn or int8, got %s" % (dtype,))
+    return code
+
+
+def _checkpoint_outputs(codes, scales, rows, cols, dtype, dev):
+    """Codes and scales of a [rows, cols] checkpoint, allocated where the caller gave none."""
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=dtype, device=dev)
+    if scales is None:
+        scales = torch.empty((rows, _pitch(cols)), dtype=torch.uint8, device=dev)
+    _vector(codes, "codes", dtype, dev, (rows, cols))
+    _vector(scales, "scales", torch.uint8, dev, (rows, _pitch(cols)))
+    return codes, scales
+
+
+def _checkpoint(codes, scales, device):
+    """Checks a checkpoint's pair; returns (MOE_CODE_*, rows, cols)."""
+    code = _code_dtype(codes.dtype)
+    if codes.dim() != 2:
+        _not_a_matrix(codes, "codes")
+    rows, cols = codes.shape
+    _vector(codes, "codes", codes.dtype, device, (rows, cols))
+    _vector(scales, "scales", torch.uint8, device, (rows, _pitch(cols)))
+    return code, rows, cols
+
+
+def moe_grouped_product(rows, weights, offsets=None, transposed=False, dtype=None, out=None,
+                        workspace=None, stream=None):
+    """y [rows,N] of rows [rows,K] sorted by expert: each times its expert's weights [E,K,N] (or
+    [K,N] without offsets); `transposed`: times the transpose of [E,N,K].  A pair of weights sums two
+    products, of the two halves of rows [rows,2K]: with `transposed` and (w_gate, w_up) the gradient
+    of rows that both projections read.  Rows past the last group are zero.  `dtype`: y's, the rows'
+    if None.  The workspace holds the status word; without one the call makes its own, waits for the
+    result and raises what the device found."""
+    if stream is not None:
+        with _launch_stream(stream, rows.device):
+            return moe_grouped_product(rows, weights, offsets, transposed, dtype, out, workspace)
+    dev, dt = rows.device, rows.dtype
+    code = _half_dtype(rows, "rows")
+    R, cols = rows.shape
+    pair = isinstance(weights, (tuple, list))
+    if pair and len(weights) != 2:
+        raise ValueError("weights must be one tensor or a pair, got %d" % len(weights))
+    w, w2 = weights if pair else (weights, None)
+    if pair and cols % 2:
+        raise ValueError("rows must have an even number of columns for a pair of weights, got %d" % cols)
+    K = cols // 2 if pair else cols
+    shape = (None, None, K) if transposed else (None, K, None)
+    E, a, b = _expert_weights(w, "weights", dev, dt, shape)
+    if pair:
+        _expert_weights(w2, "weights", dev, dt, (E, a, b))
+    N = a if transposed else b
+    ldx = _rows(rows, "rows", dev, dt, (R, cols))
+    off = _offsets(offsets, E, dev)
+    if out is None:
+        out, ldy = torch.empty((R, N), dtype=dt if dtype is None else dtype, device=dev), N
+    else:
+        ldy = _rows(out, "out", dev, out.dtype if dtype is None else dtype, (R, N))
+    ycode = _row_dtype(out, "out")
+    own, ws = _status_workspace(workspace, dev)
+    _check(lib().moe_grouped_product(rows.data_ptr(), ldx, R, code, off, w.data_ptr(),
+                                     w2.data_ptr() if pair else None, int(bool(transposed)), E, N, K,
+                                     ycode, out.data_ptr(), ldy, *ws, _raw_stream(dev)),
+           "moe_grouped_product")
+    if own is not None:
+        _own_status(own, "moe_grouped_product")
+    return out
+
+
+def moe_grouped_gated_product(rows, w_gate, w_up, offsets=None, checkpoint=None, out=None, codes=None,
+                              scales=None, workspace=None, stream=None):
+    """p [rows,I] = SiLU(g) * u with g = rows w_gate[e], u = rows w_up[e] (weights [E,H,I]).  With
+    `checkpoint`, torch.float8_e4m3fn or torch.int8, (p, codes, scales): g and u side by side in 8
+    bits, for moe_grouped_gated_product_grad.  Workspace as for moe_grouped_product."""
+    if stream is not None:
+        with _launch_stream(stream, rows.device):
+            return moe_grouped_gated_product(rows, w_gate, w_up, offsets, checkpoint, out, codes, scales,
+                                             workspace)
+    dev, dt = rows.device, rows.dtype
+    code = _half_dtype(rows, "rows")
+    R, H = rows.shape
+    E, _, I = _expert_weights(w_gate, "w_gate", dev, dt, (None, H, None))
+    _expert_weights(w_up, "w_up", dev, dt, (E, H, I))
+    ldx = _rows(rows, "rows", dev, dt, (R, H))
+    off = _offsets(offsets, E, dev)
+    if I % 32:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_grouped_gated_product")
+    if out is None:
+        out, ldp = torch.empty((R, I), dtype=dt, device=dev), I
+    else:
+        ldp = _rows(out, "out", dev, dt, (R, I))
+    kind, pc, ps = 0, None, None
+    if checkpoint is not None:
+        kind = _code_dtype(checkpoint)
+        codes, scales = _checkpoint_outputs(codes, scales, R, 2 * I, checkpoint, dev)
+        pc, ps = codes.data_ptr(), scales.data_ptr()
+    elif codes is not None or scales is not None:
+        raise ValueError("codes and scales are outputs of a checkpoint: its type is missing")
+    own, ws = _status_workspace(workspace, dev)
+    _check(lib().moe_grouped_gated_product(rows.data_ptr(), ldx, R, code, off, w_gate.data_ptr(),
+                                           w_up.data_ptr(), E, I, H, out.data_ptr(), ldp, kind, pc, ps,
+                                           *ws, _raw_stream(dev)), "moe_grouped_gated_product")
+    if own is not None:
+        _own_status(own, "moe_grouped_gated_product")
+    return out if checkpoint is None else (out, codes, scales)
+
+
+def moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, grad_gate_up=None, p=None,
+                                   workspace=None, stream=None):
+    """(grad_gate_up [rows,2I], p [rows,I]) of grad_y [rows,H], the gradient of p w_down[e]
+    (w_down [E,I,H]), and the checkpoint of g and u that moe_grouped_gated_product made.  Workspace
+    as for moe_grouped_product."""
+    if stream is not None:
+        with _launch_stream(stream, grad_y.device):
+            return moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, grad_gate_up, p,
+                                                  workspace)
+    dev, dt = grad_y.device, grad_y.dtype
+    code = _half_dtype(grad_y, "grad_y")
+    R, H = grad_y.shape
+    E, I, _ = _expert_weights(w_down, "w_down", dev, dt, (None, None, H))
+    ldg = _rows(grad_y, "grad_y", dev, dt, (R, H))
+    off = _offsets(offsets, E, dev)
+    kind, crows, cols = _checkpoint(codes, scales, dev)
+    if (crows, cols) != (R, 2 * I):
+        raise ValueError("codes must have shape %s, got %s" % ((R, 2 * I), (crows, cols)))
+    if I % 32:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_grouped_gated_product_grad")
+    if grad_gate_up is None:
+        grad_gate_up = torch.empty((R, 2 * I), dtype=dt, device=dev)
+    else:
+        _vector(grad_gate_up, "grad_gate_up", dt, dev, (R, 2 * I))
+    if p is None:
+        p = torch.empty((R, I), dtype=dt, device=dev)
+    else:
+        _vector(p, "p", dt, dev, (R, I))
+    own, ws = _status_workspace(workspace, dev)
+    _check(lib().moe_grouped_gated_product_grad(grad_y.data_ptr(), ldg, R, code, off, w_down.data_ptr(), E,
+                                                I, H, kind, codes.data_ptr(), scales.data_ptr(),
+                                                grad_gate_up.data_ptr(), p.data_ptr(), *ws,
+                                                _raw_stream(dev)), "moe_grouped_gated_product_grad")
+    if own is not None:
+        _own_status(own, "moe_grouped_gated_product_grad")
+    return grad_gate_up, p
+
+
+def moe_grouped_weight_grad(rows, grads, offsets=None, dtype=torch.float32, out=None, workspace=None,
+                            stream=None):
+    """The gradient [E,K,N] of weights that rows [rows,K] were multiplied by, of grads [rows,N]: per
+    expert the sum of its rows' outer products, zero without rows; without offsets [1,K,N].
+    Workspace as for moe_grouped_product."""
+    if stream is not None:
+        with _launch_stream(stream, rows.device):
+            return moe_grouped_weight_grad(rows, grads, offsets, dtype, out, workspace)
+    dev, dt = rows.device, rows.dtype
+    code = _half_dtype(rows, "rows")
+    _half_dtype(grads, "grads")
+    R, K = rows.shape
+    N = grads.shape[1]
+    ldx = _rows(rows, "rows", dev, dt, (R, K))
+    ldg = _rows(grads, "grads", dev, dt, (R, N))
+    E, off = 1, None
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError("offsets must have shape (E + 1,), got %s" % (tuple(offsets.shape),))
+        E = offsets.shape[0] - 1
+        off = _offsets(offsets, E, dev)
+    if out is None:
+        out = torch.empty((E, K, N), dtype=dtype, device=dev)
+    else:
+        _vector(out, "out", out.dtype, dev, (E, K, N))
+    ocode = _ROW_DTYPES.get(out.dtype)
+    if ocode is None:
+        raise TypeError("out must be bfloat16, float16 or float32, got %s" % (out.dtype,))
+    own, ws = _status_workspace(workspace, dev)
+    _check(lib().moe_grouped_weight_grad(rows.data_ptr(), ldx, grads.data_ptr(), ldg, R, code, off, E, K, N,
+                                         ocode, out.data_ptr(), *ws, _raw_stream(dev)),
+           "moe_grouped_weight_grad")
+    if own is not None:
+        _own_status(own, "moe_grouped_weight_grad")
+    return out
+
+
+def moe_checkpoint_pitch(cols) -> int:
+    return int(lib().moe_checkpoint_pitch(cols))
+
+
+def moe_checkpoint_quantize(x, dtype=torch.float8_e4m3fn, codes=None, scales=None, stream=None):
+    """x [rows,cols] in 8 bits: codes [rows,cols] of `dtype` (float8_e4m3fn or int8) and scales, one
+    power of two per 32 columns (include/moe.h)."""
+    if stream is not None:
+        with _launch_stream(stream, x.device):
+            return moe_checkpoint_quantize(x, dtype, codes, scales)
+    dev = x.device
+    xcode = _row_dtype(x, "x")
+    kind = _code_dtype(dtype)
+    rows, cols = x.shape
+    ldx = _rows(x, "x", dev, x.dtype, (rows, cols))
+    if cols % 32:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_checkpoint_quantize")
+    codes, scales = _checkpoint_outputs(codes, scales, rows, cols, dtype, dev)
+    _check(lib().moe_checkpoint_quantize(x.data_ptr(), ldx, xcode, rows, cols, kind, codes.data_ptr(),
+                                         scales.data_ptr(), _raw_stream(dev)), "moe_checkpoint_quantize")
+    return codes, scales
+
+
+def moe_checkpoint_dequantize(codes, scales, dtype=torch.bfloat16, route_row=None, out=None, stream=None):
+    """The values [rows,cols] of a checkpoint; with route_row [rows,k] (a token plan's) in sorted
+    order, rows * k of them, zero in the rows of dropped routes."""
+    if stream is not None:
+        with _launch_stream(stream, codes.device):
+            return moe_checkpoint_dequantize(codes, scales, dtype, route_row, out)
+    dev = codes.device
+    kind, rows, cols = _checkpoint(codes, scales, dev)
+    rr, k = None, 1
+    if route_row is not None:
+        if route_row.dim() != 2:
+            _not_a_matrix(route_row, "route_row")
+        k = route_row.shape[1]
+        rr = _vector(route_row, "route_row", torch.int32, dev, (rows, k))
+    if out is None:
+        out, ldx = torch.empty((rows * k, cols), dtype=dtype, device=dev), cols
+    else:
+        ldx = _rows(out, "out", dev, out.dtype, (rows * k, cols))
+    xcode = _row_dtype(out, "out")
+    _check(lib().moe_checkpoint_dequantize(codes.data_ptr(), scales.data_ptr(), kind, rows, cols, rr, k,
+                                           out.data_ptr(), ldx, xcode, _raw_stream(dev)),
+           "moe_checkpoint_dequantize")
     return out
