@@ -37,30 +37,30 @@
 namespace moe {
 
 constexpr int kGgThreads = 384;
-constexpr int kGgK = 128;             // K per stage: two chunks of 64
-constexpr int kGgChunk = 64 * 128 * 2;  // 64 x 128 elements
 constexpr int kGgTurn = 36;           // words of a row of 32 channels that is turned round
 constexpr int kGgTurnBytes = 16 * kGgTurn * 4;
+constexpr int kGgMaxStages = 4;
 
-template <int kCtas_, int kRows_, int kStages_>
+template <int kCtas_, int kRows_, int kK_, int kStages_>
 struct GgTile {
     static constexpr int kCtas = kCtas_, kRows = kRows_, kStages = kStages_;
+    static constexpr int kK = kK_;                   // K per stage
+    static constexpr int kChunks = kK / 64;          // K-major: copies of 64 of K
     static constexpr int kCh = 128 * kCtas;          // channels of a unit
     static constexpr int kGran = 16 * kCtas;         // N is a multiple of this
     static constexpr int kSide = kRows / kCtas;      // rows of the N side a CTA holds
-    static constexpr int kABytes = 2 * kGgChunk;
-    static constexpr int kBBytes = kSide * kGgK * 2;
-    static constexpr int kBChunk = kBBytes / 2;
+    static constexpr int kABytes = 128 * kK * 2;
+    static constexpr int kBBytes = kSide * kK * 2;
+    static constexpr int kMajor = kK * 128;          // channel-major: a copy of 64 channels
+    static constexpr int kAChunk = 128 * 128, kBChunk = kSide * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr uint32_t kTmemCols = 2 * kRows;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kGgTurnBytes + 1024;
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
-    static_assert(kStageBytes % 1024 == 0 && kBChunk % 1024 == 0, "stage alignment");
+    static_assert(kStageBytes % 1024 == 0 && kBChunk % 1024 == 0 && kStages <= kGgMaxStages, "stage alignment");
 };
-using GgLarge = GgTile<2, 256, 3>;
-using GgSmall = GgTile<1, 32, 4>;
-
-constexpr int kGgMaxStages = 4;
+using GgLarge = GgTile<2, 256, 128, 3>;
+using GgSmall = GgTile<1, 32, 128, 4>;
 
 struct GgCtl {
     uint64_t full[kGgMaxStages];   // the pair's first CTA: both CTAs' copies of a stage
@@ -106,14 +106,23 @@ __device__ __forceinline__ uint32_t gg_leader(uint64_t *bar) {
     if constexpr (kCtas == 1) return smem_u32(bar);
     else return map_shared_rank(bar, 0);
 }
+// (At the scope of the CTA: what the thread has read or written before is not what a waiter in the
+// other CTA reads.  With release at cluster scope every stage waited a memory barrier out, 0.75 us,
+// and products ran at half the rate.)
 __device__ __forceinline__ void gg_arrive_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void gg_arrive(uint32_t bar, uint32_t count) {
+__device__ __forceinline__ void gg_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// What the thread has written to shared memory is visible to whoever waits for the barrier.
+__device__ __forceinline__ void gg_arrive_release(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// kCluster: what the other CTA's thread wrote before its releasing arrival is visible after.
+template <bool kCluster>
 __device__ __forceinline__ bool gg_try(uint64_t *bar, uint32_t parity) {
+    if constexpr (!kCluster) return mbar_try_wait(bar, parity);
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -125,12 +134,13 @@ __device__ __forceinline__ bool gg_try(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 // Bounded; the first tries are made without reading the timer.  A whole warp gets one answer.
+template <bool kCluster = false>
 __device__ __forceinline__ bool gg_wait(uint64_t *bar, uint32_t parity, GgCtl &ctl) {
     bool ok = false;
-    for (int i = 0; i < 32 && !ok; ++i) ok = gg_try(bar, parity);
+    for (int i = 0; i < 32 && !ok; ++i) ok = gg_try<kCluster>(bar, parity);
     if (!ok) {
         const uint64_t t0 = globaltimer_ns();
-        while (!(ok = gg_try(bar, parity)) && !ctl.abort)
+        while (!(ok = gg_try<kCluster>(bar, parity)) && !ctl.abort)
             if (globaltimer_ns() - t0 > kWaitLimitNs) ctl.abort = 1;
     }
     return __all_sync(0xffffffffu, ok);
@@ -258,7 +268,7 @@ struct GgWalk {
     }
     // Stages of a unit, and K steps of its stage s.
     __device__ __forceinline__ int stages(const GgArgs &a) const {
-        return kWeights ? (nrows + kGgK - 1) / kGgK : a.parts * ((a.K + kGgK - 1) / kGgK);
+        return kWeights ? (nrows + G::kK - 1) / G::kK : a.parts * ((a.K + G::kK - 1) / G::kK);
     }
     // Weights: the last step's rows past the group's end are zeroed before the MMA reads them.
     __device__ __forceinline__ bool ragged() const { return kWeights && nrows % 16 != 0; }
@@ -573,7 +583,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     else cluster_sync();
     tc_fence_after();
     const int tiles = kWeights ? a.E * a.nnt : carry;
-    const int nks = (a.K + kGgK - 1) / kGgK;  // stages of a part
+    const int nks = (a.K + G::kK - 1) / G::kK;  // stages of a part
     using Walk = GgWalk<kMode, G>;
 
     if (warp == 8 || warp == 9) {
@@ -582,7 +592,8 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         const bool side_m = warp == 8;
         const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
         unsigned char *const base = stages + (side_m ? 0 : G::kABytes);
-        const int chunk = side_m ? kGgChunk : (kWeights ? kGgChunk : G::kBChunk);
+        const bool major = side_m ? !kTrans : kWeights;  // channel-major
+        const int chunk = major ? G::kMajor : (side_m ? G::kAChunk : G::kBChunk);
         int stage = 0;
         uint32_t phase = 0, issued = 0, par = 0;
         bool ok = true;
@@ -597,18 +608,19 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 if (!(ok = gg_wait(&ctl.empty[stage], phase ^ 1u, ctl))) break;
                 if (lane == 0) {
                     const bool second = !kWeights && s >= nks;
-                    const int k0 = kWeights ? x.row0 + s * kGgK : (second ? s - nks : s) * kGgK;
+                    const int k0 = kWeights ? x.row0 + s * G::kK : (second ? s - nks : s) * G::kK;
+                    const int deep = (a.K - k0 + 63) / 64 < G::kChunks ? (a.K - k0 + 63) / 64 : G::kChunks;
                     // copies that bring something the MMAs read, or whose results are stored
                     int n;
                     if (side_m) {
                         n = kGated ? (c0 < a.C ? 2 : 0)
-                            : kTrans ? (c0 < a.C ? (a.K - k0 > 64 ? 2 : 1) : 0)
+                            : kTrans ? (c0 < a.C ? deep : 0)
                                      : (a.C - c0 > 64 ? 2 : (a.C > c0 ? 1 : 0));
                     } else if (kWeights) {
                         const int cols = side_end - side < x.n / kCtas ? side_end - side : x.n / kCtas;
                         n = cols > 64 ? 2 : (cols > 0 ? 1 : 0);
                     } else {
-                        n = side < side_end ? (a.K - k0 > 64 ? 2 : 1) : 0;
+                        n = side < side_end ? deep : 0;
                     }
                     const bool local = kWeights && s == ns - 1 && x.ragged();
                     const uint32_t bar = local ? smem_u32(&ctl.land[stage]) : gg_leader<kCtas>(&ctl.full[stage]);
@@ -648,8 +660,8 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             // of 64 of K apart from the next.  Channel-major: a K step is two atoms, and channels
             // 64 apart a chunk.  A step only moves the address field (16-byte units).
             constexpr bool kAMajor = !kTrans, kBMajor = kWeights;  // channel-major operands
-            const uint64_t a0 = umma_smem_desc(smem_u32(stages), kAMajor ? kGgChunk : 16, 1024, 2);
-            const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, kBMajor ? kGgChunk : 16, 1024, 2);
+            const uint64_t a0 = umma_smem_desc(smem_u32(stages), kAMajor ? G::kMajor : 16, 1024, 2);
+            const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, kBMajor ? G::kMajor : 16, 1024, 2);
             int stage = 0, buf = 0;
             uint32_t phase = 0, tphase = 1;
             bool ok = true;
@@ -660,21 +672,21 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 tc_fence_after();
                 const uint32_t d = ctl.tmem + (uint32_t)(buf * G::kRows), idesc = a.idesc | (uint32_t)(x.n >> 3) << 17;
                 for (int s = 0; s < ns; ++s) {
-                    if (!(ok = gg_wait(&ctl.full[stage], phase, ctl))) break;
+                    if (!(ok = gg_wait<kWeights>(&ctl.full[stage], phase, ctl))) break;
                     tc_fence_after();
                     if (lane == 0) {
                         const uint64_t ad = a0 + (uint32_t)(stage * (G::kStageBytes >> 4));
                         const uint64_t bd = b0 + (uint32_t)(stage * (G::kStageBytes >> 4));
-                        const int left = kWeights ? x.nrows - s * kGgK : a.K - (s < nks ? s : s - nks) * kGgK;
-                        const int steps = left >= kGgK ? kGgK / 16 : (left + 15) / 16;
+                        const int left = kWeights ? x.nrows - s * G::kK : a.K - (s < nks ? s : s - nks) * G::kK;
+                        const int steps = left >= G::kK ? G::kK / 16 : (left + 15) / 16;
                         auto step = [&](int ks) {
-                            gg_mma<kCtas>(d, ad + (kAMajor ? ks * 128 : (ks >> 2) * (kGgChunk >> 4) + (ks & 3) * 2),
+                            gg_mma<kCtas>(d, ad + (kAMajor ? ks * 128 : (ks >> 2) * (G::kAChunk >> 4) + (ks & 3) * 2),
                                           bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
                                           s > 0 || ks > 0);
                         };
-                        if (steps == kGgK / 16) {
+                        if (steps == G::kK / 16) {
 #pragma unroll
-                            for (int ks = 0; ks < kGgK / 16; ++ks) step(ks);
+                            for (int ks = 0; ks < G::kK / 16; ++ks) step(ks);
                         } else {
                             for (int ks = 0; ks < steps; ++ks) step(ks);
                         }
@@ -710,15 +722,15 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 const int stage = (total - 1) % G::kStages;
                 if (!gg_wait(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
                 phase ^= 1u << stage;
-                const int from = x.nrows % kGgK, to = (from + 15) / 16 * 16;
+                const int from = x.nrows % G::kK, to = (from + 15) / 16 * 16;
                 unsigned char *S = stages + stage * G::kStageBytes;
                 for (int i = lane; i < (to - from) * 32; i += 32) {
                     const int ch = i & 3, at = i >> 2;  // four chunks, 16-byte pieces of their rows
-                    *reinterpret_cast<uint4 *>(S + ch * kGgChunk + (from + (at >> 3)) * 128 + (at & 7) * 16) = uint4{0, 0, 0, 0};
+                    *reinterpret_cast<uint4 *>(S + ch * G::kMajor + (from + (at >> 3)) * 128 + (at & 7) * 16) = uint4{0, 0, 0, 0};
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.full[stage]), 2);
+                if (lane == 0) gg_arrive_release(gg_leader<kCtas>(&ctl.full[stage]), 2);
             }
         }
     } else {
@@ -760,7 +772,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.tempty[buf]), 1);
+            if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.tempty[buf]));
         }
         if (kWeights && lane == 0) bulk_store_wait<false>();  // stores have left shared memory and are visible
         // rows past the last group (dropped routes): zeros
@@ -824,6 +836,7 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
     GgArgs a{};
     const bool weights = g.mode == Grouped::kWeights, grad = g.mode == Grouped::kGatedGrad;
     const bool small = !weights && (g.rows <= 32 || g.rows < 8 * (int64_t)g.E);
+    const uint32_t depth = small ? GgSmall::kK : GgLarge::kK;
     const uint32_t side = small ? GgSmall::kSide : GgLarge::kSide, fmt = g.half ? 0u : 1u;
     const bool a_major = !(g.transposed || grad);  // the M side's operand is channel-major
     const int elem = g.out_dtype == MOE_DT_F32 ? 4 : 2;
@@ -850,12 +863,12 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
     auto weights_map = [&](CUtensorMap *m, const void *p) {
         const uint64_t in = a_major ? g.channels : g.K, out = a_major ? g.K : g.channels;
         const uint64_t d[3] = {in * 2, out, (uint64_t)g.E}, s[2] = {in * 2, in * out * 2};
-        const uint32_t b[3] = {128, 128, 1};
+        const uint32_t b[3] = {128, a_major ? depth : 128u, 1};
         ok = ok && make_tmap_bytes(m, p, 3, d, s, b, sw);
     };
     if (weights) {
-        rows_map(&tm.x, g.x, g.channels, g.ldx, kGgK);
-        rows_map(&tm.w, g.w, g.N, g.ldw, kGgK);
+        rows_map(&tm.x, g.x, g.channels, g.ldx, depth);
+        rows_map(&tm.w, g.w, g.N, g.ldw, depth);
         const uint64_t in = (uint64_t)g.N * elem;
         const uint64_t d[3] = {in, (uint64_t)g.channels, (uint64_t)g.E}, s[2] = {in, in * g.channels};
         const uint32_t b[3] = {64, 32, 1};
