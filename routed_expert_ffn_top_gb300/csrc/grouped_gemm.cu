@@ -39,7 +39,7 @@ namespace moe {
 constexpr int kGgThreads = 384;
 constexpr int kGgTurn = 36;           // words of a row of 32 channels that is turned round
 constexpr int kGgTurnBytes = 16 * kGgTurn * 4;
-constexpr int kGgMaxStages = 4;
+constexpr int kGgMaxStages = 6;
 
 template <int kCtas_, int kRows_, int kK_, int kStages_>
 struct GgTile {
@@ -53,13 +53,14 @@ struct GgTile {
     static constexpr int kBBytes = kSide * kK * 2;
     static constexpr int kMajor = kK * 128;          // channel-major: a copy of 64 channels
     static constexpr int kAChunk = 128 * 128, kBChunk = kSide * 128;
+    static constexpr int kPiece = 32;                // rows of a small copy of the N side
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr uint32_t kTmemCols = 2 * kRows;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kGgTurnBytes + 1024;
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
     static_assert(kStageBytes % 1024 == 0 && kBChunk % 1024 == 0 && kStages <= kGgMaxStages, "stage alignment");
 };
-using GgLarge = GgTile<2, 256, 128, 3>;
+using GgLarge = GgTile<2, 256, 64, 6>;
 using GgSmall = GgTile<1, 32, 128, 4>;
 
 struct GgCtl {
@@ -73,12 +74,14 @@ struct GgCtl {
     volatile int abort;
     int32_t wsum[kGgThreads / 32];
     int32_t valid_rows;
-    int32_t first[kGroupedMaxExperts + 1];  // row tiles before expert e
+    alignas(16) int32_t first[kGroupedMaxExperts + 4];  // row tiles before expert e; weights: its rows
+    uint16_t order[kGroupedMaxExperts];     // rows of expert e's tiles; weights: experts, those of most rows first
     int32_t begin[kGroupedMaxExperts + 1];  // first row of expert e
 };
 
+// x, x2: the rows' boxes are a CTA's side, and of the small ones (xs, x2s) 32 rows.
 struct GgMaps {
-    CUtensorMap x, x2, w, w2, y;
+    CUtensorMap x, x2, xs, x2s, w, w2, y;
 };
 
 struct GgArgs {
@@ -106,12 +109,9 @@ __device__ __forceinline__ uint32_t gg_leader(uint64_t *bar) {
     if constexpr (kCtas == 1) return smem_u32(bar);
     else return map_shared_rank(bar, 0);
 }
-// (At the scope of the CTA: what the thread has read or written before is not what a waiter in the
-// other CTA reads.  With release at cluster scope every stage waited a memory barrier out, 0.75 us,
-// and products ran at half the rate.)
-__device__ __forceinline__ void gg_arrive_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
+// (At the scope of the CTA: what the thread has written before is not what a waiter in the other CTA
+// reads.  With release at cluster scope in the producers too, every stage waited a memory barrier
+// out, 0.75 us, and products ran at half the rate.)
 __device__ __forceinline__ void gg_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -119,61 +119,89 @@ __device__ __forceinline__ void gg_arrive(uint32_t bar) {
 __device__ __forceinline__ void gg_arrive_release(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-// kCluster: what the other CTA's thread wrote before its releasing arrival is visible after.
+// Waits take a barrier's shared-memory address.  kCluster: what the other CTA's thread wrote before
+// its releasing arrival is visible after.
 template <bool kCluster>
-__device__ __forceinline__ bool gg_try(uint64_t *bar, uint32_t parity) {
-    if constexpr (!kCluster) return mbar_try_wait(bar, parity);
+__device__ __forceinline__ bool gg_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if constexpr (kCluster)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
-// Bounded; the first tries are made without reading the timer.  A whole warp gets one answer.
-template <bool kCluster = false>
-__device__ __forceinline__ bool gg_wait(uint64_t *bar, uint32_t parity, GgCtl &ctl) {
-    bool ok = false;
-    for (int i = 0; i < 32 && !ok; ++i) ok = gg_try<kCluster>(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!(ok = gg_try<kCluster>(bar, parity)) && !ctl.abort)
-            if (globaltimer_ns() - t0 > kWaitLimitNs) ctl.abort = 1;
+// Bounded.  What follows the first tries is kept out of the loops that wait, whose instructions a
+// single thread fetches anew every time.
+template <bool kCluster>
+__device__ __noinline__ bool gg_wait_slow(uint32_t bar, uint32_t parity, GgCtl *ctl) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!gg_try<kCluster>(bar, parity)) {
+        if (ctl->abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            ctl->abort = 1;
+            return false;
+        }
     }
-    return __all_sync(0xffffffffu, ok);
+    return true;
+}
+template <bool kCluster = false>
+__device__ __forceinline__ bool gg_wait_one(uint32_t bar, uint32_t parity, GgCtl &ctl) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (gg_try<kCluster>(bar, parity)) return true;
+    return gg_wait_slow<kCluster>(bar, parity, &ctl);
+}
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool gg_wait(uint64_t *bar, uint32_t parity, GgCtl &ctl) {
+    return __all_sync(0xffffffffu, gg_wait_one(smem_u32(bar), parity, ctl));
+}
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool gg_elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 template <int kCtas>
-__device__ __forceinline__ void gg_load_2d(void *dst, const CUtensorMap *tm, int x, int y, uint32_t bar, uint64_t policy) {
+__device__ __forceinline__ void gg_load_2d(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar, uint64_t policy) {
     if constexpr (kCtas == 1)
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(policy)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
-            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(policy)
             : "memory");
 }
 template <int kCtas>
-__device__ __forceinline__ void gg_load_3d(void *dst, const CUtensorMap *tm, int x, int y, int z, uint32_t bar,
+__device__ __forceinline__ void gg_load_3d(uint32_t dst, const CUtensorMap *tm, int x, int y, int z, uint32_t bar,
                                            uint64_t policy) {
     if constexpr (kCtas == 1)
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
             : "memory");
     else
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
-            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
             : "memory");
 }
@@ -220,55 +248,67 @@ __device__ __forceinline__ void gg_tmem_dealloc(uint32_t tmem, uint32_t cols) {
 }
 
 // ------------------------------------------------------------------------------------ units
-// A pair's units: u = its number, + the number of pairs, ...; unit u is channel tile u % nct of row
-// tile u / nct (weights: of column tile (u / nct) % nnt of expert u / nct / nnt).  Each warp walks
-// them on its own, without dividing, and finds the next expert with its 32 lanes at once.
+// A pair's units.  Products: u = its number, + the number of pairs, ...; unit u is channel tile u % nct
+// of row tile u / nct.  Weights: unit u is channel tile u % nct, column tile (u / nct) % nnt of the
+// expert with the (u / nct / nnt)-th most rows, and the pairs take them there and back: what one
+// takes before another in one turn it takes after it in the next.  Each warp walks them on its own.
+// A unit begins with code that no warp has run for thousands of cycles, so it is short: divisions
+// are made once (products of K = 768 took 170 us with two a unit, of some 9000 cycles each).
 template <Grouped kMode, typename G>
 struct GgWalk {
     static constexpr bool kWeights = kMode == Grouped::kWeights;
-    int t, ct, e;
+    int t, ct, e;     // row tile (weights: the expert's rank), channel tile, expert
     int row0, nrows;  // this row tile's (weights: the expert's) first row and number of rows
     int n;            // the MMA's N
     int n0;           // weights: first column
+    int dt, dn, dct;  // a step, and the next one
+    int et, en, ect;
 
     __device__ __forceinline__ void place(const GgArgs &a, const GgCtl &ctl) {
         if constexpr (kWeights) {
-            e = t / a.nnt;
-            n0 = (t - e * a.nnt) * G::kRows;
+            e = ctl.order[t];
             row0 = ctl.begin[e];
-            const int left = ctl.begin[e + 1] - row0;
-            nrows = left < 0 ? 0 : left;
+            nrows = ctl.first[e];
             n = a.N - n0 < G::kRows ? a.N - n0 : G::kRows;
         } else {
             unsigned past;
-            do {
+            do {  // the next expert with the warp's 32 lanes at once
                 const int i = e + 1 + (threadIdx.x & 31);
                 past = __ballot_sync(0xffffffffu, i <= a.E && ctl.first[i] <= t);
                 e += __popc(past);
             } while (past == 0xffffffffu);
-            // equal tiles: at most kRows, since a group of T tiles has at most T kRows rows
-            const int tiles = ctl.first[e + 1] - ctl.first[e], at = t - ctl.first[e];
-            const int count = ctl.begin[e + 1] - ctl.begin[e];
-            const int q = ((count + tiles - 1) / tiles + G::kGran - 1) / G::kGran * G::kGran;
-            row0 = ctl.begin[e] + at * q;
-            nrows = count - at * q < q ? count - at * q : q;
+            const int q = ctl.order[e], at = (t - ctl.first[e]) * q;  // rows of a tile
+            row0 = ctl.begin[e] + at;
+            const int left = ctl.begin[e + 1] - row0;
+            nrows = left < q ? left : q;
             n = nrows;
         }
         n = (n + G::kGran - 1) / G::kGran * G::kGran;
     }
     __device__ __forceinline__ GgWalk(const GgArgs &a, const GgCtl &ctl, int tiles) {
-        const int u = blockIdx.x / G::kCtas;
-        t = u / a.nct, ct = u % a.nct, e = 0;
+        const int pair = blockIdx.x / G::kCtas;
+        t = pair / a.nct, ct = pair % a.nct, e = 0, n0 = 0;
+        if constexpr (kWeights) {
+            const int pairs = gridDim.x / G::kCtas;
+            auto split = [&](int u, int &r, int &c, int &d) { d = u % a.nct, c = u / a.nct % a.nnt, r = u / a.nct / a.nnt; };
+            split(2 * pairs - 1 - 2 * pair, dt, dn, dct);
+            split(2 * pair + 1, et, en, ect);
+            n0 = t % a.nnt * G::kRows, t /= a.nnt;
+        }
         if (t < tiles) place(a, ctl);
     }
     __device__ __forceinline__ void next(const GgArgs &a, const GgCtl &ctl, int tiles) {
-        t += a.dt, ct += a.dct;
-        if (ct >= a.nct) ct -= a.nct, ++t;
+        if constexpr (kWeights) {
+            ct += dct, n0 += dn * G::kRows, t += dt;
+            if (ct >= a.nct) ct -= a.nct, n0 += G::kRows;
+            if (n0 >= a.nnt * G::kRows) n0 -= a.nnt * G::kRows, ++t;
+            int s;
+            s = dt, dt = et, et = s, s = dn, dn = en, en = s, s = dct, dct = ect, ect = s;
+        } else {
+            t += a.dt, ct += a.dct;
+            if (ct >= a.nct) ct -= a.nct, ++t;
+        }
         if (t < tiles) place(a, ctl);
-    }
-    // Stages of a unit, and K steps of its stage s.
-    __device__ __forceinline__ int stages(const GgArgs &a) const {
-        return kWeights ? (nrows + G::kK - 1) / G::kK : a.parts * ((a.K + G::kK - 1) / G::kK);
     }
     // Weights: the last step's rows past the group's end are zeroed before the MMA reads them.
     __device__ __forceinline__ bool ragged() const { return kWeights && nrows % 16 != 0; }
@@ -409,29 +449,41 @@ __device__ __forceinline__ void gg_gated(const GgArgs &a, float *turn, float *ot
     }
 }
 
+// A lane's part of the checkpoint: sixteen codes and the scale byte of g and of u.
+struct GgCodes {
+    uint4 g, u;
+    uint32_t gs, us;
+};
+__device__ __forceinline__ GgCodes gg_codes(const GgArgs &a, int64_t row, int ch, bool live) {
+    GgCodes c{};
+    if (live) {
+        const uint8_t *p = a.codes + row * (2 * a.C) + ch, *q = a.scales + row * a.pitch;
+        c.g = *reinterpret_cast<const uint4 *>(p), c.u = *reinterpret_cast<const uint4 *>(p + a.C);
+        c.gs = q[ch / 32], c.us = q[(a.C + ch) / 32];
+    }
+    return c;
+}
+
+// The checkpoint is read two steps of 16 rows ahead, the first before the unit's sums are complete:
+// read where they are used, the codes' way from memory took 3250 cycles a step.
 template <bool kInt8>
 __device__ __forceinline__ void gg_gated_grad(const GgArgs &a, float *turn, uint32_t d, int lane, int row0, int nrows,
-                                              int ch0) {
+                                              int ch0, GgCodes (&next)[2]) {
     const int r = lane & 15, h = lane >> 4, ch = ch0 + 16 * h, I = a.C;
-#pragma unroll 1
+#pragma unroll 2
     for (int c = 0; c < nrows; c += 16) {
         const bool live = c + r < nrows;
         const int64_t row = (int64_t)row0 + c + r;
-        uint4 gc{0, 0, 0, 0}, uc{0, 0, 0, 0};
-        uint32_t gs = 0, us = 0;
-        if (live) {
-            gc = *reinterpret_cast<const uint4 *>(a.codes + row * (2 * I) + ch);
-            uc = *reinterpret_cast<const uint4 *>(a.codes + row * (2 * I) + I + ch);
-            gs = a.scales[row * a.pitch + ch / 32];
-            us = a.scales[row * a.pitch + (I + ch) / 32];
-        }
+        const GgCodes now = next[0];
+        next[0] = next[1];
+        next[1] = gg_codes(a, row + 32, ch, c + 32 + r < nrows);
         float q[16], g[16], u[16];
         tmem_ld16(d + c, q);
         gg_turn_write(turn, lane, q);
         __syncwarp();
         gg_turn_read(turn, r, 16 * h, q);
-        eight_values<kInt8>(gc, gs, g);
-        eight_values<kInt8>(uc, us, u);
+        eight_values<kInt8>(now.g, now.gs, g);
+        eight_values<kInt8>(now.u, now.us, u);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float s = gg_sigmoid(g[i]), gsi = g[i] * s, t = q[i] * u[i];
@@ -504,6 +556,102 @@ __device__ __forceinline__ void gg_zero(unsigned char *p, int64_t bytes, bool wi
         for (int64_t i = 2 * (int64_t)(threadIdx.x & 127); i < bytes; i += 2 * 128) *reinterpret_cast<uint16_t *>(p + i) = 0;
 }
 
+// -------------------------------------------------------------------------------- producers
+// A warp that copies one side's operand (kSideM: the M side's); one lane does, its registers hold the
+// ring's state.  What a stage takes between its memory's release and its copies is kept short: with
+// the coordinates and addresses worked out there it took 400 cycles, in every turn of the ring.
+template <Grouped kMode, bool kTrans, typename G, bool kSideM>
+__device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, GgCtl &ctl, uint32_t base, int rank, int tiles) {
+    constexpr bool kWeights = kMode == Grouped::kWeights, kGated = kMode == Grouped::kGated;
+    constexpr int kCtas = G::kCtas;
+    constexpr bool kByK = kSideM ? kTrans : !kWeights;  // copies of 64 of K, else of 64 channels
+    constexpr int kChunk = !kByK ? G::kMajor : kSideM ? G::kAChunk : G::kBChunk;
+    // Copies of a whole stage in CTA r of the pair; those that bring nothing which the MMAs read, or
+    // whose results are stored, are left out.
+    auto wide = [&](const GgWalk<kMode, G> &x, int r) {
+        const int part = kSideM ? 128 : x.n / kCtas;
+        const int left = (kSideM ? a.C - (x.ct * kCtas) * (kGated ? 64 : 128) : kWeights ? a.N - x.n0 : x.nrows) -
+                         r * (kSideM && kGated ? 64 : part);
+        return left <= 0 ? 0 : kByK ? G::kChunks : (kSideM && kGated) || (part > 64 && left > 64) ? 2 : 1;
+    };
+    // weights that one row tile reads leave L2 first
+    const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
+    const uint32_t full0 = gg_leader<kCtas>(&ctl.full[0]), own0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
+    uint32_t dst = base, slot = 0, parity = 1, it = 0;  // slot: 8 x stage
+    bool ok = true;
+    for (GgWalk<kMode, G> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
+        if (gg_elect()) {
+            const uint64_t pol = !kWeights && kSideM && ctl.first[x.e + 1] - ctl.first[x.e] == 1 ? once : keep;
+            int n = wide(x, rank), both = kCtas == 1 ? n : wide(x, 0) + wide(x, 1), chunk = kChunk, dx = 128, dy = 0;
+            const int part_n = x.n / kCtas;
+            if (kByK && !kSideM && part_n <= G::kSide - G::kPiece) {
+                // as many copies of 32 rows as the side has, where that is fewer bytes than its whole box
+                static_assert(G::kChunks == 1 || G::kSide == G::kPiece, "one chunk of K a stage");
+                const int pieces = (part_n + G::kPiece - 1) / G::kPiece;
+                n = n ? pieces : 0, both = both * pieces, chunk = G::kPiece * 128, dx = 0, dy = G::kPiece;
+            }
+            const bool small_box = dy != 0;
+            const uint32_t tx = (uint32_t)(both * chunk);
+            // coordinates: bytes along the operand's rows, the row (of K, or a row of x or w), the expert
+            const int fixed = kSideM ? (x.ct * kCtas + rank) * (kGated ? 64 : 128)
+                                     : (kWeights ? x.n0 : x.row0) + rank * part_n;
+            const int parts = kWeights ? 1 : a.parts, length = kWeights ? x.nrows : a.K;
+            const bool ragged = x.ragged();
+            for (int part = 0; part < parts && ok; ++part) {
+                const CUtensorMap *const m = kSideM ? (kWeights ? &tm.x : part ? &tm.w2 : &tm.w)
+                                             : kWeights  ? &tm.w
+                                             : small_box ? (part ? &tm.x2s : &tm.xs)
+                                                         : (part ? &tm.x2 : &tm.x);
+                int cx = kByK ? 0 : 2 * fixed, cy = kByK ? fixed : kWeights ? x.row0 : 0;
+                for (int left = length; left > 0; left -= G::kK, ++it) {
+                    uint32_t bar = full0 + slot, bytes = tx;
+                    int copies = n;
+                    if (kByK && G::kChunks > 1 && left <= 64)
+                        copies = n > 0, bytes = (uint32_t)((both > G::kChunks ? 2 : both > 0) * chunk);
+                    if (!(ok = gg_wait_one(empty0 + slot, parity, ctl))) break;
+                    // the pair's first CTA expects both CTAs' bytes; a stage whose last rows are to be
+                    // zeroed first is each CTA's own
+                    if (kWeights && ragged && left <= G::kK) {
+                        uint64_t *const land = &ctl.land[slot / 8];
+                        bar = smem_u32(land);
+                        mbar_arrive_expect_tx(land, (uint32_t)(n * chunk));
+                    } else if (rank == 0) {
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(own0 + slot), "r"(bytes)
+                                     : "memory");
+                    }
+                    if constexpr (kSideM && kGated) {
+                        if (copies) {
+                            gg_load_3d<kCtas>(dst, m, cx, cy, x.e, bar, pol);
+                            gg_load_3d<kCtas>(dst + kChunk, &tm.w2, cx, cy, x.e, bar, pol);
+                        }
+                    } else {
+                        int px = cx, py = cy;
+                        uint32_t pd = dst;
+#pragma unroll 1
+                        for (int i = 0; i < copies; ++i, px += dx, py += dy, pd += chunk) {
+                            if constexpr (kSideM && !kWeights) gg_load_3d<kCtas>(pd, m, px, py, x.e, bar, pol);
+                            else gg_load_2d<kCtas>(pd, m, px, py, bar, pol);
+                        }
+                    }
+                    if (kByK) cx += 2 * G::kK;
+                    else cy += G::kK;
+                    slot += 8, dst += G::kStageBytes;
+                    if (slot == 8 * G::kStages) slot = 0, dst = base, parity ^= 1u;
+                }
+            }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+    }
+    // every copy has landed before the CTA can exit (after a wait that gave up; else the MMAs have read
+    // them all)
+    if (rank == 0 && gg_elect())
+        for (uint32_t i = 0; i < G::kStages && i < it; ++i) {
+            const uint32_t at = it - 1 - i;
+            if (!mbar_wait_bounded(&ctl.full[at % G::kStages], (at / G::kStages) & 1u)) ctl.abort = 1;
+        }
+    __syncwarp();
+}
+
 // ----------------------------------------------------------------------------------- kernel
 // kTrans: the M side's operand is K-major (weights [channels][K]), else channel-major.
 template <Grouped kMode, bool kTrans, typename G>
@@ -521,7 +669,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::kStages; ++s) {
-            mbar_init(&ctl.full[s], 2 * kCtas);  // two producers a CTA
+            mbar_init(&ctl.full[s], 2);  // the first CTA's producers, or the zeroing warps
             mbar_init(&ctl.empty[s], 1);
             mbar_init(&ctl.land[s], 2);
         }
@@ -568,8 +716,11 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             chunk += t;
         }
         if (e < a.E) {
-            ctl.first[e] = off + inc - tiles;
+            ctl.first[e] = kWeights ? (int)(hi - lo) : off + inc - tiles;
             ctl.begin[e] = (int)lo;
+            // equal tiles: at most kRows, since a group of T tiles has at most T kRows rows
+            if (!kWeights && tiles)
+                ctl.order[e] = (uint16_t)(((int)(hi - lo) + G::kGran * tiles - 1) / (G::kGran * tiles) * G::kGran);
             if (e == a.E - 1) {
                 ctl.first[a.E] = off + inc;
                 ctl.valid_rows = ctl.begin[a.E] = (int)hi;
@@ -578,82 +729,31 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         carry += chunk;
         __syncthreads();
     }
+    if constexpr (kWeights) {
+        // experts of many rows first, so that the pairs' last units are short
+        for (int e = threadIdx.x; e < a.E; e += kGgThreads) {
+            const int mine = ctl.first[e];
+            int rank = 0;
+            for (int i = 0; i < a.E; i += 4) {
+                const int4 q = *reinterpret_cast<const int4 *>(&ctl.first[i]);
+                rank += (q.x > mine || (q.x == mine && i < e)) +
+                        (i + 1 < a.E && (q.y > mine || (q.y == mine && i + 1 < e))) +
+                        (i + 2 < a.E && (q.z > mine || (q.z == mine && i + 2 < e))) +
+                        (i + 3 < a.E && (q.w > mine || (q.w == mine && i + 3 < e)));
+            }
+            ctl.order[rank] = (uint16_t)e;
+        }
+    }
     tc_fence_before();
     if constexpr (kCtas == 1) __syncthreads();
     else cluster_sync();
     tc_fence_after();
-    const int tiles = kWeights ? a.E * a.nnt : carry;
-    const int nks = (a.K + G::kK - 1) / G::kK;  // stages of a part
+    const int tiles = kWeights ? a.E : carry;
     using Walk = GgWalk<kMode, G>;
 
     if (warp == 8 || warp == 9) {
-        // producers: 8 the M side's operand, 9 the N side's.  Weights that one row tile reads leave
-        // L2 first.
-        const bool side_m = warp == 8;
-        const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
-        unsigned char *const base = stages + (side_m ? 0 : G::kABytes);
-        const bool major = side_m ? !kTrans : kWeights;  // channel-major
-        const int chunk = major ? G::kMajor : (side_m ? G::kAChunk : G::kBChunk);
-        int stage = 0;
-        uint32_t phase = 0, issued = 0, par = 0;
-        bool ok = true;
-        for (Walk x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
-            const int ns = x.stages(a);
-            const uint64_t pol = !kWeights && side_m && ctl.first[x.e + 1] - ctl.first[x.e] == 1 ? once : keep;
-            // this CTA's first channel, and its first row (weights: column) of the N side
-            const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128);
-            const int side = (kWeights ? x.n0 : x.row0) + rank * (x.n / kCtas);
-            const int side_end = kWeights ? a.N : x.row0 + x.nrows;
-            for (int s = 0; s < ns; ++s) {
-                if (!(ok = gg_wait(&ctl.empty[stage], phase ^ 1u, ctl))) break;
-                if (lane == 0) {
-                    const bool second = !kWeights && s >= nks;
-                    const int k0 = kWeights ? x.row0 + s * G::kK : (second ? s - nks : s) * G::kK;
-                    const int deep = (a.K - k0 + 63) / 64 < G::kChunks ? (a.K - k0 + 63) / 64 : G::kChunks;
-                    // copies that bring something the MMAs read, or whose results are stored
-                    int n;
-                    if (side_m) {
-                        n = kGated ? (c0 < a.C ? 2 : 0)
-                            : kTrans ? (c0 < a.C ? deep : 0)
-                                     : (a.C - c0 > 64 ? 2 : (a.C > c0 ? 1 : 0));
-                    } else if (kWeights) {
-                        const int cols = side_end - side < x.n / kCtas ? side_end - side : x.n / kCtas;
-                        n = cols > 64 ? 2 : (cols > 0 ? 1 : 0);
-                    } else {
-                        n = side < side_end ? deep : 0;
-                    }
-                    const bool local = kWeights && s == ns - 1 && x.ragged();
-                    const uint32_t bar = local ? smem_u32(&ctl.land[stage]) : gg_leader<kCtas>(&ctl.full[stage]);
-                    gg_arrive_tx(bar, (uint32_t)(n * chunk));
-                    unsigned char *dst = base + stage * G::kStageBytes;
-                    for (int j = 0; j < n; ++j, dst += chunk) {
-                        if (kWeights) {
-                            if (side_m) gg_load_2d<kCtas>(dst, &tm.x, (c0 + 64 * j) * 2, k0, bar, pol);
-                            else gg_load_2d<kCtas>(dst, &tm.w, (side + 64 * j) * 2, k0, bar, pol);
-                        } else if (!side_m) {
-                            gg_load_2d<kCtas>(dst, second ? &tm.x2 : &tm.x, (k0 + 64 * j) * 2, side, bar, pol);
-                        } else if (kGated) {
-                            gg_load_3d<kCtas>(dst, j ? &tm.w2 : &tm.w, c0 * 2, k0, x.e, bar, pol);
-                        } else if (kTrans) {
-                            gg_load_3d<kCtas>(dst, second ? &tm.w2 : &tm.w, (k0 + 64 * j) * 2, c0, x.e, bar, pol);
-                        } else {
-                            gg_load_3d<kCtas>(dst, second ? &tm.w2 : &tm.w, (c0 + 64 * j) * 2, k0, x.e, bar, pol);
-                        }
-                    }
-                }
-                __syncwarp();
-                issued |= 1u << stage;
-                par = (par & ~(1u << stage)) | (phase << stage);
-                if (++stage == G::kStages) stage = 0, phase ^= 1u;
-            }
-        }
-        // every copy has landed before the CTA can exit (after a wait that gave up; else the MMAs have
-        // read them all)
-        if (rank == 0)
-            for (int s = 0; s < G::kStages; ++s)
-                if ((issued >> s) & 1u)
-                    if (!mbar_wait_bounded(&ctl.full[s], (par >> s) & 1u)) ctl.abort = 1;
-        __syncwarp();
+        if (warp == 8) gg_produce<kMode, kTrans, G, true>(tm, a, ctl, smem_u32(stages), rank, tiles);
+        else gg_produce<kMode, kTrans, G, false>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank, tiles);
     } else if (warp == 10) {
         if (rank == 0) {
             // 128-byte swizzle, 8-row atoms 1 KB apart.  K-major: a K step of 16 is 32 bytes, a chunk
@@ -662,45 +762,49 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             constexpr bool kAMajor = !kTrans, kBMajor = kWeights;  // channel-major operands
             const uint64_t a0 = umma_smem_desc(smem_u32(stages), kAMajor ? G::kMajor : 16, 1024, 2);
             const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, kBMajor ? G::kMajor : 16, 1024, 2);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, tphase = 1;
+            const uint32_t full0 = smem_u32(&ctl.full[0]);
+            uint32_t stage = 0, parity = 0, unit = 0;
             bool ok = true;
             for (Walk x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
-                const int ns = x.stages(a);
-                if (kWeights && ns == 0) continue;
-                if (!(ok = gg_wait(&ctl.tempty[buf], tphase, ctl))) break;
-                tc_fence_after();
-                const uint32_t d = ctl.tmem + (uint32_t)(buf * G::kRows), idesc = a.idesc | (uint32_t)(x.n >> 3) << 17;
-                for (int s = 0; s < ns; ++s) {
-                    if (!(ok = gg_wait<kWeights>(&ctl.full[stage], phase, ctl))) break;
+                const int length = kWeights ? x.nrows : a.K;
+                if (kWeights && length == 0) continue;
+                const uint32_t buf = unit & 1u, tparity = ((unit >> 1) & 1u) ^ 1u;
+                ++unit;
+                if (gg_elect()) {
+                    const uint32_t d = ctl.tmem + buf * G::kRows, idesc = a.idesc | (uint32_t)(x.n >> 3) << 17;
+                    const int parts = kWeights ? 1 : a.parts;
+                    bool first = true;
+                    ok = gg_wait_one(smem_u32(&ctl.tempty[buf]), tparity, ctl);
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t ad = a0 + (uint32_t)(stage * (G::kStageBytes >> 4));
-                        const uint64_t bd = b0 + (uint32_t)(stage * (G::kStageBytes >> 4));
-                        const int left = kWeights ? x.nrows - s * G::kK : a.K - (s < nks ? s : s - nks) * G::kK;
-                        const int steps = left >= G::kK ? G::kK / 16 : (left + 15) / 16;
-                        auto step = [&](int ks) {
-                            gg_mma<kCtas>(d, ad + (kAMajor ? ks * 128 : (ks >> 2) * (G::kAChunk >> 4) + (ks & 3) * 2),
-                                          bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
-                                          s > 0 || ks > 0);
-                        };
-                        if (steps == G::kK / 16) {
+                    for (int part = 0; part < parts && ok; ++part)
+                        for (int left = length; left > 0; left -= G::kK) {
+                            const uint64_t ad = a0 + stage * (G::kStageBytes >> 4);
+                            const uint64_t bd = b0 + stage * (G::kStageBytes >> 4);
+                            auto step = [&](int ks, bool accumulate) {
+                                gg_mma<kCtas>(d, ad + (kAMajor ? ks * 128 : (ks >> 2) * (G::kAChunk >> 4) + (ks & 3) * 2),
+                                              bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
+                                              accumulate);
+                            };
+                            if (!(ok = gg_wait_one<kWeights && kCtas == 2>(full0 + 8 * stage, parity, ctl))) break;
+                            tc_fence_after();
+                            step(0, !first);
+                            first = false;
+                            if (left >= G::kK) {
 #pragma unroll
-                            for (int ks = 0; ks < G::kK / 16; ++ks) step(ks);
-                        } else {
-                            for (int ks = 0; ks < steps; ++ks) step(ks);
+                                for (int ks = 1; ks < G::kK / 16; ++ks) step(ks, true);
+                            } else {
+#pragma unroll 1
+                                for (int ks = 1; ks * 16 < left; ++ks) step(ks, true);
+                            }
+                            gg_commit<kCtas>(&ctl.empty[stage]);
+                            if (++stage == G::kStages) stage = 0, parity ^= 1u;
                         }
-                        gg_commit<kCtas>(&ctl.empty[stage]);
-                        if (s == ns - 1) gg_commit<kCtas>(&ctl.tfull[buf]);
-                    }
-                    __syncwarp();
-                    if (++stage == G::kStages) stage = 0, phase ^= 1u;
+                    if (ok) gg_commit<kCtas>(&ctl.tfull[buf]);
                 }
-                if (buf) tphase ^= 1u;
-                buf ^= 1;
+                ok = __all_sync(0xffffffffu, ok);
             }
             // every issued MMA has completed before the CTAs free their tensor memory
-            if (lane == 0) {
+            if (gg_elect()) {
                 if constexpr (kCtas == 1) umma_commit(&ctl.done);
                 else
                     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -717,7 +821,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             int total = 0;
             uint32_t phase = 0;
             for (Walk x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles)) {
-                total += x.stages(a);
+                total += (x.nrows + G::kK - 1) / G::kK;
                 if (!x.ragged()) continue;
                 const int stage = (total - 1) % G::kStages;
                 if (!gg_wait(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
@@ -730,7 +834,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) gg_arrive_release(gg_leader<kCtas>(&ctl.full[stage]), 2);
+                if (lane == 0) gg_arrive_release(gg_leader<kCtas>(&ctl.full[stage]), 2 / kCtas);
             }
         }
     } else {
@@ -749,6 +853,13 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             const uint32_t parity = (uint32_t)(local >> 1) & 1u;
             ++local;
             if (buf != group) continue;
+            GgCodes ahead[2];
+            if constexpr (kMode == Grouped::kGatedGrad)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 16 * i + (lane & 15);
+                    ahead[i] = gg_codes(a, (int64_t)x.row0 + r, c0 + 16 * (lane >> 4), c0 < a.C && r < x.nrows);
+                }
             bool ok = gg_wait(&ctl.tfull[buf], parity, ctl);
             if constexpr (kGated) ok = !named_bar_or(bar, 64, !ok);  // both go on or neither
             if (!ok) break;
@@ -765,8 +876,8 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     for (int r = lane; r < x.nrows; r += 32)
                         for (int b = a.C / 16; b < a.pitch; ++b) a.scales[((int64_t)x.row0 + r) * a.pitch + b] = 0;
             } else if constexpr (kMode == Grouped::kGatedGrad) {
-                if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, turn, d, lane, x.row0, x.nrows, c0);
-                else gg_gated_grad<false>(a, turn, d, lane, x.row0, x.nrows, c0);
+                if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, turn, d, lane, x.row0, x.nrows, c0, ahead);
+                else gg_gated_grad<false>(a, turn, d, lane, x.row0, x.nrows, c0, ahead);
             } else {
                 gg_weights(a, tm.y, turns + warp * 2048, d, lane, x.e, c0, x.n0, x.n, false);
             }
@@ -876,7 +987,9 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
     } else {
         rows_map(&tm.x, g.x, g.K, g.ldx, side);
         weights_map(&tm.w, g.w);
+        if (!small) rows_map(&tm.xs, g.x, g.K, g.ldx, GgLarge::kPiece);
         if (g.parts == 2) rows_map(&tm.x2, g.x2, g.K, g.ldx, side);
+        if (g.parts == 2 && !small) rows_map(&tm.x2s, g.x2, g.K, g.ldx, GgLarge::kPiece);
         if (g.w2) weights_map(&tm.w2, g.w2);
     }
     if (!ok) return cudaErrorInvalidValue;
