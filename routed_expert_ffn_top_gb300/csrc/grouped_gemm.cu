@@ -22,9 +22,10 @@
 // rows, each CTA holding half of the rows' operand: 64 KB of shared memory a stage of 128 of K.
 // Small tile, for few rows a group: one CTA, 128 channels, up to 32 rows.
 //
-// Per CTA (persistent, one an SM) 12 warps: 0-3 and 4-7 drain the two accumulators in turn, 8 and 9
+// Per CTA (persistent, one an SM) 13 warps: 0-3 and 4-7 drain every other 16 rows (weights: 32
+// columns) of an accumulator, 8 and 9
 // issue the copies of the M and N sides, 10 the MMAs (the pair's first CTA for both), 11 zeroes
-// the last rows of a weights' gradient.  The accumulators are double-buffered.  An epilogue warp
+// the last rows of a weights' gradient, 12 works out the units.  The accumulators are double-buffered.  An epilogue warp
 // has 32 channels in its lanes; it turns 16 rows of them round through shared memory, so that
 // a lane then has 16 channels of one row: whole 32-byte sectors, and half of an 8-bit block.
 #include <string.h>
@@ -36,10 +37,10 @@
 
 namespace moe {
 
-constexpr int kGgThreads = 384;
-constexpr int kGgTurn = 36;           // words of a row of 32 channels that is turned round
-constexpr int kGgTurnBytes = 16 * kGgTurn * 4;
+constexpr int kGgThreads = 416;
+constexpr int kGgTurnBytes = 16 * 32 * 4;  // 16 rows of 32 channels that are turned round
 constexpr int kGgMaxStages = 6;
+constexpr int kGgUnits = 8;            // units that are worked out ahead
 
 template <int kCtas_, int kRows_, int kK_, int kStages_>
 struct GgTile {
@@ -63,7 +64,22 @@ struct GgTile {
 using GgLarge = GgTile<2, 256, 64, 6>;
 using GgSmall = GgTile<1, 32, 128, 4>;
 
+// A unit, as every role reads it.
+struct alignas(16) GgUnit {
+    int32_t row0, nrows;  // the row tile's (weights: the expert's) first row and number of rows; < 0: none is left
+    int32_t n;            // the MMA's N
+    int32_t n0;           // weights: first column
+    int32_t e, ct;        // expert, channel tile
+    int32_t single;       // the expert has no other row tile
+    int32_t unused;
+    // weights: the last step's rows past the group's end are zeroed before the MMA reads them
+    __device__ __forceinline__ bool ragged() const { return nrows % 16 != 0; }
+};
+
 struct GgCtl {
+    GgUnit units[kGgUnits];
+    uint64_t ufull[kGgUnits];
+    uint64_t uempty[kGgUnits];     // all roles have read the unit
     uint64_t full[kGgMaxStages];   // the pair's first CTA: both CTAs' copies of a stage
     uint64_t empty[kGgMaxStages];
     uint64_t land[kGgMaxStages];   // weights: copies of a stage whose last rows are to be zeroed
@@ -81,7 +97,7 @@ struct GgCtl {
 
 // x, x2: the rows' boxes are a CTA's side, and of the small ones (xs, x2s) 32 rows.
 struct GgMaps {
-    CUtensorMap x, x2, xs, x2s, w, w2, y;
+    CUtensorMap x, x2, xs, x2s, w, w2, y, p;
 };
 
 struct GgArgs {
@@ -92,6 +108,7 @@ struct GgArgs {
     int dt, dct;      // a step of a CTA pair's units in row tiles and channel tiles
     uint32_t idesc;   // without N
     int half, out32;  // f16 (else bf16) results; fp32 ones
+    int bulk;         // kPlain: y allows tensor stores
     int vec;          // rows of out allow stores of 32, 16 bytes or elements: 2, 1, 0
     unsigned char *out;
     int64_t ldo;
@@ -248,71 +265,68 @@ __device__ __forceinline__ void gg_tmem_dealloc(uint32_t tmem, uint32_t cols) {
 }
 
 // ------------------------------------------------------------------------------------ units
+// One warp works the units out and puts them into a ring that the other roles read: where each role
+// worked them out itself, the code that a unit begins with, which no warp had run for thousands of
+// cycles, kept the MMAs from their next unit for 1450 cycles.
+//
 // A pair's units.  Products: u = its number, + the number of pairs, ...; unit u is channel tile u % nct
 // of row tile u / nct.  Weights: unit u is channel tile u % nct, column tile (u / nct) % nnt of the
 // expert with the (u / nct / nnt)-th most rows, and the pairs take them there and back: what one
-// takes before another in one turn it takes after it in the next.  Each warp walks them on its own.
-// A unit begins with code that no warp has run for thousands of cycles, so it is short: divisions
-// are made once (products of K = 768 took 170 us with two a unit, of some 9000 cycles each).
+// takes before another in one turn it takes after it in the next.
 template <Grouped kMode, typename G>
-struct GgWalk {
-    static constexpr bool kWeights = kMode == Grouped::kWeights;
-    int t, ct, e;     // row tile (weights: the expert's rank), channel tile, expert
-    int row0, nrows;  // this row tile's (weights: the expert's) first row and number of rows
-    int n;            // the MMA's N
-    int n0;           // weights: first column
-    int dt, dn, dct;  // a step, and the next one
-    int et, en, ect;
-
-    __device__ __forceinline__ void place(const GgArgs &a, const GgCtl &ctl) {
-        if constexpr (kWeights) {
-            e = ctl.order[t];
-            row0 = ctl.begin[e];
-            nrows = ctl.first[e];
-            n = a.N - n0 < G::kRows ? a.N - n0 : G::kRows;
-        } else {
+__device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int tiles) {
+    constexpr bool kWeights = kMode == Grouped::kWeights;
+    const int lane = threadIdx.x & 31, pair = blockIdx.x / G::kCtas, pairs = gridDim.x / G::kCtas;
+    int t = pair / a.nct, ct = pair % a.nct, e = 0;
+    for (uint32_t turn = 0;; ++turn) {
+        GgUnit x;
+        x.nrows = -1, x.row0 = x.n = x.n0 = x.e = x.ct = x.single = x.unused = 0;
+        if (kWeights) {
+            const int64_t u = (int64_t)turn * pairs + ((turn & 1) ? pairs - 1 - pair : pair);
+            if (u < (int64_t)a.E * a.nnt * a.nct) {
+                const int c = (int)u / a.nct, at = c / a.nnt;
+                x.e = ctl.order[at], x.ct = (int)u - c * a.nct, x.n0 = (c - at * a.nnt) * G::kRows;
+                x.row0 = ctl.begin[x.e], x.nrows = ctl.first[x.e];
+                x.n = a.N - x.n0 < G::kRows ? a.N - x.n0 : G::kRows;
+            }
+        } else if (t < tiles) {
             unsigned past;
             do {  // the next expert with the warp's 32 lanes at once
-                const int i = e + 1 + (threadIdx.x & 31);
+                const int i = e + 1 + lane;
                 past = __ballot_sync(0xffffffffu, i <= a.E && ctl.first[i] <= t);
                 e += __popc(past);
             } while (past == 0xffffffffu);
             const int q = ctl.order[e], at = (t - ctl.first[e]) * q;  // rows of a tile
-            row0 = ctl.begin[e] + at;
-            const int left = ctl.begin[e + 1] - row0;
-            nrows = left < q ? left : q;
-            n = nrows;
-        }
-        n = (n + G::kGran - 1) / G::kGran * G::kGran;
-    }
-    __device__ __forceinline__ GgWalk(const GgArgs &a, const GgCtl &ctl, int tiles) {
-        const int pair = blockIdx.x / G::kCtas;
-        t = pair / a.nct, ct = pair % a.nct, e = 0, n0 = 0;
-        if constexpr (kWeights) {
-            const int pairs = gridDim.x / G::kCtas;
-            auto split = [&](int u, int &r, int &c, int &d) { d = u % a.nct, c = u / a.nct % a.nnt, r = u / a.nct / a.nnt; };
-            split(2 * pairs - 1 - 2 * pair, dt, dn, dct);
-            split(2 * pair + 1, et, en, ect);
-            n0 = t % a.nnt * G::kRows, t /= a.nnt;
-        }
-        if (t < tiles) place(a, ctl);
-    }
-    __device__ __forceinline__ void next(const GgArgs &a, const GgCtl &ctl, int tiles) {
-        if constexpr (kWeights) {
-            ct += dct, n0 += dn * G::kRows, t += dt;
-            if (ct >= a.nct) ct -= a.nct, n0 += G::kRows;
-            if (n0 >= a.nnt * G::kRows) n0 -= a.nnt * G::kRows, ++t;
-            int s;
-            s = dt, dt = et, et = s, s = dn, dn = en, en = s, s = dct, dct = ect, ect = s;
-        } else {
+            x.row0 = ctl.begin[e] + at;
+            const int left = ctl.begin[e + 1] - x.row0;
+            x.n = x.nrows = left < q ? left : q;
+            x.e = e, x.ct = ct, x.single = ctl.first[e + 1] - ctl.first[e] == 1;
             t += a.dt, ct += a.dct;
             if (ct >= a.nct) ct -= a.nct, ++t;
         }
-        if (t < tiles) place(a, ctl);
+        x.n = (x.n + G::kGran - 1) / G::kGran * G::kGran;
+        const uint32_t slot = turn % kGgUnits;
+        if (!gg_wait(&ctl.uempty[slot], ((turn / kGgUnits) & 1u) ^ 1u, ctl)) return;
+        if (lane == 0) {
+            ctl.units[slot] = x;
+            mbar_arrive(&ctl.ufull[slot]);
+        }
+        __syncwarp();
+        if (x.nrows < 0) return;
     }
-    // Weights: the last step's rows past the group's end are zeroed before the MMA reads them.
-    __device__ __forceinline__ bool ragged() const { return kWeights && nrows % 16 != 0; }
-};
+}
+
+// The next unit, for a whole warp or for one thread; false when none is left or a wait gave up.
+template <bool kWarp>
+__device__ __forceinline__ bool gg_next(GgCtl &ctl, uint32_t &at, GgUnit &x) {
+    const uint32_t slot = at % kGgUnits, parity = (at / kGgUnits) & 1u;
+    ++at;
+    if (!(kWarp ? gg_wait(&ctl.ufull[slot], parity, ctl) : gg_wait_one(smem_u32(&ctl.ufull[slot]), parity, ctl))) return false;
+    x = ctl.units[slot];
+    if (kWarp) __syncwarp();
+    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ctl.uempty[slot]);
+    return x.nrows >= 0;
+}
 
 // -------------------------------------------------------------------------------- epilogues
 __device__ __forceinline__ uint32_t gg_pack(float lo, float hi, int half) {
@@ -358,28 +372,86 @@ __device__ __forceinline__ float gg_sigmoid(float g) {
     return r;
 }
 
-// Lane's channel of 16 rows in, lane's 16 channels (16 (lane / 16) on) of row lane % 16 out.
+// Lane's channel of 16 rows in, channels of a row out.  Rows are 128 bytes, their 16-byte pieces
+// exchanged as a tensor store's 128-byte swizzle has them: no bank conflicts either way.
 __device__ __forceinline__ void gg_turn_write(float *turn, int lane, const float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) turn[i * kGgTurn + lane] = v[i];
+    for (int i = 0; i < 16; ++i) turn[i * 32 + (lane ^ (4 * (i & 7)))] = v[i];
 }
 template <int kN>
 __device__ __forceinline__ void gg_turn_read(const float *turn, int row, int at, float (&v)[kN]) {
 #pragma unroll
     for (int i = 0; i < kN; i += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(turn + row * kGgTurn + at + i);
+        const float4 f = *reinterpret_cast<const float4 *>(turn + row * 32 + ((((at + i) >> 2) ^ (row & 7)) << 2));
         v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
     }
 }
 
+// 16 rows of 64 bytes (128 bytes of fp32) by a tensor store through a warp's staging memory, whose
+// 16-byte pieces are exchanged as the map's swizzle has them.  (Lanes' own stores of 32 bytes a row
+// took 7000 cycles a unit of 256 rows, more than the MMAs of K = 768.)  x: bytes along the row.
+__device__ __forceinline__ void gg_store(const CUtensorMap &tm, const void *staging, int x, int row, int lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+            "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&tm)),
+            "r"(x), "r"(row), "r"(smem_u32(staging))
+            : "memory");
+}
+// All but the last kLeft of this thread's stores have read their staging memory.
+template <int kLeft>
+__device__ __forceinline__ void gg_store_wait(int lane) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+    __syncwarp();
+}
+// Sixteen 16-bit results of row lane % 16, from channel 16 (lane / 16), to staging.
+__device__ __forceinline__ void gg_stage16(unsigned char *staging, int lane, const float (&v)[16], int half) {
+    const int r = lane & 15, h = lane >> 4;
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = gg_pack(v[2 * i], v[2 * i + 1], half);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint4 *>(staging + r * 64 + (((2 * h + i) ^ ((r >> 1) & 3)) << 4)) =
+            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+}
+
 template <typename G>
-__device__ __forceinline__ void gg_plain(const GgArgs &a, float *turn, uint32_t d, int lane, int row0, int nrows, int ch0) {
+__device__ __forceinline__ void gg_plain(const GgArgs &a, const CUtensorMap &tm, float *turn, uint32_t d, int lane, int group,
+                                         int row0, int nrows, int ch0) {
     const int r = lane & 15, ch = ch0 + 16 * (lane >> 4);
     const int left = a.C - ch, elem = a.out32 ? 4 : 2;
-    unsigned char *dst = a.out + ((int64_t)row0 * a.ldo + ch) * elem;
+    unsigned char *dst = a.out + ((int64_t)row0 * a.ldo + ch) * elem, *const staging = reinterpret_cast<unsigned char *>(turn);
+    uint32_t turns = 0;
 #pragma unroll 1
-    for (int c = 0; c < nrows; c += 16) {
+    for (int c = 16 * group; c < nrows; c += 32, ++turns) {
         float v[16];
+        if (a.bulk && c + 16 <= nrows) {
+            if (a.out32) {
+                gg_store_wait<0>(lane);
+                tmem_ld16(d + c, v);
+                gg_turn_write(turn, lane, v);
+                gg_store(tm, staging, ch0 * 4, row0 + c, lane);
+            } else {
+                unsigned char *const at = staging + 1024 * (turns & 1u);
+                gg_store_wait<1>(lane);
+                tmem_ld16(d + c, v);
+                // the lane's channel, as 16 bits, of 16 rows
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const uint32_t two = gg_pack(v[i], v[i + 1], a.half);
+                    unsigned char *const to = at + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2;
+                    *reinterpret_cast<uint16_t *>(to) = (uint16_t)two;
+                    *reinterpret_cast<uint16_t *>(to + 64) = (uint16_t)(two >> 16);
+                }
+                gg_store(tm, at, ch0 * 2, row0 + c, lane);
+            }
+            continue;
+        }
+        // the tile's last rows: no row behind them is written
+        gg_store_wait<0>(lane);
         tmem_ld16(d + c, v);
         gg_turn_write(turn, lane, v);
         __syncwarp();
@@ -417,35 +489,35 @@ __device__ __forceinline__ void gg_block(const GgArgs &a, const float (&v)[16], 
 }
 
 // Two warps, of 32 gate channels and of the same 32 up channels.  Each quantises its own; p of the
-// first 16 channels is the gate warp's, of the last 16 the up warp's.
-__device__ __forceinline__ void gg_gated(const GgArgs &a, float *turn, float *other, uint32_t d, int lane, int bar,
-                                         bool up, int row0, int nrows, int ch0) {
-    const int r = lane & 15, h = lane >> 4, pch = (up ? 16 : 0) + 8 * h;
+// first 8 of 16 rows is the gate warp's, of the last 8 the up warp's.
+__device__ __forceinline__ void gg_gated(const GgArgs &a, float *turn, float *other, uint32_t d, int lane, int group,
+                                         int bar, bool up, int row0, int nrows, int ch0) {
+    const int r = lane & 15, h = lane >> 4, pr = (lane & 7) + (up ? 8 : 0), pch = 8 * (lane >> 3);
     float *const tg = up ? other : turn, *const tu = up ? turn : other;
     unsigned char *dst = a.out + ((int64_t)row0 * a.ldo + ch0 + pch) * 2;
 #pragma unroll 1
-    for (int c = 0; c < nrows; c += 16) {
+    for (int c = 16 * group; c < nrows; c += 32) {
         float v[16];
         tmem_ld16(d + c, v);
         named_bar_sync(bar, 64);  // both have read the rows before
         gg_turn_write(turn, lane, v);
         named_bar_sync(bar, 64);
-        const bool live = c + r < nrows;
         if (a.codes) {
             gg_turn_read(turn, r, 16 * h, v);
             const int col = (up ? a.C : 0) + ch0;
+            const bool live = c + r < nrows;
             if (a.code == MOE_CODE_INT8) gg_block<true>(a, v, (int64_t)row0 + c + r, col, lane, live);
             else gg_block<false>(a, v, (int64_t)row0 + c + r, col, lane, live);
         }
         float g[8], u[8];
-        gg_turn_read(tg, r, pch, g);
-        gg_turn_read(tu, r, pch, u);
+        gg_turn_read(tg, pr, pch, g);
+        gg_turn_read(tu, pr, pch, u);
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             o[i] = gg_pack(g[2 * i] * gg_sigmoid(g[2 * i]) * u[2 * i], g[2 * i + 1] * gg_sigmoid(g[2 * i + 1]) * u[2 * i + 1],
                            a.half);
-        if (live) gg_put(dst + (int64_t)(c + r) * a.ldo * 2, o, 4, a.vec);
+        if (c + pr < nrows) gg_put(dst + (int64_t)(c + pr) * a.ldo * 2, o, 4, a.vec);
     }
 }
 
@@ -467,17 +539,19 @@ __device__ __forceinline__ GgCodes gg_codes(const GgArgs &a, int64_t row, int ch
 // The checkpoint is read two steps of 16 rows ahead, the first before the unit's sums are complete:
 // read where they are used, the codes' way from memory took 3250 cycles a step.
 template <bool kInt8>
-__device__ __forceinline__ void gg_gated_grad(const GgArgs &a, float *turn, uint32_t d, int lane, int row0, int nrows,
-                                              int ch0, GgCodes (&next)[2]) {
+__device__ __forceinline__ void gg_gated_grad(const GgArgs &a, const GgMaps &tm, float *turn, uint32_t d, int lane, int group, int row0,
+                                              int nrows, int ch0, GgCodes (&next)[2]) {
     const int r = lane & 15, h = lane >> 4, ch = ch0 + 16 * h, I = a.C;
 #pragma unroll 2
-    for (int c = 0; c < nrows; c += 16) {
+    for (int c = 16 * group; c < nrows; c += 32) {
         const bool live = c + r < nrows;
         const int64_t row = (int64_t)row0 + c + r;
         const GgCodes now = next[0];
         next[0] = next[1];
-        next[1] = gg_codes(a, row + 32, ch, c + 32 + r < nrows);
+        next[1] = gg_codes(a, row + 64, ch, c + 64 + r < nrows);
         float q[16], g[16], u[16];
+        unsigned char *const staging = reinterpret_cast<unsigned char *>(turn);
+        gg_store_wait<0>(lane);
         tmem_ld16(d + c, q);
         gg_turn_write(turn, lane, q);
         __syncwarp();
@@ -491,7 +565,18 @@ __device__ __forceinline__ void gg_gated_grad(const GgArgs &a, float *turn, uint
             q[i] *= gsi;                            // grad of u
             g[i] = t * (s + gsi * (1.0f - s));      // grad of g
         }
-        if (live) {
+        if (c + 16 <= nrows) {
+            __syncwarp();
+            gg_stage16(staging, lane, g, a.half);
+            gg_store(tm.y, staging, ch0 * 2, row0 + c, lane);
+            gg_stage16(staging + 1024, lane, q, a.half);
+            gg_store(tm.y, staging + 1024, (I + ch0) * 2, row0 + c, lane);
+            if (a.p) {
+                gg_store_wait<1>(lane);
+                gg_stage16(staging, lane, u, a.half);
+                gg_store(tm.p, staging, ch0 * 2, row0 + c, lane);
+            }
+        } else if (live) {
             unsigned char *dst = a.out + (row * (2 * I) + ch) * 2;
             gg_put16(dst, g, a.half, a.vec);
             gg_put16(dst + 2 * I, q, a.half, a.vec);
@@ -504,10 +589,10 @@ __device__ __forceinline__ void gg_gated_grad(const GgArgs &a, float *turn, uint
 // A warp's 32 rows of the gradient times the n columns of a unit, by tensor stores of 64-byte rows
 // (clipped at the gradient's edges) through its staging memory; zeros for an expert without rows.
 __device__ __forceinline__ void gg_weights(const GgArgs &a, const CUtensorMap &tm, unsigned char *staging, uint32_t d,
-                                           int lane, int e, int ch0, int n0, int n, bool zero) {
+                                           int lane, int group, int e, int ch0, int n0, int n, bool zero) {
     const int elem = a.out32 ? 4 : 2, parts = a.out32 ? 2 : 1;
 #pragma unroll 1
-    for (int c = 0; c < n && n0 + c < a.N; c += 32) {
+    for (int c = 32 * group; c < n && n0 + c < a.N; c += 64) {
         uint32_t v[32];
         if (zero) {
 #pragma unroll
@@ -561,14 +646,14 @@ __device__ __forceinline__ void gg_zero(unsigned char *p, int64_t bytes, bool wi
 // ring's state.  What a stage takes between its memory's release and its copies is kept short: with
 // the coordinates and addresses worked out there it took 400 cycles, in every turn of the ring.
 template <Grouped kMode, bool kTrans, typename G, bool kSideM>
-__device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, GgCtl &ctl, uint32_t base, int rank, int tiles) {
+__device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, GgCtl &ctl, uint32_t base, int rank) {
     constexpr bool kWeights = kMode == Grouped::kWeights, kGated = kMode == Grouped::kGated;
     constexpr int kCtas = G::kCtas;
     constexpr bool kByK = kSideM ? kTrans : !kWeights;  // copies of 64 of K, else of 64 channels
     constexpr int kChunk = !kByK ? G::kMajor : kSideM ? G::kAChunk : G::kBChunk;
     // Copies of a whole stage in CTA r of the pair; those that bring nothing which the MMAs read, or
     // whose results are stored, are left out.
-    auto wide = [&](const GgWalk<kMode, G> &x, int r) {
+    auto wide = [&](const GgUnit &x, int r) {
         const int part = kSideM ? 128 : x.n / kCtas;
         const int left = (kSideM ? a.C - (x.ct * kCtas) * (kGated ? 64 : 128) : kWeights ? a.N - x.n0 : x.nrows) -
                          r * (kSideM && kGated ? 64 : part);
@@ -577,11 +662,12 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
     // weights that one row tile reads leave L2 first
     const uint64_t keep = policy_evict_normal(), once = policy_evict_first();
     const uint32_t full0 = gg_leader<kCtas>(&ctl.full[0]), own0 = smem_u32(&ctl.full[0]), empty0 = smem_u32(&ctl.empty[0]);
-    uint32_t dst = base, slot = 0, parity = 1, it = 0;  // slot: 8 x stage
-    bool ok = true;
-    for (GgWalk<kMode, G> x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
-        if (gg_elect()) {
-            const uint64_t pol = !kWeights && kSideM && ctl.first[x.e + 1] - ctl.first[x.e] == 1 ? once : keep;
+    if (gg_elect()) {
+        uint32_t dst = base, slot = 0, parity = 1, it = 0, unit = 0;  // slot: 8 x stage
+        bool ok = true;
+        GgUnit x;
+        while (ok && gg_next<false>(ctl, unit, x)) {
+            const uint64_t pol = !kWeights && kSideM && x.single ? once : keep;
             int n = wide(x, rank), both = kCtas == 1 ? n : wide(x, 0) + wide(x, 1), chunk = kChunk, dx = 128, dy = 0;
             const int part_n = x.n / kCtas;
             if (kByK && !kSideM && part_n <= G::kSide - G::kPiece) {
@@ -596,7 +682,7 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
             const int fixed = kSideM ? (x.ct * kCtas + rank) * (kGated ? 64 : 128)
                                      : (kWeights ? x.n0 : x.row0) + rank * part_n;
             const int parts = kWeights ? 1 : a.parts, length = kWeights ? x.nrows : a.K;
-            const bool ragged = x.ragged();
+            const bool ragged = kWeights && x.ragged();
             for (int part = 0; part < parts && ok; ++part) {
                 const CUtensorMap *const m = kSideM ? (kWeights ? &tm.x : part ? &tm.w2 : &tm.w)
                                              : kWeights  ? &tm.w
@@ -640,15 +726,14 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
                 }
             }
         }
-        ok = __all_sync(0xffffffffu, ok);
+        // every copy has landed before the CTA can exit (after a wait that gave up; else the MMAs have
+        // read them all)
+        if (rank == 0)
+            for (uint32_t i = 0; i < G::kStages && i < it; ++i) {
+                const uint32_t at = it - 1 - i;
+                if (!mbar_wait_bounded(&ctl.full[at % G::kStages], (at / G::kStages) & 1u)) ctl.abort = 1;
+            }
     }
-    // every copy has landed before the CTA can exit (after a wait that gave up; else the MMAs have read
-    // them all)
-    if (rank == 0 && gg_elect())
-        for (uint32_t i = 0; i < G::kStages && i < it; ++i) {
-            const uint32_t at = it - 1 - i;
-            if (!mbar_wait_bounded(&ctl.full[at % G::kStages], (at / G::kStages) & 1u)) ctl.abort = 1;
-        }
     __syncwarp();
 }
 
@@ -675,7 +760,12 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&ctl.tfull[b], 1);
-            mbar_init(&ctl.tempty[b], 4 * kCtas);
+            mbar_init(&ctl.tempty[b], 8 * kCtas);
+        }
+        for (int u = 0; u < kGgUnits; ++u) {
+            mbar_init(&ctl.ufull[u], 1);
+            // eight epilogue warps, two producers, the first CTA's MMAs, weights: the zeroing warp
+            mbar_init(&ctl.uempty[u], 10 + (rank == 0) + kWeights);
         }
         mbar_init(&ctl.done, 1);
         ctl.abort = 0;
@@ -749,11 +839,10 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     else cluster_sync();
     tc_fence_after();
     const int tiles = kWeights ? a.E : carry;
-    using Walk = GgWalk<kMode, G>;
 
     if (warp == 8 || warp == 9) {
-        if (warp == 8) gg_produce<kMode, kTrans, G, true>(tm, a, ctl, smem_u32(stages), rank, tiles);
-        else gg_produce<kMode, kTrans, G, false>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank, tiles);
+        if (warp == 8) gg_produce<kMode, kTrans, G, true>(tm, a, ctl, smem_u32(stages), rank);
+        else gg_produce<kMode, kTrans, G, false>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank);
     } else if (warp == 10) {
         if (rank == 0) {
             // 128-byte swizzle, 8-row atoms 1 KB apart.  K-major: a K step of 16 is 32 bytes, a chunk
@@ -763,17 +852,19 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             const uint64_t a0 = umma_smem_desc(smem_u32(stages), kAMajor ? G::kMajor : 16, 1024, 2);
             const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, kBMajor ? G::kMajor : 16, 1024, 2);
             const uint32_t full0 = smem_u32(&ctl.full[0]);
-            uint32_t stage = 0, parity = 0, unit = 0;
-            bool ok = true;
-            for (Walk x(a, ctl, tiles); x.t < tiles && ok; x.next(a, ctl, tiles)) {
-                const int length = kWeights ? x.nrows : a.K;
-                if (kWeights && length == 0) continue;
-                const uint32_t buf = unit & 1u, tparity = ((unit >> 1) & 1u) ^ 1u;
-                ++unit;
-                if (gg_elect()) {
-                    const uint32_t d = ctl.tmem + buf * G::kRows, idesc = a.idesc | (uint32_t)(x.n >> 3) << 17;
-                    const int parts = kWeights ? 1 : a.parts;
+            if (gg_elect()) {
+                const int parts = kWeights ? 1 : a.parts, summed = a.K;
+                const uint32_t idesc0 = a.idesc, tmem = ctl.tmem;
+                uint32_t stage = 0, parity = 0, at = 0, unit = 0;
+                bool ok = true;
+                GgUnit x;
+                while (ok && gg_next<false>(ctl, at, x)) {
+                    const int length = kWeights ? x.nrows : summed;
+                    if (kWeights && length == 0) continue;
+                    const uint32_t buf = unit & 1u, tparity = ((unit >> 1) & 1u) ^ 1u;
+                    const uint32_t d = tmem + buf * G::kRows, idesc = idesc0 | (uint32_t)(x.n >> 3) << 17;
                     bool first = true;
+                    ++unit;
                     ok = gg_wait_one(smem_u32(&ctl.tempty[buf]), tparity, ctl);
                     tc_fence_after();
                     for (int part = 0; part < parts && ok; ++part)
@@ -801,10 +892,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                         }
                     if (ok) gg_commit<kCtas>(&ctl.tfull[buf]);
                 }
-                ok = __all_sync(0xffffffffu, ok);
-            }
-            // every issued MMA has completed before the CTAs free their tensor memory
-            if (gg_elect()) {
+                // every issued MMA has completed before the CTAs free their tensor memory
                 if constexpr (kCtas == 1) umma_commit(&ctl.done);
                 else
                     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -819,8 +907,9 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             // rows past the group's end within the last K step, as zeros: both operands, since what is
             // there may be a NaN
             int total = 0;
-            uint32_t phase = 0;
-            for (Walk x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles)) {
+            uint32_t phase = 0, unit = 0;
+            GgUnit x;
+            while (gg_next<true>(ctl, unit, x)) {
                 total += (x.nrows + G::kK - 1) / G::kK;
                 if (!x.ragged()) continue;
                 const int stage = (total - 1) % G::kStages;
@@ -837,27 +926,30 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 if (lane == 0) gg_arrive_release(gg_leader<kCtas>(&ctl.full[stage]), 2 / kCtas);
             }
         }
+    } else if (warp == 12) {
+        gg_schedule<kMode, G>(a, ctl, tiles);
     } else {
         const int group = warp >> 2, quad = warp & 3;
         float *const turn = reinterpret_cast<float *>(turns + warp * kGgTurnBytes);
         const int bar = 1 + 2 * group + (quad & 1);  // gated: of the gate and up warps of the same channels
         int local = 0;
-        for (Walk x(a, ctl, tiles); x.t < tiles; x.next(a, ctl, tiles)) {
+        uint32_t unit = 0;
+        GgUnit x;
+        while (gg_next<true>(ctl, unit, x)) {
             const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128) + 32 * (kGated ? quad & 1 : quad);
             if (kWeights && x.nrows == 0) {
-                if (((x.t ^ x.ct) & 1) == group && c0 < a.C)
-                    gg_weights(a, tm.y, turns + warp * 2048, 0, lane, x.e, c0, x.n0, x.n, true);
+                if (c0 < a.C)
+                    gg_weights(a, tm.y, turns + warp * kGgTurnBytes, 0, lane, group, x.e, c0, x.n0, x.n, true);
                 continue;
             }
             const int buf = local & 1;
             const uint32_t parity = (uint32_t)(local >> 1) & 1u;
             ++local;
-            if (buf != group) continue;
             GgCodes ahead[2];
             if constexpr (kMode == Grouped::kGatedGrad)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int r = 16 * i + (lane & 15);
+                    const int r = 32 * i + 16 * group + (lane & 15);
                     ahead[i] = gg_codes(a, (int64_t)x.row0 + r, c0 + 16 * (lane >> 4), c0 < a.C && r < x.nrows);
                 }
             bool ok = gg_wait(&ctl.tfull[buf], parity, ctl);
@@ -868,24 +960,24 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             if (c0 >= a.C) {
                 // no channel of this warp's lanes
             } else if constexpr (kMode == Grouped::kPlain) {
-                gg_plain<G>(a, turn, d, lane, x.row0, x.nrows, c0);
+                gg_plain<G>(a, tm.y, turn, d, lane, group, x.row0, x.nrows, c0);
             } else if constexpr (kGated) {
-                gg_gated(a, turn, reinterpret_cast<float *>(turns + (warp ^ 2) * kGgTurnBytes), d, lane, bar, quad >= 2,
+                gg_gated(a, turn, reinterpret_cast<float *>(turns + (warp ^ 2) * kGgTurnBytes), d, lane, group, bar, quad >= 2,
                          x.row0, x.nrows, c0);
                 if (a.codes && c0 == 0 && quad == 0)  // the scale rows' padding
-                    for (int r = lane; r < x.nrows; r += 32)
+                    for (int r = 32 * group + lane; r < x.nrows; r += 64)
                         for (int b = a.C / 16; b < a.pitch; ++b) a.scales[((int64_t)x.row0 + r) * a.pitch + b] = 0;
             } else if constexpr (kMode == Grouped::kGatedGrad) {
-                if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, turn, d, lane, x.row0, x.nrows, c0, ahead);
-                else gg_gated_grad<false>(a, turn, d, lane, x.row0, x.nrows, c0, ahead);
+                if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
+                else gg_gated_grad<false>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
             } else {
-                gg_weights(a, tm.y, turns + warp * 2048, d, lane, x.e, c0, x.n0, x.n, false);
+                gg_weights(a, tm.y, turns + warp * kGgTurnBytes, d, lane, group, x.e, c0, x.n0, x.n, false);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.tempty[buf]));
         }
-        if (kWeights && lane == 0) bulk_store_wait<false>();  // stores have left shared memory and are visible
+        if (lane == 0) bulk_store_wait<false>();  // stores have left shared memory and are visible
         // rows past the last group (dropped routes): zeros
         if (!kWeights && group == 0)
             for (int64_t r = ctl.valid_rows + (int64_t)blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -991,6 +1083,17 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
         if (g.parts == 2) rows_map(&tm.x2, g.x2, g.K, g.ldx, side);
         if (g.parts == 2 && !small) rows_map(&tm.x2s, g.x2, g.K, g.ldx, GgLarge::kPiece);
         if (g.w2) weights_map(&tm.w2, g.w2);
+        // results: boxes of 16 rows of 32 channels, where the rows allow tensor stores and their bytes
+        // fit the coordinates
+        auto result_map = [&](CUtensorMap *m, void *p, int64_t cols, int64_t ld, int bytes) {
+            const uint64_t d[2] = {(uint64_t)cols * bytes, (uint64_t)g.rows}, s[1] = {(uint64_t)ld * bytes};
+            const uint32_t b[2] = {32u * bytes, 16};
+            ok = ok && make_tmap_bytes(m, p, 2, d, s, b, bytes == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+        };
+        a.bulk = g.mode == Grouped::kPlain && a.vec > 0 && a.ldo < ((int64_t)1 << 34);
+        if (a.bulk) result_map(&tm.y, g.out, g.channels, g.ldo, elem);
+        if (grad) result_map(&tm.y, g.out, 2 * (int64_t)g.channels, g.ldo, 2);
+        if (grad && g.p) result_map(&tm.p, g.p, g.channels, g.channels, 2);
     }
     if (!ok) return cudaErrorInvalidValue;
     if (weights) return grouped_as<Grouped::kWeights, false, GgLarge>(tm, a, stream);
