@@ -420,13 +420,12 @@ __device__ __forceinline__ void gg_stage16(unsigned char *staging, int lane, con
 
 template <typename G>
 __device__ __forceinline__ void gg_plain(const GgArgs &a, const CUtensorMap &tm, float *turn, uint32_t d, int lane, int group,
-                                         int row0, int nrows, int ch0) {
+                                         int row0, int nrows, int ch0, uint32_t &turns) {
     const int r = lane & 15, ch = ch0 + 16 * (lane >> 4);
     const int left = a.C - ch, elem = a.out32 ? 4 : 2;
     unsigned char *dst = a.out + ((int64_t)row0 * a.ldo + ch) * elem, *const staging = reinterpret_cast<unsigned char *>(turn);
-    uint32_t turns = 0;
 #pragma unroll 1
-    for (int c = 16 * group; c < nrows; c += 32, ++turns) {
+    for (int c = 16 * group; c < nrows; c += 32) {
         float v[16];
         if (a.bulk && c + 16 <= nrows) {
             if (a.out32) {
@@ -435,7 +434,7 @@ __device__ __forceinline__ void gg_plain(const GgArgs &a, const CUtensorMap &tm,
                 gg_turn_write(turn, lane, v);
                 gg_store(tm, staging, ch0 * 4, row0 + c, lane);
             } else {
-                unsigned char *const at = staging + 1024 * (turns & 1u);
+                unsigned char *const at = staging + 1024 * (turns++ & 1u);  // (counted over all units)
                 gg_store_wait<1>(lane);
                 tmem_ld16(d + c, v);
                 // the lane's channel, as 16 bits, of 16 rows
@@ -933,7 +932,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         float *const turn = reinterpret_cast<float *>(turns + warp * kGgTurnBytes);
         const int bar = 1 + 2 * group + (quad & 1);  // gated: of the gate and up warps of the same channels
         int local = 0;
-        uint32_t unit = 0;
+        uint32_t unit = 0, stored = 0;
         GgUnit x;
         while (gg_next<true>(ctl, unit, x)) {
             const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128) + 32 * (kGated ? quad & 1 : quad);
@@ -960,7 +959,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             if (c0 >= a.C) {
                 // no channel of this warp's lanes
             } else if constexpr (kMode == Grouped::kPlain) {
-                gg_plain<G>(a, tm.y, turn, d, lane, group, x.row0, x.nrows, c0);
+                gg_plain<G>(a, tm.y, turn, d, lane, group, x.row0, x.nrows, c0, stored);
             } else if constexpr (kGated) {
                 gg_gated(a, turn, reinterpret_cast<float *>(turns + (warp ^ 2) * kGgTurnBytes), d, lane, group, bar, quad >= 2,
                          x.row0, x.nrows, c0);

@@ -69,6 +69,21 @@ def test_product_exact_sums(sizes, tail, N, K, form, dtype):
     assert status(work) == 0
 
 
+@pytest.mark.parametrize("rows,out", [(80, BF16), (48, F16), (112, F32), (208, BF16)])
+def test_product_of_many_short_units(rows, out):
+    """Few MMAs a unit, odd numbers of 16-row steps: every store's staging memory is still in use when
+    the next unit's results come."""
+    g = gen(rows)
+    offsets = ref.groups([rows] * 48)
+    x, w = ints((48 * rows, 32), g, 3, BF16), ints((48, 32, 2048), g, 3, BF16)
+    want = ref.product(x, w, offsets).to(F32).to(out)
+    work, y = workspace(), torch.empty((48 * rows, 2048), dtype=out, device="cuda")
+    for _ in range(20):
+        y.fill_(float("nan"))
+        moe.moe_grouped_product(x, w, offsets.cuda(), out=y, workspace=work)
+        assert torch.equal(y, want)
+
+
 def test_product_any_result_pitch():
     """Rows of y that allow no wide stores: odd pitch and offset."""
     g = gen(3)
