@@ -54,7 +54,7 @@ struct GgTile {
     static constexpr int kBBytes = kSide * kK * 2;
     static constexpr int kMajor = kK * 128;          // channel-major: a copy of 64 channels
     static constexpr int kAChunk = 128 * 128, kBChunk = kSide * 128;
-    static constexpr int kPiece = 32;                // rows of a small copy of the N side
+    static constexpr int kPiece = kCtas == 1 ? kRows : 32;  // rows of a small copy of the N side
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr uint32_t kTmemCols = 2 * kRows;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kGgTurnBytes + 1024;
@@ -62,7 +62,7 @@ struct GgTile {
     static_assert(kStageBytes % 1024 == 0 && kBChunk % 1024 == 0 && kStages <= kGgMaxStages, "stage alignment");
 };
 using GgLarge = GgTile<2, 256, 64, 6>;
-using GgSmall = GgTile<1, 32, 128, 4>;
+using GgSmall = GgTile<1, 16, 128, 5>;
 
 // A unit, as every role reads it.
 struct alignas(16) GgUnit {
@@ -691,8 +691,10 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
                 for (int left = length; left > 0; left -= G::kK, ++it) {
                     uint32_t bar = full0 + slot, bytes = tx;
                     int copies = n;
-                    if (kByK && G::kChunks > 1 && left <= 64)
-                        copies = n > 0, bytes = (uint32_t)((both > G::kChunks ? 2 : both > 0) * chunk);
+                    if (kByK && G::kChunks > 1 && left < G::kK) {
+                        const int deep = (left + 63) / 64;
+                        copies = n ? deep : 0, bytes = (uint32_t)(both / G::kChunks * deep * chunk);
+                    }
                     if (!(ok = gg_wait_one(empty0 + slot, parity, ctl))) break;
                     // the pair's first CTA expects both CTAs' bytes; a stage whose last rows are to be
                     // zeroed first is each CTA's own

@@ -1081,38 +1081,42 @@ def moe_microscale_ffn(h, layer, topk_ids, topk_weights, residual=None, out=None
 _CODE_DTYPES = {torch.float8_e4m3fn: MOE_CODE_E4M3, torch.int8: MOE_CODE_INT8}
 
 
+_HALF_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
+
+
 def _half_dtype(t, name):
     """MOE_DT_* of a 16-bit matrix."""
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
+    code = _HALF_DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError("%s must be bfloat16 or float16, got %s" % (name, t.dtype))
-    return _row_dtype(t, name)
+    if t.dim() != 2:
+        _not_a_matrix(t, name)
+    return code
 
 
-def _expert_weights(w, name, device, dtype, shape):
-    """Checks expert weights [E,a,b] (None in `shape` for any size) or, of one expert, [a,b];
-    returns (E, a, b)."""
-    ws = w.shape
-    if len(ws) != 2 and len(ws) != 3:
-        raise ValueError("%s must have three dimensions, or two for one expert, got shape %s" % (name, tuple(ws)))
+def _expert_weights(w, name, device, dtype):
+    """Checks expert weights [E,a,b] or, of one expert, [a,b]; returns (E, a, b)."""
+    shape = w.shape
     if not (w.dtype is dtype and w.device == device and w.is_contiguous()):
         _need(w, dtype, name, device)
-    found = (1,) + tuple(ws) if len(ws) == 2 else tuple(ws)
-    if any(want is not None and want != got for want, got in zip(shape, found)):
-        raise ValueError("%s must have shape %s, got %s" % (
-            name, tuple("any" if n is None else n for n in shape), tuple(ws)))
-    return found
+    if len(shape) == 3:
+        return shape
+    if len(shape) != 2:
+        raise ValueError("%s must have three dimensions, or two for one expert, got shape %s" % (name, tuple(shape)))
+    return 1, shape[0], shape[1]
+
+
+def _misfit(w, name, columns):
+    raise ValueError("%s has shape %s, which does not fit rows of %d columns" % (name, tuple(w.shape), columns))
 
 
 def _offsets(offsets, E, device):
     return None if offsets is None else _vector(offsets, "offsets", torch.int32, device, (E + 1,))
 
 
-def _status_workspace(workspace, device):
-    """(the workspace made here or None, (the workspace's address, its bytes))."""
-    if workspace is None:
-        workspace = torch.zeros(MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8, device=device)
-        return workspace, (workspace.data_ptr(), MOE_GROUPED_STATUS_BYTES)
-    return None, _workspace(workspace, device)
+def _status_workspace(device):
+    """A status word of a call's own."""
+    return torch.zeros(MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8, device=device)
 
 
 def _code_dtype(dtype):
@@ -1126,10 +1130,12 @@ def _checkpoint_outputs(codes, scales, rows, cols, dtype, dev):
     """Codes and scales of a [rows, cols] checkpoint, allocated where the caller gave none."""
     if codes is None:
         codes = torch.empty((rows, cols), dtype=dtype, device=dev)
+    else:
+        _vector(codes, "codes", dtype, dev, (rows, cols))
     if scales is None:
         scales = torch.empty((rows, _pitch(cols)), dtype=torch.uint8, device=dev)
-    _vector(codes, "codes", dtype, dev, (rows, cols))
-    _vector(scales, "scales", torch.uint8, dev, (rows, _pitch(cols)))
+    else:
+        _vector(scales, "scales", torch.uint8, dev, (rows, _pitch(cols)))
     return codes, scales
 
 
@@ -1144,6 +1150,8 @@ def _checkpoint(codes, scales, device):
     return code, rows, cols
 
 
+# Outputs are allocated after the checks: torch's first operation after a launch costs the host 4 us
+# more than later ones, less the longer ago the launch is.
 def moe_grouped_product(rows, weights, offsets=None, transposed=False, dtype=None, out=None,
                         workspace=None, stream=None):
     """y [rows,N] of rows [rows,K] sorted by expert: each times its expert's weights [E,K,N] (or
@@ -1158,30 +1166,44 @@ def moe_grouped_product(rows, weights, offsets=None, transposed=False, dtype=Non
     dev, dt = rows.device, rows.dtype
     code = _half_dtype(rows, "rows")
     R, cols = rows.shape
-    pair = isinstance(weights, (tuple, list))
-    if pair and len(weights) != 2:
-        raise ValueError("weights must be one tensor or a pair, got %d" % len(weights))
-    w, w2 = weights if pair else (weights, None)
-    if pair and cols % 2:
-        raise ValueError("rows must have an even number of columns for a pair of weights, got %d" % cols)
-    K = cols // 2 if pair else cols
-    shape = (None, None, K) if transposed else (None, K, None)
-    E, a, b = _expert_weights(w, "weights", dev, dt, shape)
-    if pair:
-        _expert_weights(w2, "weights", dev, dt, (E, a, b))
-    N = a if transposed else b
+    K, w, w2 = cols, weights, None
+    if not isinstance(weights, torch.Tensor):
+        if len(weights) != 2:
+            raise ValueError("weights must be one tensor or a pair, got %d" % len(weights))
+        if cols % 2:
+            raise ValueError("rows must have an even number of columns for a pair of weights, got %d" % cols)
+        K, (w, w2) = cols // 2, weights
+    E, a, b = _expert_weights(w, "weights", dev, dt)
+    N, k = (a, b) if transposed else (b, a)
+    if k != K:
+        _misfit(w, "weights", cols)
+    p2 = None
+    if w2 is not None:
+        if _expert_weights(w2, "weights", dev, dt) != (E, a, b):
+            _misfit(w2, "weights", cols)
+        p2 = w2.data_ptr()
     ldx = _rows(rows, "rows", dev, dt, (R, cols))
     off = _offsets(offsets, E, dev)
+    ws = None if workspace is None else _workspace(workspace, dev)
+    launch = _raw_stream(dev)
     if out is None:
-        out, ldy = torch.empty((R, N), dtype=dt if dtype is None else dtype, device=dev), N
+        if dtype is None:
+            dtype, ycode = dt, code
+        else:
+            ycode = _ROW_DTYPES.get(dtype)
+            if ycode is None:
+                raise TypeError("dtype must be bfloat16, float16 or float32, got %s" % (dtype,))
+        out, ldy = torch.empty((R, N), dtype=dtype, device=dev), N
     else:
         ldy = _rows(out, "out", dev, out.dtype if dtype is None else dtype, (R, N))
-    ycode = _row_dtype(out, "out")
-    own, ws = _status_workspace(workspace, dev)
-    _check(lib().moe_grouped_product(rows.data_ptr(), ldx, R, code, off, w.data_ptr(),
-                                     w2.data_ptr() if pair else None, int(bool(transposed)), E, N, K,
-                                     ycode, out.data_ptr(), ldy, *ws, _raw_stream(dev)),
-           "moe_grouped_product")
+        ycode = _row_dtype(out, "out")
+    own = None
+    if ws is None:
+        own = _status_workspace(dev)
+        ws = _workspace(own, dev)
+    _check(lib().moe_grouped_product(rows.data_ptr(), ldx, R, code, off, w.data_ptr(), p2,
+                                     1 if transposed else 0, E, N, K, ycode, out.data_ptr(), ldy, *ws,
+                                     launch), "moe_grouped_product")
     if own is not None:
         _own_status(own, "moe_grouped_product")
     return out
@@ -1199,27 +1221,35 @@ def moe_grouped_gated_product(rows, w_gate, w_up, offsets=None, checkpoint=None,
     dev, dt = rows.device, rows.dtype
     code = _half_dtype(rows, "rows")
     R, H = rows.shape
-    E, _, I = _expert_weights(w_gate, "w_gate", dev, dt, (None, H, None))
-    _expert_weights(w_up, "w_up", dev, dt, (E, H, I))
+    E, h, I = _expert_weights(w_gate, "w_gate", dev, dt)
+    if h != H:
+        _misfit(w_gate, "w_gate", H)
+    if _expert_weights(w_up, "w_up", dev, dt) != (E, H, I):
+        _misfit(w_up, "w_up", H)
     ldx = _rows(rows, "rows", dev, dt, (R, H))
     off = _offsets(offsets, E, dev)
     if I % 32:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_grouped_gated_product")
+    ws = None if workspace is None else _workspace(workspace, dev)
+    launch = _raw_stream(dev)
+    kind = 0 if checkpoint is None else _code_dtype(checkpoint)
     if out is None:
         out, ldp = torch.empty((R, I), dtype=dt, device=dev), I
     else:
         ldp = _rows(out, "out", dev, dt, (R, I))
-    kind, pc, ps = 0, None, None
+    pc = ps = None
     if checkpoint is not None:
-        kind = _code_dtype(checkpoint)
         codes, scales = _checkpoint_outputs(codes, scales, R, 2 * I, checkpoint, dev)
         pc, ps = codes.data_ptr(), scales.data_ptr()
     elif codes is not None or scales is not None:
         raise ValueError("codes and scales are outputs of a checkpoint: its type is missing")
-    own, ws = _status_workspace(workspace, dev)
+    own = None
+    if ws is None:
+        own = _status_workspace(dev)
+        ws = _workspace(own, dev)
     _check(lib().moe_grouped_gated_product(rows.data_ptr(), ldx, R, code, off, w_gate.data_ptr(),
                                            w_up.data_ptr(), E, I, H, out.data_ptr(), ldp, kind, pc, ps,
-                                           *ws, _raw_stream(dev)), "moe_grouped_gated_product")
+                                           *ws, launch), "moe_grouped_gated_product")
     if own is not None:
         _own_status(own, "moe_grouped_gated_product")
     return out if checkpoint is None else (out, codes, scales)
@@ -1237,14 +1267,18 @@ def moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, grad_
     dev, dt = grad_y.device, grad_y.dtype
     code = _half_dtype(grad_y, "grad_y")
     R, H = grad_y.shape
-    E, I, _ = _expert_weights(w_down, "w_down", dev, dt, (None, None, H))
+    E, I, h = _expert_weights(w_down, "w_down", dev, dt)
+    if h != H:
+        _misfit(w_down, "w_down", H)
     ldg = _rows(grad_y, "grad_y", dev, dt, (R, H))
     off = _offsets(offsets, E, dev)
     kind, crows, cols = _checkpoint(codes, scales, dev)
-    if (crows, cols) != (R, 2 * I):
+    if crows != R or cols != 2 * I:
         raise ValueError("codes must have shape %s, got %s" % ((R, 2 * I), (crows, cols)))
     if I % 32:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_grouped_gated_product_grad")
+    ws = None if workspace is None else _workspace(workspace, dev)
+    launch = _raw_stream(dev)
     if grad_gate_up is None:
         grad_gate_up = torch.empty((R, 2 * I), dtype=dt, device=dev)
     else:
@@ -1253,11 +1287,14 @@ def moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, grad_
         p = torch.empty((R, I), dtype=dt, device=dev)
     else:
         _vector(p, "p", dt, dev, (R, I))
-    own, ws = _status_workspace(workspace, dev)
+    own = None
+    if ws is None:
+        own = _status_workspace(dev)
+        ws = _workspace(own, dev)
     _check(lib().moe_grouped_gated_product_grad(grad_y.data_ptr(), ldg, R, code, off, w_down.data_ptr(), E,
                                                 I, H, kind, codes.data_ptr(), scales.data_ptr(),
-                                                grad_gate_up.data_ptr(), p.data_ptr(), *ws,
-                                                _raw_stream(dev)), "moe_grouped_gated_product_grad")
+                                                grad_gate_up.data_ptr(), p.data_ptr(), *ws, launch),
+           "moe_grouped_gated_product_grad")
     if own is not None:
         _own_status(own, "moe_grouped_gated_product_grad")
     return grad_gate_up, p
@@ -1273,8 +1310,9 @@ def moe_grouped_weight_grad(rows, grads, offsets=None, dtype=torch.float32, out=
             return moe_grouped_weight_grad(rows, grads, offsets, dtype, out, workspace)
     dev, dt = rows.device, rows.dtype
     code = _half_dtype(rows, "rows")
-    _half_dtype(grads, "grads")
     R, K = rows.shape
+    if grads.dim() != 2:
+        _not_a_matrix(grads, "grads")
     N = grads.shape[1]
     ldx = _rows(rows, "rows", dev, dt, (R, K))
     ldg = _rows(grads, "grads", dev, dt, (R, N))
@@ -1284,17 +1322,23 @@ def moe_grouped_weight_grad(rows, grads, offsets=None, dtype=torch.float32, out=
             raise ValueError("offsets must have shape (E + 1,), got %s" % (tuple(offsets.shape),))
         E = offsets.shape[0] - 1
         off = _offsets(offsets, E, dev)
+    ws = None if workspace is None else _workspace(workspace, dev)
+    launch = _raw_stream(dev)
+    if out is not None:
+        dtype = out.dtype
+    ocode = _ROW_DTYPES.get(dtype)
+    if ocode is None:
+        raise TypeError("the gradient must be bfloat16, float16 or float32, got %s" % (dtype,))
     if out is None:
         out = torch.empty((E, K, N), dtype=dtype, device=dev)
     else:
-        _vector(out, "out", out.dtype, dev, (E, K, N))
-    ocode = _ROW_DTYPES.get(out.dtype)
-    if ocode is None:
-        raise TypeError("out must be bfloat16, float16 or float32, got %s" % (out.dtype,))
-    own, ws = _status_workspace(workspace, dev)
+        _vector(out, "out", dtype, dev, (E, K, N))
+    own = None
+    if ws is None:
+        own = _status_workspace(dev)
+        ws = _workspace(own, dev)
     _check(lib().moe_grouped_weight_grad(rows.data_ptr(), ldx, grads.data_ptr(), ldg, R, code, off, E, K, N,
-                                         ocode, out.data_ptr(), *ws, _raw_stream(dev)),
-           "moe_grouped_weight_grad")
+                                         ocode, out.data_ptr(), *ws, launch), "moe_grouped_weight_grad")
     if own is not None:
         _own_status(own, "moe_grouped_weight_grad")
     return out
@@ -1317,9 +1361,10 @@ def moe_checkpoint_quantize(x, dtype=torch.float8_e4m3fn, codes=None, scales=Non
     ldx = _rows(x, "x", dev, x.dtype, (rows, cols))
     if cols % 32:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_checkpoint_quantize")
+    launch = _raw_stream(dev)
     codes, scales = _checkpoint_outputs(codes, scales, rows, cols, dtype, dev)
     _check(lib().moe_checkpoint_quantize(x.data_ptr(), ldx, xcode, rows, cols, kind, codes.data_ptr(),
-                                         scales.data_ptr(), _raw_stream(dev)), "moe_checkpoint_quantize")
+                                         scales.data_ptr(), launch), "moe_checkpoint_quantize")
     return codes, scales
 
 
@@ -1337,12 +1382,15 @@ def moe_checkpoint_dequantize(codes, scales, dtype=torch.bfloat16, route_row=Non
             _not_a_matrix(route_row, "route_row")
         k = route_row.shape[1]
         rr = _vector(route_row, "route_row", torch.int32, dev, (rows, k))
-    if out is None:
-        out, ldx = torch.empty((rows * k, cols), dtype=dtype, device=dev), cols
+    launch = _raw_stream(dev)
+    if out is not None:
+        ldx, xcode = _rows(out, "out", dev, out.dtype, (rows * k, cols)), _row_dtype(out, "out")
     else:
-        ldx = _rows(out, "out", dev, out.dtype, (rows * k, cols))
-    xcode = _row_dtype(out, "out")
+        xcode = _ROW_DTYPES.get(dtype)
+        if xcode is None:
+            raise TypeError("dtype must be bfloat16, float16 or float32, got %s" % (dtype,))
+        out, ldx = torch.empty((rows * k, cols), dtype=dtype, device=dev), cols
     _check(lib().moe_checkpoint_dequantize(codes.data_ptr(), scales.data_ptr(), kind, rows, cols, rr, k,
-                                           out.data_ptr(), ldx, xcode, _raw_stream(dev)),
+                                           out.data_ptr(), ldx, xcode, launch),
            "moe_checkpoint_dequantize")
     return out
