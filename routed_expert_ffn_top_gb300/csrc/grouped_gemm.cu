@@ -95,7 +95,8 @@ struct GgCtl {
     int32_t begin[kGroupedMaxExperts + 1];  // first row of expert e
 };
 
-// x, x2: the rows' boxes are a CTA's side, and of the small ones (xs, x2s) 32 rows.
+// x, x2: the rows' boxes are a CTA's side, and of the small ones (xs, x2s) 32 rows.  Weights: x the
+// rows, w the grads; xs, x2s the same in chunks of 64 channels, two a box.
 struct GgMaps {
     CUtensorMap x, x2, xs, x2s, w, w2, y, p;
 };
@@ -105,6 +106,7 @@ struct GgArgs {
     int64_t rows;
     int E, C, K, N;   // C channels; N the weights' gradient's columns
     int parts, nct, nnt;
+    int deep_m, deep_n;  // the M, N side's channels are whole chunks of 64: one copy brings two
     int dt, dct;      // a step of a CTA pair's units in row tiles and channel tiles
     uint32_t idesc;   // without N
     int half, out32;  // f16 (else bf16) results; fp32 ones
@@ -220,6 +222,23 @@ __device__ __forceinline__ void gg_load_3d(uint32_t dst, const CUtensorMap *tm, 
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
             "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+            : "memory");
+}
+
+template <int kCtas>
+__device__ __forceinline__ void gg_load_4d(uint32_t dst, const CUtensorMap *tm, int x, int y, int z, int w, uint32_t bar,
+                                           uint64_t policy) {
+    if constexpr (kCtas == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
             : "memory");
 }
 
@@ -603,8 +622,7 @@ __device__ __forceinline__ void gg_weights(const GgArgs &a, const CUtensorMap &t
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             if (q == parts) break;
-            if (lane == 0) bulk_store_wait<true>();  // the staging memory's last store has been read
-            __syncwarp();
+            gg_store_wait<0>(lane);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint4 o;
@@ -676,6 +694,8 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
                 n = n ? pieces : 0, both = both * pieces, chunk = G::kPiece * 128, dx = 0, dy = G::kPiece;
             }
             const bool small_box = dy != 0;
+            const bool deep = !kByK && !(kSideM && kGated) && (kSideM ? a.deep_m : a.deep_n && part_n % 64 == 0);
+            if (deep) both = kCtas == 1 ? n > 0 : (wide(x, 0) > 0) + (wide(x, 1) > 0), n = n > 0, chunk = 2 * kChunk;
             const uint32_t tx = (uint32_t)(both * chunk);
             // coordinates: bytes along the operand's rows, the row (of K, or a row of x or w), the expert
             const int fixed = kSideM ? (x.ct * kCtas + rank) * (kGated ? 64 : 128)
@@ -683,8 +703,8 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
             const int parts = kWeights ? 1 : a.parts, length = kWeights ? x.nrows : a.K;
             const bool ragged = kWeights && x.ragged();
             for (int part = 0; part < parts && ok; ++part) {
-                const CUtensorMap *const m = kSideM ? (kWeights ? &tm.x : part ? &tm.w2 : &tm.w)
-                                             : kWeights  ? &tm.w
+                const CUtensorMap *const m = kSideM ? (kWeights ? (deep ? &tm.xs : &tm.x) : part ? &tm.w2 : &tm.w)
+                                             : kWeights  ? (deep ? &tm.x2s : &tm.w)
                                              : small_box ? (part ? &tm.x2s : &tm.xs)
                                                          : (part ? &tm.x2 : &tm.x);
                 int cx = kByK ? 0 : 2 * fixed, cy = kByK ? fixed : kWeights ? x.row0 : 0;
@@ -710,6 +730,11 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
                         if (copies) {
                             gg_load_3d<kCtas>(dst, m, cx, cy, x.e, bar, pol);
                             gg_load_3d<kCtas>(dst + kChunk, &tm.w2, cx, cy, x.e, bar, pol);
+                        }
+                    } else if (deep) {
+                        if (copies) {
+                            if constexpr (kWeights) gg_load_3d<kCtas>(dst, m, 0, cy, fixed / 64, bar, pol);
+                            else gg_load_4d<kCtas>(dst, m, 0, cy, fixed / 64, x.e, bar, pol);
                         }
                     } else {
                         int px = cx, py = cy;
@@ -931,7 +956,8 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         gg_schedule<kMode, G>(a, ctl, tiles);
     } else {
         const int group = warp >> 2, quad = warp & 3;
-        float *const turn = reinterpret_cast<float *>(turns + warp * kGgTurnBytes);
+        unsigned char *const staging = turns + warp * kGgTurnBytes;
+        float *const turn = reinterpret_cast<float *>(staging);
         const int bar = 1 + 2 * group + (quad & 1);  // gated: of the gate and up warps of the same channels
         int local = 0;
         uint32_t unit = 0, stored = 0;
@@ -940,7 +966,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128) + 32 * (kGated ? quad & 1 : quad);
             if (kWeights && x.nrows == 0) {
                 if (c0 < a.C)
-                    gg_weights(a, tm.y, turns + warp * kGgTurnBytes, 0, lane, group, x.e, c0, x.n0, x.n, true);
+                    gg_weights(a, tm.y, staging, 0, lane, group, x.e, c0, x.n0, x.n, true);
                 continue;
             }
             const int buf = local & 1;
@@ -972,7 +998,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
                 else gg_gated_grad<false>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
             } else {
-                gg_weights(a, tm.y, turns + warp * kGgTurnBytes, d, lane, group, x.e, c0, x.n0, x.n, false);
+                gg_weights(a, tm.y, staging, d, lane, group, x.e, c0, x.n0, x.n, false);
             }
             tc_fence_before();
             __syncwarp();
@@ -1064,7 +1090,22 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
         const uint32_t b[2] = {128, box};
         ok = ok && make_tmap_bytes(m, p, 2, d, s, b, sw);
     };
+    // channels in chunks of 64, two a box
+    auto deep_map = [&](CUtensorMap *m, const void *p, int64_t cols, int64_t ld) {
+        const uint64_t d[3] = {128, (uint64_t)g.rows, (uint64_t)cols / 64}, s[2] = {(uint64_t)ld * 2, 128};
+        const uint32_t b[3] = {128, depth, 2};
+        ok = ok && make_tmap_bytes(m, p, 3, d, s, b, sw);
+    };
+    a.deep_m = a_major && g.mode != Grouped::kGated && g.channels % 64 == 0;
+    a.deep_n = weights && g.N % 64 == 0;
     auto weights_map = [&](CUtensorMap *m, const void *p) {
+        if (a.deep_m) {
+            const uint64_t row = (uint64_t)g.channels * 2;
+            const uint64_t d[4] = {128, (uint64_t)g.K, (uint64_t)g.channels / 64, (uint64_t)g.E}, s[3] = {row, 128, row * g.K};
+            const uint32_t b[4] = {128, depth, 2, 1};
+            ok = ok && make_tmap_bytes(m, p, 4, d, s, b, sw);
+            return;
+        }
         const uint64_t in = a_major ? g.channels : g.K, out = a_major ? g.K : g.channels;
         const uint64_t d[3] = {in * 2, out, (uint64_t)g.E}, s[2] = {in * 2, in * out * 2};
         const uint32_t b[3] = {128, a_major ? depth : 128u, 1};
@@ -1073,6 +1114,8 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
     if (weights) {
         rows_map(&tm.x, g.x, g.channels, g.ldx, depth);
         rows_map(&tm.w, g.w, g.N, g.ldw, depth);
+        if (a.deep_m) deep_map(&tm.xs, g.x, g.channels, g.ldx);
+        if (a.deep_n) deep_map(&tm.x2s, g.w, g.N, g.ldw);
         const uint64_t in = (uint64_t)g.N * elem;
         const uint64_t d[3] = {in, (uint64_t)g.channels, (uint64_t)g.E}, s[2] = {in, in * g.channels};
         const uint32_t b[3] = {64, 32, 1};
