@@ -40,6 +40,7 @@ namespace moe {
 constexpr int kGgThreads = 416;
 constexpr int kGgTurnBytes = 16 * 32 * 4;  // 16 rows of 32 channels that are turned round
 constexpr int kGgMaxStages = 6;
+constexpr int kGgSort = 512;           // weights: rows up to which experts keep their order
 constexpr int kGgUnits = 8;            // units that are worked out ahead
 
 template <int kCtas_, int kRows_, int kK_, int kStages_>
@@ -846,16 +847,19 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         __syncthreads();
     }
     if constexpr (kWeights) {
-        // experts of many rows first, so that the pairs' last units are short
+        // Experts of many rows first, so that the pairs' last units are short; those of up to kGgSort
+        // rows, whose units take their stores' time whatever their rows, as they lie in memory.
+        auto key = [&](int rows) { return rows < kGgSort ? kGgSort : rows; };
         for (int e = threadIdx.x; e < a.E; e += kGgThreads) {
-            const int mine = ctl.first[e];
+            const int mine = key(ctl.first[e]);
             int rank = 0;
             for (int i = 0; i < a.E; i += 4) {
                 const int4 q = *reinterpret_cast<const int4 *>(&ctl.first[i]);
-                rank += (q.x > mine || (q.x == mine && i < e)) +
-                        (i + 1 < a.E && (q.y > mine || (q.y == mine && i + 1 < e))) +
-                        (i + 2 < a.E && (q.z > mine || (q.z == mine && i + 2 < e))) +
-                        (i + 3 < a.E && (q.w > mine || (q.w == mine && i + 3 < e)));
+                auto before = [&](int rows, int at) {
+                    const int k = key(rows);
+                    return at < a.E && (k > mine || (k == mine && at < e));
+                };
+                rank += before(q.x, i) + before(q.y, i + 1) + before(q.z, i + 2) + before(q.w, i + 3);
             }
             ctl.order[rank] = (uint16_t)e;
         }
