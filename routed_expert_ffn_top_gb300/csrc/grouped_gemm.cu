@@ -966,7 +966,11 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         int local = 0;
         uint32_t unit = 0, stored = 0;
         GgUnit x;
-        while (gg_next<true>(ctl, unit, x)) {
+        for (;;) {
+            bool more = gg_next<true>(ctl, unit, x);
+            // gated: both warps of a barrier go on or neither, also after a wait that gave up
+            if constexpr (kGated) more = !named_bar_or(bar, 64, !more);
+            if (!more) break;
             const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128) + 32 * (kGated ? quad & 1 : quad);
             if (kWeights && x.nrows == 0) {
                 if (c0 < a.C)
@@ -984,7 +988,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     ahead[i] = gg_codes(a, (int64_t)x.row0 + r, c0 + 16 * (lane >> 4), c0 < a.C && r < x.nrows);
                 }
             bool ok = gg_wait(&ctl.tfull[buf], parity, ctl);
-            if constexpr (kGated) ok = !named_bar_or(bar, 64, !ok);  // both go on or neither
+            if constexpr (kGated) ok = !named_bar_or(bar, 64, !ok);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = ctl.tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * G::kRows);

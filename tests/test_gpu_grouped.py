@@ -278,6 +278,31 @@ def test_gated_product_grad(sizes, tail, H, I, dtype, code):
     close(p[:n], want, want.abs() * (HALF[dtype] + 2.0 ** -19 * (1 + gx.abs())) + 2.0 ** -25)
 
 
+def test_gated_any_result_pitch():
+    """Rows of p that allow no wide stores."""
+    rows, wg, wu, offsets = gated_inputs([40, 0, 300], 3, 136, 96, BF16)
+    want = moe.moe_grouped_gated_product(rows, wg, wu, offsets.cuda(), workspace=workspace())
+    p = torch.full((350, 107), 7.0, dtype=BF16, device="cuda")
+    moe.moe_grouped_gated_product(rows, wg, wu, offsets.cuda(), out=p[2:345, 5:101], workspace=workspace())
+    assert torch.equal(p[2:345, 5:101], want)
+    p[2:345, 5:101] = 7.0
+    assert (p == 7.0).all()
+
+
+def test_gated_grad_with_given_results():
+    """Results of the caller's own, p and the gradient side by side in one buffer."""
+    g = gen(12)
+    offsets = ref.groups([30, 200])
+    gy, wd = ints((230, 64), g, 3, BF16), ints((2, 96, 64), g, 3, BF16)
+    codes, scales = moe.moe_checkpoint_quantize(torch.randn((230, 192), generator=g, device="cuda"), dtype=INT8)
+    want = moe.moe_grouped_gated_product_grad(gy, wd, offsets.cuda(), codes, scales, workspace=workspace())
+    buf = torch.full((231, 288), 7.0, dtype=BF16, device="cuda").reshape(-1)
+    ggu, p = buf[8:8 + 230 * 192].reshape(230, 192), buf[16 + 230 * 192:16 + 230 * 288].reshape(230, 96)
+    moe.moe_grouped_gated_product_grad(gy, wd, offsets.cuda(), codes, scales, grad_gate_up=ggu, p=p, workspace=workspace())
+    assert torch.equal(ggu, want[0]) and torch.equal(p, want[1])
+    assert (buf[:8] == 7.0).all() and (buf[16 + 230 * 288:] == 7.0).all()
+
+
 def test_gated_far_values():
     """Gates far from zero, infinite and NaN ones: as the formula's limits, no NaN of its own."""
     rows = torch.eye(8, dtype=BF16, device="cuda")
