@@ -19,15 +19,28 @@
 // summed: the last rows of the last step are zeroed in shared memory before the MMA reads them.
 //
 // Large tile: two CTAs share a tile (cta_group::2): 256 channels, 128 each, times up to 256
-// rows, each CTA holding half of the rows' operand: 64 KB of shared memory a stage of 128 of K.
-// Small tile, for few rows a group: one CTA, 128 channels, up to 32 rows.
+// rows, each CTA holding half of the rows' operand: 32 KB of shared memory a stage of 64 of K, so
+// a stage's copies are 62 bytes a cycle of its MMAs (one CTA's 128 x 256 takes 94).  Small tile, for
+// few rows a group: one CTA, 128 channels (gated: 64 of each projection), up to 16 rows.
 //
 // Per CTA (persistent, one an SM) 13 warps: 0-3 and 4-7 drain every other 16 rows (weights: 32
-// columns) of an accumulator, 8 and 9
-// issue the copies of the M and N sides, 10 the MMAs (the pair's first CTA for both), 11 zeroes
-// the last rows of a weights' gradient, 12 works out the units.  The accumulators are double-buffered.  An epilogue warp
-// has 32 channels in its lanes; it turns 16 rows of them round through shared memory, so that
-// a lane then has 16 channels of one row: whole 32-byte sectors, and half of an 8-bit block.
+// columns) of an accumulator, 8 and 9 issue the copies of the M and N sides, 10 the MMAs (the pair's
+// first CTA for both), 11 zeroes the last rows of a weights' gradient, 12 works out the units.  The
+// accumulators are double-buffered.  An epilogue warp has 32 channels in its lanes; where a lane
+// needs channels of one row, 16 rows of them are turned round through shared memory.
+//
+// What bounds it, on a GB300 (H = 2048, I = 768, 128 experts, top 8, bf16, groups as a router makes
+// them, 7 to 4104 rows at 8192 tokens):
+//   one group  65536 rows, K = N = 2048: 315 us, 1.75 PFLOP/s (the library's product: 308); K = 768: 132
+//              us (121); 16384 x 8192 x 8192: 1.18 ms (1.05 to 1.28).  MMAs, and the power they take.
+//   8192       gate and up 265 us, 1.55 PFLOP/s and 4.4 TB/s; down 150 us, 1.37 PFLOP/s and 5.1 TB/s;
+//   tokens     weights' gradient in fp32 229 us, 5.1 TB/s.  The weights' first way from HBM and the MMAs
+//              both: groups of under 215 rows take longer to copy than to multiply, and equal groups of
+//              512 rows take 245 and 137 us.
+//   4096       with the checkpoint 185 us, down's gradient through the gate 130 us, 1.04 and 0.74 GB: HBM,
+//   tokens     0.83 of the copy rate.
+//   21 tokens  gate and up 68 us for 447 MB, 0.97 of the copy rate.  One token 13 us for 50 MB, down 8.8
+//              us for 25 MB: start-up, and 96 to 128 CTAs with 16 KB copies.
 #include <string.h>
 
 #include "checkpoint.cuh"
