@@ -51,7 +51,7 @@
 namespace moe {
 
 constexpr int kGgThreads = 416;
-constexpr int kGgTurnBytes = 16 * 32 * 4;  // 16 rows of 32 channels that are turned round
+constexpr int kGgStaging = 3072;       // a warp's: 16 rows of 32 fp32 channels, and 16 of 16 bits
 constexpr int kGgMaxStages = 6;
 constexpr int kGgSort = 512;           // weights: rows up to which experts keep their order
 constexpr int kGgUnits = 8;            // units that are worked out ahead
@@ -71,7 +71,7 @@ struct GgTile {
     static constexpr int kPiece = kCtas == 1 ? kRows : 32;  // rows of a small copy of the N side
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr uint32_t kTmemCols = 2 * kRows;
-    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kGgTurnBytes + 1024;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 8 * kGgStaging + 1024;
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 512, "tensor memory");
     static_assert(kStageBytes % 1024 == 0 && kBChunk % 1024 == 0 && kStages <= kGgMaxStages, "stage alignment");
 };
@@ -106,7 +106,6 @@ struct GgCtl {
     int32_t valid_rows;
     alignas(16) int32_t first[kGroupedMaxExperts + 4];  // row tiles before expert e; weights: its rows
     uint16_t order[kGroupedMaxExperts];     // rows of expert e's tiles; weights: experts, those of most rows first
-    int32_t begin[kGroupedMaxExperts + 1];  // first row of expert e
 };
 
 // x, x2: the rows' boxes are a CTA's side, and of the small ones (xs, x2s) 32 rows.  Weights: x the
@@ -306,6 +305,15 @@ __device__ __forceinline__ void gg_tmem_dealloc(uint32_t tmem, uint32_t cols) {
 // of row tile u / nct.  Weights: unit u is channel tile u % nct, column tile (u / nct) % nnt of the
 // expert with the (u / nct / nnt)-th most rows, and the pairs take them there and back: what one
 // takes before another in one turn it takes after it in the next.
+// Rows [lo, hi) of expert e; offsets outside [0, rows] or running backwards are clamped.
+__device__ __forceinline__ void gg_span(const GgArgs &a, int e, int &lo, int &hi) {
+    int64_t b = 0, c = a.rows;
+    if (a.offsets) b = a.offsets[e], c = a.offsets[e + 1];
+    b = b < 0 ? 0 : (b > a.rows ? a.rows : b);
+    c = c < b ? b : (c > a.rows ? a.rows : c);
+    lo = (int)b, hi = (int)c;
+}
+
 template <Grouped kMode, typename G>
 __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int tiles) {
     constexpr bool kWeights = kMode == Grouped::kWeights;
@@ -319,7 +327,9 @@ __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int til
             if (u < (int64_t)a.E * a.nnt * a.nct) {
                 const int c = (int)u / a.nct, at = c / a.nnt;
                 x.e = ctl.order[at], x.ct = (int)u - c * a.nct, x.n0 = (c - at * a.nnt) * G::kRows;
-                x.row0 = ctl.begin[x.e], x.nrows = ctl.first[x.e];
+                int hi;
+                gg_span(a, x.e, x.row0, hi);
+                x.nrows = ctl.first[x.e];
                 x.n = a.N - x.n0 < G::kRows ? a.N - x.n0 : G::kRows;
             }
         } else if (t < tiles) {
@@ -329,10 +339,11 @@ __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int til
                 past = __ballot_sync(0xffffffffu, i <= a.E && ctl.first[i] <= t);
                 e += __popc(past);
             } while (past == 0xffffffffu);
-            const int q = ctl.order[e], at = (t - ctl.first[e]) * q;  // rows of a tile
-            x.row0 = ctl.begin[e] + at;
-            const int left = ctl.begin[e + 1] - x.row0;
-            x.n = x.nrows = left < q ? left : q;
+            const int q = ctl.order[e];  // rows of a tile
+            int lo, hi;
+            gg_span(a, e, lo, hi);
+            x.row0 = lo + (t - ctl.first[e]) * q;
+            x.n = x.nrows = hi - x.row0 < q ? hi - x.row0 : q;
             x.e = e, x.ct = ct, x.single = ctl.first[e + 1] - ctl.first[e] == 1;
             t += a.dt, ct += a.dct;
             if (ct >= a.nct) ct -= a.nct, ++t;
@@ -387,22 +398,33 @@ __device__ __forceinline__ void gg_put(unsigned char *dst, const uint32_t (&o)[k
     }
 }
 
-// Sixteen 16-bit results to a row.
-__device__ __forceinline__ void gg_put16(unsigned char *dst, const float (&v)[16], int half, int vec) {
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = gg_pack(v[2 * i], v[2 * i + 1], half);
-    gg_put(dst, o, 8, vec);
+__device__ __forceinline__ uint32_t gg_pack(uint64_t v, int half) {
+    float lo, hi;
+    f2_split(v, lo, hi);
+    return gg_pack(lo, hi, half);
 }
 
 // s = 1 / (1 + 2^(-g log2 e)) by the approximate power and reciprocal, within 2^-21 (1 + |g| / 4) of
 // its value for negative g, 2^-21 for others: what follows is rounded to 16 bits.  Below g = -87.3
 // the reciprocal is 0, for values under 2^-119.
-__device__ __forceinline__ float gg_sigmoid(float g) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return r;
+__device__ __forceinline__ uint64_t gg_sigmoid(uint64_t g) {
+    constexpr float k = -1.4426950408889634f;
+    float a, b;
+    f2_split(f2_mul(g, f2(k, k)), a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    f2_split(f2_add(f2(a, b), f2(1.0f, 1.0f)), a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2(a, b);
+}
+
+// Sixteen 16-bit results to a row.
+__device__ __forceinline__ void gg_put16(unsigned char *dst, const uint64_t (&v)[8], int half, int vec) {
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = gg_pack(v[i], half);
+    gg_put(dst, o, 8, vec);
 }
 
 // Lane's channel of 16 rows in, channels of a row out.  Rows are 128 bytes, their 16-byte pieces
@@ -417,6 +439,14 @@ __device__ __forceinline__ void gg_turn_read(const float *turn, int row, int at,
     for (int i = 0; i < kN; i += 4) {
         const float4 f = *reinterpret_cast<const float4 *>(turn + row * 32 + ((((at + i) >> 2) ^ (row & 7)) << 2));
         v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+    }
+}
+template <int kN>
+__device__ __forceinline__ void gg_turn_read(const float *turn, int row, int at, uint64_t (&v)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 2) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(turn + row * 32 + ((((at + 2 * i) >> 2) ^ (row & 7)) << 2));
+        v[i] = f.x, v[i + 1] = f.y;
     }
 }
 
@@ -440,11 +470,11 @@ __device__ __forceinline__ void gg_store_wait(int lane) {
     __syncwarp();
 }
 // Sixteen 16-bit results of row lane % 16, from channel 16 (lane / 16), to staging.
-__device__ __forceinline__ void gg_stage16(unsigned char *staging, int lane, const float (&v)[16], int half) {
+__device__ __forceinline__ void gg_stage16(unsigned char *staging, int lane, const uint64_t (&v)[8], int half) {
     const int r = lane & 15, h = lane >> 4;
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = gg_pack(v[2 * i], v[2 * i + 1], half);
+    for (int i = 0; i < 8; ++i) o[i] = gg_pack(v[i], half);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         *reinterpret_cast<uint4 *>(staging + r * 64 + (((2 * h + i) ^ ((r >> 1) & 3)) << 4)) =
@@ -541,14 +571,12 @@ __device__ __forceinline__ void gg_gated(const GgArgs &a, float *turn, float *ot
             if (a.code == MOE_CODE_INT8) gg_block<true>(a, v, (int64_t)row0 + c + r, col, lane, live);
             else gg_block<false>(a, v, (int64_t)row0 + c + r, col, lane, live);
         }
-        float g[8], u[8];
+        uint64_t g[4], u[4];
         gg_turn_read(tg, pr, pch, g);
         gg_turn_read(tu, pr, pch, u);
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = gg_pack(g[2 * i] * gg_sigmoid(g[2 * i]) * u[2 * i], g[2 * i + 1] * gg_sigmoid(g[2 * i + 1]) * u[2 * i + 1],
-                           a.half);
+        for (int i = 0; i < 4; ++i) o[i] = gg_pack(f2_mul(f2_mul(g[i], gg_sigmoid(g[i])), u[i]), a.half);
         if (c + pr < nrows) gg_put(dst + (int64_t)(c + pr) * a.ldo * 2, o, 4, a.vec);
     }
 }
@@ -581,21 +609,24 @@ __device__ __forceinline__ void gg_gated_grad(const GgArgs &a, const GgMaps &tm,
         const GgCodes now = next[0];
         next[0] = next[1];
         next[1] = gg_codes(a, row + 64, ch, c + 64 + r < nrows);
-        float q[16], g[16], u[16];
+        float v[16];
+        uint64_t q[8], g[8], u[8];
         unsigned char *const staging = reinterpret_cast<unsigned char *>(turn);
-        gg_store_wait<0>(lane);
-        tmem_ld16(d + c, q);
-        gg_turn_write(turn, lane, q);
+        tmem_ld16(d + c, v);
+        if (a.p) gg_store_wait<1>(lane);  // all but the last store, of p from its own memory
+        else gg_store_wait<0>(lane);
+        gg_turn_write(turn, lane, v);
         __syncwarp();
         gg_turn_read(turn, r, 16 * h, q);
         eight_values<kInt8>(now.g, now.gs, g);
         eight_values<kInt8>(now.u, now.us, u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float s = gg_sigmoid(g[i]), gsi = g[i] * s, t = q[i] * u[i];
-            u[i] *= gsi;                            // p
-            q[i] *= gsi;                            // grad of u
-            g[i] = t * (s + gsi * (1.0f - s));      // grad of g
+        for (int i = 0; i < 8; ++i) {
+            const uint64_t s = gg_sigmoid(g[i]), gs = f2_mul(g[i], s), t = f2_mul(q[i], u[i]);
+            const uint64_t rest = f2_fma(s, f2(-1.0f, -1.0f), f2(1.0f, 1.0f));
+            u[i] = f2_mul(u[i], gs);                       // p
+            q[i] = f2_mul(q[i], gs);                       // grad of u
+            g[i] = f2_mul(t, f2_fma(gs, rest, s));         // grad of g
         }
         if (c + 16 <= nrows) {
             __syncwarp();
@@ -604,9 +635,9 @@ __device__ __forceinline__ void gg_gated_grad(const GgArgs &a, const GgMaps &tm,
             gg_stage16(staging + 1024, lane, q, a.half);
             gg_store(tm.y, staging + 1024, (I + ch0) * 2, row0 + c, lane);
             if (a.p) {
-                gg_store_wait<1>(lane);
-                gg_stage16(staging, lane, u, a.half);
-                gg_store(tm.p, staging, ch0 * 2, row0 + c, lane);
+                gg_store_wait<2>(lane);  // the last p
+                gg_stage16(staging + 2048, lane, u, a.half);
+                gg_store(tm.p, staging + 2048, ch0 * 2, row0 + c, lane);
             }
         } else if (live) {
             unsigned char *dst = a.out + (row * (2 * I) + ch) * 2;
@@ -819,18 +850,13 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     pdl_wait();
     pdl_launch_dependents();
 
-    // row tiles before each expert; offsets outside [0, rows] or running backwards are clamped
+    // row tiles before each expert
     int carry = 0;
     for (int e0 = 0; e0 < a.E; e0 += kGgThreads) {
         const int e = e0 + threadIdx.x;
-        int64_t lo = 0, hi = 0;
-        if (e < a.E) {
-            if (!a.offsets) hi = a.rows;
-            else lo = a.offsets[e], hi = a.offsets[e + 1];
-            lo = lo < 0 ? 0 : (lo > a.rows ? a.rows : lo);
-            hi = hi < lo ? lo : (hi > a.rows ? a.rows : hi);
-        }
-        const int tiles = (int)((hi - lo + G::kRows - 1) / G::kRows);
+        int lo = 0, hi = 0;
+        if (e < a.E) gg_span(a, e, lo, hi);
+        const int tiles = (hi - lo + G::kRows - 1) / G::kRows;
         int inc = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -846,14 +872,13 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             chunk += t;
         }
         if (e < a.E) {
-            ctl.first[e] = kWeights ? (int)(hi - lo) : off + inc - tiles;
-            ctl.begin[e] = (int)lo;
+            ctl.first[e] = kWeights ? hi - lo : off + inc - tiles;
             // equal tiles: at most kRows, since a group of T tiles has at most T kRows rows
             if (!kWeights && tiles)
-                ctl.order[e] = (uint16_t)(((int)(hi - lo) + G::kGran * tiles - 1) / (G::kGran * tiles) * G::kGran);
+                ctl.order[e] = (uint16_t)((hi - lo + G::kGran * tiles - 1) / (G::kGran * tiles) * G::kGran);
             if (e == a.E - 1) {
                 ctl.first[a.E] = off + inc;
-                ctl.valid_rows = ctl.begin[a.E] = (int)hi;
+                ctl.valid_rows = hi;
             }
         }
         carry += chunk;
@@ -973,7 +998,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         gg_schedule<kMode, G>(a, ctl, tiles);
     } else {
         const int group = warp >> 2, quad = warp & 3;
-        unsigned char *const staging = turns + warp * kGgTurnBytes;
+        unsigned char *const staging = turns + warp * kGgStaging;
         float *const turn = reinterpret_cast<float *>(staging);
         const int bar = 1 + 2 * group + (quad & 1);  // gated: of the gate and up warps of the same channels
         int local = 0;
@@ -1010,7 +1035,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
             } else if constexpr (kMode == Grouped::kPlain) {
                 gg_plain<G>(a, tm.y, turn, d, lane, group, x.row0, x.nrows, c0, stored);
             } else if constexpr (kGated) {
-                gg_gated(a, turn, reinterpret_cast<float *>(turns + (warp ^ 2) * kGgTurnBytes), d, lane, group, bar, quad >= 2,
+                gg_gated(a, turn, reinterpret_cast<float *>(turns + (warp ^ 2) * kGgStaging), d, lane, group, bar, quad >= 2,
                          x.row0, x.nrows, c0);
                 if (a.codes && c0 == 0 && quad == 0)  // the scale rows' padding
                     for (int r = 32 * group + lane; r < x.nrows; r += 64)
