@@ -297,14 +297,6 @@ __device__ __forceinline__ void gg_tmem_dealloc(uint32_t tmem, uint32_t cols) {
 }
 
 // ------------------------------------------------------------------------------------ units
-// One warp works the units out and puts them into a ring that the other roles read: where each role
-// worked them out itself, the code that a unit begins with, which no warp had run for thousands of
-// cycles, kept the MMAs from their next unit for 1450 cycles.
-//
-// A pair's units.  Products: u = its number, + the number of pairs, ...; unit u is channel tile u % nct
-// of row tile u / nct.  Weights: unit u is channel tile u % nct, column tile (u / nct) % nnt of the
-// expert with the (u / nct / nnt)-th most rows, and the pairs take them there and back: what one
-// takes before another in one turn it takes after it in the next.
 // Rows [lo, hi) of expert e; offsets outside [0, rows] or running backwards are clamped.
 __device__ __forceinline__ void gg_span(const GgArgs &a, int e, int &lo, int &hi) {
     int64_t b = 0, c = a.rows;
@@ -314,6 +306,14 @@ __device__ __forceinline__ void gg_span(const GgArgs &a, int e, int &lo, int &hi
     lo = (int)b, hi = (int)c;
 }
 
+// One warp works the units out and puts them into a ring that the other roles read: where each role
+// worked them out itself, the code that a unit begins with, which no warp had run for thousands of
+// cycles, kept the MMAs from their next unit for 1450 cycles.
+//
+// A pair's units.  Products: u = its number, + the number of pairs, ...; unit u is channel tile u % nct
+// of row tile u / nct.  Weights: unit u is channel tile u % nct, column tile (u / nct) % nnt of the
+// expert with the (u / nct / nnt)-th most rows, and the pairs take them there and back: what one
+// takes before another in one turn it takes after it in the next.
 template <Grouped kMode, typename G>
 __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int tiles) {
     constexpr bool kWeights = kMode == Grouped::kWeights;
