@@ -252,7 +252,3 @@ def test_training_runs():
         losses = ex.train(M=256, H=64, I=96, E=4, k=2, steps=5, code=code)
         assert len(losses) == 5 and all(torch.isfinite(torch.tensor(losses)))
 
-
-def test_memory_kept():
-    a, b = ex.memory()
-    assert b < a / 2
