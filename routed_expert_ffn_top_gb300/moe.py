@@ -1110,10 +1110,6 @@ def _misfit(w, name, columns):
     raise ValueError("%s has shape %s, which does not fit rows of %d columns" % (name, tuple(w.shape), columns))
 
 
-def _offsets(offsets, E, device):
-    return None if offsets is None else _vector(offsets, "offsets", torch.int32, device, (E + 1,))
-
-
 def _status_workspace(device):
     """A status word of a call's own."""
     return torch.zeros(MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8, device=device)
@@ -1132,10 +1128,11 @@ def _checkpoint_outputs(codes, scales, rows, cols, dtype, dev):
         codes = torch.empty((rows, cols), dtype=dtype, device=dev)
     else:
         _vector(codes, "codes", dtype, dev, (rows, cols))
+    pitch = -(-cols // 512) * 16
     if scales is None:
-        scales = torch.empty((rows, _pitch(cols)), dtype=torch.uint8, device=dev)
+        scales = torch.empty((rows, pitch), dtype=torch.uint8, device=dev)
     else:
-        _vector(scales, "scales", torch.uint8, dev, (rows, _pitch(cols)))
+        _vector(scales, "scales", torch.uint8, dev, (rows, pitch))
     return codes, scales
 
 
@@ -1182,8 +1179,8 @@ def moe_grouped_product(rows, weights, offsets=None, transposed=False, dtype=Non
         if _expert_weights(w2, "weights", dev, dt) != (E, a, b):
             _misfit(w2, "weights", cols)
         p2 = w2.data_ptr()
-    ldx = _rows(rows, "rows", dev, dt, (R, cols))
-    off = _offsets(offsets, E, dev)
+    ldx = cols if rows.is_contiguous() else _rows(rows, "rows", dev, dt, (R, cols))
+    off = None if offsets is None else _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     ws = None if workspace is None else _workspace(workspace, dev)
     launch = _raw_stream(dev)
     if out is None:
@@ -1226,8 +1223,8 @@ def moe_grouped_gated_product(rows, w_gate, w_up, offsets=None, checkpoint=None,
         _misfit(w_gate, "w_gate", H)
     if _expert_weights(w_up, "w_up", dev, dt) != (E, H, I):
         _misfit(w_up, "w_up", H)
-    ldx = _rows(rows, "rows", dev, dt, (R, H))
-    off = _offsets(offsets, E, dev)
+    ldx = H if rows.is_contiguous() else _rows(rows, "rows", dev, dt, (R, H))
+    off = None if offsets is None else _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     if I % 32:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_grouped_gated_product")
     ws = None if workspace is None else _workspace(workspace, dev)
@@ -1270,8 +1267,8 @@ def moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, grad_
     E, I, h = _expert_weights(w_down, "w_down", dev, dt)
     if h != H:
         _misfit(w_down, "w_down", H)
-    ldg = _rows(grad_y, "grad_y", dev, dt, (R, H))
-    off = _offsets(offsets, E, dev)
+    ldg = H if grad_y.is_contiguous() else _rows(grad_y, "grad_y", dev, dt, (R, H))
+    off = None if offsets is None else _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     kind, crows, cols = _checkpoint(codes, scales, dev)
     if crows != R or cols != 2 * I:
         raise ValueError("codes must have shape %s, got %s" % ((R, 2 * I), (crows, cols)))
@@ -1314,14 +1311,14 @@ def moe_grouped_weight_grad(rows, grads, offsets=None, dtype=torch.float32, out=
     if grads.dim() != 2:
         _not_a_matrix(grads, "grads")
     N = grads.shape[1]
-    ldx = _rows(rows, "rows", dev, dt, (R, K))
+    ldx = K if rows.is_contiguous() else _rows(rows, "rows", dev, dt, (R, K))
     ldg = _rows(grads, "grads", dev, dt, (R, N))
     E, off = 1, None
     if offsets is not None:
         if offsets.dim() != 1 or offsets.shape[0] < 2:
             raise ValueError("offsets must have shape (E + 1,), got %s" % (tuple(offsets.shape),))
         E = offsets.shape[0] - 1
-        off = _offsets(offsets, E, dev)
+        off = None if offsets is None else _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     ws = None if workspace is None else _workspace(workspace, dev)
     launch = _raw_stream(dev)
     if out is not None:
@@ -1358,7 +1355,7 @@ def moe_checkpoint_quantize(x, dtype=torch.float8_e4m3fn, codes=None, scales=Non
     xcode = _row_dtype(x, "x")
     kind = _code_dtype(dtype)
     rows, cols = x.shape
-    ldx = _rows(x, "x", dev, x.dtype, (rows, cols))
+    ldx = cols if x.is_contiguous() else _rows(x, "x", dev, x.dtype, (rows, cols))
     if cols % 32:
         raise MoeError(MOE_ERR_UNSUPPORTED, "moe_checkpoint_quantize")
     launch = _raw_stream(dev)
