@@ -7,7 +7,8 @@ namespace moe {
 
 constexpr int kGroupedMaxExperts = 1024;
 
-enum class Grouped { kPlain, kGated, kGatedGrad, kWeights };
+// kWeights32: kWeights with an fp32 gradient.
+enum class Grouped { kPlain, kGated, kGatedGrad, kWeights, kWeights32 };
 
 // One grouped product (grouped_gemm.cu).  Channels: the columns of the result that lie on the
 // MMA's M side (kPlain the output's, kGated and kGatedGrad I, kWeights the rows' columns K).

@@ -17,6 +17,9 @@
 // Groups need no padding: a copy may run into the next expert's rows, whose results are dropped
 // by the epilogue (a row only reaches its own results).  In a weights' gradient rows are what is
 // summed: the last rows of the last step are zeroed in shared memory before the MMA reads them.
+// The tensor core's accumulators truncate: a chain of n MMAs is off by about n 2^-24, which a long
+// group would see in an fp32 gradient, so there 512 rows at a time are added up in registers (8192
+// tokens 4.3e-7 off in the 2-norm for 1.1e-6, in 234 us for 230; 256 rows at a time 2.2e-7, 240 us).
 //
 // Large tile: two CTAs share a tile (cta_group::2): 256 channels, 128 each, times up to 256
 // rows, each CTA holding half of the rows' operand: 32 KB of shared memory a stage of 64 of K, so
@@ -34,7 +37,7 @@
 //   one group  65536 rows, K = N = 2048: 315 us, 1.75 PFLOP/s (the library's product: 308); K = 768: 132
 //              us (121); 16384 x 8192 x 8192: 1.18 ms (1.05 to 1.28).  MMAs, and the power they take.
 //   8192       gate and up 265 us, 1.55 PFLOP/s and 4.4 TB/s; down 150 us, 1.37 PFLOP/s and 5.1 TB/s;
-//   tokens     weights' gradient in fp32 229 us, 5.1 TB/s.  The weights' first way from HBM and the MMAs
+//   tokens     weights' gradient in fp32 234 us, 5.0 TB/s.  The weights' first way from HBM and the MMAs
 //              both: groups of under 215 rows take longer to copy than to multiply, and equal groups of
 //              512 rows take 245 and 137 us.
 //   4096       with the checkpoint 185 us, down's gradient through the gate 130 us, 1.04 and 0.74 GB: HBM,
@@ -50,7 +53,8 @@
 
 namespace moe {
 
-constexpr int kGgThreads = 416;
+constexpr int kGgWarps = 13;           // fp32 weights: 16, whose registers are shared out (below)
+constexpr int kGgChain = 512;          // fp32 weights: rows that one accumulator sums
 constexpr int kGgStaging = 3072;       // a warp's: 16 rows of 32 fp32 channels, and 16 of 16 bits
 constexpr int kGgMaxStages = 6;
 constexpr int kGgSort = 512;           // weights: rows up to which experts keep their order
@@ -90,6 +94,9 @@ struct alignas(16) GgUnit {
     __device__ __forceinline__ bool ragged() const { return nrows % 16 != 0; }
 };
 
+__host__ __device__ constexpr bool gg_sums(Grouped m) { return m == Grouped::kWeights || m == Grouped::kWeights32; }
+__host__ __device__ constexpr int gg_threads(Grouped m) { return 32 * (m == Grouped::kWeights32 ? 16 : kGgWarps); }
+
 struct GgCtl {
     GgUnit units[kGgUnits];
     uint64_t ufull[kGgUnits];
@@ -102,7 +109,7 @@ struct GgCtl {
     uint64_t done;
     uint32_t tmem;
     volatile int abort;
-    int32_t wsum[kGgThreads / 32];
+    int32_t wsum[16];
     int32_t valid_rows;
     alignas(16) int32_t first[kGroupedMaxExperts + 4];  // row tiles before expert e; weights: its rows
     uint16_t order[kGroupedMaxExperts];     // rows of expert e's tiles; weights: experts, those of most rows first
@@ -188,16 +195,24 @@ __device__ __noinline__ bool gg_wait_slow(uint32_t bar, uint32_t parity, GgCtl *
     }
     return true;
 }
-template <bool kCluster = false>
+// kInline: without a call, for kernels whose warps share their registers out.
+template <bool kCluster = false, bool kInline = false>
 __device__ __forceinline__ bool gg_wait_one(uint32_t bar, uint32_t parity, GgCtl &ctl) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
         if (gg_try<kCluster>(bar, parity)) return true;
-    return gg_wait_slow<kCluster>(bar, parity, &ctl);
+    if constexpr (!kInline) return gg_wait_slow<kCluster>(bar, parity, &ctl);
+    const uint64_t t0 = globaltimer_ns();
+    while (!gg_try<kCluster>(bar, parity)) {
+        if (!ctl.abort && globaltimer_ns() - t0 > kWaitLimitNs) ctl.abort = 1;
+        if (ctl.abort) return false;
+    }
+    return true;
 }
 // The same for a whole warp, with one answer.
+template <bool kInline = false>
 __device__ __forceinline__ bool gg_wait(uint64_t *bar, uint32_t parity, GgCtl &ctl) {
-    return __all_sync(0xffffffffu, gg_wait_one(smem_u32(bar), parity, ctl));
+    return __all_sync(0xffffffffu, gg_wait_one<false, kInline>(smem_u32(bar), parity, ctl));
 }
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool gg_elect() {
@@ -316,7 +331,7 @@ __device__ __forceinline__ void gg_span(const GgArgs &a, int e, int &lo, int &hi
 // takes before another in one turn it takes after it in the next.
 template <Grouped kMode, typename G>
 __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int tiles) {
-    constexpr bool kWeights = kMode == Grouped::kWeights;
+    constexpr bool kWeights = gg_sums(kMode);
     const int lane = threadIdx.x & 31, pair = blockIdx.x / G::kCtas, pairs = gridDim.x / G::kCtas;
     int t = pair / a.nct, ct = pair % a.nct, e = 0;
     for (uint32_t turn = 0;; ++turn) {
@@ -350,7 +365,7 @@ __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int til
         }
         x.n = (x.n + G::kGran - 1) / G::kGran * G::kGran;
         const uint32_t slot = turn % kGgUnits;
-        if (!gg_wait(&ctl.uempty[slot], ((turn / kGgUnits) & 1u) ^ 1u, ctl)) return;
+        if (!gg_wait<kMode == Grouped::kWeights32>(&ctl.uempty[slot], ((turn / kGgUnits) & 1u) ^ 1u, ctl)) return;
         if (lane == 0) {
             ctl.units[slot] = x;
             mbar_arrive(&ctl.ufull[slot]);
@@ -361,11 +376,11 @@ __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int til
 }
 
 // The next unit, for a whole warp or for one thread; false when none is left or a wait gave up.
-template <bool kWarp>
+template <bool kWarp, bool kInline = false>
 __device__ __forceinline__ bool gg_next(GgCtl &ctl, uint32_t &at, GgUnit &x) {
     const uint32_t slot = at % kGgUnits, parity = (at / kGgUnits) & 1u;
     ++at;
-    if (!(kWarp ? gg_wait(&ctl.ufull[slot], parity, ctl) : gg_wait_one(smem_u32(&ctl.ufull[slot]), parity, ctl))) return false;
+    if (!(kWarp ? gg_wait<kInline>(&ctl.ufull[slot], parity, ctl) : gg_wait_one<false, kInline>(smem_u32(&ctl.ufull[slot]), parity, ctl))) return false;
     x = ctl.units[slot];
     if (kWarp) __syncwarp();
     if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ctl.uempty[slot]);
@@ -649,48 +664,55 @@ __device__ __forceinline__ void gg_gated_grad(const GgArgs &a, const GgMaps &tm,
     }
 }
 
-// A warp's 32 rows of the gradient times the n columns of a unit, by tensor stores of 64-byte rows
-// (clipped at the gradient's edges) through its staging memory; zeros for an expert without rows.
+// A warp's 32 rows of 32 columns of the gradient, by tensor stores of 64-byte rows (clipped at the
+// gradient's edges) through its staging memory.
+template <bool k32>
+__device__ __forceinline__ void gg_weights_put(const GgArgs &a, const CUtensorMap &tm, unsigned char *staging, int lane, int e,
+                                               int ch0, int col, const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < (k32 ? 2 : 1); ++q) {
+        gg_store_wait<0>(lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 o;
+            if constexpr (k32) {
+                o = make_uint4(__float_as_uint(v[16 * q + 4 * i]), __float_as_uint(v[16 * q + 4 * i + 1]),
+                               __float_as_uint(v[16 * q + 4 * i + 2]), __float_as_uint(v[16 * q + 4 * i + 3]));
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = gg_pack(v[8 * i + 2 * j], v[8 * i + 2 * j + 1], a.half);
+                o = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4 *>(staging + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            asm volatile(
+                "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&tm)),
+                "r"(col * (k32 ? 4 : 2) + 64 * q), "r"(ch0), "r"(e), "r"(smem_u32(staging))
+                : "memory");
+    }
+}
+
+// The warp's part of a unit: every other 32 of its n columns; zeros for an expert without rows.
+template <bool k32>
 __device__ __forceinline__ void gg_weights(const GgArgs &a, const CUtensorMap &tm, unsigned char *staging, uint32_t d,
                                            int lane, int group, int e, int ch0, int n0, int n, bool zero) {
-    const int elem = a.out32 ? 4 : 2, parts = a.out32 ? 2 : 1;
 #pragma unroll 1
     for (int c = 32 * group; c < n && n0 + c < a.N; c += 64) {
-        uint32_t v[32];
-        if (zero) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-        } else {
-            tmem_ld32(d + c, v);
-            tmem_ld_wait(v);
+        float v[32];
+        uint32_t w[32];
+        if (!zero) {
+            tmem_ld32(d + c, w);
+            tmem_ld_wait(w);
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            if (q == parts) break;
-            gg_store_wait<0>(lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint4 o;
-                if (a.out32) {
-                    o = make_uint4(v[16 * q + 4 * i], v[16 * q + 4 * i + 1], v[16 * q + 4 * i + 2], v[16 * q + 4 * i + 3]);
-                } else {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = gg_pack(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]), a.half);
-                    o = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                *reinterpret_cast<uint4 *>(staging + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = o;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                asm volatile(
-                    "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
-                    "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&tm)),
-                    "r"((n0 + c) * elem + 64 * q), "r"(ch0), "r"(e), "r"(smem_u32(staging))
-                    : "memory");
-        }
+        for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : __uint_as_float(w[i]);
+        gg_weights_put<k32>(a, tm, staging, lane, e, ch0, n0 + c, v);
     }
 }
 
@@ -709,7 +731,7 @@ __device__ __forceinline__ void gg_zero(unsigned char *p, int64_t bytes, bool wi
 // the coordinates and addresses worked out there it took 400 cycles, in every turn of the ring.
 template <Grouped kMode, bool kTrans, typename G, bool kSideM>
 __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, GgCtl &ctl, uint32_t base, int rank) {
-    constexpr bool kWeights = kMode == Grouped::kWeights, kGated = kMode == Grouped::kGated;
+    constexpr bool kWeights = gg_sums(kMode), kGated = kMode == Grouped::kGated;
     constexpr int kCtas = G::kCtas;
     constexpr bool kByK = kSideM ? kTrans : !kWeights;  // copies of 64 of K, else of 64 channels
     constexpr int kChunk = !kByK ? G::kMajor : kSideM ? G::kAChunk : G::kBChunk;
@@ -728,7 +750,7 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
         uint32_t dst = base, slot = 0, parity = 1, it = 0, unit = 0;  // slot: 8 x stage
         bool ok = true;
         GgUnit x;
-        while (ok && gg_next<false>(ctl, unit, x)) {
+        while (ok && gg_next<false, kMode == Grouped::kWeights32>(ctl, unit, x)) {
             const uint64_t pol = !kWeights && kSideM && x.single ? once : keep;
             int n = wide(x, rank), both = kCtas == 1 ? n : wide(x, 0) + wide(x, 1), chunk = kChunk, dx = 128, dy = 0;
             const int part_n = x.n / kCtas;
@@ -760,7 +782,7 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
                         const int deep = (left + 63) / 64;
                         copies = n ? deep : 0, bytes = (uint32_t)(both / G::kChunks * deep * chunk);
                     }
-                    if (!(ok = gg_wait_one(empty0 + slot, parity, ctl))) break;
+                    if (!(ok = gg_wait_one<false, kMode == Grouped::kWeights32>(empty0 + slot, parity, ctl))) break;
                     // the pair's first CTA expects both CTAs' bytes; a stage whose last rows are to be
                     // zeroed first is each CTA's own
                     if (kWeights && ragged && left <= G::kK) {
@@ -811,10 +833,11 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
 // ----------------------------------------------------------------------------------- kernel
 // kTrans: the M side's operand is K-major (weights [channels][K]), else channel-major.
 template <Grouped kMode, bool kTrans, typename G>
-__global__ void __launch_bounds__(kGgThreads, 1)
+__global__ void __launch_bounds__(gg_threads(kMode), 1)
 grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
-    constexpr bool kWeights = kMode == Grouped::kWeights, kGated = kMode == Grouped::kGated;
-    constexpr int kCtas = G::kCtas;
+    constexpr bool kWeights = gg_sums(kMode), kGated = kMode == Grouped::kGated;
+    constexpr int kCtas = G::kCtas, kThreads = gg_threads(kMode);
+    constexpr bool kLong = kMode == Grouped::kWeights32;
     extern __shared__ unsigned char smem_raw[];
     // the same offset in both CTAs of a pair: their descriptors are the first one's
     unsigned char *stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -852,7 +875,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
 
     // row tiles before each expert
     int carry = 0;
-    for (int e0 = 0; e0 < a.E; e0 += kGgThreads) {
+    for (int e0 = 0; e0 < a.E; e0 += kThreads) {
         const int e = e0 + threadIdx.x;
         int lo = 0, hi = 0;
         if (e < a.E) gg_span(a, e, lo, hi);
@@ -866,7 +889,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         if (lane == 31) ctl.wsum[warp] = inc;
         __syncthreads();
         int off = carry, chunk = 0;
-        for (int w = 0; w < kGgThreads / 32; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             const int t = ctl.wsum[w];
             if (w < warp) off += t;
             chunk += t;
@@ -888,7 +911,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         // Experts of many rows first, so that the pairs' last units are short; those of up to kGgSort
         // rows, whose units take their stores' time whatever their rows, as they lie in memory.
         auto key = [&](int rows) { return rows < kGgSort ? kGgSort : rows; };
-        for (int e = threadIdx.x; e < a.E; e += kGgThreads) {
+        for (int e = threadIdx.x; e < a.E; e += kThreads) {
             const int mine = key(ctl.first[e]);
             int rank = 0;
             for (int i = 0; i < a.E; i += 4) {
@@ -907,96 +930,10 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     else cluster_sync();
     tc_fence_after();
     const int tiles = kWeights ? a.E : carry;
-
-    if (warp == 8 || warp == 9) {
-        if (warp == 8) gg_produce<kMode, kTrans, G, true>(tm, a, ctl, smem_u32(stages), rank);
-        else gg_produce<kMode, kTrans, G, false>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank);
-    } else if (warp == 10) {
-        if (rank == 0) {
-            // 128-byte swizzle, 8-row atoms 1 KB apart.  K-major: a K step of 16 is 32 bytes, a chunk
-            // of 64 of K apart from the next.  Channel-major: a K step is two atoms, and channels
-            // 64 apart a chunk.  A step only moves the address field (16-byte units).
-            constexpr bool kAMajor = !kTrans, kBMajor = kWeights;  // channel-major operands
-            const uint64_t a0 = umma_smem_desc(smem_u32(stages), kAMajor ? G::kMajor : 16, 1024, 2);
-            const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, kBMajor ? G::kMajor : 16, 1024, 2);
-            const uint32_t full0 = smem_u32(&ctl.full[0]);
-            if (gg_elect()) {
-                const int parts = kWeights ? 1 : a.parts, summed = a.K;
-                const uint32_t idesc0 = a.idesc, tmem = ctl.tmem;
-                uint32_t stage = 0, parity = 0, at = 0, unit = 0;
-                bool ok = true;
-                GgUnit x;
-                while (ok && gg_next<false>(ctl, at, x)) {
-                    const int length = kWeights ? x.nrows : summed;
-                    if (kWeights && length == 0) continue;
-                    const uint32_t buf = unit & 1u, tparity = ((unit >> 1) & 1u) ^ 1u;
-                    const uint32_t d = tmem + buf * G::kRows, idesc = idesc0 | (uint32_t)(x.n >> 3) << 17;
-                    bool first = true;
-                    ++unit;
-                    ok = gg_wait_one(smem_u32(&ctl.tempty[buf]), tparity, ctl);
-                    tc_fence_after();
-                    for (int part = 0; part < parts && ok; ++part)
-                        for (int left = length; left > 0; left -= G::kK) {
-                            const uint64_t ad = a0 + stage * (G::kStageBytes >> 4);
-                            const uint64_t bd = b0 + stage * (G::kStageBytes >> 4);
-                            auto step = [&](int ks, bool accumulate) {
-                                gg_mma<kCtas>(d, ad + (kAMajor ? ks * 128 : (ks >> 2) * (G::kAChunk >> 4) + (ks & 3) * 2),
-                                              bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
-                                              accumulate);
-                            };
-                            if (!(ok = gg_wait_one<kWeights && kCtas == 2>(full0 + 8 * stage, parity, ctl))) break;
-                            tc_fence_after();
-                            step(0, !first);
-                            first = false;
-                            if (left >= G::kK) {
-#pragma unroll
-                                for (int ks = 1; ks < G::kK / 16; ++ks) step(ks, true);
-                            } else {
-#pragma unroll 1
-                                for (int ks = 1; ks * 16 < left; ++ks) step(ks, true);
-                            }
-                            gg_commit<kCtas>(&ctl.empty[stage]);
-                            if (++stage == G::kStages) stage = 0, parity ^= 1u;
-                        }
-                    if (ok) gg_commit<kCtas>(&ctl.tfull[buf]);
-                }
-                // every issued MMA has completed before the CTAs free their tensor memory
-                if constexpr (kCtas == 1) umma_commit(&ctl.done);
-                else
-                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                                     smem_u32(&ctl.done))
-                                 : "memory");
-                if (!mbar_wait_bounded(&ctl.done, 0)) ctl.abort = 1;
-            }
-            __syncwarp();
-        }
-    } else if (warp == 11) {
-        if constexpr (kWeights) {
-            // rows past the group's end within the last K step, as zeros: both operands, since what is
-            // there may be a NaN
-            int total = 0;
-            uint32_t phase = 0, unit = 0;
-            GgUnit x;
-            while (gg_next<true>(ctl, unit, x)) {
-                total += (x.nrows + G::kK - 1) / G::kK;
-                if (!x.ragged()) continue;
-                const int stage = (total - 1) % G::kStages;
-                if (!gg_wait(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
-                phase ^= 1u << stage;
-                const int from = x.nrows % G::kK, to = (from + 15) / 16 * 16;
-                unsigned char *S = stages + stage * G::kStageBytes;
-                for (int i = lane; i < (to - from) * 32; i += 32) {
-                    const int ch = i & 3, at = i >> 2;  // four chunks, 16-byte pieces of their rows
-                    *reinterpret_cast<uint4 *>(S + ch * G::kMajor + (from + (at >> 3)) * 128 + (at & 7) * 16) = uint4{0, 0, 0, 0};
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) gg_arrive_release(gg_leader<kCtas>(&ctl.full[stage]), 2 / kCtas);
-            }
-        }
-    } else if (warp == 12) {
-        gg_schedule<kMode, G>(a, ctl, tiles);
-    } else {
+    if (warp < 8) {
+        // fp32 weights: 128 registers a thread at the launch, 200 for the two warpgroups here and 56 for the
+        // other two: in all the launch's 65,536
+        if constexpr (kLong) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int group = warp >> 2, quad = warp & 3;
         unsigned char *const staging = turns + warp * kGgStaging;
         float *const turn = reinterpret_cast<float *>(staging);
@@ -1005,14 +942,50 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         uint32_t unit = 0, stored = 0;
         GgUnit x;
         for (;;) {
-            bool more = gg_next<true>(ctl, unit, x);
+            bool more = gg_next<true, kLong>(ctl, unit, x);
             // gated: both warps of a barrier go on or neither, also after a wait that gave up
             if constexpr (kGated) more = !named_bar_or(bar, 64, !more);
             if (!more) break;
             const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128) + 32 * (kGated ? quad & 1 : quad);
             if (kWeights && x.nrows == 0) {
                 if (c0 < a.C)
-                    gg_weights(a, tm.y, staging, 0, lane, group, x.e, c0, x.n0, x.n, true);
+                    gg_weights<kLong>(a, tm.y, staging, 0, lane, group, x.e, c0, x.n0, x.n, true);
+                continue;
+            }
+            if (kLong && x.nrows > kGgChain) {
+                // The accumulators truncate, so a long chain of MMAs loses what rounded sums keep: kGgChain
+                // rows at a time are added up here, in registers.  The tensor memory is free again
+                // before the results are stored.
+                float sum[4][32];
+#pragma unroll
+                for (int i = 0; i < 128; ++i) sum[i / 32][i % 32] = 0.0f;
+                bool ok = true;
+#pragma unroll 1
+                for (int rest = x.nrows; rest > 0; rest -= kGgChain, ++local) {
+                    const int buf = local & 1;
+                    if (!(ok = gg_wait<true>(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl))) break;
+                    tc_fence_after();
+                    const uint32_t d = ctl.tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * G::kRows) + 32 * group;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (c0 >= a.C || 64 * i + 32 * group >= x.n) continue;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float v[16];
+                            tmem_ld16(d + 64 * i + 16 * h, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[i][16 * h + j] += v[j];
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.tempty[buf]));
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c0 < a.C && 64 * i + 32 * group < x.n && x.n0 + 64 * i + 32 * group < a.N)
+                        gg_weights_put<true>(a, tm.y, staging, lane, x.e, c0, x.n0 + 64 * i + 32 * group, sum[i]);
                 continue;
             }
             const int buf = local & 1;
@@ -1025,7 +998,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     const int r = 32 * i + 16 * group + (lane & 15);
                     ahead[i] = gg_codes(a, (int64_t)x.row0 + r, c0 + 16 * (lane >> 4), c0 < a.C && r < x.nrows);
                 }
-            bool ok = gg_wait(&ctl.tfull[buf], parity, ctl);
+            bool ok = gg_wait<kLong>(&ctl.tfull[buf], parity, ctl);
             if constexpr (kGated) ok = !named_bar_or(bar, 64, !ok);
             if (!ok) break;
             tc_fence_after();
@@ -1044,7 +1017,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
                 else gg_gated_grad<false>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
             } else {
-                gg_weights(a, tm.y, staging, d, lane, group, x.e, c0, x.n0, x.n, false);
+                gg_weights<kLong>(a, tm.y, staging, d, lane, group, x.e, c0, x.n0, x.n, false);
             }
             tc_fence_before();
             __syncwarp();
@@ -1062,6 +1035,102 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     gg_zero(a.scales + r * a.pitch, a.pitch, true);
                 }
             }
+    } else {
+        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 8 || warp == 9) {
+            if (warp == 8) gg_produce<kMode, kTrans, G, true>(tm, a, ctl, smem_u32(stages), rank);
+            else gg_produce<kMode, kTrans, G, false>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank);
+        } else if (warp == 10) {
+            if (rank == 0) {
+                // 128-byte swizzle, 8-row atoms 1 KB apart.  K-major: a K step of 16 is 32 bytes, a chunk
+                // of 64 of K apart from the next.  Channel-major: a K step is two atoms, and channels
+                // 64 apart a chunk.  A step only moves the address field (16-byte units).
+                constexpr bool kAMajor = !kTrans, kBMajor = kWeights;  // channel-major operands
+                const uint64_t a0 = umma_smem_desc(smem_u32(stages), kAMajor ? G::kMajor : 16, 1024, 2);
+                const uint64_t b0 = umma_smem_desc(smem_u32(stages) + G::kABytes, kBMajor ? G::kMajor : 16, 1024, 2);
+                const uint32_t full0 = smem_u32(&ctl.full[0]);
+                if (gg_elect()) {
+                    const int parts = kWeights ? 1 : a.parts, summed = a.K;
+                    const uint32_t idesc0 = a.idesc, tmem = ctl.tmem;
+                    uint32_t stage = 0, parity = 0, at = 0, unit = 0;
+                    bool ok = true;
+                    GgUnit x;
+                    while (ok && gg_next<false, kLong>(ctl, at, x)) {
+                        const int length = kWeights ? x.nrows : summed;
+                        if (kWeights && length == 0) continue;
+                        const uint32_t idesc = idesc0 | (uint32_t)(x.n >> 3) << 17;
+                        for (int rest = length; rest > 0 && ok; rest -= kGgChain) {
+                            const int take = kLong && rest > kGgChain ? kGgChain : rest;
+                            const uint32_t buf = unit & 1u, tparity = ((unit >> 1) & 1u) ^ 1u;
+                            const uint32_t d = tmem + buf * G::kRows;
+                            bool first = true;
+                            ++unit;
+                            ok = gg_wait_one<false, kLong>(smem_u32(&ctl.tempty[buf]), tparity, ctl);
+                            tc_fence_after();
+                            for (int part = 0; part < parts && ok; ++part)
+                                for (int left = take; left > 0; left -= G::kK) {
+                                    const uint64_t ad = a0 + stage * (G::kStageBytes >> 4);
+                                    const uint64_t bd = b0 + stage * (G::kStageBytes >> 4);
+                                    auto step = [&](int ks, bool accumulate) {
+                                        gg_mma<kCtas>(d, ad + (kAMajor ? ks * 128 : (ks >> 2) * (G::kAChunk >> 4) + (ks & 3) * 2),
+                                                      bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
+                                                      accumulate);
+                                    };
+                                    if (!(ok = gg_wait_one<kWeights && kCtas == 2, kLong>(full0 + 8 * stage, parity, ctl))) break;
+                                    tc_fence_after();
+                                    step(0, !first);
+                                    first = false;
+                                    if (left >= G::kK) {
+#pragma unroll
+                                        for (int ks = 1; ks < G::kK / 16; ++ks) step(ks, true);
+                                    } else {
+#pragma unroll 1
+                                        for (int ks = 1; ks * 16 < left; ++ks) step(ks, true);
+                                    }
+                                    gg_commit<kCtas>(&ctl.empty[stage]);
+                                    if (++stage == G::kStages) stage = 0, parity ^= 1u;
+                                }
+                            if (ok) gg_commit<kCtas>(&ctl.tfull[buf]);
+                            if (!kLong) break;  // one accumulator sums the whole unit
+                        }
+                    }
+                    // every issued MMA has completed before the CTAs free their tensor memory
+                    if constexpr (kCtas == 1) umma_commit(&ctl.done);
+                    else
+                        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                                         smem_u32(&ctl.done))
+                                     : "memory");
+                    if (!mbar_wait_bounded(&ctl.done, 0)) ctl.abort = 1;
+                }
+                __syncwarp();
+            }
+        } else if (warp == 11) {
+            if constexpr (kWeights) {
+                // rows past the group's end within the last K step, as zeros: both operands, since what is
+                // there may be a NaN
+                int total = 0;
+                uint32_t phase = 0, unit = 0;
+                GgUnit x;
+                while (gg_next<true, kLong>(ctl, unit, x)) {
+                    total += (x.nrows + G::kK - 1) / G::kK;
+                    if (!x.ragged()) continue;
+                    const int stage = (total - 1) % G::kStages;
+                    if (!gg_wait<kLong>(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
+                    phase ^= 1u << stage;
+                    const int from = x.nrows % G::kK, to = (from + 15) / 16 * 16;
+                    unsigned char *S = stages + stage * G::kStageBytes;
+                    for (int i = lane; i < (to - from) * 32; i += 32) {
+                        const int ch = i & 3, at = i >> 2;  // four chunks, 16-byte pieces of their rows
+                        *reinterpret_cast<uint4 *>(S + ch * G::kMajor + (from + (at >> 3)) * 128 + (at & 7) * 16) = uint4{0, 0, 0, 0};
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) gg_arrive_release(gg_leader<kCtas>(&ctl.full[stage]), 2 / kCtas);
+                }
+            }
+        } else if (warp == 12) {
+            gg_schedule<kMode, G>(a, ctl, tiles);
+        }
     }
 
     tc_fence_before();
@@ -1078,7 +1147,7 @@ static cudaError_t grouped_as(const GgMaps &tm, GgArgs a, cudaStream_t stream) {
     constexpr int per = kMode == Grouped::kGated ? G::kCh / 2 : G::kCh;
     a.nct = (a.C + per - 1) / per;
     a.nnt = (a.N + G::kRows - 1) / G::kRows;
-    const int64_t tiles = kMode == Grouped::kWeights ? (int64_t)a.E * a.nnt : (a.rows < a.E ? a.rows : a.rows / G::kRows + a.E);
+    const int64_t tiles = gg_sums(kMode) ? (int64_t)a.E * a.nnt : (a.rows < a.E ? a.rows : a.rows / G::kRows + a.E);
     const int64_t units = tiles * a.nct, most = num_sms() / G::kCtas;
     const int64_t pairs = units < 1 ? 1 : (units < most ? units : most);
     a.dt = (int)(pairs / a.nct), a.dct = (int)(pairs % a.nct);
@@ -1086,7 +1155,7 @@ static cudaError_t grouped_as(const GgMaps &tm, GgArgs a, cudaStream_t stream) {
     cudaError_t err = ensure_smem((const void *)fn, G::kSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
-    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)(pairs * G::kCtas)), dim3(kGgThreads), G::kSmem, stream, attrs,
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)(pairs * G::kCtas)), dim3(gg_threads(kMode)), G::kSmem, stream, attrs,
                                            G::kCtas > 1 ? G::kCtas : 0);
     return cudaLaunchKernelEx(&cfg, fn, tm, a);
 }
@@ -1186,7 +1255,9 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
         if (grad && g.p) result_map(&tm.p, g.p, g.channels, g.channels, 2);
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (weights) return grouped_as<Grouped::kWeights, false, GgLarge>(tm, a, stream);
+    if (weights)
+        return a.out32 ? grouped_as<Grouped::kWeights32, false, GgLarge>(tm, a, stream)
+                       : grouped_as<Grouped::kWeights, false, GgLarge>(tm, a, stream);
     return small ? grouped_tile<GgSmall>(tm, a, g, stream) : grouped_tile<GgLarge>(tm, a, g, stream);
 }
 

@@ -177,6 +177,20 @@ def test_weight_grad_keeps_a_bad_row_within_its_group():
     assert torch.isnan(got[1]).all() and torch.isnan(got[3]).all()
 
 
+def test_weight_grad_of_long_groups():
+    """An fp32 gradient of 65,536 rows in one group.  Chains of 32 MMAs, each of whose additions truncates
+    by at most 2^-23 of the sum so far, added up by 127 rounded additions of at most 2^-24: 32 2^-23 +
+    127 2^-24 of the 2-norm.  (One chain of 4096 MMAs would be off by up to 4096 2^-23.)"""
+    g = gen(13)
+    rows = torch.randn((65536 + 77, 72), generator=g, device="cuda").to(BF16)
+    grads = torch.randn((65536 + 77, 40), generator=g, device="cuda").to(BF16)
+    offsets = torch.tensor([0, 30, 65566, 65613], dtype=torch.int32)
+    got = moe.moe_grouped_weight_grad(rows, grads, offsets.cuda(), workspace=workspace())
+    want = ref.weight_grad(rows, grads, offsets)
+    for e in range(3):
+        assert float((got[e].double() - want[e]).norm()) <= (32 * 2.0 ** -23 + 127 * 2.0 ** -24) * float(want[e].norm())
+
+
 def test_weight_grad_of_column_halves():
     """The two halves of one matrix of gradients, by their pitch."""
     g = gen(10)
