@@ -17,9 +17,10 @@
 // Groups need no padding: a copy may run into the next expert's rows, whose results are dropped
 // by the epilogue (a row only reaches its own results).  In a weights' gradient rows are what is
 // summed: the last rows of the last step are zeroed in shared memory before the MMA reads them.
-// The tensor core's accumulators truncate: a chain of n MMAs is off by about n 2^-24, which a long
-// group would see in an fp32 gradient, so there 512 rows at a time are added up in registers (8192
-// tokens 4.3e-7 off in the 2-norm for 1.1e-6, in 234 us for 230; 256 rows at a time 2.2e-7, 240 us).
+// The tensor core's accumulators truncate: a chain of n MMAs is off by about n 2^-24.  Rows, unlike K, have
+// no bound, so a long group's sums are added up in registers: of 512 rows at a time for an fp32 gradient
+// (8192 tokens 4.3e-7 off in the 2-norm for 1.1e-6, in 234 us for 230; 256 rows at a time 2.2e-7, 240 us),
+// of 8192 rows for a 16-bit one (2^-15, a sixteenth of f16's half step).
 //
 // Large tile: two CTAs share a tile (cta_group::2): 256 channels, 128 each, times up to 256
 // rows, each CTA holding half of the rows' operand: 32 KB of shared memory a stage of 64 of K, so
@@ -53,8 +54,7 @@
 
 namespace moe {
 
-constexpr int kGgWarps = 13;           // fp32 weights: 16, whose registers are shared out (below)
-constexpr int kGgChain = 512;          // fp32 weights: rows that one accumulator sums
+constexpr int kGgWarps = 13;           // weights: 16, whose registers are shared out (below)
 constexpr int kGgStaging = 3072;       // a warp's: 16 rows of 32 fp32 channels, and 16 of 16 bits
 constexpr int kGgMaxStages = 6;
 constexpr int kGgSort = 512;           // weights: rows up to which experts keep their order
@@ -95,7 +95,9 @@ struct alignas(16) GgUnit {
 };
 
 __host__ __device__ constexpr bool gg_sums(Grouped m) { return m == Grouped::kWeights || m == Grouped::kWeights32; }
-__host__ __device__ constexpr int gg_threads(Grouped m) { return 32 * (m == Grouped::kWeights32 ? 16 : kGgWarps); }
+__host__ __device__ constexpr int gg_threads(Grouped m) { return 32 * (gg_sums(m) ? 16 : kGgWarps); }
+// Weights: rows that one accumulator sums.
+__host__ __device__ constexpr int gg_chain(Grouped m) { return m == Grouped::kWeights32 ? 512 : 8192; }
 
 struct GgCtl {
     GgUnit units[kGgUnits];
@@ -110,7 +112,7 @@ struct GgCtl {
     uint32_t tmem;
     volatile int abort;
     int32_t wsum[16];
-    int32_t valid_rows;
+    int32_t first_row, valid_rows;  // of all groups
     alignas(16) int32_t first[kGroupedMaxExperts + 4];  // row tiles before expert e; weights: its rows
     uint16_t order[kGroupedMaxExperts];     // rows of expert e's tiles; weights: experts, those of most rows first
 };
@@ -365,7 +367,7 @@ __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int til
         }
         x.n = (x.n + G::kGran - 1) / G::kGran * G::kGran;
         const uint32_t slot = turn % kGgUnits;
-        if (!gg_wait<kMode == Grouped::kWeights32>(&ctl.uempty[slot], ((turn / kGgUnits) & 1u) ^ 1u, ctl)) return;
+        if (!gg_wait<kWeights>(&ctl.uempty[slot], ((turn / kGgUnits) & 1u) ^ 1u, ctl)) return;
         if (lane == 0) {
             ctl.units[slot] = x;
             mbar_arrive(&ctl.ufull[slot]);
@@ -750,7 +752,7 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
         uint32_t dst = base, slot = 0, parity = 1, it = 0, unit = 0;  // slot: 8 x stage
         bool ok = true;
         GgUnit x;
-        while (ok && gg_next<false, kMode == Grouped::kWeights32>(ctl, unit, x)) {
+        while (ok && gg_next<false, kWeights>(ctl, unit, x)) {
             const uint64_t pol = !kWeights && kSideM && x.single ? once : keep;
             int n = wide(x, rank), both = kCtas == 1 ? n : wide(x, 0) + wide(x, 1), chunk = kChunk, dx = 128, dy = 0;
             const int part_n = x.n / kCtas;
@@ -782,7 +784,7 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
                         const int deep = (left + 63) / 64;
                         copies = n ? deep : 0, bytes = (uint32_t)(both / G::kChunks * deep * chunk);
                     }
-                    if (!(ok = gg_wait_one<false, kMode == Grouped::kWeights32>(empty0 + slot, parity, ctl))) break;
+                    if (!(ok = gg_wait_one<false, kWeights>(empty0 + slot, parity, ctl))) break;
                     // the pair's first CTA expects both CTAs' bytes; a stage whose last rows are to be
                     // zeroed first is each CTA's own
                     if (kWeights && ragged && left <= G::kK) {
@@ -837,7 +839,8 @@ __global__ void __launch_bounds__(gg_threads(kMode), 1)
 grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     constexpr bool kWeights = gg_sums(kMode), kGated = kMode == Grouped::kGated;
     constexpr int kCtas = G::kCtas, kThreads = gg_threads(kMode);
-    constexpr bool kLong = kMode == Grouped::kWeights32;
+    constexpr bool kWide = kMode == Grouped::kWeights32;  // an fp32 gradient
+    constexpr int kChain = gg_chain(kMode);
     extern __shared__ unsigned char smem_raw[];
     // the same offset in both CTAs of a pair: their descriptors are the first one's
     unsigned char *stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -903,6 +906,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 ctl.first[a.E] = off + inc;
                 ctl.valid_rows = hi;
             }
+            if (e == 0) ctl.first_row = lo;
         }
         carry += chunk;
         __syncthreads();
@@ -931,9 +935,9 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     tc_fence_after();
     const int tiles = kWeights ? a.E : carry;
     if (warp < 8) {
-        // fp32 weights: 128 registers a thread at the launch, 200 for the two warpgroups here and 56 for the
+        // weights: 128 registers a thread at the launch, 200 for the two warpgroups here and 56 for the
         // other two: in all the launch's 65,536
-        if constexpr (kLong) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if constexpr (kWeights) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int group = warp >> 2, quad = warp & 3;
         unsigned char *const staging = turns + warp * kGgStaging;
         float *const turn = reinterpret_cast<float *>(staging);
@@ -942,18 +946,18 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         uint32_t unit = 0, stored = 0;
         GgUnit x;
         for (;;) {
-            bool more = gg_next<true, kLong>(ctl, unit, x);
+            bool more = gg_next<true, kWeights>(ctl, unit, x);
             // gated: both warps of a barrier go on or neither, also after a wait that gave up
             if constexpr (kGated) more = !named_bar_or(bar, 64, !more);
             if (!more) break;
             const int c0 = (x.ct * kCtas + rank) * (kGated ? 64 : 128) + 32 * (kGated ? quad & 1 : quad);
             if (kWeights && x.nrows == 0) {
                 if (c0 < a.C)
-                    gg_weights<kLong>(a, tm.y, staging, 0, lane, group, x.e, c0, x.n0, x.n, true);
+                    gg_weights<kWide>(a, tm.y, staging, 0, lane, group, x.e, c0, x.n0, x.n, true);
                 continue;
             }
-            if (kLong && x.nrows > kGgChain) {
-                // The accumulators truncate, so a long chain of MMAs loses what rounded sums keep: kGgChain
+            if (kWeights && x.nrows > kChain) {
+                // The accumulators truncate, so a long chain of MMAs loses what rounded sums keep: kChain
                 // rows at a time are added up here, in registers.  The tensor memory is free again
                 // before the results are stored.
                 float sum[4][32];
@@ -961,7 +965,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 for (int i = 0; i < 128; ++i) sum[i / 32][i % 32] = 0.0f;
                 bool ok = true;
 #pragma unroll 1
-                for (int rest = x.nrows; rest > 0; rest -= kGgChain, ++local) {
+                for (int rest = x.nrows; rest > 0; rest -= kChain, ++local) {
                     const int buf = local & 1;
                     if (!(ok = gg_wait<true>(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl))) break;
                     tc_fence_after();
@@ -985,7 +989,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (c0 < a.C && 64 * i + 32 * group < x.n && x.n0 + 64 * i + 32 * group < a.N)
-                        gg_weights_put<true>(a, tm.y, staging, lane, x.e, c0, x.n0 + 64 * i + 32 * group, sum[i]);
+                        gg_weights_put<kWide>(a, tm.y, staging, lane, x.e, c0, x.n0 + 64 * i + 32 * group, sum[i]);
                 continue;
             }
             const int buf = local & 1;
@@ -998,7 +1002,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     const int r = 32 * i + 16 * group + (lane & 15);
                     ahead[i] = gg_codes(a, (int64_t)x.row0 + r, c0 + 16 * (lane >> 4), c0 < a.C && r < x.nrows);
                 }
-            bool ok = gg_wait<kLong>(&ctl.tfull[buf], parity, ctl);
+            bool ok = gg_wait<kWeights>(&ctl.tfull[buf], parity, ctl);
             if constexpr (kGated) ok = !named_bar_or(bar, 64, !ok);
             if (!ok) break;
             tc_fence_after();
@@ -1017,16 +1021,17 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 if (a.code == MOE_CODE_INT8) gg_gated_grad<true>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
                 else gg_gated_grad<false>(a, tm, turn, d, lane, group, x.row0, x.nrows, c0, ahead);
             } else {
-                gg_weights<kLong>(a, tm.y, staging, d, lane, group, x.e, c0, x.n0, x.n, false);
+                gg_weights<kWide>(a, tm.y, staging, d, lane, group, x.e, c0, x.n0, x.n, false);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.tempty[buf]));
         }
         if (lane == 0) bulk_store_wait<false>();  // stores have left shared memory and are visible
-        // rows past the last group (dropped routes): zeros
+        // rows of no group (past the last: dropped routes): zeros
         if (!kWeights && group == 0)
-            for (int64_t r = ctl.valid_rows + (int64_t)blockIdx.x; r < a.rows; r += gridDim.x) {
+            for (int64_t i = blockIdx.x; i < ctl.first_row + a.rows - ctl.valid_rows; i += gridDim.x) {
+                const int64_t r = i < ctl.first_row ? i : i - ctl.first_row + ctl.valid_rows;
                 const int elem = a.out32 ? 4 : 2, width = kMode == Grouped::kGatedGrad ? 2 * a.C : a.C;
                 gg_zero(a.out + r * a.ldo * elem, (int64_t)width * elem, a.vec > 0);
                 if (kMode == Grouped::kGatedGrad && a.p) gg_zero(a.p + r * a.C * 2, (int64_t)a.C * 2, a.pvec > 0);
@@ -1036,7 +1041,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 }
             }
     } else {
-        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if constexpr (kWeights) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 8 || warp == 9) {
             if (warp == 8) gg_produce<kMode, kTrans, G, true>(tm, a, ctl, smem_u32(stages), rank);
             else gg_produce<kMode, kTrans, G, false>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank);
@@ -1055,17 +1060,17 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     uint32_t stage = 0, parity = 0, at = 0, unit = 0;
                     bool ok = true;
                     GgUnit x;
-                    while (ok && gg_next<false, kLong>(ctl, at, x)) {
+                    while (ok && gg_next<false, kWeights>(ctl, at, x)) {
                         const int length = kWeights ? x.nrows : summed;
                         if (kWeights && length == 0) continue;
                         const uint32_t idesc = idesc0 | (uint32_t)(x.n >> 3) << 17;
-                        for (int rest = length; rest > 0 && ok; rest -= kGgChain) {
-                            const int take = kLong && rest > kGgChain ? kGgChain : rest;
+                        for (int rest = length; rest > 0 && ok; rest -= kChain) {
+                            const int take = kWeights && rest > kChain ? kChain : rest;
                             const uint32_t buf = unit & 1u, tparity = ((unit >> 1) & 1u) ^ 1u;
                             const uint32_t d = tmem + buf * G::kRows;
                             bool first = true;
                             ++unit;
-                            ok = gg_wait_one<false, kLong>(smem_u32(&ctl.tempty[buf]), tparity, ctl);
+                            ok = gg_wait_one<false, kWeights>(smem_u32(&ctl.tempty[buf]), tparity, ctl);
                             tc_fence_after();
                             for (int part = 0; part < parts && ok; ++part)
                                 for (int left = take; left > 0; left -= G::kK) {
@@ -1076,7 +1081,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                                                       bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
                                                       accumulate);
                                     };
-                                    if (!(ok = gg_wait_one<kWeights && kCtas == 2, kLong>(full0 + 8 * stage, parity, ctl))) break;
+                                    if (!(ok = gg_wait_one<kWeights && kCtas == 2, kWeights>(full0 + 8 * stage, parity, ctl))) break;
                                     tc_fence_after();
                                     step(0, !first);
                                     first = false;
@@ -1091,7 +1096,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                                     if (++stage == G::kStages) stage = 0, parity ^= 1u;
                                 }
                             if (ok) gg_commit<kCtas>(&ctl.tfull[buf]);
-                            if (!kLong) break;  // one accumulator sums the whole unit
+                            if (!kWeights) break;  // one accumulator sums the whole unit
                         }
                     }
                     // every issued MMA has completed before the CTAs free their tensor memory
@@ -1111,11 +1116,11 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 int total = 0;
                 uint32_t phase = 0, unit = 0;
                 GgUnit x;
-                while (gg_next<true, kLong>(ctl, unit, x)) {
+                while (gg_next<true, kWeights>(ctl, unit, x)) {
                     total += (x.nrows + G::kK - 1) / G::kK;
                     if (!x.ragged()) continue;
                     const int stage = (total - 1) % G::kStages;
-                    if (!gg_wait<kLong>(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
+                    if (!gg_wait<kWeights>(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
                     phase ^= 1u << stage;
                     const int from = x.nrows % G::kK, to = (from + 15) / 16 * 16;
                     unsigned char *S = stages + stage * G::kStageBytes;

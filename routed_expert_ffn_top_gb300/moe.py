@@ -1154,7 +1154,7 @@ def moe_grouped_product(rows, weights, offsets=None, transposed=False, dtype=Non
     """y [rows,N] of rows [rows,K] sorted by expert: each times its expert's weights [E,K,N] (or
     [K,N] without offsets); `transposed`: times the transpose of [E,N,K].  A pair of weights sums two
     products, of the two halves of rows [rows,2K]: with `transposed` and (w_gate, w_up) the gradient
-    of rows that both projections read.  Rows past the last group are zero.  `dtype`: y's, the rows'
+    of rows that both projections read.  Rows of no group are zero.  `dtype`: y's, the rows'
     if None.  The workspace holds the status word; without one the call makes its own, waits for the
     result and raises what the device found."""
     if stream is not None:

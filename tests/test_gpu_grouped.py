@@ -178,9 +178,10 @@ def test_weight_grad_keeps_a_bad_row_within_its_group():
 
 
 def test_weight_grad_of_long_groups():
-    """An fp32 gradient of 65,536 rows in one group.  Chains of 32 MMAs, each of whose additions truncates
-    by at most 2^-23 of the sum so far, added up by 127 rounded additions of at most 2^-24: 32 2^-23 +
-    127 2^-24 of the 2-norm.  (One chain of 4096 MMAs would be off by up to 4096 2^-23.)"""
+    """65,536 rows in one group.  fp32: chains of 32 MMAs, each of whose additions truncates by at most
+    2^-23 of the sum so far, added up by 127 rounded additions of at most 2^-24: 32 2^-23 + 127 2^-24 of
+    the 2-norm (one chain of 4096 MMAs would be off by up to 4096 2^-23).  16 bits: chains of 512 MMAs,
+    seven additions, and the result's rounding, 2^-8."""
     g = gen(13)
     rows = torch.randn((65536 + 77, 72), generator=g, device="cuda").to(BF16)
     grads = torch.randn((65536 + 77, 40), generator=g, device="cuda").to(BF16)
@@ -189,6 +190,34 @@ def test_weight_grad_of_long_groups():
     want = ref.weight_grad(rows, grads, offsets)
     for e in range(3):
         assert float((got[e].double() - want[e]).norm()) <= (32 * 2.0 ** -23 + 127 * 2.0 ** -24) * float(want[e].norm())
+    got = moe.moe_grouped_weight_grad(rows, grads, offsets.cuda(), dtype=BF16, workspace=workspace())
+    for e in range(3):
+        bound = 512 * 2.0 ** -23 + 7 * 2.0 ** -24 + 2.0 ** -8
+        assert float((got[e].double() - want[e]).norm()) <= bound * float(want[e].norm())
+
+
+@pytest.mark.parametrize("rows", (20, 900))
+def test_some_of_a_layers_experts(rows):
+    """Offsets of experts in the middle of the rows: the rows of others are zero, and add to nothing."""
+    g = gen(14)
+    lo, mid, hi = rows // 4, rows // 2, rows - 3
+    offsets = torch.tensor([lo, mid, mid, hi], dtype=torch.int32)
+    x, w, v = ints((rows, 64), g, 3, BF16), ints((3, 64, 32), g, 3, BF16), ints((3, 64, 32), g, 3, BF16)
+    full = torch.tensor([0, lo, mid, mid, hi], dtype=torch.int32)
+    nothing = torch.zeros((1, 64, 32), dtype=BF16, device="cuda")
+    whole_w, whole_v = torch.cat((nothing, w)), torch.cat((nothing, v))
+    work = workspace()
+    assert torch.equal(moe.moe_grouped_product(x, w, offsets.cuda(), workspace=work),
+                       moe.moe_grouped_product(x, whole_w, full.cuda(), workspace=work))
+    got = moe.moe_grouped_gated_product(x, w, v, offsets.cuda(), checkpoint=torch.int8, workspace=work)
+    want = moe.moe_grouped_gated_product(x, whole_w, whole_v, full.cuda(), checkpoint=torch.int8, workspace=work)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    down, whole_down = w.transpose(1, 2).contiguous(), whole_w.transpose(1, 2).contiguous()
+    got = moe.moe_grouped_gated_product_grad(x, down, offsets.cuda(), *got[1:], workspace=work)
+    want = moe.moe_grouped_gated_product_grad(x, whole_down, full.cuda(), *want[1:], workspace=work)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(moe.moe_grouped_weight_grad(x, x, offsets.cuda(), workspace=work),
+                       moe.moe_grouped_weight_grad(x, x, full.cuda(), workspace=work)[1:])
 
 
 def test_weight_grad_of_column_halves():
