@@ -22,11 +22,13 @@ from routed_expert_ffn_top_gb300 import moe
 
 class ExpertMLP(torch.autograd.Function):
     """out [M,H] of x [M,H], its routes' plan (offsets, route_row) and router weights [M,k] fp32, and
-    w_gate, w_up [E,H,I], w_down [E,I,H] of x's type; `code`: the checkpoints' type."""
+    w_gate, w_up [E,H,I], w_down [E,I,H] of x's type; `code`: the checkpoints' type; `work`: the calls'
+    status word, one of its own if None."""
 
     @staticmethod
-    def forward(ctx, x, weights, w_gate, w_up, w_down, offsets, route_row, code):
-        work = torch.zeros(moe.MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8, device=x.device)
+    def forward(ctx, x, weights, w_gate, w_up, w_down, offsets, route_row, code, work=None):
+        if work is None:
+            work = torch.zeros(moe.MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8, device=x.device)
         rows = moe.moe_token_sort(x, route_row)
         p, codes, scales = moe.moe_grouped_gated_product(rows, w_gate, w_up, offsets, checkpoint=code, workspace=work)
         y = moe.moe_grouped_product(p, w_down, offsets, workspace=work)
@@ -47,7 +49,7 @@ class ExpertMLP(torch.autograd.Function):
         grad_gate = moe.moe_grouped_weight_grad(rows, grad_gu[:, :I], offsets, dtype=w_gate.dtype, workspace=work)
         grad_up = moe.moe_grouped_weight_grad(rows, grad_gu[:, I:], offsets, dtype=w_up.dtype, workspace=work)
         grad_rows = moe.moe_grouped_product(grad_gu, (w_gate, w_up), offsets, transposed=True, workspace=work)
-        return moe.moe_token_sort_grad(grad_rows, route_row), grad_weights, grad_gate, grad_up, grad_down, None, None, None
+        return moe.moe_token_sort_grad(grad_rows, route_row), grad_weights, grad_gate, grad_up, grad_down, None, None, None, None
 
 
 class GroupedExperts(torch.nn.Module):
@@ -60,12 +62,13 @@ class GroupedExperts(torch.nn.Module):
         self.w_gate = torch.nn.Parameter((torch.randn(E, H, I) * H ** -0.5).to(dtype))
         self.w_up = torch.nn.Parameter((torch.randn(E, H, I) * H ** -0.5).to(dtype))
         self.w_down = torch.nn.Parameter((torch.randn(E, I, H) * I ** -0.5).to(dtype))
+        self.register_buffer("work", torch.zeros(moe.MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8), persistent=False)
 
     def forward(self, x):
         top = (x.float() @ self.router).topk(self.k, dim=1)
         offsets, _, route_row = moe.moe_token_plan(top.indices.to(torch.int32), self.E)
         return ExpertMLP.apply(x, torch.softmax(top.values, dim=1), self.w_gate, self.w_up, self.w_down, offsets, route_row,
-                               self.code)
+                               self.code, self.work)
 
 
 def train(M=512, H=128, I=192, E=8, k=2, steps=60, device="cuda", seed=0, code=torch.float8_e4m3fn):
@@ -82,6 +85,8 @@ def train(M=512, H=128, I=192, E=8, k=2, steps=60, device="cuda", seed=0, code=t
         loss.backward()
         opt.step()
         losses.append(float(loss.detach()))
+    if moe.moe_read_device_status(layer.work):
+        raise RuntimeError("device status set")
     return losses
 
 
