@@ -55,7 +55,7 @@
 namespace moe {
 
 constexpr int kGgWarps = 13;           // weights: 16, whose registers are shared out (below)
-constexpr int kGgStaging = 3072;       // a warp's: 16 rows of 32 fp32 channels, and 16 of 16 bits
+constexpr int kGgStaging = 3 * 1024;   // a warp's: 16 rows of 32 fp32 channels, and 16 of 16 bits
 constexpr int kGgMaxStages = 6;
 constexpr int kGgSort = 512;           // weights: rows up to which experts keep their order
 constexpr int kGgUnits = 8;            // units that are worked out ahead
