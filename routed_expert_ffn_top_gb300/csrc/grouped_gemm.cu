@@ -9,7 +9,8 @@
 //               dg = q u s (1 + g (1 - s)), du = q g s, and p again;
 //   weights     G[e] = sum_r x[r]^T d[r], a product summed over the expert's rows.
 // Operands bf16 or f16, sums in the tensor core's fp32 accumulators in the order of K (or of the
-// rows), each result rounded once: a row's result does not depend on its group, tile or grid.
+// rows), long ones split at fixed places, each result rounded once: a row's result does not depend on
+// its group, tile or grid.
 //
 // A unit is a row tile of one expert times a tile of channels.  The channels are the MMA's M side
 // and the rows its N side: N is a group's own number of rows, rounded up to 16 a CTA, so a
@@ -17,10 +18,20 @@
 // Groups need no padding: a copy may run into the next expert's rows, whose results are dropped
 // by the epilogue (a row only reaches its own results).  In a weights' gradient rows are what is
 // summed: the last rows of the last step are zeroed in shared memory before the MMA reads them.
-// The tensor core's accumulators truncate: a chain of n MMAs is off by about n 2^-24.  Rows, unlike K, have
-// no bound, so a long group's sums are added up in registers: of 512 rows at a time for an fp32 gradient
-// (8192 tokens 4.3e-7 off in the 2-norm for 1.1e-6, in 234 us for 230; 256 rows at a time 2.2e-7, 240 us),
-// of 8192 rows for a 16-bit one (2^-15, a sixteenth of f16's half step).
+// The tensor core's accumulators truncate: a chain of n MMAs is off by about n 2^-24 (all addends of one
+// sign: f16 twice that).  So an accumulator sums a bounded chain, and those of a longer sum are added up
+// in registers, with rounding, at fixed places of K or of the rows.  Chains are
+//   8192 of K or rows for 16-bit results: 2^-15, a sixteenth of f16's half step;
+//   256 of K for fp32 results (random values, K = 2048: 3.5e-7 off in the 2-norm for 2.5e-6, torch's fp32
+//   product 4e-7; 512: 6.5e-7), at 8192 tokens and K = 2048 175 us in place of 166, K = 768 245 of 205,
+//   65536 x 2048 x 2048 325 of 290;
+//   256 of K for the codes of f16 rows, which a gradient in f16 sees: with codes next to a border on the
+//   other side, what is computed from them was up to twice as far off as from fp32 sums (H = 2048,
+//   int8: 4.5e-4 for 2.2e-4, now 2.3e-4).  4096 tokens 220 us in place of 185, 8192 tokens 407 of 299: a
+//   unit's codes are made while the next unit's first chain runs, no longer the whole unit.  bf16's
+//   rounding, 1.7e-3, hides it: bf16 rows are not split;
+//   512 rows for an fp32 gradient of weights (8192 tokens 4.3e-7 off in the 2-norm for 1.1e-6, in 234 us for
+//   230; 256 rows at a time 2.2e-7, 240 us).
 //
 // Large tile: two CTAs share a tile (cta_group::2): 256 channels, 128 each, times up to 256
 // rows, each CTA holding half of the rows' operand: 32 KB of shared memory a stage of 64 of K, so
@@ -54,7 +65,7 @@
 
 namespace moe {
 
-constexpr int kGgWarps = 13;           // weights: 16, whose registers are shared out (below)
+constexpr int kGgWarps = 13;           // 16 where several accumulators are added up, their registers shared out (below)
 constexpr int kGgStaging = 3 * 1024;   // a warp's: 16 rows of 32 fp32 channels, and 16 of 16 bits
 constexpr int kGgMaxStages = 6;
 constexpr int kGgSort = 512;           // weights: rows up to which experts keep their order
@@ -95,9 +106,17 @@ struct alignas(16) GgUnit {
 };
 
 __host__ __device__ constexpr bool gg_sums(Grouped m) { return m == Grouped::kWeights || m == Grouped::kWeights32; }
-__host__ __device__ constexpr int gg_threads(Grouped m) { return 32 * (gg_sums(m) ? 16 : kGgWarps); }
+// Whether the epilogue's warps add up several accumulators, of up to 256 rows or columns, and so get more
+// registers than the others.
+template <typename G>
+__host__ __device__ constexpr bool gg_shares(Grouped m, bool split) {
+    return gg_sums(m) || (split && G::kRows > 32);
+}
+__host__ __device__ constexpr int gg_threads(bool shares) { return 32 * (shares ? 16 : kGgWarps); }
 // Weights: rows that one accumulator sums.
 __host__ __device__ constexpr int gg_chain(Grouped m) { return m == Grouped::kWeights32 ? 512 : 8192; }
+// Products: the K that one accumulator sums, for fp32 results and f16 rows' codes, and for other results.
+constexpr int kGgChainFine = 256, kGgChain = 8192;
 
 struct GgCtl {
     GgUnit units[kGgUnits];
@@ -128,6 +147,7 @@ struct GgArgs {
     int64_t rows;
     int E, C, K, N;   // C channels; N the weights' gradient's columns
     int parts, nct, nnt;
+    int chain, pieces;   // split: the K of an accumulator, a unit's accumulators
     int deep_m, deep_n;  // the M, N side's channels are whole chunks of 64: one copy brings two
     int dt, dct;      // a step of a CTA pair's units in row tiles and channel tiles
     uint32_t idesc;   // without N
@@ -331,7 +351,7 @@ __device__ __forceinline__ void gg_span(const GgArgs &a, int e, int &lo, int &hi
 // of row tile u / nct.  Weights: unit u is channel tile u % nct, column tile (u / nct) % nnt of the
 // expert with the (u / nct / nnt)-th most rows, and the pairs take them there and back: what one
 // takes before another in one turn it takes after it in the next.
-template <Grouped kMode, typename G>
+template <Grouped kMode, typename G, bool kInline>
 __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int tiles) {
     constexpr bool kWeights = gg_sums(kMode);
     const int lane = threadIdx.x & 31, pair = blockIdx.x / G::kCtas, pairs = gridDim.x / G::kCtas;
@@ -367,7 +387,7 @@ __device__ __forceinline__ void gg_schedule(const GgArgs &a, GgCtl &ctl, int til
         }
         x.n = (x.n + G::kGran - 1) / G::kGran * G::kGran;
         const uint32_t slot = turn % kGgUnits;
-        if (!gg_wait<kWeights>(&ctl.uempty[slot], ((turn / kGgUnits) & 1u) ^ 1u, ctl)) return;
+        if (!gg_wait<kInline>(&ctl.uempty[slot], ((turn / kGgUnits) & 1u) ^ 1u, ctl)) return;
         if (lane == 0) {
             ctl.units[slot] = x;
             mbar_arrive(&ctl.ufull[slot]);
@@ -387,6 +407,28 @@ __device__ __forceinline__ bool gg_next(GgCtl &ctl, uint32_t &at, GgUnit &x) {
     if (kWarp) __syncwarp();
     if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ctl.uempty[slot]);
     return x.nrows >= 0;
+}
+
+// ------------------------------------------------------------------------------- split sums
+// kN blocks of 16 columns, 32 apart, by one wait.
+template <int kN>
+__device__ __forceinline__ void gg_read(uint32_t d, uint32_t (&r)[kN][16]) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[i][0]), "=r"(r[i][1]), "=r"(r[i][2]), "=r"(r[i][3]), "=r"(r[i][4]), "=r"(r[i][5]), "=r"(r[i][6]),
+              "=r"(r[i][7]), "=r"(r[i][8]), "=r"(r[i][9]), "=r"(r[i][10]), "=r"(r[i][11]), "=r"(r[i][12]), "=r"(r[i][13]),
+              "=r"(r[i][14]), "=r"(r[i][15])
+            : "r"(d + 32 * i));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // (operands, so that no use of them moves above the wait)
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; j += 8)
+            asm volatile("" : "+r"(r[i][j]), "+r"(r[i][j + 1]), "+r"(r[i][j + 2]), "+r"(r[i][j + 3]), "+r"(r[i][j + 4]),
+                              "+r"(r[i][j + 5]), "+r"(r[i][j + 6]), "+r"(r[i][j + 7]));
 }
 
 // -------------------------------------------------------------------------------- epilogues
@@ -731,7 +773,7 @@ __device__ __forceinline__ void gg_zero(unsigned char *p, int64_t bytes, bool wi
 // A warp that copies one side's operand (kSideM: the M side's); one lane does, its registers hold the
 // ring's state.  What a stage takes between its memory's release and its copies is kept short: with
 // the coordinates and addresses worked out there it took 400 cycles, in every turn of the ring.
-template <Grouped kMode, bool kTrans, typename G, bool kSideM>
+template <Grouped kMode, bool kTrans, typename G, bool kSideM, bool kInline>
 __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, GgCtl &ctl, uint32_t base, int rank) {
     constexpr bool kWeights = gg_sums(kMode), kGated = kMode == Grouped::kGated;
     constexpr int kCtas = G::kCtas;
@@ -752,7 +794,7 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
         uint32_t dst = base, slot = 0, parity = 1, it = 0, unit = 0;  // slot: 8 x stage
         bool ok = true;
         GgUnit x;
-        while (ok && gg_next<false, kWeights>(ctl, unit, x)) {
+        while (ok && gg_next<false, kInline>(ctl, unit, x)) {
             const uint64_t pol = !kWeights && kSideM && x.single ? once : keep;
             int n = wide(x, rank), both = kCtas == 1 ? n : wide(x, 0) + wide(x, 1), chunk = kChunk, dx = 128, dy = 0;
             const int part_n = x.n / kCtas;
@@ -784,7 +826,7 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
                         const int deep = (left + 63) / 64;
                         copies = n ? deep : 0, bytes = (uint32_t)(both / G::kChunks * deep * chunk);
                     }
-                    if (!(ok = gg_wait_one<false, kWeights>(empty0 + slot, parity, ctl))) break;
+                    if (!(ok = gg_wait_one<false, kInline>(empty0 + slot, parity, ctl))) break;
                     // the pair's first CTA expects both CTAs' bytes; a stage whose last rows are to be
                     // zeroed first is each CTA's own
                     if (kWeights && ragged && left <= G::kK) {
@@ -833,12 +875,14 @@ __device__ __forceinline__ void gg_produce(const GgMaps &tm, const GgArgs &a, Gg
 }
 
 // ----------------------------------------------------------------------------------- kernel
-// kTrans: the M side's operand is K-major (weights [channels][K]), else channel-major.
-template <Grouped kMode, bool kTrans, typename G>
-__global__ void __launch_bounds__(gg_threads(kMode), 1)
+// kTrans: the M side's operand is K-major (weights [channels][K]), else channel-major.  kSplit: a product
+// whose units take several accumulators one after the other, of a.chain of K each.
+template <Grouped kMode, bool kTrans, typename G, bool kSplit>
+__global__ void __launch_bounds__(gg_threads(gg_shares<G>(kMode, kSplit)), 1)
 grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     constexpr bool kWeights = gg_sums(kMode), kGated = kMode == Grouped::kGated;
-    constexpr int kCtas = G::kCtas, kThreads = gg_threads(kMode);
+    constexpr bool kShare = gg_shares<G>(kMode, kSplit);
+    constexpr int kCtas = G::kCtas, kThreads = gg_threads(kShare);
     constexpr bool kWide = kMode == Grouped::kWeights32;  // an fp32 gradient
     constexpr int kChain = gg_chain(kMode);
     extern __shared__ unsigned char smem_raw[];
@@ -935,9 +979,9 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
     tc_fence_after();
     const int tiles = kWeights ? a.E : carry;
     if (warp < 8) {
-        // weights: 128 registers a thread at the launch, 200 for the two warpgroups here and 56 for the
-        // other two: in all the launch's 65,536
-        if constexpr (kWeights) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // 128 registers a thread at the launch, 200 for the two warpgroups here and 56 for the other two:
+        // in all the launch's 65,536
+        if constexpr (kShare) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int group = warp >> 2, quad = warp & 3;
         unsigned char *const staging = turns + warp * kGgStaging;
         float *const turn = reinterpret_cast<float *>(staging);
@@ -946,7 +990,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
         uint32_t unit = 0, stored = 0;
         GgUnit x;
         for (;;) {
-            bool more = gg_next<true, kWeights>(ctl, unit, x);
+            bool more = gg_next<true, kShare>(ctl, unit, x);
             // gated: both warps of a barrier go on or neither, also after a wait that gave up
             if constexpr (kGated) more = !named_bar_or(bar, 64, !more);
             if (!more) break;
@@ -967,7 +1011,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
 #pragma unroll 1
                 for (int rest = x.nrows; rest > 0; rest -= kChain, ++local) {
                     const int buf = local & 1;
-                    if (!(ok = gg_wait<true>(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl))) break;
+                    if (!(ok = gg_wait<kShare>(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl))) break;
                     tc_fence_after();
                     const uint32_t d = ctl.tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * G::kRows) + 32 * group;
 #pragma unroll
@@ -992,9 +1036,6 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                         gg_weights_put<kWide>(a, tm.y, staging, lane, x.e, c0, x.n0 + 64 * i + 32 * group, sum[i]);
                 continue;
             }
-            const int buf = local & 1;
-            const uint32_t parity = (uint32_t)(local >> 1) & 1u;
-            ++local;
             GgCodes ahead[2];
             if constexpr (kMode == Grouped::kGatedGrad)
 #pragma unroll
@@ -1002,11 +1043,53 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     const int r = 32 * i + 16 * group + (lane & 15);
                     ahead[i] = gg_codes(a, (int64_t)x.row0 + r, c0 + 16 * (lane >> 4), c0 < a.C && r < x.nrows);
                 }
-            bool ok = gg_wait<kWeights>(&ctl.tfull[buf], parity, ctl);
+            // A split product's accumulators are added up in registers, all but the last one's tensor memory
+            // free again at once; the sums go back into the last one's, from where the results are made.
+            // (Made from the registers, eight blocks moved up one by one: f16 codes 4096 tokens 226 against
+            // 219 us.  One wait for each 16 columns in place of two: 65536 x 2048 x 2048 347 against 318 us.)
+            constexpr int kBlocks = kSplit ? (G::kRows + 31) / 32 : 1, kRead = kBlocks < 2 ? kBlocks : 2;
+            float sum[kBlocks][16];
+#pragma unroll
+            for (int i = 0; i < 16 * kBlocks; ++i) sum[i / 16][i % 16] = 0.0f;
+            bool ok = true;
+            uint32_t d = 0;
+            int buf = 0;
+            const int pieces = kSplit ? a.pieces : 1;
+#pragma unroll 1
+            for (int piece = 0; piece < pieces; ++piece, ++local) {
+                buf = local & 1;
+                if (!(ok = gg_wait<kShare>(&ctl.tfull[buf], (uint32_t)(local >> 1) & 1u, ctl))) break;
+                tc_fence_after();
+                d = ctl.tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * G::kRows);
+                if constexpr (kSplit) {
+#pragma unroll
+                    for (int i = 0; i < kBlocks; i += kRead) {
+                        if (c0 >= a.C || 32 * i + 16 * group >= x.n) continue;
+                        uint32_t v[kRead][16];
+                        gg_read(d + 32 * i + 16 * group, v);
+#pragma unroll
+                        for (int j = 0; j < 16 * kRead; ++j) sum[i + j / 16][j % 16] += __uint_as_float(v[j / 16][j % 16]);
+                    }
+                    if (piece + 1 < pieces) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) gg_arrive(gg_leader<kCtas>(&ctl.tempty[buf]));
+                    }
+                }
+            }
             if constexpr (kGated) ok = !named_bar_or(bar, 64, !ok);
             if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = ctl.tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * G::kRows);
+            if constexpr (kSplit) {
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+                    if (c0 >= a.C || 32 * i + 16 * group >= x.n) continue;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(sum[i][j]);
+                    tmem_st16(d + 32 * i + 16 * group, w);
+                }
+                tmem_st_wait();
+            }
             if (c0 >= a.C) {
                 // no channel of this warp's lanes
             } else if constexpr (kMode == Grouped::kPlain) {
@@ -1041,10 +1124,10 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 }
             }
     } else {
-        if constexpr (kWeights) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if constexpr (kShare) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 8 || warp == 9) {
-            if (warp == 8) gg_produce<kMode, kTrans, G, true>(tm, a, ctl, smem_u32(stages), rank);
-            else gg_produce<kMode, kTrans, G, false>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank);
+            if (warp == 8) gg_produce<kMode, kTrans, G, true, kShare>(tm, a, ctl, smem_u32(stages), rank);
+            else gg_produce<kMode, kTrans, G, false, kShare>(tm, a, ctl, smem_u32(stages) + G::kABytes, rank);
         } else if (warp == 10) {
             if (rank == 0) {
                 // 128-byte swizzle, 8-row atoms 1 KB apart.  K-major: a K step of 16 is 32 bytes, a chunk
@@ -1060,19 +1143,23 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                     uint32_t stage = 0, parity = 0, at = 0, unit = 0;
                     bool ok = true;
                     GgUnit x;
-                    while (ok && gg_next<false, kWeights>(ctl, at, x)) {
+                    while (ok && gg_next<false, kShare>(ctl, at, x)) {
                         const int length = kWeights ? x.nrows : summed;
                         if (kWeights && length == 0) continue;
                         const uint32_t idesc = idesc0 | (uint32_t)(x.n >> 3) << 17;
-                        for (int rest = length; rest > 0 && ok; rest -= kChain) {
-                            const int take = kWeights && rest > kChain ? kChain : rest;
+                        // an accumulator sums a chain of a part's K (weights: of the rows), or the whole unit
+                        constexpr bool kChained = kWeights || kSplit;
+                        const int chain = kWeights ? kChain : a.chain;
+                        for (int outer = 0; outer < (kSplit ? parts : 1) && ok; ++outer)
+                        for (int rest = length; rest > 0 && ok; rest -= chain) {
+                            const int take = kChained && rest > chain ? chain : rest;
                             const uint32_t buf = unit & 1u, tparity = ((unit >> 1) & 1u) ^ 1u;
                             const uint32_t d = tmem + buf * G::kRows;
                             bool first = true;
                             ++unit;
-                            ok = gg_wait_one<false, kWeights>(smem_u32(&ctl.tempty[buf]), tparity, ctl);
+                            ok = gg_wait_one<false, kShare>(smem_u32(&ctl.tempty[buf]), tparity, ctl);
                             tc_fence_after();
-                            for (int part = 0; part < parts && ok; ++part)
+                            for (int part = 0; part < (kSplit ? 1 : parts) && ok; ++part)
                                 for (int left = take; left > 0; left -= G::kK) {
                                     const uint64_t ad = a0 + stage * (G::kStageBytes >> 4);
                                     const uint64_t bd = b0 + stage * (G::kStageBytes >> 4);
@@ -1081,7 +1168,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                                                       bd + (kBMajor ? ks * 128 : (ks >> 2) * (G::kBChunk >> 4) + (ks & 3) * 2), idesc,
                                                       accumulate);
                                     };
-                                    if (!(ok = gg_wait_one<kWeights && kCtas == 2, kWeights>(full0 + 8 * stage, parity, ctl))) break;
+                                    if (!(ok = gg_wait_one<kWeights && kCtas == 2, kShare>(full0 + 8 * stage, parity, ctl))) break;
                                     tc_fence_after();
                                     step(0, !first);
                                     first = false;
@@ -1096,7 +1183,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                                     if (++stage == G::kStages) stage = 0, parity ^= 1u;
                                 }
                             if (ok) gg_commit<kCtas>(&ctl.tfull[buf]);
-                            if (!kWeights) break;  // one accumulator sums the whole unit
+                            if (!kChained) break;
                         }
                     }
                     // every issued MMA has completed before the CTAs free their tensor memory
@@ -1116,11 +1203,11 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 int total = 0;
                 uint32_t phase = 0, unit = 0;
                 GgUnit x;
-                while (gg_next<true, kWeights>(ctl, unit, x)) {
+                while (gg_next<true, kShare>(ctl, unit, x)) {
                     total += (x.nrows + G::kK - 1) / G::kK;
                     if (!x.ragged()) continue;
                     const int stage = (total - 1) % G::kStages;
-                    if (!gg_wait<kWeights>(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
+                    if (!gg_wait<kShare>(&ctl.land[stage], (phase >> stage) & 1u, ctl)) break;
                     phase ^= 1u << stage;
                     const int from = x.nrows % G::kK, to = (from + 15) / 16 * 16;
                     unsigned char *S = stages + stage * G::kStageBytes;
@@ -1134,7 +1221,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
                 }
             }
         } else if (warp == 12) {
-            gg_schedule<kMode, G>(a, ctl, tiles);
+            gg_schedule<kMode, G, kShare>(a, ctl, tiles);
         }
     }
 
@@ -1147,7 +1234,7 @@ grouped_gemm_kernel(const __grid_constant__ GgMaps tm, const GgArgs a) {
 }
 
 // ---------------------------------------------------------------------------------- launcher
-template <Grouped kMode, bool kTrans, typename G>
+template <Grouped kMode, bool kTrans, typename G, bool kSplit = false>
 static cudaError_t grouped_as(const GgMaps &tm, GgArgs a, cudaStream_t stream) {
     constexpr int per = kMode == Grouped::kGated ? G::kCh / 2 : G::kCh;
     a.nct = (a.C + per - 1) / per;
@@ -1156,23 +1243,23 @@ static cudaError_t grouped_as(const GgMaps &tm, GgArgs a, cudaStream_t stream) {
     const int64_t units = tiles * a.nct, most = num_sms() / G::kCtas;
     const int64_t pairs = units < 1 ? 1 : (units < most ? units : most);
     a.dt = (int)(pairs / a.nct), a.dct = (int)(pairs % a.nct);
-    const auto fn = grouped_gemm_kernel<kMode, kTrans, G>;
+    const auto fn = grouped_gemm_kernel<kMode, kTrans, G, kSplit>;
     cudaError_t err = ensure_smem((const void *)fn, G::kSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attrs[2];
-    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)(pairs * G::kCtas)), dim3(gg_threads(kMode)), G::kSmem, stream, attrs,
+    cudaLaunchConfig_t cfg = launch_config(dim3((unsigned)(pairs * G::kCtas)), dim3(gg_threads(gg_shares<G>(kMode, kSplit))), G::kSmem, stream, attrs,
                                            G::kCtas > 1 ? G::kCtas : 0);
     return cudaLaunchKernelEx(&cfg, fn, tm, a);
 }
 
-template <typename G>
+template <typename G, bool kSplit>
 static cudaError_t grouped_tile(const GgMaps &tm, const GgArgs &a, const GroupedArgs &g, cudaStream_t stream) {
     switch (g.mode) {
-        case Grouped::kGated: return grouped_as<Grouped::kGated, false, G>(tm, a, stream);
-        case Grouped::kGatedGrad: return grouped_as<Grouped::kGatedGrad, true, G>(tm, a, stream);
+        case Grouped::kGated: return grouped_as<Grouped::kGated, false, G, kSplit>(tm, a, stream);
+        case Grouped::kGatedGrad: return grouped_as<Grouped::kGatedGrad, true, G, kSplit>(tm, a, stream);
         default:
-            return g.transposed ? grouped_as<Grouped::kPlain, true, G>(tm, a, stream)
-                                : grouped_as<Grouped::kPlain, false, G>(tm, a, stream);
+            return g.transposed ? grouped_as<Grouped::kPlain, true, G, kSplit>(tm, a, stream)
+                                : grouped_as<Grouped::kPlain, false, G, kSplit>(tm, a, stream);
     }
 }
 
@@ -1200,6 +1287,9 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
     a.p = static_cast<unsigned char *>(g.p), a.pvec = store_width(g.p, 2 * (int64_t)g.channels);
     a.code = g.code, a.codes = g.codes, a.scales = g.scales, a.pitch = microscale_pitch(2 * g.channels);
     a.status = g.status;
+    a.chain = a.out32 || (g.mode == Grouped::kGated && g.codes && g.half) ? kGgChainFine : kGgChain;
+    const bool split = !weights && (int64_t)g.parts * g.K > a.chain;
+    a.pieces = split ? g.parts * ((g.K + a.chain - 1) / a.chain) : 1;
 
     GgMaps tm;
     memset(&tm, 0, sizeof tm);
@@ -1263,7 +1353,8 @@ cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
     if (weights)
         return a.out32 ? grouped_as<Grouped::kWeights32, false, GgLarge>(tm, a, stream)
                        : grouped_as<Grouped::kWeights, false, GgLarge>(tm, a, stream);
-    return small ? grouped_tile<GgSmall>(tm, a, g, stream) : grouped_tile<GgLarge>(tm, a, g, stream);
+    if (split) return small ? grouped_tile<GgSmall, true>(tm, a, g, stream) : grouped_tile<GgLarge, true>(tm, a, g, stream);
+    return small ? grouped_tile<GgSmall, false>(tm, a, g, stream) : grouped_tile<GgLarge, false>(tm, a, g, stream);
 }
 
 }  // namespace moe
