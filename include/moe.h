@@ -537,10 +537,10 @@ int moe_microscale_ffn(const void *h, const moe_microscale_weights_t *w, int M, 
  * to 2^20 (else MOE_ERR_UNSUPPORTED); E <= 1024, rows < 2^24.  Groups may be empty and of any
  * size.  Sums are the tensor cores' fp32 accumulators in a fixed order (n steps of 16 are off by
  * about n 2^-24); sums of 8192 of K or of the rows, for an fp32 result and the codes of f16 rows
- * 256 of K or 512 rows, are added up with rounding.  Each result is rounded once, and a row's
- * bits do not depend on the other rows.  Result rows of no expert, before offsets[0] or past
- * offsets[E] (dropped routes), are zero.  Outputs must not overlap inputs.  workspace: ws_bytes
- * >= MOE_GROUPED_STATUS_BYTES, 16-byte aligned, a status word that must be zero before the first
+ * of 256, are added up with rounding.  Each result is rounded once, and a row's bits do not depend
+ * on the other rows.  Result rows of no expert, before offsets[0] or past offsets[E] (dropped
+ * routes), are zero.  Outputs must not overlap inputs.  workspace: ws_bytes >=
+ * MOE_GROUPED_STATUS_BYTES, 16-byte aligned, a status word that must be zero before the first
  * call, read back with moe_read_device_status.
  */
 #define MOE_GROUPED_STATUS_BYTES 256

@@ -30,8 +30,8 @@
 //   int8: 4.5e-4 for 2.2e-4, now 2.3e-4).  4096 tokens 220 us in place of 185, 8192 tokens 407 of 299: a
 //   unit's codes are made while the next unit's first chain runs, no longer the whole unit.  bf16's
 //   rounding, 1.7e-3, hides it: bf16 rows are not split;
-//   512 rows for an fp32 gradient of weights (8192 tokens 4.3e-7 off in the 2-norm for 1.1e-6, in 234 us for
-//   230; 256 rows at a time 2.2e-7, 240 us).
+//   256 rows for an fp32 gradient of weights (8192 tokens 2.2e-7 off in the 2-norm, torch's fp32 products
+//   2.7e-7; 512 rows 4.3e-7, one chain 1.1e-6; 241, 232 and 230 us).
 //
 // Large tile: two CTAs share a tile (cta_group::2): 256 channels, 128 each, times up to 256
 // rows, each CTA holding half of the rows' operand: 32 KB of shared memory a stage of 64 of K, so
@@ -114,7 +114,7 @@ __host__ __device__ constexpr bool gg_shares(Grouped m, bool split) {
 }
 __host__ __device__ constexpr int gg_threads(bool shares) { return 32 * (shares ? 16 : kGgWarps); }
 // Weights: rows that one accumulator sums.
-__host__ __device__ constexpr int gg_chain(Grouped m) { return m == Grouped::kWeights32 ? 512 : 8192; }
+__host__ __device__ constexpr int gg_chain(Grouped m) { return m == Grouped::kWeights32 ? 256 : 8192; }
 // Products: the K that one accumulator sums, for fp32 results and f16 rows' codes, and for other results.
 constexpr int kGgChainFine = 256, kGgChain = 8192;
 

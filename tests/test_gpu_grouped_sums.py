@@ -2,8 +2,8 @@
 
 An accumulator truncates: what an MMA's 16 products add below the last of its 24 bits is gone, and
 at worst each of the MMA's 17 addends is cut by 2^-23 of the largest.  So the sums of long
-products are split into chains, which are added up with rounding: of 256 of K for results in
-fp32 and for the 8-bit codes of f16 rows, of 8192 for 16-bit ones.
+products and of long groups are split into chains, which are added up with rounding: of 256 of K (or
+rows) for results in fp32 and for the 8-bit codes of f16 rows, of 8192 for 16-bit ones.
 """
 import pytest
 import torch
@@ -185,4 +185,25 @@ def test_split_sums_of_ragged_groups(form, sizes, tail, N, K):
     for _ in range(5):
         got = moe.moe_grouped_product(rows, ws[0] if parts == 1 else tuple(ws), offsets.cuda(), form != "plain", dtype=F32, workspace=work)
         assert torch.equal(got.double(), want)
+    assert moe.moe_read_device_status(work) == 0
+
+
+@pytest.mark.parametrize("sizes", [[2048], [300, 0, 5000, 17, 1100]])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_fp32_weight_grad_keeps_small_shares(dtype, sizes):
+    """As of the products, along an expert's rows: the first row of each gives 2^24, then a row in 16 a share
+    of 1."""
+    offsets = ref.groups(sizes)
+    x = torch.zeros((sum(sizes), 72), dtype=torch.float64, device="cuda")
+    for _, lo, hi in ref.spans(offsets):
+        if hi > lo:
+            x[lo:hi] = shares(hi - lo).unsqueeze(1)
+            x[lo] = 4096
+    d = x[:, :40].contiguous()
+    d[:, 1::2] *= -1
+    work = workspace()
+    got = moe.moe_grouped_weight_grad(x.to(dtype), d.to(dtype), offsets.cuda(), workspace=work).double()
+    want = ref.weight_grad(x, d, offsets)
+    for e, n in enumerate(sizes):
+        assert float((got[e] - want[e]).abs().max()) <= (15 + (-(-n // FINE) - 1) if n else 0)
     assert moe.moe_read_device_status(work) == 0
