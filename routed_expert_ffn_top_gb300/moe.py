@@ -1297,11 +1297,10 @@ def moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, grad_
     return grad_gate_up, p
 
 
-def moe_grouped_weight_grad(rows, grads, offsets=None, dtype=torch.float32, out=None, workspace=None,
-                            stream=None):
+def moe_grouped_weight_grad(rows, grads, offsets=None, dtype=None, out=None, workspace=None, stream=None):
     """The gradient [E,K,N] of weights that rows [rows,K] were multiplied by, of grads [rows,N]: per
     expert the sum of its rows' outer products, zero without rows; without offsets [1,K,N].
-    Workspace as for moe_grouped_product."""
+    `dtype`: the gradient's, out's or float32 if None.  Workspace as for moe_grouped_product."""
     if stream is not None:
         with _launch_stream(stream, rows.device):
             return moe_grouped_weight_grad(rows, grads, offsets, dtype, out, workspace)
@@ -1321,8 +1320,8 @@ def moe_grouped_weight_grad(rows, grads, offsets=None, dtype=torch.float32, out=
         off = None if offsets is None else _vector(offsets, "offsets", torch.int32, dev, (E + 1,))
     ws = None if workspace is None else _workspace(workspace, dev)
     launch = _raw_stream(dev)
-    if out is not None:
-        dtype = out.dtype
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
     ocode = _ROW_DTYPES.get(dtype)
     if ocode is None:
         raise TypeError("the gradient must be bfloat16, float16 or float32, got %s" % (dtype,))
@@ -1365,9 +1364,10 @@ def moe_checkpoint_quantize(x, dtype=torch.float8_e4m3fn, codes=None, scales=Non
     return codes, scales
 
 
-def moe_checkpoint_dequantize(codes, scales, dtype=torch.bfloat16, route_row=None, out=None, stream=None):
+def moe_checkpoint_dequantize(codes, scales, dtype=None, route_row=None, out=None, stream=None):
     """The values [rows,cols] of a checkpoint; with route_row [rows,k] (a token plan's) in sorted
-    order, rows * k of them, zero in the rows of dropped routes."""
+    order, rows * k of them, zero in the rows of dropped routes.  `dtype`: theirs, out's or bfloat16
+    if None."""
     if stream is not None:
         with _launch_stream(stream, codes.device):
             return moe_checkpoint_dequantize(codes, scales, dtype, route_row, out)
@@ -1380,13 +1380,15 @@ def moe_checkpoint_dequantize(codes, scales, dtype=torch.bfloat16, route_row=Non
         k = route_row.shape[1]
         rr = _vector(route_row, "route_row", torch.int32, dev, (rows, k))
     launch = _raw_stream(dev)
-    if out is not None:
-        ldx, xcode = _rows(out, "out", dev, out.dtype, (rows * k, cols)), _row_dtype(out, "out")
-    else:
-        xcode = _ROW_DTYPES.get(dtype)
-        if xcode is None:
-            raise TypeError("dtype must be bfloat16, float16 or float32, got %s" % (dtype,))
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    xcode = _ROW_DTYPES.get(dtype)
+    if xcode is None:
+        raise TypeError("dtype must be bfloat16, float16 or float32, got %s" % (dtype,))
+    if out is None:
         out, ldx = torch.empty((rows * k, cols), dtype=dtype, device=dev), cols
+    else:
+        ldx = _rows(out, "out", dev, dtype, (rows * k, cols))
     _check(lib().moe_checkpoint_dequantize(codes.data_ptr(), scales.data_ptr(), kind, rows, cols, rr, k,
                                            out.data_ptr(), ldx, xcode, launch),
            "moe_checkpoint_dequantize")
