@@ -23,12 +23,11 @@ from routed_expert_ffn_top_gb300 import moe
 class ExpertMLP(torch.autograd.Function):
     """out [M,H] of x [M,H], its routes' plan (offsets, route_row) and router weights [M,k] fp32, and
     w_gate, w_up [E,H,I], w_down [E,I,H] of x's type; `code`: the checkpoints' type; `work`: the calls'
-    status word, one of its own if None."""
+    status word, which the caller reads.  Without one every call waits for its result and raises what
+    the device found."""
 
     @staticmethod
     def forward(ctx, x, weights, w_gate, w_up, w_down, offsets, route_row, code, work=None):
-        if work is None:
-            work = torch.zeros(moe.MOE_GROUPED_STATUS_BYTES, dtype=torch.uint8, device=x.device)
         rows = moe.moe_token_sort(x, route_row)
         p, codes, scales = moe.moe_grouped_gated_product(rows, w_gate, w_up, offsets, checkpoint=code, workspace=work)
         y = moe.moe_grouped_product(p, w_down, offsets, workspace=work)
