@@ -41,14 +41,23 @@ class ExpertMLP(torch.autograd.Function):
     def backward(ctx, grad_out):
         x8, xs, codes, scales, y, weights, w_gate, w_up, w_down, offsets, route_row = ctx.saved_tensors
         work, I = ctx.work, w_gate.shape[2]
+        need_x, need_weights, need_gate, need_up, need_down = ctx.needs_input_grad[:5]
+        grad_x = grad_gate = grad_up = grad_down = None
         grad_y, grad_weights = moe.moe_token_unsort_grad(grad_out.contiguous(), y, route_row, weights)
-        grad_gu, p = moe.moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, workspace=work)
-        grad_down = moe.moe_grouped_weight_grad(p, grad_y, offsets, dtype=w_down.dtype, workspace=work)
-        rows = moe.moe_checkpoint_dequantize(x8, xs, dtype=y.dtype, route_row=route_row)
-        grad_gate = moe.moe_grouped_weight_grad(rows, grad_gu[:, :I], offsets, dtype=w_gate.dtype, workspace=work)
-        grad_up = moe.moe_grouped_weight_grad(rows, grad_gu[:, I:], offsets, dtype=w_up.dtype, workspace=work)
-        grad_rows = moe.moe_grouped_product(grad_gu, (w_gate, w_up), offsets, transposed=True, workspace=work)
-        return moe.moe_token_sort_grad(grad_rows, route_row), grad_weights, grad_gate, grad_up, grad_down, None, None, None, None
+        if need_x or need_gate or need_up or need_down:
+            grad_gu, p = moe.moe_grouped_gated_product_grad(grad_y, w_down, offsets, codes, scales, workspace=work)
+        if need_down:
+            grad_down = moe.moe_grouped_weight_grad(p, grad_y, offsets, dtype=w_down.dtype, workspace=work)
+        if need_gate or need_up:
+            rows = moe.moe_checkpoint_dequantize(x8, xs, dtype=y.dtype, route_row=route_row)
+        if need_gate:
+            grad_gate = moe.moe_grouped_weight_grad(rows, grad_gu[:, :I], offsets, dtype=w_gate.dtype, workspace=work)
+        if need_up:
+            grad_up = moe.moe_grouped_weight_grad(rows, grad_gu[:, I:], offsets, dtype=w_up.dtype, workspace=work)
+        if need_x:
+            grad_rows = moe.moe_grouped_product(grad_gu, (w_gate, w_up), offsets, transposed=True, workspace=work)
+            grad_x = moe.moe_token_sort_grad(grad_rows, route_row)
+        return grad_x, grad_weights if need_weights else None, grad_gate, grad_up, grad_down, None, None, None, None
 
 
 class GroupedExperts(torch.nn.Module):
