@@ -1272,7 +1272,19 @@ static int store_width(const void *p, int64_t pitch_bytes) {
 cudaError_t launch_grouped(const GroupedArgs &g, cudaStream_t stream) {
     GgArgs a{};
     const bool weights = g.mode == Grouped::kWeights, grad = g.mode == Grouped::kGatedGrad;
-    const bool small = !weights && (g.rows <= 32 || g.rows < 8 * (int64_t)g.E);
+    // Small tile up to 128 rows, whatever their experts, and below 8 rows an expert up to 1024 rows.  Large /
+    // small, us, gate and up with codes, down, down transposed, H = 2048, I = 768 (H = 1056, I = 352):
+    //   128 rows, 4 experts of 4            12.0/10.0  7.6/7.1   11.2/8.9   (8.6/7.0   6.1/5.0   7.7/6.3)
+    //   128 rows, one expert                13.7/9.3   8.5/6.1   12.1/8.1   (9.9/7.0   7.0/5.1   8.9/6.3)
+    //   256 rows, 4 experts of 4            12.7/14.1  8.2/8.7   11.6/9.3   (8.9/7.3   6.4/5.2   7.9/6.3)
+    //   512 rows, routed to 24              27.2/28.9  13.1/14.3 12.3/13.8  (9.0/10.5  7.9/7.6   8.2/6.9)
+    //   512 rows, routed to 128: 103        96.1/94.5  50.7/48.4 53.9/49.4  (28.7/26.0 16.2/13.9 15.7/13.8)
+    //   1016 rows, routed to 128: 115       105/110    55.5/52.8 58.1/53.0  (31.1/26.4 18.0/15.4 18.6/13.9)
+    //   2048 rows, routed to 128: 121       111/120    57.6/63.8 62.4/63.0
+    // The groups' sizes are not known here.  Rows that all go to one expert of many, whose weights every 16 of
+    // them read again from L2, cost the small tile 31 us for 19 with 1016 rows and 96 for 26 with 4096: hence
+    // the bound of 1024.
+    const bool small = !weights && (g.rows <= 128 || (g.rows < 8 * (int64_t)g.E && g.rows < 1024));
     const uint32_t depth = small ? GgSmall::kK : GgLarge::kK;
     const uint32_t side = small ? GgSmall::kSide : GgLarge::kSide, fmt = g.half ? 0u : 1u;
     const bool a_major = !(g.transposed || grad);  // the M side's operand is channel-major

@@ -207,3 +207,17 @@ def test_fp32_weight_grad_keeps_small_shares(dtype, sizes):
     for e, n in enumerate(sizes):
         assert float((got[e] - want[e]).abs().max()) <= (15 + (-(-n // FINE) - 1) if n else 0)
     assert moe.moe_read_device_status(work) == 0
+
+
+@pytest.mark.parametrize("rows,E", [(127, 3), (128, 3), (129, 3), (129, 40), (1023, 150), (1024, 150)])
+def test_tiles_at_the_borders_of_their_choice(rows, E):
+    """All rows of one expert, and rows spread over all: around the numbers at which the tile changes."""
+    g = gen(rows + E)
+    x = torch.randint(-3, 4, (rows, 72), generator=g, device="cuda").to(BF16)
+    w = torch.randint(-3, 4, (E, 72, 136), generator=g, device="cuda").to(BF16)
+    work = workspace()
+    for sizes in ([0] * (E - 1) + [rows], [rows // E + (e < rows % E) for e in range(E)]):
+        offsets = ref.groups(sizes)
+        got = moe.moe_grouped_product(x, w, offsets.cuda(), dtype=F32, workspace=work)
+        assert torch.equal(got.double(), ref.product(x, w, offsets))
+    assert moe.moe_read_device_status(work) == 0
