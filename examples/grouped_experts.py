@@ -100,8 +100,11 @@ def train(M=512, H=128, I=192, E=8, k=2, steps=60, device="cuda", seed=0, code=t
 
 def memory(M=8192, H=2048, I=768, k=8):
     """Bytes kept between the passes for M tokens: (in 16 bits: sorted rows, g, u, p and y; in 8)."""
-    R, eight = M * k, 1 + 1 / 32
-    return 2 * R * (2 * H + 3 * I), int(eight * (M * H + 2 * R * I)) + 2 * R * H
+    R = M * k
+
+    def eight(rows, cols):  # codes, and scales in rows of whole 16 bytes
+        return rows * (cols + -(-cols // 512) * 16)
+    return 2 * R * (2 * H + 3 * I), eight(M, H) + eight(R, 2 * I) + 2 * R * H
 
 
 def main():
