@@ -4,9 +4,10 @@
 // A block is 32 consecutive values of a row.  Its scale is a power of two 2^X held as the byte
 // X + 127, with X the smallest integer from -127 up with max|x| <= Q 2^X; Q is the largest code,
 // 448 (E4M3) or 127 (int8).  A value's code is x / 2^X rounded to the nearest code, ties to even.
-// Division by 2^X is exact and no code saturates, so a value is off by at most half a step of its
-// code: 2^-4 of itself in E4M3 (from 2^-6 2^X up), 2^X / 2 <= max / 127 in int8.  (A scale of any
-// other value would round the quotient first, and a code next to a border would depend on how.)
+// Division by 2^X is exact and no code saturates, so a value x is off by at most half a step of its
+// code: 2^-4 |x| or, below 2^-6 2^X, 2^-10 2^X in E4M3; 2^X / 2 in int8, which is max / 127 at most where
+// X > -127.  (A scale of any other value would round the quotient first, and a code next to a border
+// would depend on how.)
 // A block without a nonzero value has scale byte 0; a block with an infinity or a NaN has scale
 // byte 255, which makes all its values NaN, and codes 0.  int8 keeps no sign of zero.
 //
@@ -82,9 +83,9 @@ __device__ __forceinline__ void store16(T *dst, const T (&o)[16]) {
 }
 
 // A unit as above.  With route_row a token's codes are read once and its values stored to the rows
-// of its k routes (zeros to a dropped route's row).  A value is exact in bf16 and fp32 (fp32 alone
-// holds those below 2^-133); fp16 rounds it, to infinity past its range.  Memory bound: 8192 tokens of
-// 2048 into 65,536 rows in 45 us, 6.3 TB/s, 0.93 of the copy rate.
+// of its k routes (zeros to a dropped route's row).  A value is exact in fp32, and in bf16 from 2^-126 up;
+// fp16 rounds it, to infinity past its range.  Memory bound: 8192 tokens of 2048 into 65,536 rows in 45
+// us, 6.3 TB/s, 0.93 of the copy rate.
 template <typename T, int kBytes, bool kInt8, bool kRouted>
 __global__ void __launch_bounds__(256) eight_dequantize_kernel(const EightArgs a) {
     pdl_wait();
