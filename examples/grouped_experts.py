@@ -3,7 +3,8 @@
 ``ExpertMLP``: the gated expert MLPs of a layer as one function with gradients. The tokens are
 sorted by expert, multiplied by the experts' weights group by group, and brought back with the
 router's weights. Between the passes it keeps x, g and u in 8 bits (and y, which the router's
-gradient needs); p is computed again and the sorted rows are restored from the tokens.
+gradient needs); p is computed again and the sorted rows are restored from the tokens. What goes from
+call to call is of x's type, so outputs and gradients pass three to four roundings to it.
 
 ``train``: a few steps of it towards a fixed target; ``memory``: what it keeps, beside 16 bits.
 

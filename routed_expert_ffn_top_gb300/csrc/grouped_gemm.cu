@@ -48,8 +48,8 @@
 // them, 7 to 4104 rows at 8192 tokens):
 //   one group  65536 rows, K = N = 2048: 315 us, 1.75 PFLOP/s (the library's product: 308); K = 768: 132
 //              us (121); 16384 x 8192 x 8192: 1.18 ms (1.05 to 1.28).  MMAs, and the power they take.
-//   8192       gate and up 265 us, 1.55 PFLOP/s and 4.4 TB/s; down 150 us, 1.37 PFLOP/s and 5.1 TB/s;
-//   tokens     weights' gradient in fp32 234 us, 5.0 TB/s.  The weights' first way from HBM and the MMAs
+//   8192       gate and up 270 us, 1.52 PFLOP/s and 4.3 TB/s; down 155 us, 1.33 PFLOP/s and 5.0 TB/s;
+//   tokens     weights' gradient in fp32 241 us, 4.9 TB/s.  The weights' first way from HBM and the MMAs
 //              both: groups of under 215 rows take longer to copy than to multiply, and equal groups of
 //              512 rows take 245 and 137 us.
 //   4096       with the checkpoint 185 us, down's gradient through the gate 130 us, 1.04 and 0.74 GB: HBM,
